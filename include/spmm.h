@@ -39,6 +39,7 @@ extern "C" {
 #endif
 
 typedef struct spmm_handle_s *spmm_handle;
+typedef struct spmm_adapters_s *spmm_adapters;
 
 typedef enum {
     SPMM_OK = 0,
@@ -332,6 +333,134 @@ spmm_status spmm_wcsr_run_noalloc(const int64_t *window_row_ptr, const int32_t *
  * Errors: CUDA (the copy or the synchronisation).
  */
 spmm_status spmm_wcsr_noalloc_check(void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside the shared projection, the layer
+ * a server of one pruned weight with per-request fine-tunings runs, and the
+ * one that tunes such adapters on the frozen weight.  The AsyncSparse pages
+ * have no counterpart; the projection is spmm_run_linear's.
+ *
+ * The rows of a batch are grouped into segments (a request, or an expert's
+ * tokens): rows [seg_ptr[s], seg_ptr[s + 1]) use adapter seg_adapter[s], or
+ * none where that is -1; rows outside every segment use none.  For a row n with
+ * adapter a
+ *     h[n] = scale[a] * D_a x[n]        Y[n] = A x[n] + U_a h[n]
+ * with D_a rank x k ("down") and U_a m x rank ("up"); other rows get A x[n].
+ * Rows are independent: an adapter that holds infinities or NaN reaches its
+ * own rows only.
+ *
+ * A set holds the shapes and the workspace of one layer's adapters, not their
+ * weights: those are the caller's and are passed to every call.  Like a handle
+ * it must not be used by two host threads at once, and calls on it in
+ * different streams must not overlap on the GPU.
+ *
+ * spmm_adapters_create
+ *   m, k          the projection's shape, multiples of 8.
+ *   n_adapters    adapters in the pool, 1..65535; n_adapters * max(m, k) < 2^31.
+ *   rank          of every adapter in the pool, a multiple of 8 up to 128
+ *                 (adapters of lower rank are padded with zeros).
+ *   in_t          SPMM_F16 or SPMM_BF16, the type of X and of the adapters.
+ *   max_rows, max_segments   the largest batch that calls will bring.
+ *   grad          nonzero to hold the workspace of spmm_adapters_grad too.
+ * Errors: INVALID_ARG, UNSUPPORTED (m, k or rank not a multiple of 8, rank
+ * above 128), OOM, CUDA.  spmm_adapters_destroy waits for the device and frees
+ * the set.
+ */
+spmm_status spmm_adapters_create(spmm_adapters *out, int64_t m, int64_t k, int32_t n_adapters, int32_t rank,
+                                 spmm_dtype in_t, int64_t max_rows, int64_t max_segments, int32_t grad);
+spmm_status spmm_adapters_destroy(spmm_adapters a);
+
+/*
+ * spmm_run_linear_adapters -- Y = X * A^T plus each row's adapter.
+ *   h            a BCSR handle (64 x 64 blocks) of the set's m, k and in_t.
+ *   X, Y         as for spmm_run_linear (Y of the handle's out_t).
+ *   N            rows, 0..max_rows; N = 0 does nothing.
+ *   down, up     device, n_adapters x rank x k and n_adapters x m x rank,
+ *                in_t, 16-byte aligned.
+ *   scale        device float[n_adapters].
+ *   seg_ptr      device int64[n_seg + 1], non-decreasing, each in [0, N].
+ *   seg_adapter  device int32[n_seg], -1 or an index into the pool.
+ * The segments are read on the device only, so a batch can be described by
+ * arrays that earlier work on the stream writes (spmm_route_sort's offsets).
+ * An index outside the pool counts as -1 and is reported by spmm_check(h) as
+ * SPMM_ERR_DEVICE_CHECK.  fp32 sums throughout; asynchronous; results are
+ * bitwise reproducible run to run.
+ * Errors: as spmm_run_linear, plus INVALID_ARG for shapes, types or devices
+ * that do not match and batches above the set's limits.
+ */
+spmm_status spmm_run_linear_adapters(spmm_handle h, spmm_adapters a, const void *X, void *Y, int64_t N,
+                                     const void *down, const void *up, const float *scale, const int64_t *seg_ptr,
+                                     const int32_t *seg_adapter, int64_t n_seg, void *stream);
+
+/*
+ * spmm_adapters_grad -- the gradients of spmm_run_linear_adapters with respect
+ * to X and to the adapters' weights, the shared weight being frozen:
+ *     dh[n] = scale[a] * U_a^T dY[n]
+ *     dX[n] = A^T dY[n] + D_a^T dh[n]
+ *     d_up_a = sum_n dY[n] h[n]^T       d_down_a = sum_n dh[n] X[n]^T
+ * the sums over the rows of adapter a, in a fixed order.
+ *   h_t      a BCSR handle of A^T (k x m), of the set's in_t; dX has its out_t.
+ *   X, dY    N x k and N x m row-major, in_t, 16-byte aligned.
+ *   dX       N x k, or NULL where no gradient of the input is wanted.
+ *   d_down, d_up   device, shaped as down and up, in_t, fully overwritten
+ *            (adapters without rows get 0, also when N = 0).
+ *   others   as for spmm_run_linear_adapters.
+ * Errors: as spmm_run_linear_adapters; INVALID_ARG for a set created without
+ * the gradient's workspace.
+ */
+spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, const void *dY, void *dX, void *d_down,
+                               void *d_up, int64_t N, const void *down, const void *up, const float *scale,
+                               const int64_t *seg_ptr, const int32_t *seg_adapter, int64_t n_seg, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Tokens sorted by expert and back.  A routing is T x topk expert ids; entry
+ * t * topk + j is token t's j-th expert.  An id outside [0, n_experts) (-1 for
+ * a token over capacity) drops its entry.
+ *
+ * spmm_route_sort -- stable counting sort of the entries by expert.
+ *   ids        device int32[T * topk].
+ *   n_experts  1..2048;  topk 1..32;  T * topk < 2^31;  T = 0 is an empty batch.
+ *   offsets    device int64[n_experts + 1]: expert e's slots are
+ *              [offsets[e], offsets[e + 1]); offsets[n_experts] entries are kept.
+ *              Usable as seg_ptr of the adapters' calls.
+ *   order      device int32[T * topk]: the entry of every slot, -1 past the last.
+ *   position   device int32[T * topk]: the slot of every entry, -1 if dropped.
+ *   workspace  device, spmm_route_workspace_bytes(...) bytes, 4-byte aligned
+ *              (NULL where that is 0); free for other use once the call's work
+ *              has run.
+ */
+int64_t spmm_route_workspace_bytes(int64_t T, int32_t topk, int32_t n_experts);
+spmm_status spmm_route_sort(const int32_t *ids, int64_t T, int32_t topk, int32_t n_experts, int64_t *offsets,
+                            int32_t *order, int32_t *position, void *workspace, void *stream);
+
+/*
+ * Rows of d elements (dtype F16, BF16 or F32; any d >= 1) between token order
+ * (T rows) and slot order (T * topk rows), all row-major, asynchronous, fp32
+ * arithmetic, bitwise reproducible.  Entries whose position lies outside
+ * [0, T * topk) are dropped; position has no slot twice.
+ *
+ * spmm_route_gather        out[position[t, j]] = x[t]; slots from *n_kept (device,
+ *                          &offsets[n_experts]) on are set to 0.
+ * spmm_route_combine       out[t] = sum over j of weights[t, j] * y[position[t, j]]
+ *                          (weights NULL: ones); a token without entries gets 0.
+ *                          With NULL weights it is the gradient of the gather.
+ * spmm_route_combine_grad  dy[position[t, j]] = weights[t, j] * dout[t], slots from
+ *                          *n_kept on 0; dweights[t, j] = <dout[t], y[position[t, j]]>,
+ *                          0 for dropped entries.
+ * Bases that are 16-byte aligned with d * element size a multiple of 16 take
+ * 16-byte accesses; others run element by element.
+ * Errors: INVALID_ARG (NULL, sizes, dtype), UNSUPPORTED (topk > 32, T * topk
+ * >= 2^31, a base not aligned to its element), CUDA (launch).
+ */
+spmm_status spmm_route_gather(const void *x, const int32_t *position, const int64_t *n_kept, void *out, int64_t T,
+                              int32_t topk, int64_t d, spmm_dtype dtype, void *stream);
+spmm_status spmm_route_combine(const void *y, const int32_t *position, const float *weights, void *out, int64_t T,
+                               int32_t topk, int64_t d, spmm_dtype dtype, void *stream);
+spmm_status spmm_route_combine_grad(const void *dout, const void *y, const int32_t *position, const float *weights,
+                                    const int64_t *n_kept, void *dy, float *dweights, int64_t T, int32_t topk, int64_t d,
+                                    spmm_dtype dtype, void *stream);
 
 /* spmm_status_str -- static English name of a status. */
 const char *spmm_status_str(spmm_status s);

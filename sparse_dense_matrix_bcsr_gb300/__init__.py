@@ -12,7 +12,10 @@ plus ``spmm_format_info``, ``spmm_export_format``, ``spmm_check``,
 ``spmm_set_max_ctas``, ``spmm_run_host``, the host-only converters
 ``spmm_bcsr_convert`` / ``spmm_wcsr_convert`` and
 ``spmm_selftest_wait_timeout``.  ``run_torch`` is a convenience that passes
-torch tensors and the current stream.
+torch tensors and the current stream; ``Adapters`` (low-rank adapters beside
+the block-sparse linear layer) and ``route_sort`` / ``route_gather`` /
+``route_combine`` / ``route_combine_grad`` (tokens sorted by expert and back)
+do the same for the ``spmm_adapters_*`` and ``spmm_route_*`` calls.
 
 There is no fallback: if the shared library cannot be loaded, importing a
 function that needs it raises.
@@ -50,6 +53,9 @@ EXPORTS = (
     "spmm_check", "spmm_set_max_ctas", "spmm_selftest_wait_timeout", "spmm_status_str",
     "spmm_last_error", "spmm_wcsr_run_noalloc", "spmm_run_linear", "spmm_set_schedule",
     "spmm_probe_l2_read", "spmm_wcsr_noalloc_check",
+    "spmm_adapters_create", "spmm_adapters_destroy", "spmm_run_linear_adapters", "spmm_adapters_grad",
+    "spmm_route_workspace_bytes", "spmm_route_sort", "spmm_route_gather", "spmm_route_combine",
+    "spmm_route_combine_grad",
 )
 
 
@@ -102,11 +108,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "spmm_probe_l2_read": [P, I64, I32, P, P],
         "spmm_wcsr_noalloc_check": [P],
         "spmm_wcsr_run_noalloc": [P, P, P, I64, I64, I64, I32, I32, P, P, I64, P],
+        "spmm_adapters_create": [ctypes.POINTER(P), I64, I64, I32, I32, I32, I64, I64, I32],
+        "spmm_adapters_destroy": [P],
+        "spmm_run_linear_adapters": [P, P, P, P, I64, P, P, P, P, P, I64, P],
+        "spmm_adapters_grad": [P, P, P, P, P, P, P, I64, P, P, P, P, P, I64, P],
+        "spmm_route_sort": [P, I64, I32, I32, P, P, P, P, P],
+        "spmm_route_gather": [P, P, P, P, I64, I32, I64, I32, P],
+        "spmm_route_combine": [P, P, P, P, I64, I32, I64, I32, P],
+        "spmm_route_combine_grad": [P, P, P, P, P, P, P, I64, I32, I64, I32, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = st
+    lib.spmm_route_workspace_bytes.argtypes = [I64, I32, I32]
+    lib.spmm_route_workspace_bytes.restype = I64
     lib.spmm_status_str.argtypes = [st]
     lib.spmm_status_str.restype = ctypes.c_char_p
     lib.spmm_last_error.argtypes = []
@@ -290,6 +306,59 @@ def spmm_wcsr_convert(m, k, row_ptr, col_idx, vals, window_h=16, col_pad=16):
     return ptr, idx[:P], values[: P * window_h].reshape(window_h, P)
 
 
+def spmm_adapters_create(m, k, n_adapters, rank, in_t="bf16", max_rows=0, max_segments=0, grad=False) -> int:
+    a = ctypes.c_void_p()
+    _check(load_library().spmm_adapters_create(ctypes.byref(a), m, k, n_adapters, rank, _dt(in_t), max_rows,
+                                               max_segments, int(grad)), "spmm_adapters_create")
+    return a.value
+
+
+def spmm_adapters_destroy(a: int) -> None:
+    _check(load_library().spmm_adapters_destroy(a), "spmm_adapters_destroy")
+
+
+def spmm_run_linear_adapters(h: int, a: int, X: int, Y: int, N: int, down: int, up: int, scale: int, seg_ptr: int,
+                             seg_adapter: int, n_seg: int, stream: int = 0) -> None:
+    """Y = X * A^T plus each row's low-rank adapter (device pointers; see include/spmm.h)."""
+    _check(load_library().spmm_run_linear_adapters(h, a, X, Y, N, down, up, scale, seg_ptr, seg_adapter, n_seg,
+                                                   stream or None), "spmm_run_linear_adapters")
+
+
+def spmm_adapters_grad(h_t: int, a: int, X: int, dY: int, dX: int, d_down: int, d_up: int, N: int, down: int, up: int,
+                       scale: int, seg_ptr: int, seg_adapter: int, n_seg: int, stream: int = 0) -> None:
+    """Gradients of spmm_run_linear_adapters (h_t: handle of A^T; dX may be None)."""
+    _check(load_library().spmm_adapters_grad(h_t, a, X, dY, dX, d_down, d_up, N, down, up, scale, seg_ptr, seg_adapter,
+                                             n_seg, stream or None), "spmm_adapters_grad")
+
+
+def spmm_route_workspace_bytes(T: int, topk: int, n_experts: int) -> int:
+    return load_library().spmm_route_workspace_bytes(T, topk, n_experts)
+
+
+def spmm_route_sort(ids: int, T: int, topk: int, n_experts: int, offsets: int, order: int, position: int,
+                    workspace: int, stream: int = 0) -> None:
+    """Stable sort of T x topk expert ids: offsets, order and position (device pointers)."""
+    _check(load_library().spmm_route_sort(ids, T, topk, n_experts, offsets, order, position, workspace, stream or None),
+           "spmm_route_sort")
+
+
+def spmm_route_gather(x: int, position: int, n_kept: int, out: int, T: int, topk: int, d: int, dtype, stream: int = 0) -> None:
+    _check(load_library().spmm_route_gather(x, position, n_kept, out, T, topk, d, _dt(dtype), stream or None),
+           "spmm_route_gather")
+
+
+def spmm_route_combine(y: int, position: int, weights: int, out: int, T: int, topk: int, d: int, dtype,
+                       stream: int = 0) -> None:
+    _check(load_library().spmm_route_combine(y, position, weights, out, T, topk, d, _dt(dtype), stream or None),
+           "spmm_route_combine")
+
+
+def spmm_route_combine_grad(dout: int, y: int, position: int, weights: int, n_kept: int, dy: int, dweights: int, T: int,
+                            topk: int, d: int, dtype, stream: int = 0) -> None:
+    _check(load_library().spmm_route_combine_grad(dout, y, position, weights, n_kept, dy, dweights, T, topk, d, _dt(dtype),
+                                                  stream or None), "spmm_route_combine_grad")
+
+
 # ---------------------------------------------------------------- torch glue
 def _torch_stream_ptr():
     import torch
@@ -340,3 +409,136 @@ class SpMM:
             self.close()
         except Exception:
             pass
+
+
+def _tensor(t, name, dtype, shape):
+    """Raises ValueError unless t is a contiguous CUDA tensor of this dtype and shape."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor {dtype} {shape}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+class Adapters:
+    """Low-rank adapters of many requests beside one block-sparse linear layer.
+
+    Holds the shapes and the workspace for batches of up to `max_rows` rows in
+    up to `max_segments` segments; the adapters' weights are the caller's:
+    down [n_adapters, rank, k], up [n_adapters, m, rank], scale [n_adapters]
+    (fp32).  Rows [seg_ptr[s], seg_ptr[s + 1]) use adapter seg_adapter[s], -1 for
+    none (int64 / int32 CUDA tensors, read on the device only)."""
+
+    def __init__(self, m: int, k: int, n_adapters: int, rank: int, in_t="bf16", max_rows: int = 0,
+                 max_segments: int = 0, grad: bool = True):
+        import torch
+        self.m, self.k, self.n_adapters, self.rank = m, k, n_adapters, rank
+        self._dtype = {SPMM_F16: torch.float16, SPMM_BF16: torch.bfloat16}.get(_dt(in_t))
+        self._out = {SPMM_BF16: torch.bfloat16, SPMM_F32: torch.float32}
+        self._index, self._ids, self._scale = torch.int64, torch.int32, torch.float32
+        self.a = spmm_adapters_create(m, k, n_adapters, rank, in_t, max_rows, max_segments, grad)
+
+    def _batch(self, down, up, scale, seg_ptr, seg_adapter):
+        n_seg = seg_adapter.shape[0]
+        return (_tensor(down, "down", self._dtype, (self.n_adapters, self.rank, self.k)),
+                _tensor(up, "up", self._dtype, (self.n_adapters, self.m, self.rank)),
+                _tensor(scale, "scale", self._scale, (self.n_adapters,)),
+                _tensor(seg_ptr, "seg_ptr", self._index, (n_seg + 1,)),
+                _tensor(seg_adapter, "seg_adapter", self._ids, (n_seg,)), n_seg)
+
+    def linear(self, layer: SpMM, X, Y, down, up, scale, seg_ptr, seg_adapter, stream=None):
+        """Y = X * A^T plus each row's adapter, for a BCSR layer A (m x k); returns Y."""
+        N = X.shape[0]
+        x = _tensor(X, "X", self._dtype, (N, self.k))
+        y = _tensor(Y, "Y", self._out[_dt(layer.out_t)], (N, self.m))
+        spmm_run_linear_adapters(layer.h, self.a, x, y, N, *self._batch(down, up, scale, seg_ptr, seg_adapter),
+                                 stream.cuda_stream if stream is not None else _torch_stream_ptr())
+        return Y
+
+    def grad(self, layer_t: SpMM, X, dY, dX, d_down, d_up, down, up, scale, seg_ptr, seg_adapter, stream=None):
+        """Gradients of `linear` into dX (None to leave it out), d_down and d_up; layer_t holds A^T (k x m)."""
+        N = X.shape[0]
+        x = _tensor(X, "X", self._dtype, (N, self.k))
+        dy = _tensor(dY, "dY", self._dtype, (N, self.m))
+        dx = None if dX is None else _tensor(dX, "dX", self._out[_dt(layer_t.out_t)], (N, self.k))
+        dd = _tensor(d_down, "d_down", self._dtype, (self.n_adapters, self.rank, self.k))
+        du = _tensor(d_up, "d_up", self._dtype, (self.n_adapters, self.m, self.rank))
+        spmm_adapters_grad(layer_t.h, self.a, x, dy, dx, dd, du, N, *self._batch(down, up, scale, seg_ptr, seg_adapter),
+                           stream.cuda_stream if stream is not None else _torch_stream_ptr())
+
+    def close(self):
+        if getattr(self, "a", None):
+            spmm_adapters_destroy(self.a)
+            self.a = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _kept_ptr(offsets):
+    """Address of offsets[n_experts], the number of kept entries."""
+    import torch
+    n = offsets.shape[0]
+    return _tensor(offsets, "offsets", torch.int64, (n,)) + 8 * (n - 1)
+
+
+def _row_dtype(t):
+    import torch
+    dt = {torch.float16: SPMM_F16, torch.bfloat16: SPMM_BF16, torch.float32: SPMM_F32}.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"rows must be float16, bfloat16 or float32, got {t.dtype}")
+    return dt
+
+
+def route_sort(ids, n_experts: int):
+    """(offsets [n_experts + 1] int64, order [T * topk] int32, position [T, topk] int32) of expert ids [T, topk]
+    (int32; ids outside [0, n_experts) are dropped), on the current stream."""
+    import torch
+    T, topk = ids.shape
+    p = _tensor(ids, "ids", torch.int32, (T, topk))
+    offsets = torch.empty(n_experts + 1, dtype=torch.int64, device=ids.device)
+    both = torch.empty((2, T * topk), dtype=torch.int32, device=ids.device)
+    order, position = both[0], both[1].view(T, topk)
+    size = spmm_route_workspace_bytes(T, topk, n_experts)
+    work = torch.empty(size, dtype=torch.uint8, device=ids.device).data_ptr() if size else None
+    spmm_route_sort(p, T, topk, n_experts, offsets.data_ptr(), order.data_ptr(), position.data_ptr(), work,
+                    _torch_stream_ptr())
+    return offsets, order, position
+
+
+def route_gather(x, position, offsets):
+    """Rows of x [T, d] in slot order [T * topk, d]; slots that no entry takes are 0.  Current stream."""
+    import torch
+    (T, topk), d = position.shape, x.shape[1]
+    out = torch.empty((T * topk, d), dtype=x.dtype, device=x.device)
+    spmm_route_gather(_tensor(x, "x", x.dtype, (T, d)), _tensor(position, "position", torch.int32, (T, topk)),
+                      _kept_ptr(offsets), out.data_ptr(), T, topk, d, _row_dtype(x),
+                      _torch_stream_ptr())
+    return out
+
+
+def route_combine(y, position, weights=None):
+    """out[t] = sum_j weights[t, j] * y[position[t, j]] (weights None: ones), fp32 sums.  Current stream."""
+    import torch
+    (T, topk), d = position.shape, y.shape[1]
+    out = torch.empty((T, d), dtype=y.dtype, device=y.device)
+    spmm_route_combine(_tensor(y, "y", y.dtype, (T * topk, d)), _tensor(position, "position", torch.int32, (T, topk)),
+                       None if weights is None else _tensor(weights, "weights", torch.float32, (T, topk)),
+                       out.data_ptr(), T, topk, d, _row_dtype(y), _torch_stream_ptr())
+    return out
+
+
+def route_combine_grad(dout, y, position, weights, offsets):
+    """(dy [T * topk, d], dweights [T, topk] fp32) of route_combine.  Current stream."""
+    import torch
+    (T, topk), d = position.shape, y.shape[1]
+    dy = torch.empty_like(y)
+    dw = torch.empty((T, topk), dtype=torch.float32, device=y.device)
+    spmm_route_combine_grad(_tensor(dout, "dout", y.dtype, (T, d)), _tensor(y, "y", y.dtype, (T * topk, d)),
+                            _tensor(position, "position", torch.int32, (T, topk)),
+                            None if weights is None else _tensor(weights, "weights", torch.float32, (T, topk)),
+                            _kept_ptr(offsets), dy.data_ptr(), dw.data_ptr(), T, topk, d,
+                            _row_dtype(y), _torch_stream_ptr())
+    return dy, dw

@@ -1,0 +1,285 @@
+// adapters.cu -- low-rank adapters of many requests beside the shared
+// block-sparse projection (spmm_run_linear_adapters, spmm_adapters_grad):
+//   h[n] = scale[a] * D_a x[n],   y[n] = W x[n] + U_a h[n]
+// with a the adapter of row n's segment, D_a rank x k and U_a m x rank.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "segments.cuh"
+
+namespace spmm {
+namespace {
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&f)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 p;
+    if constexpr (BF16)
+      p = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[i]));
+    else
+      p = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+
+// ---------------------------------------------------------------- down projection, a few rows per segment
+// h[n][j] = scale * <D_a[j], x[n]> in fp32.  One block per (row that starts a
+// run, group of kShrinkRanks ranks): a run is the rows of one segment within 8
+// consecutive rows, so a row of D is read once for up to 8 rows of X and every
+// single-row request still has its own block.  The block's warps take 256-column
+// pieces of k in turn and add their sums in warp order.
+constexpr int kShrinkThreads = 256;
+constexpr int kShrinkWarps = kShrinkThreads / 32;
+constexpr int kShrinkRanks = 4;
+constexpr int kShrinkRows = 8;
+
+template <bool BF16, int ROWS>
+__device__ __forceinline__ void shrink_run(const uint4 *__restrict__ D, const uint4 *__restrict__ X, int32_t k8, int rows,
+                                           float (&acc)[kShrinkRanks][ROWS]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int32_t c = warp * 32 + lane; c < k8; c += kShrinkThreads) {
+    uint4 w[kShrinkRanks], x[ROWS];
+#pragma unroll
+    for (int j = 0; j < kShrinkRanks; ++j) w[j] = D[static_cast<int64_t>(j) * k8 + c];
+#pragma unroll
+    for (int t = 0; t < ROWS; ++t)
+      if (t < rows) x[t] = X[static_cast<int64_t>(t) * k8 + c];
+    float wf[kShrinkRanks][8];
+#pragma unroll
+    for (int j = 0; j < kShrinkRanks; ++j) unpack8<BF16>(w[j], wf[j]);
+#pragma unroll
+    for (int t = 0; t < ROWS; ++t) {
+      if (t >= rows) continue;
+      float xf[8];
+      unpack8<BF16>(x[t], xf);
+#pragma unroll
+      for (int j = 0; j < kShrinkRanks; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[j][t] = fmaf(wf[j][i], xf[i], acc[j][t]);
+    }
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kShrinkThreads) shrink_rows_kernel(const AdapterParams p) {
+  const int64_t n = blockIdx.x;
+  const int32_t s = find_segment(p.seg_ptr, p.n_seg, n);
+  if (s < 0) return;
+  const int64_t b = p.seg_ptr[s], e = min(p.seg_ptr[s + 1], static_cast<int64_t>(p.N));
+  const int64_t group = n / kShrinkRows * kShrinkRows;
+  if (n != max(b, group)) return;
+  const int rows = static_cast<int>(min(e, group + kShrinkRows) - n);
+  const int32_t a = segment_adapter(p.seg_adapter, s, p.n_adapters, p.status);
+  if (a < 0) return;
+  const int32_t j0 = blockIdx.y * kShrinkRanks;
+  const int32_t k8 = p.K / 8;
+  const uint4 *D = static_cast<const uint4 *>(p.down) + (static_cast<int64_t>(a) * p.rank + j0) * k8;
+  const uint4 *X = static_cast<const uint4 *>(p.X) + n * k8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float sums[kShrinkWarps][kShrinkRanks][kShrinkRows];
+  if (rows == 1) {
+    float acc[kShrinkRanks][1] = {};
+    shrink_run<BF16, 1>(D, X, k8, 1, acc);
+#pragma unroll
+    for (int j = 0; j < kShrinkRanks; ++j) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[j][0] += __shfl_xor_sync(0xffffffffu, acc[j][0], o);
+      if (lane == 0) sums[warp][j][0] = acc[j][0];
+    }
+  } else {
+    float acc[kShrinkRanks][kShrinkRows] = {};
+    shrink_run<BF16, kShrinkRows>(D, X, k8, rows, acc);
+#pragma unroll
+    for (int j = 0; j < kShrinkRanks; ++j)
+#pragma unroll
+      for (int t = 0; t < kShrinkRows; ++t) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc[j][t] += __shfl_xor_sync(0xffffffffu, acc[j][t], o);
+        if (lane == 0) sums[warp][j][t] = acc[j][t];
+      }
+  }
+  __syncthreads();
+  const int t = threadIdx.x / kShrinkRanks, j = threadIdx.x % kShrinkRanks;
+  if (t < rows) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kShrinkWarps; ++w) v += sums[w][j][t];
+    p.H[(n + t) * p.rank + j0 + j] = v * p.scale[a];
+  }
+}
+
+// ---------------------------------------------------------------- projection with adapters
+// One block per (block row, 16 rows of X): a thread holds one output feature of
+// four rows, walks the block row's stored blocks 8 columns at a time and adds
+// its rows' adapters.
+constexpr int kExpandThreads = 256;
+constexpr int kExpandRows = 16;
+template <bool BF16, bool OUT_BF16>
+__global__ void __launch_bounds__(kExpandThreads) linear_adapters_kernel(const AdapterParams p) {
+  __shared__ int32_t adapter[kExpandRows];
+  const int32_t br = blockIdx.x;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kExpandRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = warp; r < kExpandRows; r += kExpandThreads / 32) {
+    int32_t a = -1;
+    if (n0 + r < p.N) {
+      const int32_t s = find_segment(p.seg_ptr, p.n_seg, n0 + r);
+      if (s >= 0) a = segment_adapter(p.seg_adapter, s, p.n_adapters, p.status);
+    }
+    if (lane == 0) adapter[r] = a;
+  }
+  __syncthreads();
+  const int f = threadIdx.x & 63, q = threadIdx.x >> 6;
+  float acc[4] = {};
+  for (int64_t j = p.block_row_ptr[br]; j < p.block_row_ptr[br + 1]; ++j) {
+    const int32_t c0 = p.block_col_idx[j] * 64;
+    const uint4 *blk = static_cast<const uint4 *>(p.blocks) + (j * 64 + f) * 8;
+    for (int c = 0; c < 8 && c0 + c * 8 < p.K; ++c) {
+      float w[8];
+      unpack8<BF16>(blk[c], w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t n = n0 + q * 4 + i;
+        if (n >= p.N) continue;
+        float x[8];
+        unpack8<BF16>(static_cast<const uint4 *>(p.X)[(n * p.K + c0) / 8 + c], x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[i] = fmaf(w[e], x[e], acc[i]);
+      }
+    }
+  }
+  const int32_t feature = br * 64 + f;
+  if (feature >= p.M) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t n = n0 + q * 4 + i;
+    if (n >= p.N) continue;
+    const int32_t a = adapter[q * 4 + i];
+    if (a >= 0) {
+      const uint4 *U = static_cast<const uint4 *>(p.up) + (static_cast<int64_t>(a) * p.M + feature) * (p.rank / 8);
+      for (int c = 0; c < p.rank / 8; ++c) {
+        float u[8];
+        unpack8<BF16>(U[c], u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[i] = fmaf(u[e], p.H[n * p.rank + c * 8 + e], acc[i]);
+      }
+    }
+    if constexpr (OUT_BF16)
+      static_cast<__nv_bfloat16 *>(p.Y)[n * p.M + feature] = __float2bfloat16_rn(acc[i]);
+    else
+      static_cast<float *>(p.Y)[n * p.M + feature] = acc[i];
+  }
+}
+
+// ---------------------------------------------------------------- adapter weights, transposed
+// out[a][c][r] = in[a][r][c]: the gradient runs the forward kernels with the
+// roles of D and U exchanged, which want both in the other order.
+__global__ void __launch_bounds__(256) transpose_kernel(const uint16_t *__restrict__ in, uint16_t *__restrict__ out,
+                                                        int32_t rows, int32_t cols) {
+  __shared__ uint16_t tile[32][33];
+  const int64_t base = static_cast<int64_t>(blockIdx.z) * rows * cols;
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int c0 = blockIdx.x * 32, r0 = blockIdx.y * 32;
+  for (int i = ty; i < 32; i += 8)
+    if (r0 + i < rows && c0 + tx < cols) tile[i][tx] = in[base + static_cast<int64_t>(r0 + i) * cols + c0 + tx];
+  __syncthreads();
+  for (int i = ty; i < 32; i += 8)
+    if (c0 + i < cols && r0 + tx < rows) out[base + static_cast<int64_t>(c0 + i) * rows + r0 + tx] = tile[tx][i];
+}
+
+// ---------------------------------------------------------------- adapter weight gradients
+// G_a[f][i] = sum over rows n of adapter a of V[n][f] * H[n][i]: one block per
+// (64 features, adapter), which walks the adapter's segments in order.
+// UP writes G as [feature][rank] (dU), else as [rank][feature] (dD).
+constexpr int kWgradThreads = 256;
+template <bool BF16, bool UP>
+__global__ void __launch_bounds__(kWgradThreads) wgrad_kernel(const AdapterParams p, const uint16_t *__restrict__ V,
+                                                              int32_t F, uint16_t *__restrict__ G) {
+  const int32_t a = blockIdx.y;
+  const int32_t feature = blockIdx.x * 64 + (threadIdx.x & 63);
+  const int q = threadIdx.x >> 6;
+  float acc[32] = {};
+  for (int32_t s = 0; s < p.n_seg; ++s) {
+    if (p.seg_adapter[s] != a) continue;
+    const int64_t b = max(p.seg_ptr[s], int64_t{0}), e = min(p.seg_ptr[s + 1], static_cast<int64_t>(p.N));
+    for (int64_t n = b; n < e; ++n) {
+      float v = 0.0f;
+      if (feature < F) {
+        const uint16_t bits = V[n * F + feature];
+        v = BF16 ? __bfloat162float(__ushort_as_bfloat16(bits)) : __half2float(__ushort_as_half(bits));
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (q + 4 * i < p.rank) acc[i] = fmaf(v, p.H[n * p.rank + q + 4 * i], acc[i]);
+    }
+  }
+  if (feature >= F) return;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const int32_t r = q + 4 * i;
+    if (r >= p.rank) continue;
+    const uint16_t bits = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(acc[i])) : __half_as_ushort(__float2half_rn(acc[i]));
+    const int64_t base = static_cast<int64_t>(a) * p.rank * F;
+    G[base + (UP ? static_cast<int64_t>(feature) * p.rank + r : static_cast<int64_t>(r) * F + feature)] = bits;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_shrink(const AdapterParams &p, bool bf16, cudaStream_t s) {
+  if (p.n_seg == 0) return cudaSuccess;
+  const dim3 grid(static_cast<unsigned>(p.N), static_cast<unsigned>(p.rank / kShrinkRanks));
+  if (bf16)
+    shrink_rows_kernel<true><<<grid, kShrinkThreads, 0, s>>>(p);
+  else
+    shrink_rows_kernel<false><<<grid, kShrinkThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_linear_adapters(const AdapterParams &p, bool bf16, bool out_bf16, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((p.M + 63) / 64), static_cast<unsigned>((p.N + kExpandRows - 1) / kExpandRows));
+  if (bf16) {
+    if (out_bf16)
+      linear_adapters_kernel<true, true><<<grid, kExpandThreads, 0, s>>>(p);
+    else
+      linear_adapters_kernel<true, false><<<grid, kExpandThreads, 0, s>>>(p);
+  } else {
+    if (out_bf16)
+      linear_adapters_kernel<false, true><<<grid, kExpandThreads, 0, s>>>(p);
+    else
+      linear_adapters_kernel<false, false><<<grid, kExpandThreads, 0, s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_transpose(const void *in, void *out, int32_t n, int32_t rows, int32_t cols, cudaStream_t s) {
+  const dim3 grid((cols + 31) / 32, (rows + 31) / 32, n);
+  transpose_kernel<<<grid, 256, 0, s>>>(static_cast<const uint16_t *>(in), static_cast<uint16_t *>(out), rows, cols);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_wgrad(const AdapterParams &p, const void *V, int32_t features, void *G, bool up, bool bf16,
+                         cudaStream_t s) {
+  const dim3 grid((features + 63) / 64, p.n_adapters);
+  const uint16_t *v = static_cast<const uint16_t *>(V);
+  uint16_t *g = static_cast<uint16_t *>(G);
+  if (bf16) {
+    if (up)
+      wgrad_kernel<true, true><<<grid, kWgradThreads, 0, s>>>(p, v, features, g);
+    else
+      wgrad_kernel<true, false><<<grid, kWgradThreads, 0, s>>>(p, v, features, g);
+  } else {
+    if (up)
+      wgrad_kernel<false, true><<<grid, kWgradThreads, 0, s>>>(p, v, features, g);
+    else
+      wgrad_kernel<false, false><<<grid, kWgradThreads, 0, s>>>(p, v, features, g);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace spmm

@@ -1,0 +1,319 @@
+// adapters_api.cu -- C entry points of the low-rank adapters beside the
+// block-sparse projection and of the expert routing (include/spmm.h):
+// argument checks, workspaces and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+#include <initializer_list>
+#include <new>
+
+#include "handle.h"
+
+using spmm::fail;
+
+struct spmm_adapters_s {
+  int64_t m = 0, k = 0;
+  int32_t n_adapters = 0, rank = 0;
+  spmm_dtype in_t = SPMM_BF16;
+  int64_t max_rows = 0, max_segments = 0;
+  bool grad = false;
+  int device = 0;
+  int num_sms = 0;
+  bool sm103 = false;
+
+  float *d_h = nullptr;        // max_rows x rank: scale * D x
+  float *d_dh = nullptr;       // gradient: max_rows x rank: scale * U^T dy
+  uint16_t *d_down_t = nullptr;  // gradient: n_adapters x k x rank
+  uint16_t *d_up_t = nullptr;    // gradient: n_adapters x rank x m
+};
+
+namespace {
+
+void free_adapters(spmm_adapters a) {
+  if (!a) return;
+  cudaFree(a->d_h);
+  cudaFree(a->d_dh);
+  cudaFree(a->d_down_t);
+  cudaFree(a->d_up_t);
+  delete a;
+}
+
+bool misaligned(std::initializer_list<const void *> ps) {
+  uintptr_t bits = 0;
+  for (const void *p : ps) bits |= reinterpret_cast<uintptr_t>(p);
+  return (bits & 15) != 0;
+}
+
+// What both directions check of the layer's handle, the batch and the pool.
+// `rows` x `cols` is the layer as the handle has it.
+spmm_status check_batch(spmm_handle h, spmm_adapters a, int64_t rows, int64_t cols, int64_t N, const void *down,
+                        const void *up, const float *scale, const int64_t *seg_ptr, const int32_t *seg_adapter,
+                        int64_t n_seg) {
+  if (h) {
+    if (h->format != SPMM_FORMAT_BCSR) return fail(SPMM_ERR_UNSUPPORTED, "adapters run beside a BCSR handle");
+    if (h->b_row != 64 || h->b_col != 64) return fail(SPMM_ERR_UNSUPPORTED, "the BCSR kernel takes 64 x 64 blocks");
+    if (h->m != rows || h->k != cols)
+      return fail(SPMM_ERR_INVALID_ARG, "the handle is %lld x %lld, the adapters need %lld x %lld",
+                  static_cast<long long>(h->m), static_cast<long long>(h->k), static_cast<long long>(rows),
+                  static_cast<long long>(cols));
+    if (h->in_t != a->in_t) return fail(SPMM_ERR_INVALID_ARG, "the handle and the adapters have different in_t");
+    if (h->device != a->device) return fail(SPMM_ERR_INVALID_ARG, "the handle and the adapters are on different devices");
+  }
+  if (N < 0 || n_seg < 0) return fail(SPMM_ERR_INVALID_ARG, "N and n_seg must not be negative");
+  if (N > a->max_rows)
+    return fail(SPMM_ERR_INVALID_ARG, "N = %lld exceeds max_rows = %lld", static_cast<long long>(N),
+                static_cast<long long>(a->max_rows));
+  if (n_seg > a->max_segments)
+    return fail(SPMM_ERR_INVALID_ARG, "n_seg = %lld exceeds max_segments = %lld", static_cast<long long>(n_seg),
+                static_cast<long long>(a->max_segments));
+  if (!down || !up || !scale) return fail(SPMM_ERR_INVALID_ARG, "down, up or scale is NULL");
+  if (n_seg > 0 && (!seg_ptr || !seg_adapter)) return fail(SPMM_ERR_INVALID_ARG, "seg_ptr or seg_adapter is NULL");
+  if (!a->sm103) return fail(SPMM_ERR_UNSUPPORTED, "the kernels need an sm_103 (GB300) device");
+  return SPMM_OK;
+}
+
+spmm::AdapterParams make_params(spmm_handle h, spmm_adapters a, int64_t N, const float *scale, const int64_t *seg_ptr,
+                                const int32_t *seg_adapter, int64_t n_seg) {
+  spmm::AdapterParams p;
+  std::memset(&p, 0, sizeof p);
+  p.scale = scale;
+  p.seg_ptr = seg_ptr;
+  p.seg_adapter = seg_adapter;
+  p.n_seg = static_cast<int32_t>(n_seg);
+  p.n_adapters = a->n_adapters;
+  p.rank = a->rank;
+  p.N = static_cast<int32_t>(N);
+  p.num_sms = std::max(a->num_sms, 1);
+  p.wait_limit_ns = spmm::kWaitLimitNs;
+  if (h) {
+    p.block_row_ptr = h->d_ptr;
+    p.block_col_idx = h->d_idx;
+    p.blocks = h->d_vals;
+    p.status = h->d_status;
+  }
+  return p;
+}
+
+// Y = X W^T + adapters, with D rank x K and U M x rank per adapter.
+spmm_status project(spmm_handle h, spmm::AdapterParams p, const void *X, void *Y, const void *down, const void *up, float *H,
+                    cudaStream_t s) {
+  const bool bf16 = h->in_t == SPMM_BF16;
+  p.X = X;
+  p.Y = Y;
+  p.H = H;
+  p.down = down;
+  p.up = up;
+  p.M = static_cast<int32_t>(h->m);
+  p.K = static_cast<int32_t>(h->k);
+  CUDA_TRY(spmm::launch_shrink(p, bf16, s), "adapter down projection launch");
+  CUDA_TRY(spmm::launch_linear_adapters(p, bf16, h->out_t == SPMM_BF16, s), "projection with adapters launch");
+  return SPMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+spmm_status spmm_adapters_create(spmm_adapters *out, int64_t m, int64_t k, int32_t n_adapters, int32_t rank, spmm_dtype in_t,
+                                 int64_t max_rows, int64_t max_segments, int32_t grad) {
+  if (!out) return fail(SPMM_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  if (m < 1 || k < 1 || m >= (1ll << 31) || k >= (1ll << 31)) return fail(SPMM_ERR_INVALID_ARG, "m, k must be in [1, 2^31)");
+  if (n_adapters < 1 || n_adapters > 65535) return fail(SPMM_ERR_INVALID_ARG, "n_adapters must be in [1, 65535]");
+  if (rank < 1) return fail(SPMM_ERR_INVALID_ARG, "rank must be positive");
+  if (in_t != SPMM_F16 && in_t != SPMM_BF16) return fail(SPMM_ERR_INVALID_ARG, "in_t must be F16 or BF16");
+  if (max_rows < 0 || max_rows >= (1ll << 31) || max_segments < 0 || max_segments >= (1ll << 31))
+    return fail(SPMM_ERR_INVALID_ARG, "max_rows and max_segments must be in [0, 2^31)");
+  if (m % 8 != 0 || k % 8 != 0) return fail(SPMM_ERR_UNSUPPORTED, "m and k must be multiples of 8 (16-byte rows)");
+  if (rank % 8 != 0 || rank > spmm::kMaxRank)
+    return fail(SPMM_ERR_UNSUPPORTED, "rank must be a multiple of 8, at most %d (pad smaller adapters with zeros)",
+                spmm::kMaxRank);
+  if (static_cast<int64_t>(n_adapters) * std::max(m, k) >= (1ll << 31))
+    return fail(SPMM_ERR_UNSUPPORTED, "n_adapters * max(m, k) must be below 2^31");
+  spmm_adapters a = new (std::nothrow) spmm_adapters_s;
+  if (!a) return fail(SPMM_ERR_OOM, "host allocation failed");
+  a->m = m;
+  a->k = k;
+  a->n_adapters = n_adapters;
+  a->rank = rank;
+  a->in_t = in_t;
+  a->max_rows = max_rows;
+  a->max_segments = max_segments;
+  a->grad = grad != 0;
+  auto setup = [&]() -> spmm_status {
+    CUDA_TRY(cudaGetDevice(&a->device), "cudaGetDevice");
+    int major = 0, minor = 0;
+    CUDA_TRY(cudaDeviceGetAttribute(&a->num_sms, cudaDevAttrMultiProcessorCount, a->device), "device attribute");
+    CUDA_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, a->device), "device attribute");
+    CUDA_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, a->device), "device attribute");
+    a->sm103 = major == 10 && minor == 3;
+    const size_t h = static_cast<size_t>(std::max<int64_t>(max_rows, 1)) * rank * sizeof(float);
+    CUDA_TRY(cudaMalloc(&a->d_h, h), "cudaMalloc(adapter activations)");
+    if (a->grad) {
+      CUDA_TRY(cudaMalloc(&a->d_dh, h), "cudaMalloc(adapter gradients)");
+      CUDA_TRY(cudaMalloc(&a->d_down_t, static_cast<size_t>(n_adapters) * k * rank * 2), "cudaMalloc(transposed down)");
+      CUDA_TRY(cudaMalloc(&a->d_up_t, static_cast<size_t>(n_adapters) * m * rank * 2), "cudaMalloc(transposed up)");
+    }
+    return SPMM_OK;
+  };
+  const spmm_status st = setup();
+  if (st != SPMM_OK) {
+    free_adapters(a);
+    cudaGetLastError();
+    return st;
+  }
+  *out = a;
+  return SPMM_OK;
+}
+
+spmm_status spmm_adapters_destroy(spmm_adapters a) {
+  if (!a) return fail(SPMM_ERR_INVALID_ARG, "adapters is NULL");
+  cudaSetDevice(a->device);
+  cudaDeviceSynchronize();
+  free_adapters(a);
+  return SPMM_OK;
+}
+
+spmm_status spmm_run_linear_adapters(spmm_handle h, spmm_adapters a, const void *X, void *Y, int64_t N, const void *down,
+                                     const void *up, const float *scale, const int64_t *seg_ptr,
+                                     const int32_t *seg_adapter, int64_t n_seg, void *stream) {
+  if (!h || !a) return fail(SPMM_ERR_INVALID_ARG, "handle or adapters is NULL");
+  spmm_status st = check_batch(h, a, a->m, a->k, N, down, up, scale, seg_ptr, seg_adapter, n_seg);
+  if (st != SPMM_OK) return st;
+  if (N == 0) return SPMM_OK;
+  if (!X || !Y) return fail(SPMM_ERR_INVALID_ARG, "X or Y is NULL");
+  if (misaligned({X, Y, down, up})) return fail(SPMM_ERR_UNSUPPORTED, "X, Y, down and up must be 16-byte aligned");
+  return project(h, make_params(h, a, N, scale, seg_ptr, seg_adapter, n_seg), X, Y, down, up, a->d_h,
+                 static_cast<cudaStream_t>(stream));
+}
+
+spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, const void *dY, void *dX, void *d_down,
+                               void *d_up, int64_t N, const void *down, const void *up, const float *scale,
+                               const int64_t *seg_ptr, const int32_t *seg_adapter, int64_t n_seg, void *stream) {
+  if (!h_t || !a) return fail(SPMM_ERR_INVALID_ARG, "handle or adapters is NULL");
+  if (!a->grad) return fail(SPMM_ERR_INVALID_ARG, "the adapters were created without the gradient's workspace");
+  spmm_status st = check_batch(h_t, a, a->k, a->m, N, down, up, scale, seg_ptr, seg_adapter, n_seg);
+  if (st != SPMM_OK) return st;
+  if (!d_down || !d_up) return fail(SPMM_ERR_INVALID_ARG, "d_down or d_up is NULL");
+  if (N > 0 && (!X || !dY)) return fail(SPMM_ERR_INVALID_ARG, "X or dY is NULL");
+  if (misaligned({X, dY, dX, down, up, d_down, d_up}))
+    return fail(SPMM_ERR_UNSUPPORTED, "X, dY, dX and the adapters' weights and gradients must be 16-byte aligned");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf16 = a->in_t == SPMM_BF16;
+  const int32_t m = static_cast<int32_t>(a->m), k = static_cast<int32_t>(a->k);
+  spmm::AdapterParams p = make_params(h_t, a, N, scale, seg_ptr, seg_adapter, N > 0 ? n_seg : 0);
+  if (N > 0) {
+    CUDA_TRY(spmm::launch_transpose(up, a->d_up_t, a->n_adapters, m, a->rank, s), "adapter transpose launch");
+    CUDA_TRY(spmm::launch_transpose(down, a->d_down_t, a->n_adapters, a->rank, k, s), "adapter transpose launch");
+    p.X = X;
+    p.K = k;
+    p.down = down;
+    p.H = a->d_h;
+    CUDA_TRY(spmm::launch_shrink(p, bf16, s), "adapter down projection launch");
+    if (dX) {
+      st = project(h_t, p, dY, dX, a->d_up_t, a->d_down_t, a->d_dh, s);
+      if (st != SPMM_OK) return st;
+    } else {
+      p.X = dY;
+      p.K = m;
+      p.down = a->d_up_t;
+      p.H = a->d_dh;
+      CUDA_TRY(spmm::launch_shrink(p, bf16, s), "adapter gradient launch");
+    }
+  }
+  p.H = a->d_h;
+  CUDA_TRY(spmm::launch_wgrad(p, dY, m, d_up, true, bf16, s), "adapter weight gradient launch");
+  p.H = a->d_dh;
+  CUDA_TRY(spmm::launch_wgrad(p, X, k, d_down, false, bf16, s), "adapter weight gradient launch");
+  return SPMM_OK;
+}
+
+// ---------------------------------------------------------------- routing
+namespace {
+
+spmm_status check_routing(int64_t T, int32_t topk, int64_t d, spmm_dtype dtype) {
+  if (T < 0 || T >= (1ll << 31)) return fail(SPMM_ERR_INVALID_ARG, "T must be in [0, 2^31)");
+  if (topk < 1) return fail(SPMM_ERR_INVALID_ARG, "topk must be positive");
+  if (topk > spmm::kRouteMaxTopk) return fail(SPMM_ERR_UNSUPPORTED, "topk must be at most %d", spmm::kRouteMaxTopk);
+  if (T * topk >= (1ll << 31)) return fail(SPMM_ERR_UNSUPPORTED, "T * topk must be below 2^31");
+  if (d < 1 || d >= (1ll << 31)) return fail(SPMM_ERR_INVALID_ARG, "d must be in [1, 2^31)");
+  if (dtype != SPMM_F16 && dtype != SPMM_BF16 && dtype != SPMM_F32)
+    return fail(SPMM_ERR_INVALID_ARG, "dtype must be F16, BF16 or F32");
+  return SPMM_OK;
+}
+
+// Rows are read and written element by element or in 16-byte words, so a base
+// has to be aligned to its elements only.
+spmm_status check_rows(std::initializer_list<const void *> ps, spmm_dtype dtype) {
+  const uintptr_t mask = dtype == SPMM_F32 ? 3 : 1;
+  for (const void *p : ps) {
+    if (!p) return fail(SPMM_ERR_INVALID_ARG, "a row pointer is NULL");
+    if (reinterpret_cast<uintptr_t>(p) & mask) return fail(SPMM_ERR_UNSUPPORTED, "a row pointer is not aligned to its type");
+  }
+  return SPMM_OK;
+}
+
+}  // namespace
+
+int64_t spmm_route_workspace_bytes(int64_t T, int32_t topk, int32_t n_experts) {
+  if (T < 0 || topk < 1 || n_experts < 1 || n_experts > spmm::kRouteMaxExperts || T >= (1ll << 31) / topk) return 0;
+  const int64_t chunks = spmm::route_chunks(T * topk);
+  return chunks > 1 ? chunks * n_experts * static_cast<int64_t>(sizeof(int32_t)) : 0;
+}
+
+spmm_status spmm_route_sort(const int32_t *ids, int64_t T, int32_t topk, int32_t n_experts, int64_t *offsets, int32_t *order,
+                            int32_t *position, void *workspace, void *stream) {
+  spmm_status st = check_routing(T, topk, 1, SPMM_F32);
+  if (st != SPMM_OK) return st;
+  if (n_experts < 1) return fail(SPMM_ERR_INVALID_ARG, "n_experts must be positive");
+  if (n_experts > spmm::kRouteMaxExperts)
+    return fail(SPMM_ERR_UNSUPPORTED, "n_experts must be at most %d", spmm::kRouteMaxExperts);
+  if (!offsets || (T > 0 && (!ids || !order || !position))) return fail(SPMM_ERR_INVALID_ARG, "a pointer is NULL");
+  if (!workspace && spmm_route_workspace_bytes(T, topk, n_experts) > 0)
+    return fail(SPMM_ERR_INVALID_ARG, "workspace is NULL; spmm_route_workspace_bytes gives its size");
+  CUDA_TRY(spmm::launch_route_sort(ids, T * topk, n_experts, offsets, order, position, static_cast<int32_t *>(workspace),
+                                   static_cast<cudaStream_t>(stream)),
+           "routing sort launch");
+  return SPMM_OK;
+}
+
+spmm_status spmm_route_gather(const void *x, const int32_t *position, const int64_t *n_kept, void *out, int64_t T,
+                              int32_t topk, int64_t d, spmm_dtype dtype, void *stream) {
+  spmm_status st = check_routing(T, topk, d, dtype);
+  if (st != SPMM_OK || T == 0) return st;
+  if (!position || !n_kept) return fail(SPMM_ERR_INVALID_ARG, "position or n_kept is NULL");
+  st = check_rows({x, out}, dtype);
+  if (st != SPMM_OK) return st;
+  spmm::RouteRows r{x, nullptr, out, position, nullptr, n_kept, nullptr, T, d, topk};
+  CUDA_TRY(spmm::launch_route_gather(r, dtype, static_cast<cudaStream_t>(stream)), "routing gather launch");
+  return SPMM_OK;
+}
+
+spmm_status spmm_route_combine(const void *y, const int32_t *position, const float *weights, void *out, int64_t T,
+                               int32_t topk, int64_t d, spmm_dtype dtype, void *stream) {
+  spmm_status st = check_routing(T, topk, d, dtype);
+  if (st != SPMM_OK || T == 0) return st;
+  if (!position) return fail(SPMM_ERR_INVALID_ARG, "position is NULL");
+  st = check_rows({y, out}, dtype);
+  if (st != SPMM_OK) return st;
+  spmm::RouteRows r{y, nullptr, out, position, weights, nullptr, nullptr, T, d, topk};
+  CUDA_TRY(spmm::launch_route_combine(r, dtype, static_cast<cudaStream_t>(stream)), "routing combine launch");
+  return SPMM_OK;
+}
+
+spmm_status spmm_route_combine_grad(const void *dout, const void *y, const int32_t *position, const float *weights,
+                                    const int64_t *n_kept, void *dy, float *dweights, int64_t T, int32_t topk, int64_t d,
+                                    spmm_dtype dtype, void *stream) {
+  spmm_status st = check_routing(T, topk, d, dtype);
+  if (st != SPMM_OK || T == 0) return st;
+  if (!position || !n_kept || !dweights) return fail(SPMM_ERR_INVALID_ARG, "position, n_kept or dweights is NULL");
+  st = check_rows({dout, y, dy}, dtype);
+  if (st != SPMM_OK) return st;
+  spmm::RouteRows r{y, dout, dy, position, weights, n_kept, dweights, T, d, topk};
+  CUDA_TRY(spmm::launch_route_grad(r, dtype, static_cast<cudaStream_t>(stream)), "routing gradient launch");
+  return SPMM_OK;
+}
+
+}  // extern "C"

@@ -212,6 +212,65 @@ int wcsr64_ctas_per_sm();
 cudaError_t launch_wcsr64(const CUtensorMap &tmC, const WcsrParams &p, bool in_bf16, bool out_bf16,
                           cudaStream_t stream);
 
+// ---------------------------------------------------------------- low-rank adapters (adapters.cu)
+// Rank of an adapter: at most this, a multiple of 8 (16-byte rows of U).
+constexpr int kMaxRank = 128;
+
+struct AdapterParams {
+  const int64_t *block_row_ptr;  // the shared weight in BCSR
+  const int32_t *block_col_idx;
+  const void *blocks;
+  const void *X;                 // device, N x K row-major
+  void *Y;                       // device, N x M row-major
+  float *H;                      // device, N x rank: scale * D x of the rows with an adapter
+  const void *down, *up;         // device, n_adapters x rank x K, n_adapters x M x rank
+  const float *scale;            // device, n_adapters
+  const int64_t *seg_ptr;        // device, n_seg + 1
+  const int32_t *seg_adapter;    // device, n_seg
+  int32_t n_seg, n_adapters, rank;
+  int32_t M, N, K;
+  int32_t num_sms;
+  uint32_t *status;
+  uint64_t wait_limit_ns;
+};
+
+// H = scale * X D^T of the rows with an adapter (other rows of H are left alone).
+cudaError_t launch_shrink(const AdapterParams &p, bool bf16, cudaStream_t s);
+// Y = X W^T + U H per row.
+cudaError_t launch_linear_adapters(const AdapterParams &p, bool bf16, bool out_bf16, cudaStream_t s);
+// n matrices of rows x cols 16-bit elements, each transposed.
+cudaError_t launch_transpose(const void *in, void *out, int32_t n, int32_t rows, int32_t cols, cudaStream_t s);
+// G_a = sum over the rows of adapter a of V[n] H[n]^T, V N x features; G as
+// n_adapters x features x rank (up) or n_adapters x rank x features.
+cudaError_t launch_wgrad(const AdapterParams &p, const void *V, int32_t features, void *G, bool up, bool bf16,
+                         cudaStream_t s);
+
+// ---------------------------------------------------------------- expert routing (route.cu)
+constexpr int kRouteChunk = 8192;        // ids per block of the sort
+constexpr int kRouteMaxExperts = 2048;   // the sort's counts of a block lie in shared memory
+constexpr int kRouteMaxTopk = 32;        // a warp holds a token's positions, one a lane
+
+// A row movement: src / dst rows of d elements, the routing's positions.
+struct RouteRows {
+  const void *src;
+  const void *dout;              // gradient: rows of the output's gradient
+  void *dst;
+  const int32_t *position;       // T x topk
+  const float *weights;          // T x topk, or NULL for ones
+  const int64_t *kept;           // device: number of slots taken (offsets[n_experts])
+  float *dweights;
+  int64_t T, d;
+  int32_t topk;
+};
+
+int64_t route_chunks(int64_t n);
+cudaError_t launch_route_sort(const int32_t *ids, int64_t n, int32_t n_experts, int64_t *offsets, int32_t *order,
+                              int32_t *position, int32_t *counts, cudaStream_t s);
+// dtype: spmm_dtype of the rows.
+cudaError_t launch_route_gather(const RouteRows &r, int dtype, cudaStream_t s);
+cudaError_t launch_route_combine(const RouteRows &r, int dtype, cudaStream_t s);
+cudaError_t launch_route_grad(const RouteRows &r, int dtype, cudaStream_t s);
+
 // Failure-detection self test: wait on an mbarrier nothing arrives at.
 cudaError_t launch_wait_selftest(uint32_t *status, uint64_t limit_ns, cudaStream_t stream);
 

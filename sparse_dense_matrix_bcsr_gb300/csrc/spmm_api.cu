@@ -13,6 +13,7 @@
 
 #include "../../include/spmm.h"
 #include "format.h"
+#include "handle.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -21,6 +22,12 @@ using spmm::HostFormat;
 namespace {
 
 thread_local std::string g_last_error;
+
+constexpr uint64_t kDefaultWaitLimitNs = spmm::kWaitLimitNs;
+
+}  // namespace
+
+namespace spmm {
 
 spmm_status fail(spmm_status s, const char *fmt, ...) {
   char buf[512];
@@ -36,19 +43,7 @@ spmm_status cuda_fail(cudaError_t e, const char *what) {
   return fail(e == cudaErrorMemoryAllocation ? SPMM_ERR_OOM : SPMM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-#define CUDA_TRY(call, what)                      \
-  do {                                            \
-    cudaError_t e_ = (call);                      \
-    if (e_ != cudaSuccess) return cuda_fail(e_, what); \
-  } while (0)
-
-constexpr uint64_t kDefaultWaitLimitNs = 4000000000ull;  // 4 s per mbarrier wait
-
 // ---------------------------------------------------------------- driver entry
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
   static std::once_flag once;
@@ -80,26 +75,6 @@ spmm_status encode_2d(CUtensorMap *map, const void *base, bool bf16, uint64_t ro
   return SPMM_OK;
 }
 
-// C as the destination of TMA stores: `rows` x `cols` row-major elements of
-// bf16 or fp32.  Narrow (N <= 128) tiles store 16-row x 128-byte boxes with the
-// 128-byte swizzle, wide ones 32-row x 64-byte boxes with the 64-byte swizzle
-// (see bcsr_wide_tiles).
-spmm_status encode_c(CUtensorMap *map, void *base, bool bf16, uint64_t rows, uint64_t cols, bool wide) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return fail(SPMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const uint64_t esz = bf16 ? 2 : 4;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * esz};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>((wide ? 64 : 128) / esz), wide ? 32u : 16u};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims,
-                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  wide ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(SPMM_ERR_CUDA, "cuTensorMapEncodeTiled (C) failed (%d)", static_cast<int>(r));
-  return SPMM_OK;
-}
-
 // X of the linear-layer product as a TMA source: N rows x k columns of
 // 16-bit elements, 256-row x 64-column boxes, 128-byte swizzle.
 spmm_status encode_x(CUtensorMap *map, const void *base, bool bf16, uint64_t rows, uint64_t cols) {
@@ -123,60 +98,39 @@ spmm_status encode_y(CUtensorMap *map, void *base, bool bf16, uint64_t rows, uin
   return SPMM_OK;
 }
 
+}  // namespace spmm
+
+namespace {
+
+using spmm::cuda_fail;
+using spmm::encode_2d;
+using spmm::encode_fn;
+using spmm::encode_x;
+using spmm::encode_y;
+using spmm::EncodeTiledFn;
+using spmm::fail;
+
+// C as the destination of TMA stores: `rows` x `cols` row-major elements of
+// bf16 or fp32.  Narrow (N <= 128) tiles store 16-row x 128-byte boxes with the
+// 128-byte swizzle, wide ones 32-row x 64-byte boxes with the 64-byte swizzle
+// (see bcsr_wide_tiles).
+spmm_status encode_c(CUtensorMap *map, void *base, bool bf16, uint64_t rows, uint64_t cols, bool wide) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(SPMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const uint64_t esz = bf16 ? 2 : 4;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * esz};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>((wide ? 64 : 128) / esz), wide ? 32u : 16u};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  wide ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SPMM_ERR_CUDA, "cuTensorMapEncodeTiled (C) failed (%d)", static_cast<int>(r));
+  return SPMM_OK;
+}
+
 }  // namespace
-
-struct spmm_handle_s {
-  int format = 0;
-  int64_t m = 0, k = 0, nnz = 0;
-  int b_row = 0, b_col = 0;
-  spmm_dtype in_t = SPMM_BF16, out_t = SPMM_F32;
-  int device = 0;
-  int num_sms = 0;
-  bool sm103 = false;
-  int64_t n_groups = 0, n_units = 0, stored = 0;
-
-  int64_t *d_ptr = nullptr;
-  int32_t *d_idx = nullptr;
-  uint16_t *d_vals = nullptr;
-  size_t vals_bytes = 0;
-  CUtensorMap tm_vals;  // BCSR: the blocks array as [n_blocks*64 rows, 64 cols] for TMA
-
-  const void *b_cached = nullptr;
-  int64_t n_cached = -1;
-  CUtensorMap tm_B;
-  void *c_cached = nullptr;
-  int64_t nc_cached = -1;
-  CUtensorMap tm_C;
-  // the linear-layer product's X and Y
-  const void *x_cached = nullptr;
-  int64_t nx_cached = -1;
-  CUtensorMap tm_X;
-  void *y_cached = nullptr;
-  int64_t ny_cached = -1;
-  CUtensorMap tm_Y;
-
-  // Work decomposition.  WCSR: stages of <= 64 packed columns.  BCSR: the
-  // prefix sums of max(1, blocks) per block row (the split schedule's stage
-  // list).  Both: the partial-sum workspace of groups cut between persistent
-  // CTAs (BCSR: allocated only when the split schedule can be chosen).
-  int32_t max_ctas = 0;  // 0: the kernels' default CTAs per SM
-  int32_t schedule = SPMM_SCHEDULE_AUTO;
-  int64_t n_stages = 0;
-  int64_t *d_stage_row_ptr = nullptr;
-  uint8_t *d_stage_pack = nullptr;
-  float *d_ws = nullptr;
-  spmm::PartialRec *d_partials = nullptr;
-  int64_t ws_slots = 0;
-  std::vector<int32_t> stage_first;  // host copy of the stage list's first-stage flags (for statistics)
-
-  uint32_t *d_status = nullptr;
-  uint64_t wait_limit_ns = kDefaultWaitLimitNs;
-
-  void *d_bstage = nullptr;
-  size_t bstage_bytes = 0;
-  void *d_cstage = nullptr;
-  size_t cstage_bytes = 0;
-};
 
 namespace {
 
