@@ -1,0 +1,314 @@
+// adapter_down_kernel.cu -- the adapters' down projection for long batches,
+//   H[n] = scale[a] * D_a X[n]    (spmm_run_linear_adapters, spmm_adapters_grad)
+// on the tensor cores, with H in the 16-bit type that the projection's MMAs
+// take it in.
+//
+// Work unit = 128 rows of X (the M operand) and all ranks (the N operand, D_a's
+// rows, both K-major as they lie in memory); one stage is 64 columns of both,
+// two TMA boxes.  A tile that several segments share runs its columns once per
+// segment, each time updating that segment's lanes only (the MMA's lane mask),
+// so every row meets its own adapter alone.  X is read once for tiles of one
+// segment; the product is 2 N r k FLOP against 2 N k bytes, far below the tensor
+// rate, so HBM bounds it for prompts.  Short batches have few tiles: a cluster
+// of up to 8 CTAs then splits a tile's columns and adds the fp32 sums through
+// distributed shared memory in CTA order (no atomics, no second launch).
+//
+// Where the projection's output is fp32, H is kept as two 16-bit parts (the
+// value rounded, and the rest rounded), which holds 16 (bf16) or 22 (fp16) bits.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "segments.cuh"
+
+namespace spmm {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kXBytes = kRows * 128;  // 128 rows x 64 columns
+constexpr int kMaxQ = 8;
+constexpr int kThreads = 192;
+constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2;
+constexpr int kMiscBytes = 4096;
+constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
+
+__host__ __device__ constexpr int rank16(int rank) { return (rank + 15) / 16 * 16; }
+__host__ __device__ constexpr int d_bytes(int rank) { return (rank16(rank) * 128 + 1023) / 1024 * 1024; }
+__host__ __device__ constexpr int part_pitch(int rank) { return rank16(rank) + 4; }  // floats per row of the CTA's sums
+
+struct Misc {
+  uint64_t full[kMaxQ], empty[kMaxQ], acc_full, drain;
+  TileSegment segs[kRows];
+  float scale[kRows];
+  int32_t n_segs;
+  uint32_t tmem;
+  volatile int32_t abort_flag;
+};
+static_assert(sizeof(Misc) <= kMiscBytes, "misc area");
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t u) {
+  if constexpr (BF16) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u));
+  return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+
+// Eight ranks of one row of H, rounded; with two parts also what the rounding left.
+template <bool BF16>
+__device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int64_t N, int32_t rank, int32_t j, int parts,
+                                        const float (&v)[8]) {
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    hi[i] = pack2<BF16>(v[2 * i], v[2 * i + 1]);
+    const float2 f = unpack2<BF16>(hi[i]);
+    lo[i] = pack2<BF16>(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+  }
+  *reinterpret_cast<uint4 *>(H + row * rank + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  if (parts == 2) *reinterpret_cast<uint4 *>(H + (N + row) * rank + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 2)
+    adapter_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmD,
+                        const AdapterDownParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int stage_bytes = kXBytes + d_bytes(p.rank);
+  Misc *mi = reinterpret_cast<Misc *>(smem + p.q * stage_bytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t tile = blockIdx.x / p.split, part = blockIdx.x % p.split;  // part = rank in the cluster
+  const int64_t row0 = static_cast<int64_t>(tile) * kRows;
+  const int n16 = rank16(p.rank);
+  uint32_t tmem_cols = 32;
+  while (static_cast<int>(tmem_cols) < n16) tmem_cols <<= 1;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      for (int q = 0; q < p.q; ++q) {
+        mbar_init(smem_addr(&mi->full[q]), 1);
+        mbar_init(smem_addr(&mi->empty[q]), 1);
+      }
+      mbar_init(smem_addr(&mi->acc_full), 1);
+      mbar_init(smem_addr(&mi->drain), 1);
+      mi->abort_flag = 0;
+      fence_barrier_init();
+      tma_prefetch_desc(&tmX);
+      tma_prefetch_desc(&tmD);
+    }
+    __syncwarp();
+    const int32_t c = list_segments(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, row0,
+                                    min(row0 + kRows, static_cast<int64_t>(p.N)), mi->segs, kRows, p.status);
+    if (lane == 0) mi->n_segs = c;
+    for (int r = lane; r < kRows; r += 32) mi->scale[r] = 0.0f;
+    __syncwarp();
+    for (int i = 0; i < c; ++i) {
+      const TileSegment s = mi->segs[i];
+      const float f = p.scale[s.adapter];
+      for (int r = s.begin + lane; r < s.end; r += 32) mi->scale[r] = f;
+    }
+  } else if (warp == kMmaWarp) {
+    tmem_alloc(smem_addr(&mi->tmem), tmem_cols);
+    tmem_relinquish();
+  } else if (warp == kEpiWarp0 && part == 0 && tile % (kAdapterTileRows / kRows) == 0) {
+    // the projection's own tiles: their segments, for its producers
+    const int32_t t = tile / (kAdapterTileRows / kRows);
+    const int32_t c = list_segments(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, row0,
+                                    min(row0 + kAdapterTileRows, static_cast<int64_t>(p.N)),
+                                    p.tile_segs + static_cast<int64_t>(t) * kAdapterTileRows, kAdapterTileRows, p.status);
+    if (lane == 0) p.tile_count[t] = c;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = mi->tmem;
+  const int32_t n_segs = mi->n_segs;
+  const int32_t nk = (p.K + 63) / 64;
+  const int32_t k_begin = static_cast<int32_t>(static_cast<int64_t>(nk) * part / p.split);
+  const int32_t k_end = static_cast<int32_t>(static_cast<int64_t>(nk) * (part + 1) / p.split);
+
+  if (n_segs > 0) {
+    if (warp == kTmaWarp) {
+      uint32_t stage = 0, phase = 0;
+      int64_t seq = 0;
+      bool ok = true;
+      for (int i = 0; i < n_segs && ok; ++i) {
+        const int32_t a = mi->segs[i].adapter;
+        for (int32_t c = k_begin; c < k_end; ++c) {
+          const bool r = mbar_wait_warp(smem_addr(&mi->empty[stage]), phase ^ 1u, p.wait_limit_ns);
+          ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t fb = smem_addr(&mi->full[stage]);
+            const uint32_t st = smem_addr(smem + stage * stage_bytes);
+            mbar_arrive_expect_tx(fb, kXBytes + p.rank * 128);
+            tma_load_2d(st, &tmX, fb, c * 64, static_cast<int32_t>(row0));
+            tma_load_2d(st + kXBytes, &tmD, fb, c * 64, a * p.rank);
+          }
+          __syncwarp();
+          ++seq;
+          if (++stage == static_cast<uint32_t>(p.q)) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && lane == 0) {
+        atomicOr(p.status, kDevTimeout);
+        mi->abort_flag = 1;
+        // let the copies in flight land before the block ends
+        for (int64_t i = seq > p.q ? seq - p.q : 0; i < seq; ++i)
+          mbar_wait(smem_addr(&mi->full[i % p.q]), static_cast<uint32_t>((i / p.q) & 1), 1000000ull);
+      }
+    } else if (warp == kMmaWarp) {
+      const uint32_t idesc = idesc_f16(BF16, false, false, kRows, static_cast<uint32_t>(n16));
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (int i = 0; i < n_segs && ok; ++i) {
+        const TileSegment s = mi->segs[i];
+        uint32_t off[4];
+        lanes_off(s.begin, s.end, off);
+        for (int32_t c = k_begin; c < k_end; ++c) {
+          const bool r = mbar_wait_warp(smem_addr(&mi->full[stage]), phase, p.wait_limit_ns);
+          ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
+          if (!ok) break;
+          if (lane == 0) {
+            tc_fence_after_sync();
+            const uint32_t st = smem_addr(smem + stage * stage_bytes);
+            const uint64_t x = smem_desc_sw128(st, 16, 1024);
+            const uint64_t d = smem_desc_sw128(st + kXBytes, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16_lanes(tmem, smem_desc_add(x, kk * 32), smem_desc_add(d, kk * 32), idesc,
+                             (c == k_begin && kk == 0) ? 0u : 1u, off);
+            umma_commit(smem_addr(&mi->empty[stage]));
+          }
+          __syncwarp();
+          if (++stage == static_cast<uint32_t>(p.q)) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (lane == 0) {
+        if (!ok) {
+          atomicOr(p.status, kDevTimeout);
+          mi->abort_flag = 1;
+        }
+        umma_commit(smem_addr(&mi->acc_full));  // also waits for what was issued when giving up
+      }
+    }
+    if (warp >= kEpiWarp0) {
+      const int sp = warp & 3;
+      const int r = sp * 32 + lane;
+      const bool ok = mbar_wait_warp(smem_addr(&mi->acc_full), 0, p.wait_limit_ns);
+      if (!ok && lane == 0) {
+        atomicOr(p.status, kDevTimeout);
+        mi->abort_flag = 1;
+      }
+      tc_fence_after_sync();
+      float *sums = reinterpret_cast<float *>(smem);  // the stages are done with
+      const float f = mi->scale[r];
+      bool has = false;
+      for (int i = 0; i < n_segs; ++i) has |= r >= mi->segs[i].begin && r < mi->segs[i].end;
+      for (int c0 = 0; c0 < n16 && ok; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(sp * 32) << 16) + c0, v);
+        tmem_ld_wait();
+        if (p.split > 1) {
+          float4 *dst = reinterpret_cast<float4 *>(sums + r * part_pitch(p.rank) + c0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                                 __uint_as_float(v[4 * i + 3]));
+        } else if (row0 + r < p.N) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (c0 + 8 * h >= p.rank) continue;
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = has ? f * __uint_as_float(v[8 * h + i]) : 0.0f;
+            store_h<BF16>(p.H, row0 + r, p.N, p.rank, c0 + 8 * h, p.parts, o);
+          }
+        }
+      }
+      tc_fence_before_sync();
+    }
+  }
+  if (p.split > 1) {
+    // every CTA of the cluster comes here, whatever happened before
+    cluster_sync();
+    if (n_segs > 0) {
+      const int rows = kRows / p.split, r0 = part * rows, units = p.rank / 8;
+      const uint32_t base = smem_addr(smem);
+      for (int u = threadIdx.x; u < rows * units; u += kThreads) {
+        const int r = r0 + u / units, j = (u % units) * 8;
+        if (row0 + r >= p.N) continue;
+        float o[8] = {};
+        for (int c = 0; c < p.split; ++c) {
+          const uint32_t at = cluster_map(base + (r * part_pitch(p.rank) + j) * 4, c);
+          const float4 x = cluster_load_f4(at), y = cluster_load_f4(at + 16);
+          o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
+          o[4] += y.x, o[5] += y.y, o[6] += y.z, o[7] += y.w;
+        }
+        bool has = false;
+        for (int i = 0; i < n_segs; ++i) has |= r >= mi->segs[i].begin && r < mi->segs[i].end;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = has ? mi->scale[r] * o[i] : 0.0f;
+        store_h<BF16>(p.H, row0 + r, p.N, p.rank, j, p.parts, o);
+      }
+    }
+    cluster_sync();  // the others may still read this CTA's sums
+  }
+  __syncthreads();
+  grid_launch_dependents();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, tmem_cols);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_adapter_down(const CUtensorMap &tmX, const CUtensorMap &tmD, AdapterDownParams p, int num_sms, bool bf16,
+                                cudaStream_t s) {
+  const int64_t tiles = (static_cast<int64_t>(p.N) + kRows - 1) / kRows;
+  const int nk = (p.K + 63) / 64;
+  // as many CTAs per tile (a cluster) as keep the grid within two per SM, with
+  // at least four stages each
+  p.split = 1;
+  while (p.split < 8 && tiles * p.split * 2 <= 2ll * num_sms && nk >= 8 * p.split) p.split *= 2;
+  const int stage = kXBytes + d_bytes(p.rank);
+  p.q = (kSmemLimit - kMiscBytes - 1024) / stage;
+  if (p.q > kMaxQ) p.q = kMaxQ;
+  const int smem = p.q * stage + kMiscBytes + 1024;
+  auto kern = bf16 ? adapter_down_kernel<true> : adapter_down_kernel<false>;
+  static std::atomic<uint64_t> smem_set[2];
+  cudaError_t e = set_smem_limit_once(kern, kSmemLimit, smem_set[bf16 ? 1 : 0]);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tmX, tmD, p);
+}
+
+}  // namespace spmm

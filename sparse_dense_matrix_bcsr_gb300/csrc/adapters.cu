@@ -6,7 +6,6 @@
 #include <cuda_fp16.h>
 
 #include "internal.h"
-#include "ptx.cuh"
 #include "segments.cuh"
 
 namespace spmm {

@@ -23,10 +23,12 @@ struct spmm_adapters_s {
   int num_sms = 0;
   bool sm103 = false;
 
-  float *d_h = nullptr;        // max_rows x rank: scale * D x
+  float *d_h = nullptr;        // max_rows x rank: scale * D x, or as many values in two 16-bit parts
   float *d_dh = nullptr;       // gradient: max_rows x rank: scale * U^T dy
   uint16_t *d_down_t = nullptr;  // gradient: n_adapters x k x rank
   uint16_t *d_up_t = nullptr;    // gradient: n_adapters x rank x m
+  spmm::TileSegment *d_tile_segs = nullptr;  // the projection's row tiles: their segments with an adapter
+  int32_t *d_tile_count = nullptr;
 };
 
 namespace {
@@ -37,6 +39,8 @@ void free_adapters(spmm_adapters a) {
   cudaFree(a->d_dh);
   cudaFree(a->d_down_t);
   cudaFree(a->d_up_t);
+  cudaFree(a->d_tile_segs);
+  cudaFree(a->d_tile_count);
   delete a;
 }
 
@@ -96,9 +100,77 @@ spmm::AdapterParams make_params(spmm_handle h, spmm_adapters a, int64_t N, const
   return p;
 }
 
+// H = scale * X D^T in 16 bits (`parts` of them), with the projection's tile lists.
+spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, int parts, cudaStream_t s) {
+  const bool bf16 = a->in_t == SPMM_BF16;
+  CUtensorMap tmX, tmD;
+  spmm_status st = spmm::encode_2d(&tmX, p.X, bf16, p.N, p.K, p.K, 128, 64);
+  if (st != SPMM_OK) return st;
+  st = spmm::encode_2d(&tmD, p.down, bf16, static_cast<uint64_t>(p.n_adapters) * p.rank, p.K, p.K, p.rank, 64);
+  if (st != SPMM_OK) return st;
+  spmm::AdapterDownParams d;
+  std::memset(&d, 0, sizeof d);
+  d.H = reinterpret_cast<uint16_t *>(p.H);
+  d.tile_segs = a->d_tile_segs;
+  d.tile_count = a->d_tile_count;
+  d.scale = p.scale;
+  d.seg_ptr = p.seg_ptr;
+  d.seg_adapter = p.seg_adapter;
+  d.n_seg = p.n_seg;
+  d.n_adapters = p.n_adapters;
+  d.rank = p.rank;
+  d.parts = parts;
+  d.N = p.N;
+  d.K = p.K;
+  d.status = p.status;
+  d.wait_limit_ns = p.wait_limit_ns;
+  CUDA_TRY(spmm::launch_adapter_down(tmX, tmD, d, p.num_sms, bf16, s), "adapter down projection launch");
+  return SPMM_OK;
+}
+
+// Y = X W^T + U H per row, H and the tile lists from down_project.
+spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams &p, int parts, cudaStream_t s) {
+  const bool bf16 = h->in_t == SPMM_BF16, out_bf16 = h->out_t == SPMM_BF16;
+  CUtensorMap tmX, tmY;
+  spmm::LinearAdapters ad;
+  spmm_status st = spmm::encode_x(&tmX, p.X, bf16, p.N, p.K);
+  if (st == SPMM_OK) st = spmm::encode_y(&tmY, p.Y, out_bf16, p.N, p.M);
+  if (st == SPMM_OK)
+    st = spmm::encode_2d(&ad.tmU, p.up, bf16, static_cast<uint64_t>(p.n_adapters) * p.M, p.rank, p.rank, 64, 64);
+  if (st == SPMM_OK)
+    st = spmm::encode_2d(&ad.tmH, p.H, bf16, static_cast<uint64_t>(parts) * p.N, p.rank, p.rank, spmm::kAdapterTileRows, 64);
+  if (st != SPMM_OK) return st;
+  ad.tile_segs = a->d_tile_segs;
+  ad.tile_count = a->d_tile_count;
+  ad.rank = p.rank;
+  ad.parts = parts;
+  spmm::BcsrParams b;
+  std::memset(&b, 0, sizeof b);
+  b.block_row_ptr = p.block_row_ptr;
+  b.block_col_idx = p.block_col_idx;
+  b.blocks = p.blocks;
+  b.B = p.X;
+  b.C = p.Y;
+  b.ldc = p.M;
+  b.M = p.M;
+  b.N = p.N;
+  b.K = p.K;
+  b.n_block_rows = static_cast<int32_t>(h->n_groups);
+  b.max_ctas = h->max_ctas;
+  b.num_sms = p.num_sms;
+  b.status = p.status;
+  b.wait_limit_ns = p.wait_limit_ns;
+  CUDA_TRY(spmm::launch_bcsr_linear_adapters(h->tm_vals, tmX, tmY, b, ad, bf16, out_bf16, s),
+           "projection with adapters launch");
+  return SPMM_OK;
+}
+
+// Batches up to this many rows take the row kernels, longer ones the tiled ones.
+constexpr int64_t kRowsPath = 64;
+
 // Y = X W^T + adapters, with D rank x K and U M x rank per adapter.
-spmm_status project(spmm_handle h, spmm::AdapterParams p, const void *X, void *Y, const void *down, const void *up, float *H,
-                    cudaStream_t s) {
+spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const void *X, void *Y, const void *down,
+                    const void *up, float *H, bool tiled, cudaStream_t s) {
   const bool bf16 = h->in_t == SPMM_BF16;
   p.X = X;
   p.Y = Y;
@@ -107,6 +179,11 @@ spmm_status project(spmm_handle h, spmm::AdapterParams p, const void *X, void *Y
   p.up = up;
   p.M = static_cast<int32_t>(h->m);
   p.K = static_cast<int32_t>(h->k);
+  if (tiled) {
+    const int parts = h->out_t == SPMM_F32 ? 2 : 1;
+    const spmm_status st = down_project(a, p, parts, s);
+    return st != SPMM_OK ? st : up_project(h, a, p, parts, s);
+  }
   CUDA_TRY(spmm::launch_shrink(p, bf16, s), "adapter down projection launch");
   CUDA_TRY(spmm::launch_linear_adapters(p, bf16, h->out_t == SPMM_BF16, s), "projection with adapters launch");
   return SPMM_OK;
@@ -151,6 +228,10 @@ spmm_status spmm_adapters_create(spmm_adapters *out, int64_t m, int64_t k, int32
     a->sm103 = major == 10 && minor == 3;
     const size_t h = static_cast<size_t>(std::max<int64_t>(max_rows, 1)) * rank * sizeof(float);
     CUDA_TRY(cudaMalloc(&a->d_h, h), "cudaMalloc(adapter activations)");
+    const size_t tiles = static_cast<size_t>(max_rows) / spmm::kAdapterTileRows + 1;
+    CUDA_TRY(cudaMalloc(&a->d_tile_segs, tiles * spmm::kAdapterTileRows * sizeof(spmm::TileSegment)),
+             "cudaMalloc(tile segments)");
+    CUDA_TRY(cudaMalloc(&a->d_tile_count, tiles * sizeof(int32_t)), "cudaMalloc(tile counts)");
     if (a->grad) {
       CUDA_TRY(cudaMalloc(&a->d_dh, h), "cudaMalloc(adapter gradients)");
       CUDA_TRY(cudaMalloc(&a->d_down_t, static_cast<size_t>(n_adapters) * k * rank * 2), "cudaMalloc(transposed down)");
@@ -185,7 +266,7 @@ spmm_status spmm_run_linear_adapters(spmm_handle h, spmm_adapters a, const void 
   if (N == 0) return SPMM_OK;
   if (!X || !Y) return fail(SPMM_ERR_INVALID_ARG, "X or Y is NULL");
   if (misaligned({X, Y, down, up})) return fail(SPMM_ERR_UNSUPPORTED, "X, Y, down and up must be 16-byte aligned");
-  return project(h, make_params(h, a, N, scale, seg_ptr, seg_adapter, n_seg), X, Y, down, up, a->d_h,
+  return project(h, a, make_params(h, a, N, scale, seg_ptr, seg_adapter, n_seg), X, Y, down, up, a->d_h, N > kRowsPath,
                  static_cast<cudaStream_t>(stream));
 }
 
@@ -213,7 +294,7 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
     p.H = a->d_h;
     CUDA_TRY(spmm::launch_shrink(p, bf16, s), "adapter down projection launch");
     if (dX) {
-      st = project(h_t, p, dY, dX, a->d_up_t, a->d_down_t, a->d_dh, s);
+      st = project(h_t, a, p, dY, dX, a->d_up_t, a->d_down_t, a->d_dh, false, s);
       if (st != SPMM_OK) return st;
     } else {
       p.X = dY;

@@ -21,7 +21,18 @@
 // which stay in L2); two TMEM accumulators alternate between tiles; two CTAs
 // per SM.  6 warps, as in bcsr_kernel.cu: a TMA producer, an MMA issuer and
 // four epilogue warps (warp w reads TMEM lanes 32 (w % 4) .. + 31, rows of X).
+//
+// With adapters (spmm_run_linear_adapters) a tile has further stages after its
+// blocks: for every segment with an adapter among its rows, the block row's 64
+// rows of U_a as the N operand and the tile's rows of H as the M operand, 64
+// ranks a stage.  Their MMAs update the segment's lanes only (the MMA's lane
+// mask), so the other rows' sums do not see the product at all: no zeroed copy
+// of H, and an adapter with infinities cannot reach other rows as 0 * inf.  The
+// product with adapters reads X and writes Y once; a second pass over Y would
+// move 5 GB more for 64K tokens x 18944 features.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -29,9 +40,11 @@
 namespace spmm {
 namespace {
 
+struct NoAdapters {};
+
 constexpr int kBlk = 64;
 constexpr int kBlkBytes = kBlk * kBlk * 2;
-constexpr int kTileN = 256;                    // rows of X per tile
+constexpr int kTileN = kAdapterTileRows;       // rows of X per tile (256)
 constexpr int kXBytes = kTileN * kBlk * 2;     // one 256 x 64 box of X
 constexpr int kStageBytes = kBlkBytes + kXBytes;
 constexpr int kQ = 2;                          // stages per CTA
@@ -52,8 +65,9 @@ struct TileRec {
   int32_t br;
   int32_t nt;
   int32_t flags;
-  int32_t pad_;
+  int32_t rows;  // adapter stage: its rows of the tile, begin | end << 16
 };
+constexpr int32_t kRecAdapter = 16, kRecStepsShift = 8;  // adapter stage, with its 16-rank steps
 
 constexpr int kGroupN = 8;
 __device__ __forceinline__ void tile_coords(int64_t t, int n_block_rows, int n_tiles_n, int &br, int &nt) {
@@ -68,10 +82,12 @@ __device__ __forceinline__ void tile_coords(int64_t t, int n_block_rows, int n_t
 // Y's parts per tile and warp: 2 halves of 128 rows (the warp's 32 rows of
 // each) x 64 output features, as 128-byte box rows: one box per half for bf16
 // Y, two (32 features each) for fp32.
-template <bool IN_BF16, bool OUT_BF16>
+template <bool IN_BF16, bool OUT_BF16, class Adapters>
 __global__ void __launch_bounds__(kThreads, 2)
     bcsr_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmX,
-                       const __grid_constant__ CUtensorMap tmY, const BcsrParams p) {
+                       const __grid_constant__ CUtensorMap tmY, const BcsrParams p,
+                       const __grid_constant__ Adapters ad) {
+  constexpr bool kAdapt = std::is_same_v<Adapters, LinearAdapters>;
   constexpr int kOutBytes = OUT_BF16 ? 2 : 4;
   constexpr int kBoxCols = 128 / kOutBytes;      // features per box row
   constexpr int kParts = 2 * (kBlk / kBoxCols);  // store boxes per warp and tile
@@ -136,11 +152,27 @@ __global__ void __launch_bounds__(kThreads, 2)
         phase ^= 1u;
       }
     };
+    if constexpr (kAdapt) grid_dependency_wait();  // the tile lists and H
     for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
       int br, nt;
       tile_coords(t, p.n_block_rows, n_tiles_n, br, nt);
       const int64_t jb = p.block_row_ptr[br], je = p.block_row_ptr[br + 1];
-      if (jb == je) {
+      int32_t segs = 0;  // segments with an adapter in the tile
+      if constexpr (kAdapt) segs = ad.tile_count[nt];
+      if (jb == je && segs > 0) {
+        // no block to start the sums with: a stage of zeros, read past the end of the blocks and of X
+        ok = claim();
+        if (!ok) break;
+        if (lane == 0) {
+          tile_rec[stage] = TileRec{br, nt, kRecFirst, 0};
+          const uint32_t fb = full0 + 8 * stage;
+          const uint32_t st = smem_addr(smem + stage * kStageBytes);
+          mbar_arrive_expect_tx(fb, kStageBytes);
+          tma_load_2d(st, &tmA, fb, kBlk, 0);
+          tma_load_2d(st + kBlkBytes, &tmX, fb, (p.K + kBlk - 1) / kBlk * kBlk, 0);
+        }
+        advance();
+      } else if (jb == je) {
         ok = claim();
         if (!ok) break;
         if (lane == 0) {
@@ -159,7 +191,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (!ok) break;
           if (lane == 0) {
             const int64_t j = jbase + i;
-            tile_rec[stage] = TileRec{br, nt, (j == jb ? kRecFirst : 0) | (j == je - 1 ? kRecLast : 0), 0};
+            tile_rec[stage] =
+                TileRec{br, nt, (j == jb ? kRecFirst : 0) | (j == je - 1 && segs == 0 ? kRecLast : 0), 0};
             const uint32_t fb = full0 + 8 * stage;
             const uint32_t st = smem_addr(smem + stage * kStageBytes);
             mbar_arrive_expect_tx(fb, kStageBytes);
@@ -167,6 +200,35 @@ __global__ void __launch_bounds__(kThreads, 2)
             tma_load_2d(st + kBlkBytes, &tmX, fb, bcol * kBlk, nt * kTileN);
           }
           advance();
+        }
+      }
+      if constexpr (kAdapt) {
+        const int chunks = (ad.rank + kBlk - 1) / kBlk;
+        for (int32_t base = 0; base < segs && ok; base += 32) {
+          TileSegment my{};
+          if (base + lane < segs) my = ad.tile_segs[static_cast<int64_t>(nt) * kAdapterTileRows + base + lane];
+          const int cnt = min(segs - base, 32);
+          for (int i = 0; i < cnt && ok; ++i) {
+            const int32_t a = __shfl_sync(0xffffffffu, my.adapter, i);
+            const int32_t rows = __shfl_sync(0xffffffffu, my.begin | my.end << 16, i);
+            for (int c = 0; c < chunks * ad.parts; ++c) {
+              ok = claim();
+              if (!ok) break;
+              if (lane == 0) {
+                const int part = c / chunks, r0 = (c - part * chunks) * kBlk;
+                const int steps = (min(ad.rank - r0, kBlk) + 15) / 16;
+                const bool last = base + i == segs - 1 && c == chunks * ad.parts - 1;
+                tile_rec[stage] =
+                    TileRec{br, nt, kRecAdapter | steps << kRecStepsShift | (last ? kRecLast : 0), rows};
+                const uint32_t fb = full0 + 8 * stage;
+                const uint32_t st = smem_addr(smem + stage * kStageBytes);
+                mbar_arrive_expect_tx(fb, kStageBytes);
+                tma_load_2d(st, &ad.tmU, fb, r0, a * p.M + br * kBlk);
+                tma_load_2d(st + kBlkBytes, &ad.tmH, fb, r0, part * p.N + nt * kTileN);
+              }
+              advance();
+            }
+          }
         }
       }
     }
@@ -220,13 +282,27 @@ __global__ void __launch_bounds__(kThreads, 2)
           // half h: rows 128h .. 128h + 127 of the tile
           const uint64_t bdesc0 = smem_desc_sw128(blk, 16, 1024);
           const uint64_t adesc0 = smem_desc_sw128(xt, 16, 1024);
+          if (kAdapt && (rec.flags & kRecAdapter)) {
+            const int steps = rec.flags >> kRecStepsShift;
+            const int begin = rec.rows & 0xffff, end = rec.rows >> 16;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t bdesc = smem_desc_add(bdesc0, kk * 32);
+            for (int h = 0; h < 2; ++h) {
+              if (end <= 128 * h || begin >= 128 * (h + 1)) continue;
+              uint32_t off[4];
+              lanes_off(begin - 128 * h, end - 128 * h, off);
+              for (int kk = 0; kk < steps; ++kk)
+                umma_f16_lanes(acc + h * kBlk, smem_desc_add(adesc0, h * (kXBytes / 2) + kk * 32),
+                               smem_desc_add(bdesc0, kk * 32), idesc, 1u, off);
+            }
+          } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              umma_f16(acc + h * kBlk, smem_desc_add(adesc0, h * (kXBytes / 2) + kk * 32), bdesc, idesc,
-                       (first && kk == 0) ? 0u : 1u);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t bdesc = smem_desc_add(bdesc0, kk * 32);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                umma_f16(acc + h * kBlk, smem_desc_add(adesc0, h * (kXBytes / 2) + kk * 32), bdesc, idesc,
+                         (first && kk == 0) ? 0u : 1u);
+            }
           }
         }
         umma_commit(empty0 + 8 * stage);
@@ -350,30 +426,57 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-template <bool IN_BF16, bool OUT_BF16>
+template <bool IN_BF16, bool OUT_BF16, class Adapters>
 cudaError_t launch_linear_variant(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,
-                                  const BcsrParams &p, cudaStream_t stream) {
-  auto kern = bcsr_linear_kernel<IN_BF16, OUT_BF16>;
+                                  const BcsrParams &p, const Adapters &ad, cudaStream_t stream) {
+  auto kern = bcsr_linear_kernel<IN_BF16, OUT_BF16, Adapters>;
   static std::atomic<uint64_t> smem_set{0};
   cudaError_t e = set_smem_limit_once(kern, kSmemBytes, smem_set);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(p.n_block_rows) * ((p.N + kTileN - 1) / kTileN);
   const int64_t cap = p.max_ctas > 0 ? p.max_ctas : 2ll * p.num_sms;
   const int64_t grid = tiles < cap ? tiles : cap;
-  kern<<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(tmA, tmX, tmY, p);
-  return cudaGetLastError();
+  if constexpr (std::is_same_v<Adapters, LinearAdapters>) {
+    // a dependent of the down projection: set up while it ends
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, tmA, tmX, tmY, p, ad);
+  } else {
+    kern<<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(tmA, tmX, tmY, p, ad);
+    return cudaGetLastError();
+  }
+}
+
+template <class Adapters>
+cudaError_t launch_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY, const BcsrParams &p,
+                          const Adapters &ad, bool in_bf16, bool out_bf16, cudaStream_t stream) {
+  if (p.n_block_rows == 0 || p.N == 0) return cudaSuccess;
+  if (in_bf16)
+    return out_bf16 ? launch_linear_variant<true, true>(tmA, tmX, tmY, p, ad, stream)
+                    : launch_linear_variant<true, false>(tmA, tmX, tmY, p, ad, stream);
+  return out_bf16 ? launch_linear_variant<false, true>(tmA, tmX, tmY, p, ad, stream)
+                  : launch_linear_variant<false, false>(tmA, tmX, tmY, p, ad, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_bcsr_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,
                                const BcsrParams &p, bool in_bf16, bool out_bf16, cudaStream_t stream) {
-  if (p.n_block_rows == 0 || p.N == 0) return cudaSuccess;
-  if (in_bf16)
-    return out_bf16 ? launch_linear_variant<true, true>(tmA, tmX, tmY, p, stream)
-                    : launch_linear_variant<true, false>(tmA, tmX, tmY, p, stream);
-  return out_bf16 ? launch_linear_variant<false, true>(tmA, tmX, tmY, p, stream)
-                  : launch_linear_variant<false, false>(tmA, tmX, tmY, p, stream);
+  return launch_linear(tmA, tmX, tmY, p, NoAdapters{}, in_bf16, out_bf16, stream);
+}
+
+cudaError_t launch_bcsr_linear_adapters(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,
+                                        const BcsrParams &p, const LinearAdapters &ad, bool in_bf16, bool out_bf16,
+                                        cudaStream_t stream) {
+  return launch_linear(tmA, tmX, tmY, p, ad, in_bf16, out_bf16, stream);
 }
 
 }  // namespace spmm

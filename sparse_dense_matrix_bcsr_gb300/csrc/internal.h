@@ -99,6 +99,28 @@ cudaError_t launch_bcsr(const CUtensorMap &tmA, const CUtensorMap &tmB, const CU
 cudaError_t launch_bcsr_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,
                                const BcsrParams &p, bool in_bf16, bool out_bf16, cudaStream_t stream);
 
+// Rows of X per tile of that kernel.
+constexpr int kAdapterTileRows = 256;
+// A segment with an adapter among a tile's rows: rows [begin, end) of the tile.
+struct TileSegment {
+  int32_t adapter, begin, end, pad_;
+};
+// The adapters of the same product (launch_bcsr_linear_adapters): tmU covers
+// the up matrices as [n_adapters * M rows, rank cols] with 64 x 64 boxes, tmH
+// covers H as [parts * N rows, rank cols] with 256 x 64 boxes, both 128-byte
+// swizzle; parts > 1: H is the sum of its parts.
+struct LinearAdapters {
+  CUtensorMap tmU, tmH;
+  const TileSegment *tile_segs;  // device, kAdapterTileRows per tile
+  const int32_t *tile_count;     // device, per tile: its segments with an adapter
+  int32_t rank, parts;
+};
+// Launched as a programmatic dependent of the kernel that writes H and the
+// tile lists.
+cudaError_t launch_bcsr_linear_adapters(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,
+                                        const BcsrParams &p, const LinearAdapters &ad, bool in_bf16, bool out_bf16,
+                                        cudaStream_t stream);
+
 // WCSR work is a list of stages: at most 64 packed columns of one window.
 // Every window has at least one stage (ncols = 0 for a window without
 // columns), and stages are listed in window order.
@@ -233,6 +255,26 @@ struct AdapterParams {
   uint32_t *status;
   uint64_t wait_limit_ns;
 };
+
+// H on the tensor cores (adapter_down_kernel.cu) and the projection's tile
+// lists.  tmX covers X as [N rows, K cols] with 128 x 64 boxes, tmD the down
+// matrices as [n_adapters * rank rows, K cols] with rank x 64 boxes, both
+// 128-byte swizzle.
+struct AdapterDownParams {
+  uint16_t *H;                   // device, parts x N x rank: the rows of segments with an adapter
+  TileSegment *tile_segs;
+  int32_t *tile_count;
+  const float *scale;
+  const int64_t *seg_ptr;
+  const int32_t *seg_adapter;
+  int32_t n_seg, n_adapters, rank, parts;
+  int32_t N, K;
+  int32_t split, q;              // filled in by the launch: CTAs per tile, stages
+  uint32_t *status;
+  uint64_t wait_limit_ns;
+};
+cudaError_t launch_adapter_down(const CUtensorMap &tmX, const CUtensorMap &tmD, AdapterDownParams p, int num_sms, bool bf16,
+                                cudaStream_t s);
 
 // H = scale * X D^T of the rows with an adapter (other rows of H are left alone).
 cudaError_t launch_shrink(const AdapterParams &p, bool bf16, cudaStream_t s);

@@ -213,6 +213,28 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- clusters
+// Barrier of all threads of the cluster's CTAs; what they wrote to shared
+// memory before it is visible to the others after it.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address that shared-memory address `saddr` of this CTA has in CTA `cta`.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t cta) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(cta));
+  return r;
+}
+__device__ __forceinline__ float4 cluster_load_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- cluster launch control
 // Asks the hardware to cancel the launch of one CTA of this grid that has not
 // started yet; the 16-byte answer is written to `resp` (16-byte aligned
@@ -274,6 +296,30 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint6
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// The same with some of the accumulator's lanes left as they are: bit l of
+// off[w] set keeps lane 32 w + l (row 32 w + l of an M = 128 product) out of the
+// update, whatever the operands hold there.
+__device__ __forceinline__ void umma_f16_lanes(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate, const uint32_t (&off)[4]) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
+      : "memory");
+}
+
+// Lanes [begin, end) of an M = 128 product enabled, as umma_f16_lanes takes them.
+__device__ __forceinline__ void lanes_off(int begin, int end, uint32_t (&off)[4]) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int b = min(max(begin - 32 * w, 0), 32), e = min(max(end - 32 * w, 0), 32);
+    const uint32_t below_e = e == 32 ? 0xffffffffu : (1u << e) - 1u;
+    const uint32_t below_b = b == 32 ? 0xffffffffu : (1u << b) - 1u;
+    off[w] = ~(below_e & ~below_b);
+  }
 }
 
 // Arrive once on `bar` when all tcgen05 operations issued so far by this
