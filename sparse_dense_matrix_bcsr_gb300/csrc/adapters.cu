@@ -191,43 +191,6 @@ __global__ void __launch_bounds__(256) transpose_kernel(const uint16_t *__restri
     if (c0 + i < cols && r0 + tx < rows) out[base + static_cast<int64_t>(c0 + i) * rows + r0 + tx] = tile[tx][i];
 }
 
-// ---------------------------------------------------------------- adapter weight gradients
-// G_a[f][i] = sum over rows n of adapter a of V[n][f] * H[n][i]: one block per
-// (64 features, adapter), which walks the adapter's segments in order.
-// UP writes G as [feature][rank] (dU), else as [rank][feature] (dD).
-constexpr int kWgradThreads = 256;
-template <bool BF16, bool UP>
-__global__ void __launch_bounds__(kWgradThreads) wgrad_kernel(const AdapterParams p, const uint16_t *__restrict__ V,
-                                                              int32_t F, uint16_t *__restrict__ G) {
-  const int32_t a = blockIdx.y;
-  const int32_t feature = blockIdx.x * 64 + (threadIdx.x & 63);
-  const int q = threadIdx.x >> 6;
-  float acc[32] = {};
-  for (int32_t s = 0; s < p.n_seg; ++s) {
-    if (p.seg_adapter[s] != a) continue;
-    const int64_t b = max(p.seg_ptr[s], int64_t{0}), e = min(p.seg_ptr[s + 1], static_cast<int64_t>(p.N));
-    for (int64_t n = b; n < e; ++n) {
-      float v = 0.0f;
-      if (feature < F) {
-        const uint16_t bits = V[n * F + feature];
-        v = BF16 ? __bfloat162float(__ushort_as_bfloat16(bits)) : __half2float(__ushort_as_half(bits));
-      }
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (q + 4 * i < p.rank) acc[i] = fmaf(v, p.H[n * p.rank + q + 4 * i], acc[i]);
-    }
-  }
-  if (feature >= F) return;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const int32_t r = q + 4 * i;
-    if (r >= p.rank) continue;
-    const uint16_t bits = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(acc[i])) : __half_as_ushort(__float2half_rn(acc[i]));
-    const int64_t base = static_cast<int64_t>(a) * p.rank * F;
-    G[base + (UP ? static_cast<int64_t>(feature) * p.rank + r : static_cast<int64_t>(r) * F + feature)] = bits;
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_shrink(const AdapterParams &p, bool bf16, cudaStream_t s) {
@@ -259,25 +222,6 @@ cudaError_t launch_linear_adapters(const AdapterParams &p, bool bf16, bool out_b
 cudaError_t launch_transpose(const void *in, void *out, int32_t n, int32_t rows, int32_t cols, cudaStream_t s) {
   const dim3 grid((cols + 31) / 32, (rows + 31) / 32, n);
   transpose_kernel<<<grid, 256, 0, s>>>(static_cast<const uint16_t *>(in), static_cast<uint16_t *>(out), rows, cols);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_wgrad(const AdapterParams &p, const void *V, int32_t features, void *G, bool up, bool bf16,
-                         cudaStream_t s) {
-  const dim3 grid((features + 63) / 64, p.n_adapters);
-  const uint16_t *v = static_cast<const uint16_t *>(V);
-  uint16_t *g = static_cast<uint16_t *>(G);
-  if (bf16) {
-    if (up)
-      wgrad_kernel<true, true><<<grid, kWgradThreads, 0, s>>>(p, v, features, g);
-    else
-      wgrad_kernel<true, false><<<grid, kWgradThreads, 0, s>>>(p, v, features, g);
-  } else {
-    if (up)
-      wgrad_kernel<false, true><<<grid, kWgradThreads, 0, s>>>(p, v, features, g);
-    else
-      wgrad_kernel<false, false><<<grid, kWgradThreads, 0, s>>>(p, v, features, g);
-  }
   return cudaGetLastError();
 }
 

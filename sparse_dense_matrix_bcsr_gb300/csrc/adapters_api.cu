@@ -168,7 +168,8 @@ spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams
 // Batches up to this many rows take the row kernels, longer ones the tiled ones.
 constexpr int64_t kRowsPath = 64;
 
-// Y = X W^T + adapters, with D rank x K and U M x rank per adapter.
+// Y = X W^T + adapters, with D rank x K and U M x rank per adapter; tiled: by the
+// tensor-core kernels, which leave H in 16 bits.
 spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const void *X, void *Y, const void *down,
                     const void *up, float *H, bool tiled, cudaStream_t s) {
   const bool bf16 = h->in_t == SPMM_BF16;
@@ -284,30 +285,50 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = a->in_t == SPMM_BF16;
   const int32_t m = static_cast<int32_t>(a->m), k = static_cast<int32_t>(a->k);
-  spmm::AdapterParams p = make_params(h_t, a, N, scale, seg_ptr, seg_adapter, N > 0 ? n_seg : 0);
-  if (N > 0) {
-    CUDA_TRY(spmm::launch_transpose(up, a->d_up_t, a->n_adapters, m, a->rank, s), "adapter transpose launch");
-    CUDA_TRY(spmm::launch_transpose(down, a->d_down_t, a->n_adapters, a->rank, k, s), "adapter transpose launch");
-    p.X = X;
-    p.K = k;
-    p.down = down;
-    p.H = a->d_h;
-    CUDA_TRY(spmm::launch_shrink(p, bf16, s), "adapter down projection launch");
-    if (dX) {
-      st = project(h_t, a, p, dY, dX, a->d_up_t, a->d_down_t, a->d_dh, false, s);
-      if (st != SPMM_OK) return st;
-    } else {
-      p.X = dY;
-      p.K = m;
-      p.down = a->d_up_t;
-      p.H = a->d_dh;
-      CUDA_TRY(spmm::launch_shrink(p, bf16, s), "adapter gradient launch");
-    }
+  spmm::AdapterParams p = make_params(h_t, a, N, scale, seg_ptr, seg_adapter, n_seg);
+  if (N == 0) {
+    const size_t bytes = static_cast<size_t>(a->n_adapters) * a->rank * 2;
+    CUDA_TRY(cudaMemsetAsync(d_up, 0, bytes * m, s), "clear d_up");
+    CUDA_TRY(cudaMemsetAsync(d_down, 0, bytes * k, s), "clear d_down");
+    return SPMM_OK;
   }
+  CUDA_TRY(spmm::launch_transpose(up, a->d_up_t, a->n_adapters, m, a->rank, s), "adapter transpose launch");
+  CUDA_TRY(spmm::launch_transpose(down, a->d_down_t, a->n_adapters, a->rank, k, s), "adapter transpose launch");
+  p.X = X;
+  p.K = k;
+  p.down = down;
   p.H = a->d_h;
-  CUDA_TRY(spmm::launch_wgrad(p, dY, m, d_up, true, bf16, s), "adapter weight gradient launch");
-  p.H = a->d_dh;
-  CUDA_TRY(spmm::launch_wgrad(p, X, k, d_down, false, bf16, s), "adapter weight gradient launch");
+  st = down_project(a, p, 1, s);
+  if (st != SPMM_OK) return st;
+  if (dX) {
+    st = project(h_t, a, p, dY, dX, a->d_up_t, a->d_down_t, a->d_dh, true, s);
+  } else {
+    p.X = dY;
+    p.K = m;
+    p.down = a->d_up_t;
+    p.H = a->d_dh;
+    st = down_project(a, p, 1, s);
+  }
+  spmm::AdapterWgradParams w;
+  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dy, dY, bf16, N, m, m, 64, 64);
+  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_x, X, bf16, N, k, k, 64, 64);
+  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_h, a->d_h, bf16, N, a->rank, a->rank, 64, 64);
+  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dh, a->d_dh, bf16, N, a->rank, a->rank, 64, 64);
+  if (st != SPMM_OK) return st;
+  w.d_up = static_cast<uint16_t *>(d_up);
+  w.d_down = static_cast<uint16_t *>(d_down);
+  w.seg_ptr = seg_ptr;
+  w.seg_adapter = seg_adapter;
+  w.n_seg = p.n_seg;
+  w.n_adapters = p.n_adapters;
+  w.rank = p.rank;
+  w.M = m;
+  w.N = p.N;
+  w.K = k;
+  w.up_tiles = w.split = w.q = 0;
+  w.status = p.status;
+  w.wait_limit_ns = p.wait_limit_ns;
+  CUDA_TRY(spmm::launch_adapter_wgrad(w, p.num_sms, bf16, s), "adapter weight gradient launch");
   return SPMM_OK;
 }
 

@@ -282,10 +282,22 @@ cudaError_t launch_shrink(const AdapterParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_linear_adapters(const AdapterParams &p, bool bf16, bool out_bf16, cudaStream_t s);
 // n matrices of rows x cols 16-bit elements, each transposed.
 cudaError_t launch_transpose(const void *in, void *out, int32_t n, int32_t rows, int32_t cols, cudaStream_t s);
-// G_a = sum over the rows of adapter a of V[n] H[n]^T, V N x features; G as
-// n_adapters x features x rank (up) or n_adapters x rank x features.
-cudaError_t launch_wgrad(const AdapterParams &p, const void *V, int32_t features, void *G, bool up, bool bf16,
-                         cudaStream_t s);
+
+// Gradients of the adapters' weights (adapter_wgrad_kernel.cu).  tm_dy and tm_x
+// cover dY [N rows, M cols] and X [N rows, K cols], tm_h and tm_dh H and dH
+// [N rows, rank cols], all with 64 x 64 boxes, 128-byte swizzle.
+struct AdapterWgradParams {
+  CUtensorMap tm_dy, tm_x, tm_h, tm_dh;
+  uint16_t *d_up, *d_down;
+  const int64_t *seg_ptr;
+  const int32_t *seg_adapter;
+  int32_t n_seg, n_adapters, rank;
+  int32_t M, N, K;
+  int32_t up_tiles, split, q;    // filled in by the launch
+  uint32_t *status;
+  uint64_t wait_limit_ns;
+};
+cudaError_t launch_adapter_wgrad(AdapterWgradParams p, int num_sms, bool bf16, cudaStream_t s);
 
 // ---------------------------------------------------------------- expert routing (route.cu)
 constexpr int kRouteChunk = 8192;        // ids per block of the sort
