@@ -66,6 +66,7 @@ __device__ __forceinline__ void shrink_run(const uint4 *__restrict__ D, const ui
 
 template <bool BF16>
 __global__ void __launch_bounds__(kShrinkThreads) shrink_rows_kernel(const AdapterParams p) {
+  grid_launch_dependents();  // the projection may set up and run its shared product beside this
   const int64_t n = blockIdx.x;
   const int32_t s = find_segment(p.seg_ptr, p.n_seg, n);
   if (s < 0) return;
@@ -112,69 +113,6 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_rows_kernel(const Adapt
   }
 }
 
-// ---------------------------------------------------------------- projection with adapters
-// One block per (block row, 16 rows of X): a thread holds one output feature of
-// four rows, walks the block row's stored blocks 8 columns at a time and adds
-// its rows' adapters.
-constexpr int kExpandThreads = 256;
-constexpr int kExpandRows = 16;
-template <bool BF16, bool OUT_BF16>
-__global__ void __launch_bounds__(kExpandThreads) linear_adapters_kernel(const AdapterParams p) {
-  __shared__ int32_t adapter[kExpandRows];
-  const int32_t br = blockIdx.x;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kExpandRows;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < kExpandRows; r += kExpandThreads / 32) {
-    int32_t a = -1;
-    if (n0 + r < p.N) {
-      const int32_t s = find_segment(p.seg_ptr, p.n_seg, n0 + r);
-      if (s >= 0) a = segment_adapter(p.seg_adapter, s, p.n_adapters, p.status);
-    }
-    if (lane == 0) adapter[r] = a;
-  }
-  __syncthreads();
-  const int f = threadIdx.x & 63, q = threadIdx.x >> 6;
-  float acc[4] = {};
-  for (int64_t j = p.block_row_ptr[br]; j < p.block_row_ptr[br + 1]; ++j) {
-    const int32_t c0 = p.block_col_idx[j] * 64;
-    const uint4 *blk = static_cast<const uint4 *>(p.blocks) + (j * 64 + f) * 8;
-    for (int c = 0; c < 8 && c0 + c * 8 < p.K; ++c) {
-      float w[8];
-      unpack8<BF16>(blk[c], w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t n = n0 + q * 4 + i;
-        if (n >= p.N) continue;
-        float x[8];
-        unpack8<BF16>(static_cast<const uint4 *>(p.X)[(n * p.K + c0) / 8 + c], x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i] = fmaf(w[e], x[e], acc[i]);
-      }
-    }
-  }
-  const int32_t feature = br * 64 + f;
-  if (feature >= p.M) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t n = n0 + q * 4 + i;
-    if (n >= p.N) continue;
-    const int32_t a = adapter[q * 4 + i];
-    if (a >= 0) {
-      const uint4 *U = static_cast<const uint4 *>(p.up) + (static_cast<int64_t>(a) * p.M + feature) * (p.rank / 8);
-      for (int c = 0; c < p.rank / 8; ++c) {
-        float u[8];
-        unpack8<BF16>(U[c], u);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i] = fmaf(u[e], p.H[n * p.rank + c * 8 + e], acc[i]);
-      }
-    }
-    if constexpr (OUT_BF16)
-      static_cast<__nv_bfloat16 *>(p.Y)[n * p.M + feature] = __float2bfloat16_rn(acc[i]);
-    else
-      static_cast<float *>(p.Y)[n * p.M + feature] = acc[i];
-  }
-}
-
 // ---------------------------------------------------------------- adapter weights, transposed
 // out[a][c][r] = in[a][r][c]: the gradient runs the forward kernels with the
 // roles of D and U exchanged, which want both in the other order.
@@ -194,28 +132,11 @@ __global__ void __launch_bounds__(256) transpose_kernel(const uint16_t *__restri
 }  // namespace
 
 cudaError_t launch_shrink(const AdapterParams &p, bool bf16, cudaStream_t s) {
-  if (p.n_seg == 0) return cudaSuccess;
   const dim3 grid(static_cast<unsigned>(p.N), static_cast<unsigned>(p.rank / kShrinkRanks));
   if (bf16)
     shrink_rows_kernel<true><<<grid, kShrinkThreads, 0, s>>>(p);
   else
     shrink_rows_kernel<false><<<grid, kShrinkThreads, 0, s>>>(p);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_linear_adapters(const AdapterParams &p, bool bf16, bool out_bf16, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((p.M + 63) / 64), static_cast<unsigned>((p.N + kExpandRows - 1) / kExpandRows));
-  if (bf16) {
-    if (out_bf16)
-      linear_adapters_kernel<true, true><<<grid, kExpandThreads, 0, s>>>(p);
-    else
-      linear_adapters_kernel<true, false><<<grid, kExpandThreads, 0, s>>>(p);
-  } else {
-    if (out_bf16)
-      linear_adapters_kernel<false, true><<<grid, kExpandThreads, 0, s>>>(p);
-    else
-      linear_adapters_kernel<false, false><<<grid, kExpandThreads, 0, s>>>(p);
-  }
   return cudaGetLastError();
 }
 

@@ -185,8 +185,29 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
     const spmm_status st = down_project(a, p, parts, s);
     return st != SPMM_OK ? st : up_project(h, a, p, parts, s);
   }
+  spmm::AdapterDecodeParams d;
+  std::memset(&d, 0, sizeof d);
+  d.block_row_ptr = p.block_row_ptr;
+  d.block_col_idx = p.block_col_idx;
+  d.up = p.up;
+  d.H = p.H;
+  d.Y = p.Y;
+  d.seg_ptr = p.seg_ptr;
+  d.seg_adapter = p.seg_adapter;
+  d.n_seg = p.n_seg;
+  d.n_adapters = p.n_adapters;
+  d.rank = p.rank;
+  d.tile = p.N <= 16 ? 16 : p.N <= 32 ? 32 : spmm::kAdapterDecodeRows;
+  d.M = p.M;
+  d.N = p.N;
+  d.status = p.status;
+  d.wait_limit_ns = p.wait_limit_ns;
+  CUtensorMap tmX;
+  const spmm_status st = spmm::encode_2d(&tmX, p.X, bf16, p.N, p.K, p.K, d.tile, 64);
+  if (st != SPMM_OK) return st;
   CUDA_TRY(spmm::launch_shrink(p, bf16, s), "adapter down projection launch");
-  CUDA_TRY(spmm::launch_linear_adapters(p, bf16, h->out_t == SPMM_BF16, s), "projection with adapters launch");
+  CUDA_TRY(spmm::launch_adapter_decode(h->tm_vals, tmX, d, bf16, h->out_t == SPMM_BF16, s),
+           "projection with adapters launch");
   return SPMM_OK;
 }
 

@@ -276,10 +276,32 @@ struct AdapterDownParams {
 cudaError_t launch_adapter_down(const CUtensorMap &tmX, const CUtensorMap &tmD, AdapterDownParams p, int num_sms, bool bf16,
                                 cudaStream_t s);
 
-// H = scale * X D^T of the rows with an adapter (other rows of H are left alone).
+// H = scale * X D^T in fp32 of the rows with an adapter (other rows of H are
+// left alone), for few rows per adapter (adapters.cu).
 cudaError_t launch_shrink(const AdapterParams &p, bool bf16, cudaStream_t s);
-// Y = X W^T + U H per row.
-cudaError_t launch_linear_adapters(const AdapterParams &p, bool bf16, bool out_bf16, cudaStream_t s);
+
+// Y = X W^T + U H per row for such batches (adapter_decode_kernel.cu): tiles of
+// `tile` (16, 32 or 64) rows.  tmA as for launch_bcsr, tmX covers X as
+// [N rows, K cols] with tile x 64 boxes, 128-byte swizzle.  Launched as a
+// programmatic dependent of launch_shrink's kernel.
+constexpr int kAdapterDecodeRows = 64;
+struct AdapterDecodeParams {
+  const int64_t *block_row_ptr;
+  const int32_t *block_col_idx;
+  const void *up;
+  const float *H;                // device, N x rank fp32
+  void *Y;
+  const int64_t *seg_ptr;
+  const int32_t *seg_adapter;
+  int32_t n_seg, n_adapters, rank, tile;
+  int32_t M, N;
+  int32_t q, qu;                 // filled in by the launch: stages, slots of U
+  uint32_t *status;
+  uint64_t wait_limit_ns;
+};
+cudaError_t launch_adapter_decode(const CUtensorMap &tmA, const CUtensorMap &tmX, AdapterDecodeParams p, bool bf16,
+                                  bool out_bf16, cudaStream_t s);
+
 // n matrices of rows x cols 16-bit elements, each transposed.
 cudaError_t launch_transpose(const void *in, void *out, int32_t n, int32_t rows, int32_t cols, cudaStream_t s);
 
