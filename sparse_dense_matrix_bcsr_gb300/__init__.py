@@ -411,10 +411,29 @@ class SpMM:
             pass
 
 
+# What the calls below need of torch, looked up once at their first use: a
+# decoding step makes several of them, each a few microseconds of host time.
+_torch = None
+_raw_stream = None
+_ROW_DTYPES = {}
+
+
+def _load_torch():
+    global _torch, _raw_stream
+    import torch
+    _ROW_DTYPES.update({torch.float16: SPMM_F16, torch.bfloat16: SPMM_BF16, torch.float32: SPMM_F32})
+    # the current stream's handle without building a Stream object around it (3 us)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    load_library()
+    _torch = torch
+    return torch
+
+
 def _tensor(t, name, dtype, shape):
-    """Raises ValueError unless t is a contiguous CUDA tensor of this dtype and shape."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous CUDA tensor {dtype} {shape}, "
+    """Address of t; raises ValueError unless it is a contiguous CUDA tensor of this dtype and shape."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor {dtype} {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
     return t.data_ptr()
 
@@ -430,40 +449,45 @@ class Adapters:
 
     def __init__(self, m: int, k: int, n_adapters: int, rank: int, in_t="bf16", max_rows: int = 0,
                  max_segments: int = 0, grad: bool = True):
-        import torch
+        torch = _torch or _load_torch()
         self.m, self.k, self.n_adapters, self.rank = m, k, n_adapters, rank
         self._dtype = {SPMM_F16: torch.float16, SPMM_BF16: torch.bfloat16}.get(_dt(in_t))
-        self._out = {SPMM_BF16: torch.bfloat16, SPMM_F32: torch.float32}
-        self._index, self._ids, self._scale = torch.int64, torch.int32, torch.float32
+        self._down, self._up, self._scale = (n_adapters, rank, k), (n_adapters, m, rank), (n_adapters,)
         self.a = spmm_adapters_create(m, k, n_adapters, rank, in_t, max_rows, max_segments, grad)
 
-    def _batch(self, down, up, scale, seg_ptr, seg_adapter):
-        n_seg = seg_adapter.shape[0]
-        return (_tensor(down, "down", self._dtype, (self.n_adapters, self.rank, self.k)),
-                _tensor(up, "up", self._dtype, (self.n_adapters, self.m, self.rank)),
-                _tensor(scale, "scale", self._scale, (self.n_adapters,)),
-                _tensor(seg_ptr, "seg_ptr", self._index, (n_seg + 1,)),
-                _tensor(seg_adapter, "seg_adapter", self._ids, (n_seg,)), n_seg)
+    def _out(self, layer):
+        return _torch.bfloat16 if _dt(layer.out_t) == SPMM_BF16 else _torch.float32
 
     def linear(self, layer: SpMM, X, Y, down, up, scale, seg_ptr, seg_adapter, stream=None):
         """Y = X * A^T plus each row's adapter, for a BCSR layer A (m x k); returns Y."""
-        N = X.shape[0]
+        N, n_seg = X.shape[0], seg_adapter.shape[0]
         x = _tensor(X, "X", self._dtype, (N, self.k))
-        y = _tensor(Y, "Y", self._out[_dt(layer.out_t)], (N, self.m))
-        spmm_run_linear_adapters(layer.h, self.a, x, y, N, *self._batch(down, up, scale, seg_ptr, seg_adapter),
-                                 stream.cuda_stream if stream is not None else _torch_stream_ptr())
+        status = _lib.spmm_run_linear_adapters(
+            layer.h, self.a, x, _tensor(Y, "Y", self._out(layer), (N, self.m)), N,
+            _tensor(down, "down", self._dtype, self._down), _tensor(up, "up", self._dtype, self._up),
+            _tensor(scale, "scale", _torch.float32, self._scale),
+            _tensor(seg_ptr, "seg_ptr", _torch.int64, (n_seg + 1,)),
+            _tensor(seg_adapter, "seg_adapter", _torch.int32, (n_seg,)), n_seg,
+            (stream.cuda_stream if stream is not None else _raw_stream(X.get_device())) or None)
+        if status:
+            _check(status, "spmm_run_linear_adapters")
         return Y
 
     def grad(self, layer_t: SpMM, X, dY, dX, d_down, d_up, down, up, scale, seg_ptr, seg_adapter, stream=None):
         """Gradients of `linear` into dX (None to leave it out), d_down and d_up; layer_t holds A^T (k x m)."""
-        N = X.shape[0]
+        N, n_seg = X.shape[0], seg_adapter.shape[0]
         x = _tensor(X, "X", self._dtype, (N, self.k))
-        dy = _tensor(dY, "dY", self._dtype, (N, self.m))
-        dx = None if dX is None else _tensor(dX, "dX", self._out[_dt(layer_t.out_t)], (N, self.k))
-        dd = _tensor(d_down, "d_down", self._dtype, (self.n_adapters, self.rank, self.k))
-        du = _tensor(d_up, "d_up", self._dtype, (self.n_adapters, self.m, self.rank))
-        spmm_adapters_grad(layer_t.h, self.a, x, dy, dx, dd, du, N, *self._batch(down, up, scale, seg_ptr, seg_adapter),
-                           stream.cuda_stream if stream is not None else _torch_stream_ptr())
+        status = _lib.spmm_adapters_grad(
+            layer_t.h, self.a, x, _tensor(dY, "dY", self._dtype, (N, self.m)),
+            None if dX is None else _tensor(dX, "dX", self._out(layer_t), (N, self.k)),
+            _tensor(d_down, "d_down", self._dtype, self._down), _tensor(d_up, "d_up", self._dtype, self._up), N,
+            _tensor(down, "down", self._dtype, self._down), _tensor(up, "up", self._dtype, self._up),
+            _tensor(scale, "scale", _torch.float32, self._scale),
+            _tensor(seg_ptr, "seg_ptr", _torch.int64, (n_seg + 1,)),
+            _tensor(seg_adapter, "seg_adapter", _torch.int32, (n_seg,)), n_seg,
+            (stream.cuda_stream if stream is not None else _raw_stream(X.get_device())) or None)
+        if status:
+            _check(status, "spmm_adapters_grad")
 
     def close(self):
         if getattr(self, "a", None):
@@ -477,68 +501,77 @@ class Adapters:
             pass
 
 
-def _kept_ptr(offsets):
-    """Address of offsets[n_experts], the number of kept entries."""
-    import torch
-    n = offsets.shape[0]
-    return _tensor(offsets, "offsets", torch.int64, (n,)) + 8 * (n - 1)
-
-
 def _row_dtype(t):
-    import torch
-    dt = {torch.float16: SPMM_F16, torch.bfloat16: SPMM_BF16, torch.float32: SPMM_F32}.get(t.dtype)
+    dt = _ROW_DTYPES.get(t.dtype)
     if dt is None:
         raise ValueError(f"rows must be float16, bfloat16 or float32, got {t.dtype}")
     return dt
 
 
+def _kept_ptr(offsets):
+    """Address of offsets[n_experts], the number of kept entries."""
+    n = offsets.shape[0]
+    return _tensor(offsets, "offsets", _torch.int64, (n,)) + 8 * (n - 1)
+
+
 def route_sort(ids, n_experts: int):
     """(offsets [n_experts + 1] int64, order [T * topk] int32, position [T, topk] int32) of expert ids [T, topk]
     (int32; ids outside [0, n_experts) are dropped), on the current stream."""
-    import torch
-    T, topk = ids.shape
-    p = _tensor(ids, "ids", torch.int32, (T, topk))
-    offsets = torch.empty(n_experts + 1, dtype=torch.int64, device=ids.device)
-    both = torch.empty((2, T * topk), dtype=torch.int32, device=ids.device)
-    order, position = both[0], both[1].view(T, topk)
-    size = spmm_route_workspace_bytes(T, topk, n_experts)
-    work = torch.empty(size, dtype=torch.uint8, device=ids.device).data_ptr() if size else None
-    spmm_route_sort(p, T, topk, n_experts, offsets.data_ptr(), order.data_ptr(), position.data_ptr(), work,
-                    _torch_stream_ptr())
+    torch = _torch or _load_torch()
+    T, topk = shape = ids.shape
+    p, device = _tensor(ids, "ids", torch.int32, shape), ids.device
+    offsets = torch.empty(n_experts + 1, dtype=torch.int64, device=device)
+    order = torch.empty(T * topk, dtype=torch.int32, device=device)
+    position = torch.empty_like(ids)
+    size = _lib.spmm_route_workspace_bytes(T, topk, n_experts)
+    work = torch.empty(size, dtype=torch.uint8, device=device) if size else None
+    status = _lib.spmm_route_sort(p, T, topk, n_experts, offsets.data_ptr(), order.data_ptr(), position.data_ptr(),
+                                  work.data_ptr() if size else None, _raw_stream(ids.get_device()) or None)
+    if status:
+        _check(status, "spmm_route_sort")
     return offsets, order, position
 
 
 def route_gather(x, position, offsets):
     """Rows of x [T, d] in slot order [T * topk, d]; slots that no entry takes are 0.  Current stream."""
-    import torch
-    (T, topk), d = position.shape, x.shape[1]
-    out = torch.empty((T * topk, d), dtype=x.dtype, device=x.device)
-    spmm_route_gather(_tensor(x, "x", x.dtype, (T, d)), _tensor(position, "position", torch.int32, (T, topk)),
-                      _kept_ptr(offsets), out.data_ptr(), T, topk, d, _row_dtype(x),
-                      _torch_stream_ptr())
+    torch = _torch or _load_torch()
+    T, topk = shape = position.shape
+    d, dt = x.shape[1], x.dtype
+    out = torch.empty((T * topk, d), dtype=dt, device=x.device)
+    status = _lib.spmm_route_gather(_tensor(x, "x", dt, (T, d)), _tensor(position, "position", torch.int32, shape),
+                                    _kept_ptr(offsets), out.data_ptr(), T, topk, d, _row_dtype(x),
+                                    _raw_stream(x.get_device()) or None)
+    if status:
+        _check(status, "spmm_route_gather")
     return out
 
 
 def route_combine(y, position, weights=None):
     """out[t] = sum_j weights[t, j] * y[position[t, j]] (weights None: ones), fp32 sums.  Current stream."""
-    import torch
-    (T, topk), d = position.shape, y.shape[1]
-    out = torch.empty((T, d), dtype=y.dtype, device=y.device)
-    spmm_route_combine(_tensor(y, "y", y.dtype, (T * topk, d)), _tensor(position, "position", torch.int32, (T, topk)),
-                       None if weights is None else _tensor(weights, "weights", torch.float32, (T, topk)),
-                       out.data_ptr(), T, topk, d, _row_dtype(y), _torch_stream_ptr())
+    torch = _torch or _load_torch()
+    T, topk = shape = position.shape
+    d, dt = y.shape[1], y.dtype
+    out = torch.empty((T, d), dtype=dt, device=y.device)
+    status = _lib.spmm_route_combine(_tensor(y, "y", dt, (T * topk, d)), _tensor(position, "position", torch.int32, shape),
+                                     None if weights is None else _tensor(weights, "weights", torch.float32, shape),
+                                     out.data_ptr(), T, topk, d, _row_dtype(y), _raw_stream(y.get_device()) or None)
+    if status:
+        _check(status, "spmm_route_combine")
     return out
 
 
 def route_combine_grad(dout, y, position, weights, offsets):
     """(dy [T * topk, d], dweights [T, topk] fp32) of route_combine.  Current stream."""
-    import torch
-    (T, topk), d = position.shape, y.shape[1]
+    torch = _torch or _load_torch()
+    T, topk = shape = position.shape
+    d, dt = y.shape[1], y.dtype
     dy = torch.empty_like(y)
-    dw = torch.empty((T, topk), dtype=torch.float32, device=y.device)
-    spmm_route_combine_grad(_tensor(dout, "dout", y.dtype, (T, d)), _tensor(y, "y", y.dtype, (T * topk, d)),
-                            _tensor(position, "position", torch.int32, (T, topk)),
-                            None if weights is None else _tensor(weights, "weights", torch.float32, (T, topk)),
-                            _kept_ptr(offsets), dy.data_ptr(), dw.data_ptr(), T, topk, d,
-                            _row_dtype(y), _torch_stream_ptr())
+    dw = torch.empty(shape, dtype=torch.float32, device=y.device)
+    status = _lib.spmm_route_combine_grad(
+        _tensor(dout, "dout", dt, (T, d)), _tensor(y, "y", dt, (T * topk, d)),
+        _tensor(position, "position", torch.int32, shape),
+        None if weights is None else _tensor(weights, "weights", torch.float32, shape), _kept_ptr(offsets), dy.data_ptr(),
+        dw.data_ptr(), T, topk, d, _row_dtype(y), _raw_stream(y.get_device()) or None)
+    if status:
+        _check(status, "spmm_route_combine_grad")
     return dy, dw

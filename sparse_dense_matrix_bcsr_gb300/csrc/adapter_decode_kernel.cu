@@ -9,8 +9,10 @@
 // CUDA cores in fp32, since every row has its own U_a and an MMA would run for one
 // row: the 64 rows of U_a that the block row needs are contiguous (64 * rank
 // values), come by one bulk copy each through a ring of their own and are
-// multiplied with h, kept in fp32, as they arrive.  A row meets its own adapter
-// alone.
+// multiplied with h, kept in fp32, as they arrive.  A warp (two or four above 32
+// ranks) takes a piece of up to 8 rows of one segment with a copy of U of its own, so 64 requests and one
+// request of 64 rows keep all summing warps busy alike.  A row meets its own
+// adapter alone.
 //
 // HBM bounds it: the blocks once (2 nnz bytes), each adapter's U once.  The ring
 // of U starts filling, and the shared product runs, before the down projection's
@@ -28,6 +30,7 @@ namespace {
 constexpr int kBlk = 64;
 constexpr int kBlkBytes = kBlk * kBlk * 2;
 constexpr int kMaxQ = 8, kMaxQU = 32;
+constexpr int kPiece = 8;               // rows of a segment that one warp takes
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kUpWarp = 2, kSumWarp0 = 4, kSumWarps = 8;
 constexpr int kThreads = (kSumWarp0 + kSumWarps) * 32;
 constexpr int kPitch = kBlk + 4;        // floats per row of y in shared memory
@@ -36,9 +39,9 @@ constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
 constexpr int kUpRing = 32 * 1024;
 
 struct Misc {
-  uint64_t full[kMaxQ], empty[kMaxQ], up_full[kMaxQU], up_empty[kMaxQU], acc_full;
-  TileSegment segs[kAdapterDecodeRows];
-  int32_t n_segs;
+  uint64_t full[kMaxQ], empty[kMaxQ], up_full[kMaxQU], up_empty[kMaxQU], acc_full, listed;
+  TileSegment segs[kAdapterDecodeRows], pieces[kAdapterDecodeRows];
+  int32_t n_pieces;
   uint32_t tmem;
   volatile int32_t abort_flag;
 };
@@ -61,49 +64,56 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float (&f)[8]) {
 
 __device__ __forceinline__ void sum_warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSumWarps * 32) : "memory"); }
 
-// y[row][feature] += U_a[feature] . h[row] for the segments g, g + GROUPS, ...: a
-// group of 64 * TPF threads takes a segment, TPF adjacent lanes a feature, each
-// every TPF-th 8 ranks of it.
-template <bool BF16, int TPF>
-__device__ __forceinline__ bool add_adapters(const AdapterDecodeParams &p, Misc *mi, const uint8_t *ring, int slot_bytes,
-                                             const float *h, float *y) {
-  constexpr int kGroups = kSumWarps * 32 / (kBlk * TPF);
-  constexpr int kMaxChunks = TPF < 4 ? 1 : kMaxRank / 8 / 4;
-  const int tid = threadIdx.x - kSumWarp0 * 32;
-  const int g = tid / (kBlk * TPF), f = tid % (kBlk * TPF) / TPF, q = tid % TPF;
-  const int chunks = p.rank / 8;
-  const int lane = threadIdx.x & 31;
-  for (int i = g; i < mi->n_segs; i += kGroups) {
-    const int slot = i % p.qu;
-    const bool r = mbar_wait_warp(smem_addr(&mi->up_full[slot]), static_cast<uint32_t>(i / p.qu) & 1u, p.wait_limit_ns);
-    if (!__shfl_sync(0xffffffffu, r && !mi->abort_flag, 0)) return false;
-    const TileSegment s = mi->segs[i];
-    const uint4 *src = reinterpret_cast<const uint4 *>(ring + slot * slot_bytes) + f * chunks;
-    float u[kMaxChunks][8];
+// y[row][feature] += U_a[feature] . h[row] for one piece, by one warp.  SPAN
+// adjacent lanes share a feature, each with 8 of its ranks (SPAN is rank / 8
+// rounded up to a power of two), so the warp reads U as contiguous 16-byte
+// words and passes 2 * SPAN times over 32 / SPAN features; where several warps
+// share a piece each takes passes [pass0, pass1).
+template <bool BF16, int SPAN>
+__device__ __forceinline__ void add_piece(const TileSegment s, const uint4 *__restrict__ U, const float *__restrict__ h,
+                                          float *__restrict__ y, int rank, int sub, int subs) {
+  const int pass0 = 2 * SPAN * sub / subs, pass1 = 2 * SPAN * (sub + 1) / subs;
+  const int lane = threadIdx.x & 31, c = lane % SPAN, f0 = lane / SPAN;
+  const int chunks = rank / 8;
+  const bool on = c < chunks;
+  auto load_h = [&](int n, float (&v)[8]) {
+    const float4 *src = reinterpret_cast<const float4 *>(h + n * rank) + c * 2;
+    const float4 a = on ? src[0] : make_float4(0, 0, 0, 0), b = on ? src[1] : make_float4(0, 0, 0, 0);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  };
+  auto load_u = [&](int pass, float (&u)[8]) {
+    const int f = pass * (32 / SPAN) + f0;
+    unpack8<BF16>(on ? U[f * chunks + c] : make_uint4(0, 0, 0, 0), u);
+  };
+  auto add = [&](int n, int pass, const float (&u)[8], const float (&v)[8]) {
+    float dot = 0.0f;
 #pragma unroll
-    for (int c = 0; c < kMaxChunks; ++c)
-      if (q + c * TPF < chunks) unpack8<BF16>(src[q + c * TPF], u[c]);
-    for (int n = s.begin; n < s.end; ++n) {
-      float dot = 0.0f;
+    for (int i = 0; i < 8; ++i) dot = fmaf(u[i], v[i], dot);
 #pragma unroll
-      for (int c = 0; c < kMaxChunks; ++c) {
-        if (q + c * TPF < chunks) {
-          const float4 *hr = reinterpret_cast<const float4 *>(h + n * p.rank) + (q + c * TPF) * 2;
-          const float4 a = hr[0], b = hr[1];
-          dot = fmaf(u[c][0], a.x, dot), dot = fmaf(u[c][1], a.y, dot);
-          dot = fmaf(u[c][2], a.z, dot), dot = fmaf(u[c][3], a.w, dot);
-          dot = fmaf(u[c][4], b.x, dot), dot = fmaf(u[c][5], b.y, dot);
-          dot = fmaf(u[c][6], b.z, dot), dot = fmaf(u[c][7], b.w, dot);
-        }
-      }
-#pragma unroll
-      for (int o = TPF / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (q == 0) y[n * kPitch + f] += dot;
+    for (int o = SPAN / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (c == 0) y[n * kPitch + pass * (32 / SPAN) + f0] += dot;
+  };
+  if (s.end - s.begin == 1) {
+    float v[8];
+    load_h(s.begin, v);
+#pragma unroll 4
+    for (int pass = pass0; pass < pass1; ++pass) {
+      float u[8];
+      load_u(pass, u);
+      add(s.begin, pass, u, v);
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_addr(&mi->up_empty[slot]));
+  } else {
+    for (int pass = pass0; pass < pass1; ++pass) {
+      float u[8];
+      load_u(pass, u);
+#pragma unroll 4
+      for (int n = s.begin; n < s.end; ++n) {
+        float v[8];
+        load_h(n, v);
+        add(n, pass, u, v);
+      }
+    }
   }
-  return true;
 }
 
 template <bool BF16, bool OUT_BF16>
@@ -116,15 +126,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int slot_bytes = kBlk * p.rank * 2;
   uint8_t *ring = smem + p.q * stage_bytes;                                    // U
   float *h = reinterpret_cast<float *>(ring + p.qu * slot_bytes);              // [tile][rank]
-  float *y = h + p.tile * p.rank;                                              // [tile][kPitch]
-  Misc *mi = reinterpret_cast<Misc *>(y + p.tile * kPitch);
+  Misc *mi = reinterpret_cast<Misc *>(h + p.tile * p.rank);
+  float *y = reinterpret_cast<float *>(smem);                                  // [tile][kPitch], once the stages are done with
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t br = blockIdx.x;
   const int32_t row0 = blockIdx.y * p.tile;
   const int32_t rows = min(p.N - row0, p.tile);
   const int32_t feats = min(p.M - br * kBlk, kBlk);
   const uint32_t tmem_cols = p.tile < 32 ? 32 : p.tile;
-  const int groups = p.rank == 8 ? 4 : p.rank == 16 ? 2 : 1;  // segments that the summing warps take at a time
+  // Every slot of U's ring belongs to the same summing warps each time round (a
+  // warp that skipped uses of a slot could mistake an older phase of its
+  // barrier for the one it waits for): as many groups as slots, or one warp each.
+  const int groups = min(p.qu, kSumWarps), subs = kSumWarps / groups;
   const int64_t jb = p.block_row_ptr[br], je = p.block_row_ptr[br + 1];
 
   if (threadIdx.x == 0) {
@@ -134,9 +147,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     for (int q = 0; q < p.qu; ++q) {
       mbar_init(smem_addr(&mi->up_full[q]), 1);
-      mbar_init(smem_addr(&mi->up_empty[q]), kSumWarps / groups);
+      mbar_init(smem_addr(&mi->up_empty[q]), subs);
     }
     mbar_init(smem_addr(&mi->acc_full), 1);
+    mbar_init(smem_addr(&mi->listed), 1);
     mi->abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmA);
@@ -145,11 +159,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(&mi->tmem), tmem_cols);
     tmem_relinquish();
-  }
-  if (warp == kUpWarp) {
-    const int32_t c = list_segments(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, row0, row0 + rows, mi->segs,
-                                    kAdapterDecodeRows, p.status);
-    if (lane == 0) mi->n_segs = c;
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -220,10 +229,35 @@ __global__ void __launch_bounds__(kThreads, 2)
       umma_commit(smem_addr(&mi->acc_full));
     }
   } else if (warp == kUpWarp) {
+    const int32_t n_segs = list_segments(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, row0, row0 + rows, mi->segs,
+                                         kAdapterDecodeRows, p.status);
+    __syncwarp();
+    int32_t n_pieces = 0;
+    for (int32_t base = 0; base < n_segs; base += 32) {
+      TileSegment s{-1, 0, 0, 0};
+      if (base + lane < n_segs) s = mi->segs[base + lane];
+      const int32_t count = (s.end - s.begin + kPiece - 1) / kPiece;
+      int32_t incl = count;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int32_t up = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += up;
+      }
+      for (int32_t i = 0; i < count; ++i) {
+        const int32_t at = n_pieces + incl - count + i;  // at most one per row
+        if (at < kAdapterDecodeRows)
+          mi->pieces[at] = TileSegment{s.adapter, s.begin + i * kPiece, min(s.begin + (i + 1) * kPiece, s.end), 0};
+      }
+      n_pieces += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    n_pieces = min(n_pieces, kAdapterDecodeRows);
+    if (lane == 0) mi->n_pieces = n_pieces;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&mi->listed));
     const uint32_t bytes = feats * p.rank * 2;
     bool ok = true;
     int32_t i = 0;
-    for (; i < mi->n_segs; ++i) {
+    for (; i < n_pieces; ++i) {
       const int slot = i % p.qu;
       const bool r = mbar_wait_warp(smem_addr(&mi->up_empty[slot]), (static_cast<uint32_t>(i / p.qu) & 1u) ^ 1u,
                                     p.wait_limit_ns);
@@ -234,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_arrive_expect_tx(fb, bytes);
         tma_bulk_load(smem_addr(ring + slot * slot_bytes),
                       static_cast<const uint16_t *>(p.up) +
-                          (static_cast<int64_t>(mi->segs[i].adapter) * p.M + br * kBlk) * p.rank,
+                          (static_cast<int64_t>(mi->pieces[i].adapter) * p.M + br * kBlk) * p.rank,
                       bytes, fb);
       }
       __syncwarp();
@@ -276,17 +310,32 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = tid - 128; i < rows * p.rank / 4; i += 128) reinterpret_cast<float4 *>(h)[i] = src[i];
     }
     sum_warps_sync();
-    if (ok) {
+    ok = ok && mbar_wait_warp(smem_addr(&mi->listed), 0, p.wait_limit_ns);
+    const int32_t n_pieces = ok ? mi->n_pieces : 0;
+    const int sub = (warp - kSumWarp0) % subs;
+    for (int32_t i = (warp - kSumWarp0) / subs; i < n_pieces; i += groups) {
+      const int slot = i % p.qu;
+      const bool r = mbar_wait_warp(smem_addr(&mi->up_full[slot]), static_cast<uint32_t>(i / p.qu) & 1u, p.wait_limit_ns);
+      ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
+      if (!ok) break;
+      const TileSegment s = mi->pieces[i];
+      const uint4 *U = reinterpret_cast<const uint4 *>(ring + slot * slot_bytes);
       if (p.rank == 8)
-        ok = add_adapters<BF16, 1>(p, mi, ring, slot_bytes, h, y);
+        add_piece<BF16, 1>(s, U, h, y, p.rank, sub, subs);
       else if (p.rank == 16)
-        ok = add_adapters<BF16, 2>(p, mi, ring, slot_bytes, h, y);
+        add_piece<BF16, 2>(s, U, h, y, p.rank, sub, subs);
+      else if (p.rank <= 32)
+        add_piece<BF16, 4>(s, U, h, y, p.rank, sub, subs);
+      else if (p.rank <= 64)
+        add_piece<BF16, 8>(s, U, h, y, p.rank, sub, subs);
       else
-        ok = add_adapters<BF16, 4>(p, mi, ring, slot_bytes, h, y);
-      if (!ok && lane == 0) {
-        atomicOr(p.status, kDevTimeout);
-        mi->abort_flag = 1;
-      }
+        add_piece<BF16, 16>(s, U, h, y, p.rank, sub, subs);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&mi->up_empty[slot]));
+    }
+    if (!ok && lane == 0) {
+      atomicOr(p.status, kDevTimeout);
+      mi->abort_flag = 1;
     }
     sum_warps_sync();
     for (int i = tid; i < rows * (kBlk / 8); i += kSumWarps * 32) {
@@ -317,12 +366,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 cudaError_t launch_adapter_decode(const CUtensorMap &tmA, const CUtensorMap &tmX, AdapterDecodeParams p, bool bf16,
                                   bool out_bf16, cudaStream_t s) {
-  // the stages get what U's ring, h and y leave of half an SM
+  // the stages get what U's ring and h leave of half an SM; y takes their place at the end
   const int slot = kBlk * p.rank * 2, stage = kBlkBytes + p.tile * 128;
-  p.qu = kUpRing / slot < kMaxQU ? kUpRing / slot : kMaxQU;
-  const int fixed = p.qu * slot + p.tile * (p.rank + kPitch) * 4 + kMiscBytes + 1024;
+  p.qu = kMaxQU;  // a power of two
+  while (p.qu * slot > kUpRing) p.qu /= 2;
+  const int fixed = p.qu * slot + p.tile * p.rank * 4 + kMiscBytes + 1024;
   p.q = (kSmemLimit - fixed) / stage;
   if (p.q < 2) p.q = 2;
+  static_assert(2 * (kBlkBytes + 16 * 128) >= 16 * kPitch * 4 && 2 * (kBlkBytes + 64 * 128) >= 64 * kPitch * 4,
+                "y fits in two stages");
   if (p.q > kMaxQ) p.q = kMaxQ;
   const int smem = fixed + p.q * stage;
   auto kern = bf16 ? (out_bf16 ? adapter_decode_kernel<true, true> : adapter_decode_kernel<true, false>)

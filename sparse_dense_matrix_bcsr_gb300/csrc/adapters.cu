@@ -68,14 +68,11 @@ template <bool BF16>
 __global__ void __launch_bounds__(kShrinkThreads) shrink_rows_kernel(const AdapterParams p) {
   grid_launch_dependents();  // the projection may set up and run its shared product beside this
   const int64_t n = blockIdx.x;
-  const int32_t s = find_segment(p.seg_ptr, p.n_seg, n);
-  if (s < 0) return;
-  const int64_t b = p.seg_ptr[s], e = min(p.seg_ptr[s + 1], static_cast<int64_t>(p.N));
+  const RowSegment seg = find_row(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, n, p.status);
+  const int32_t a = seg.adapter;
   const int64_t group = n / kShrinkRows * kShrinkRows;
-  if (n != max(b, group)) return;
-  const int rows = static_cast<int>(min(e, group + kShrinkRows) - n);
-  const int32_t a = segment_adapter(p.seg_adapter, s, p.n_adapters, p.status);
-  if (a < 0) return;
+  if (a < 0 || n != max(seg.begin, group)) return;
+  const int rows = static_cast<int>(min(min(seg.end, static_cast<int64_t>(p.N)), group + kShrinkRows) - n);
   const int32_t j0 = blockIdx.y * kShrinkRanks;
   const int32_t k8 = p.K / 8;
   const uint4 *D = static_cast<const uint4 *>(p.down) + (static_cast<int64_t>(a) * p.rank + j0) * k8;

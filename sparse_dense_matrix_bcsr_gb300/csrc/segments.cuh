@@ -28,17 +28,9 @@ __device__ __forceinline__ int32_t last_segment_from(const int64_t *__restrict__
   return -1;
 }
 
-// The segment that holds row n, or -1.
-__device__ __forceinline__ int32_t find_segment(const int64_t *__restrict__ seg_ptr, int32_t n_seg, int64_t n) {
-  const int32_t s = last_segment_from(seg_ptr, n_seg, n);
-  return s >= 0 && seg_ptr[s + 1] > n ? s : -1;
-}
-
 // The adapter of segment s: -1 for none; an index outside the pool is recorded
 // in the status word and taken as none.
-__device__ __forceinline__ int32_t segment_adapter(const int32_t *__restrict__ seg_adapter, int32_t s, int32_t n_adapters,
-                                                   uint32_t *status) {
-  const int32_t a = seg_adapter[s];
+__device__ __forceinline__ int32_t checked_adapter(int32_t a, int32_t n_adapters, uint32_t *status) {
   if (a < -1 || a >= n_adapters) {
     atomicOr(status, kDevIndex);
     return -1;
@@ -46,34 +38,96 @@ __device__ __forceinline__ int32_t segment_adapter(const int32_t *__restrict__ s
   return a;
 }
 
+// Batches of up to kFewSegments are looked through whole, with every load in
+// flight at once: one memory round trip instead of a search's three or four,
+// which is what a decoding step waits for.
+constexpr int kFewGroups = 4;
+constexpr int32_t kFewSegments = 32 * kFewGroups;
+
+// Lane l holds segments l, l + 32, ... of such a batch; segments that do not
+// exist are empty.
+struct FewSegments {
+  int64_t begin[kFewGroups], end[kFewGroups];
+  int32_t adapter[kFewGroups];
+  __device__ __forceinline__ FewSegments(const int64_t *__restrict__ seg_ptr, const int32_t *__restrict__ seg_adapter,
+                                         int32_t n_seg) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int g = 0; g < kFewGroups; ++g) {
+      const int32_t s = 32 * g + lane;
+      const bool in = s < n_seg;
+      begin[g] = in ? seg_ptr[s] : 0;
+      end[g] = in ? seg_ptr[s + 1] : 0;
+      adapter[g] = in ? seg_adapter[s] : -1;
+    }
+  }
+};
+
+// The segment that holds row n, by one warp: its rows and adapter (-1 for none).
+struct RowSegment {
+  int64_t begin, end;
+  int32_t adapter;
+};
+__device__ __forceinline__ RowSegment find_row(const int64_t *__restrict__ seg_ptr, const int32_t *__restrict__ seg_adapter,
+                                               int32_t n_seg, int32_t n_adapters, int64_t n, uint32_t *status) {
+  RowSegment r{0, 0, -1};
+  if (n_seg <= kFewSegments) {
+    const FewSegments few(seg_ptr, seg_adapter, n_seg);
+#pragma unroll
+    for (int g = 0; g < kFewGroups; ++g) {
+      const uint32_t hit = __ballot_sync(0xffffffffu, few.begin[g] <= n && n < few.end[g]);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        r.begin = __shfl_sync(0xffffffffu, few.begin[g], l);
+        r.end = __shfl_sync(0xffffffffu, few.end[g], l);
+        r.adapter = __shfl_sync(0xffffffffu, few.adapter[g], l);
+      }
+    }
+  } else {
+    const int32_t s = last_segment_from(seg_ptr, n_seg, n);
+    if (s < 0) return r;
+    r.begin = seg_ptr[s];
+    r.end = seg_ptr[s + 1];
+    r.adapter = n < r.end ? seg_adapter[s] : -1;
+  }
+  r.adapter = checked_adapter(r.adapter, n_adapters, status);
+  return r;
+}
+
 // The segments with an adapter among rows [row0, row1), in order, by one warp:
-// their rows relative to row0.  Returns how many (at most cap; row1 - row0 is
-// enough, as segments share no row).
+// out[i] with rows relative to row0.  Returns how many (at most cap; row1 - row0 is enough, as segments
+// share no row).
 __device__ __forceinline__ int32_t list_segments(const int64_t *__restrict__ seg_ptr,
                                                  const int32_t *__restrict__ seg_adapter, int32_t n_seg,
                                                  int32_t n_adapters, int64_t row0, int64_t row1, TileSegment *out,
                                                  int32_t cap, uint32_t *status) {
   const int lane = threadIdx.x & 31;
   int32_t count = 0;
-  for (int32_t base = max(last_segment_from(seg_ptr, n_seg, row0), 0); base < n_seg; base += 32) {
-    const int32_t s = base + lane;
-    bool past = true;
+  auto group = [&](int64_t begin, int64_t end, int32_t adapter) {
     TileSegment t{-1, 0, 0, 0};
-    if (s < n_seg) {
-      const int64_t b = seg_ptr[s], e = seg_ptr[s + 1];
-      past = b >= row1;
-      const int64_t lo = max(b, row0), hi = min(e, row1);
-      if (lo < hi) {
-        t.adapter = segment_adapter(seg_adapter, s, n_adapters, status);
-        t.begin = static_cast<int32_t>(lo - row0);
-        t.end = static_cast<int32_t>(hi - row0);
-      }
+    const int64_t lo = max(begin, row0), hi = min(end, row1);
+    if (lo < hi) {
+      t.adapter = checked_adapter(adapter, n_adapters, status);
+      t.begin = static_cast<int32_t>(lo - row0);
+      t.end = static_cast<int32_t>(hi - row0);
     }
     const uint32_t active = __ballot_sync(0xffffffffu, t.adapter >= 0);
     const int32_t at = count + __popc(active & ((1u << lane) - 1u));
     if (t.adapter >= 0 && at < cap) out[at] = t;
     count = min(count + __popc(active), cap);
-    if (__any_sync(0xffffffffu, past)) break;
+  };
+  if (n_seg <= kFewSegments) {
+    const FewSegments few(seg_ptr, seg_adapter, n_seg);
+#pragma unroll
+    for (int g = 0; g < kFewGroups; ++g) group(few.begin[g], few.end[g], few.adapter[g]);
+    return count;
+  }
+  for (int32_t base = max(last_segment_from(seg_ptr, n_seg, row0), 0); base < n_seg; base += 32) {
+    const int32_t s = base + lane;
+    const bool in = s < n_seg;
+    const int64_t b = in ? seg_ptr[s] : row1, e = in ? seg_ptr[s + 1] : row1;
+    group(b, e, in ? seg_adapter[s] : -1);
+    if (__any_sync(0xffffffffu, b >= row1)) break;
   }
   return count;
 }
