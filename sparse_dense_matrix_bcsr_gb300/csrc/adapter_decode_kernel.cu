@@ -8,15 +8,24 @@
 // 2-8 KB of X per block instead of a 256-row tile.  The adapters follow on the
 // CUDA cores in fp32, since every row has its own U_a and an MMA would run for one
 // row: the 64 rows of U_a that the block row needs are contiguous (64 * rank
-// values), come by one bulk copy each through a ring of their own and are
-// multiplied with h, kept in fp32, as they arrive.  A warp (two or four above 32
-// ranks) takes a piece of up to 8 rows of one segment with a copy of U of its own, so 64 requests and one
-// request of 64 rows keep all summing warps busy alike.  A row meets its own
-// adapter alone.
+// values), and the summing warps read them straight into registers, 2 KB at a
+// time with the next 2 KB in flight, and multiply them with h, kept in fp32.  (A
+// ring of bulk copies through shared memory in their place took 26 us for 64
+// single-row requests of rank 16 through 18944 features whatever the bytes: an
+// SM's copy engine starts one copy per ~110 cycles.)  A row meets its own adapter
+// alone.
 //
-// HBM bounds it: the blocks once (2 nnz bytes), each adapter's U once.  The ring
-// of U starts filling, and the shared product runs, before the down projection's
-// kernel has ended (a programmatic dependent launch); only h is waited for.
+// HBM bounds large batches of adapters (the blocks once, 2 nnz bytes, and each
+// adapter's U once), the chain of dependent loads the small ones: block row
+// pointer -> block and its column -> rows of X -> MMA -> sums -> store.  So
+// everything that does not hang on something else starts at once: blocks are
+// fetched before their columns are known, the first of U as soon as the segments
+// are, and all of it before the down projection's kernel has ended (a
+// programmatic dependent launch); only h is waited for, and the adapters' sums
+// and the shared product run side by side and meet in the store.  A layer with few block rows is
+// split over a cluster of up to 8 CTAs, each with a share of the blocks and of
+// the adapters, whose fp32 sums are added through distributed shared memory in
+// CTA order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -29,17 +38,16 @@ namespace {
 
 constexpr int kBlk = 64;
 constexpr int kBlkBytes = kBlk * kBlk * 2;
-constexpr int kMaxQ = 8, kMaxQU = 32;
+constexpr int kMaxQ = 8;
 constexpr int kPiece = 8;               // rows of a segment that one warp takes
-constexpr int kTmaWarp = 0, kMmaWarp = 1, kUpWarp = 2, kSumWarp0 = 4, kSumWarps = 8;
+constexpr int kTmaWarp = 0, kMmaWarp = 1, kSumWarp0 = 2, kSumWarps = 8;
 constexpr int kThreads = (kSumWarp0 + kSumWarps) * 32;
 constexpr int kPitch = kBlk + 4;        // floats per row of y in shared memory
-constexpr int kMiscBytes = 3072;
+constexpr int kMiscBytes = 2560;
 constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
-constexpr int kUpRing = 32 * 1024;
 
 struct Misc {
-  uint64_t full[kMaxQ], empty[kMaxQ], up_full[kMaxQU], up_empty[kMaxQU], acc_full, listed;
+  uint64_t full[kMaxQ], empty[kMaxQ], acc_full, listed;
   TileSegment segs[kAdapterDecodeRows], pieces[kAdapterDecodeRows];
   int32_t n_pieces;
   uint32_t tmem;
@@ -64,55 +72,105 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float (&f)[8]) {
 
 __device__ __forceinline__ void sum_warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSumWarps * 32) : "memory"); }
 
-// y[row][feature] += U_a[feature] . h[row] for one piece, by one warp.  SPAN
+// The adapters' share of y: y[row][feature] += U_a[feature] . h[row].  SPAN
 // adjacent lanes share a feature, each with 8 of its ranks (SPAN is rank / 8
-// rounded up to a power of two), so the warp reads U as contiguous 16-byte
-// words and passes 2 * SPAN times over 32 / SPAN features; where several warps
-// share a piece each takes passes [pass0, pass1).
+// rounded up to a power of two), so a warp reads U as contiguous 16-byte words,
+// 32 / SPAN features a pass.  A unit is up to four passes of one piece (up to
+// kPiece rows of one segment); the warps take units in turn.  Pieces share no
+// row and units of a piece no feature, so no two warps add to the same sum.
 template <bool BF16, int SPAN>
-__device__ __forceinline__ void add_piece(const TileSegment s, const uint4 *__restrict__ U, const float *__restrict__ h,
-                                          float *__restrict__ y, int rank, int sub, int subs) {
-  const int pass0 = 2 * SPAN * sub / subs, pass1 = 2 * SPAN * (sub + 1) / subs;
-  const int lane = threadIdx.x & 31, c = lane % SPAN, f0 = lane / SPAN;
-  const int chunks = rank / 8;
-  const bool on = c < chunks;
-  auto load_h = [&](int n, float (&v)[8]) {
-    const float4 *src = reinterpret_cast<const float4 *>(h + n * rank) + c * 2;
-    const float4 a = on ? src[0] : make_float4(0, 0, 0, 0), b = on ? src[1] : make_float4(0, 0, 0, 0);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+struct Adders {
+  static constexpr int kPasses = SPAN == 1 ? 2 : 4;              // per unit
+  static constexpr int kUnits = kBlk * SPAN / 32 / kPasses;      // per piece
+  static constexpr int kFeats = 32 / SPAN;                       // per pass
+  struct Unit {
+    uint4 w[kPasses];
   };
-  auto load_u = [&](int pass, float (&u)[8]) {
-    const int f = pass * (32 / SPAN) + f0;
-    unpack8<BF16>(on ? U[f * chunks + c] : make_uint4(0, 0, 0, 0), u);
-  };
-  auto add = [&](int n, int pass, const float (&u)[8], const float (&v)[8]) {
-    float dot = 0.0f;
+  const AdapterDecodeParams &p;
+  const Misc *mi;
+  int32_t br, feats, part, n_units;
+  int c, f0, chunks;
+
+  __device__ __forceinline__ Adders(const AdapterDecodeParams &p_, const Misc *mi_, int32_t br_, int32_t feats_, int32_t part_)
+      : p(p_), mi(mi_), br(br_), feats(feats_), part(part_) {
+    const int lane = threadIdx.x & 31;
+    c = lane % SPAN;
+    f0 = lane / SPAN;
+    chunks = p.rank / 8;
+    const int32_t mine = mi->n_pieces > part ? (mi->n_pieces - part + p.split - 1) / p.split : 0;
+    n_units = mine * kUnits;
+  }
+  __device__ __forceinline__ TileSegment piece(int32_t v) const { return mi->pieces[part + v / kUnits * p.split]; }
+  __device__ __forceinline__ int feature(int32_t v, int pass) const { return (v % kUnits * kPasses + pass) * kFeats + f0; }
+  __device__ __forceinline__ void load(int32_t v, Unit &u) const {
+    if (v >= n_units) return;
+    const uint4 *U = static_cast<const uint4 *>(p.up) +
+                     (static_cast<int64_t>(piece(v).adapter) * p.M + br * kBlk) * chunks;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dot = fmaf(u[i], v[i], dot);
-#pragma unroll
-    for (int o = SPAN / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (c == 0) y[n * kPitch + pass * (32 / SPAN) + f0] += dot;
-  };
-  if (s.end - s.begin == 1) {
-    float v[8];
-    load_h(s.begin, v);
-#pragma unroll 4
-    for (int pass = pass0; pass < pass1; ++pass) {
-      float u[8];
-      load_u(pass, u);
-      add(s.begin, pass, u, v);
+    for (int i = 0; i < kPasses; ++i) {
+      const int f = feature(v, i);
+      u.w[i] = c < chunks && f < feats ? __ldg(U + f * chunks + c) : make_uint4(0, 0, 0, 0);
     }
-  } else {
-    for (int pass = pass0; pass < pass1; ++pass) {
-      float u[8];
-      load_u(pass, u);
-#pragma unroll 4
-      for (int n = s.begin; n < s.end; ++n) {
-        float v[8];
-        load_h(n, v);
-        add(n, pass, u, v);
+  }
+  __device__ __forceinline__ void add(int32_t v, const Unit &u, const float *__restrict__ h, float *__restrict__ y) const {
+    const TileSegment s = piece(v);
+    float uf[kPasses][8];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) unpack8<BF16>(u.w[i], uf[i]);
+    for (int n = s.begin; n < s.end; ++n) {
+      float hv[8] = {};
+      if (c < chunks) {
+        const float4 *src = reinterpret_cast<const float4 *>(h + n * p.rank) + c * 2;
+        const float4 a = src[0], b = src[1];
+        hv[0] = a.x, hv[1] = a.y, hv[2] = a.z, hv[3] = a.w, hv[4] = b.x, hv[5] = b.y, hv[6] = b.z, hv[7] = b.w;
+      }
+      float d[kPasses];
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        d[i] = uf[i][0] * hv[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) d[i] = fmaf(uf[i][e], hv[e], d[i]);
+      }
+      float *row = y + n * kPitch;
+      if constexpr (SPAN == 1) {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) row[feature(v, i)] += d[i];
+      } else {
+        // the lanes of a feature add up and share the passes out between them
+        const bool up = (c & (SPAN / 2)) != 0;
+        float e0 = (up ? d[2] : d[0]) + __shfl_xor_sync(0xffffffffu, up ? d[0] : d[2], SPAN / 2);
+        float e1 = (up ? d[3] : d[1]) + __shfl_xor_sync(0xffffffffu, up ? d[1] : d[3], SPAN / 2);
+        if constexpr (SPAN == 2) {
+          row[feature(v, up ? 2 : 0)] += e0;
+          row[feature(v, up ? 3 : 1)] += e1;
+        } else {
+          const bool odd = (c & (SPAN / 4)) != 0;
+          float e = (odd ? e1 : e0) + __shfl_xor_sync(0xffffffffu, odd ? e0 : e1, SPAN / 4);
+#pragma unroll
+          for (int o = SPAN / 8; o > 0; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+          if (c % (SPAN / 4) == 0) row[feature(v, c / (SPAN / 4))] += e;
+        }
       }
     }
+  }
+};
+
+// The summing warps' part, from the list of pieces to y complete in shared memory.
+// ready() returns once y is cleared and h is there.
+template <bool BF16, int SPAN, class Ready>
+__device__ __forceinline__ void sum_adapters(const AdapterDecodeParams &p, const Misc *mi, int32_t br, int32_t feats,
+                                             int32_t part, const float *h, float *y, Ready &&ready) {
+  const Adders<BF16, SPAN> a(p, mi, br, feats, part);
+  typename Adders<BF16, SPAN>::Unit cur, next;
+  int32_t v = (threadIdx.x >> 5) - kSumWarp0;
+  a.load(v, cur);
+  a.load(v + kSumWarps, next);
+  ready();
+  for (; v < a.n_units; v += kSumWarps) {
+    const typename Adders<BF16, SPAN>::Unit u = cur;
+    cur = next;
+    a.load(v + 2 * kSumWarps, next);
+    a.add(v, u, h, y);
   }
 }
 
@@ -123,37 +181,37 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int stage_bytes = kBlkBytes + p.tile * 128;
-  const int slot_bytes = kBlk * p.rank * 2;
-  uint8_t *ring = smem + p.q * stage_bytes;                                    // U
-  float *h = reinterpret_cast<float *>(ring + p.qu * slot_bytes);              // [tile][rank]
-  Misc *mi = reinterpret_cast<Misc *>(h + p.tile * p.rank);
-  float *y = reinterpret_cast<float *>(smem);                                  // [tile][kPitch], once the stages are done with
+  float *h = reinterpret_cast<float *>(smem + p.q * stage_bytes);  // [tile][rank]
+  float *y = h + p.tile * p.rank;                                  // [tile][kPitch]
+  Misc *mi = reinterpret_cast<Misc *>(y + p.tile * kPitch);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t br = blockIdx.x;
+  const int32_t br = blockIdx.x / p.split, part = blockIdx.x % p.split;  // part = rank in the cluster
   const int32_t row0 = blockIdx.y * p.tile;
   const int32_t rows = min(p.N - row0, p.tile);
   const int32_t feats = min(p.M - br * kBlk, kBlk);
   const uint32_t tmem_cols = p.tile < 32 ? 32 : p.tile;
-  // Every slot of U's ring belongs to the same summing warps each time round (a
-  // warp that skipped uses of a slot could mistake an older phase of its
-  // barrier for the one it waits for): as many groups as slots, or one warp each.
-  const int groups = min(p.qu, kSumWarps), subs = kSumWarps / groups;
-  const int64_t jb = p.block_row_ptr[br], je = p.block_row_ptr[br + 1];
+  const int64_t row_begin = p.block_row_ptr[br];
+  const int64_t blocks = p.block_row_ptr[br + 1] - row_begin;
+
+  const int64_t jb = row_begin + blocks * part / p.split;
+  const int64_t je = row_begin + blocks * (part + 1) / p.split;
+  int32_t ahead = static_cast<int32_t>(min(je - jb, static_cast<int64_t>(p.q)));
 
   if (threadIdx.x == 0) {
     for (int q = 0; q < p.q; ++q) {
       mbar_init(smem_addr(&mi->full[q]), 1);
       mbar_init(smem_addr(&mi->empty[q]), 1);
     }
-    for (int q = 0; q < p.qu; ++q) {
-      mbar_init(smem_addr(&mi->up_full[q]), 1);
-      mbar_init(smem_addr(&mi->up_empty[q]), subs);
-    }
     mbar_init(smem_addr(&mi->acc_full), 1);
     mbar_init(smem_addr(&mi->listed), 1);
     mi->abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&tmA);
+    // the blocks of the first stages, before their columns have arrived
+    for (int q = 0; q < ahead; ++q) {
+      const uint32_t fb = smem_addr(&mi->full[q]);
+      mbar_arrive_expect_tx(fb, stage_bytes);
+      tma_load_2d(smem_addr(smem + q * stage_bytes), &tmA, fb, 0, static_cast<int32_t>((jb + q) * kBlk));
+    }
     tma_prefetch_desc(&tmX);
   }
   if (warp == kMmaWarp) {
@@ -174,17 +232,22 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int cnt = static_cast<int>(min(je - jbase, int64_t{32}));
       for (int i = 0; i < cnt; ++i) {
         const int32_t bcol = __shfl_sync(0xffffffffu, my_col, i);
-        const bool r = mbar_wait_warp(smem_addr(&mi->empty[stage]), phase ^ 1u, p.wait_limit_ns);
-        ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
-        if (!ok) break;
+        if (ahead <= 0) {
+          const bool r = mbar_wait_warp(smem_addr(&mi->empty[stage]), phase ^ 1u, p.wait_limit_ns);
+          ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
+          if (!ok) break;
+        }
         if (lane == 0) {
           const uint32_t fb = smem_addr(&mi->full[stage]);
           const uint32_t st = smem_addr(smem + stage * stage_bytes);
-          mbar_arrive_expect_tx(fb, stage_bytes);
-          tma_load_2d(st, &tmA, fb, 0, static_cast<int32_t>((jbase + i) * kBlk));
+          if (ahead <= 0) {
+            mbar_arrive_expect_tx(fb, stage_bytes);
+            tma_load_2d(st, &tmA, fb, 0, static_cast<int32_t>((jbase + i) * kBlk));
+          }
           tma_load_2d(st + kBlkBytes, &tmX, fb, bcol * kBlk, row0);
         }
         __syncwarp();
+        --ahead;
         ++seq;
         if (++stage == static_cast<uint32_t>(p.q)) {
           stage = 0;
@@ -199,36 +262,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_wait(smem_addr(&mi->full[i % p.q]), static_cast<uint32_t>((i / p.q) & 1), 1000000ull);
     }
   } else if (warp == kMmaWarp) {
-    const uint32_t idesc = idesc_f16(BF16, false, false, kBlk, static_cast<uint32_t>(p.tile));
-    uint32_t stage = 0, phase = 0;
-    bool ok = true;
-    for (int64_t j = jb; j < je; ++j) {
-      const bool r = mbar_wait_warp(smem_addr(&mi->full[stage]), phase, p.wait_limit_ns);
-      ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
-      if (!ok) break;
-      if (lane == 0) {
-        tc_fence_after_sync();
-        const uint32_t st = smem_addr(smem + stage * stage_bytes);
-        const uint64_t a = smem_desc_sw128(st, 16, 1024), b = smem_desc_sw128(st + kBlkBytes, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_f16(tmem, smem_desc_add(a, kk * 32), smem_desc_add(b, kk * 32), idesc, (j > jb || kk > 0) ? 1u : 0u);
-        umma_commit(smem_addr(&mi->empty[stage]));
-      }
-      __syncwarp();
-      if (++stage == static_cast<uint32_t>(p.q)) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    }
-    if (lane == 0) {
-      if (!ok) {
-        atomicOr(p.status, kDevTimeout);
-        mi->abort_flag = 1;
-      }
-      umma_commit(smem_addr(&mi->acc_full));
-    }
-  } else if (warp == kUpWarp) {
+    // first the list of pieces, while the first stage is on its way
     const int32_t n_segs = list_segments(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, row0, row0 + rows, mi->segs,
                                          kAdapterDecodeRows, p.status);
     __syncwarp();
@@ -254,95 +288,101 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) mi->n_pieces = n_pieces;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&mi->listed));
-    const uint32_t bytes = feats * p.rank * 2;
+
+    const uint32_t idesc = idesc_f16(BF16, false, false, kBlk, static_cast<uint32_t>(p.tile));
+    uint32_t stage = 0, phase = 0;
     bool ok = true;
-    int32_t i = 0;
-    for (; i < n_pieces; ++i) {
-      const int slot = i % p.qu;
-      const bool r = mbar_wait_warp(smem_addr(&mi->up_empty[slot]), (static_cast<uint32_t>(i / p.qu) & 1u) ^ 1u,
-                                    p.wait_limit_ns);
+    for (int64_t j = jb; j < je; ++j) {
+      const bool r = mbar_wait_warp(smem_addr(&mi->full[stage]), phase, p.wait_limit_ns);
       ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
       if (!ok) break;
-      if (lane == 0) {
-        const uint32_t fb = smem_addr(&mi->up_full[slot]);
-        mbar_arrive_expect_tx(fb, bytes);
-        tma_bulk_load(smem_addr(ring + slot * slot_bytes),
-                      static_cast<const uint16_t *>(p.up) +
-                          (static_cast<int64_t>(mi->pieces[i].adapter) * p.M + br * kBlk) * p.rank,
-                      bytes, fb);
+      tc_fence_after_sync();
+      const uint32_t st = smem_addr(smem + stage * stage_bytes);
+      const uint64_t a = smem_desc_sw128(st, 16, 1024), b = smem_desc_sw128(st + kBlkBytes, 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        umma_f16_elect(tmem, smem_desc_add(a, kk * 32), smem_desc_add(b, kk * 32), idesc, (j > jb || kk > 0) ? 1u : 0u);
+      umma_commit_elect(smem_addr(&mi->empty[stage]));
+      if (++stage == static_cast<uint32_t>(p.q)) {
+        stage = 0;
+        phase ^= 1u;
       }
-      __syncwarp();
     }
     if (!ok && lane == 0) {
       atomicOr(p.status, kDevTimeout);
       mi->abort_flag = 1;
-      for (int32_t j = i > p.qu ? i - p.qu : 0; j < i; ++j)
-        mbar_wait(smem_addr(&mi->up_full[j % p.qu]), static_cast<uint32_t>(j / p.qu) & 1u, 1000000ull);
     }
-  } else if (warp >= kSumWarp0) {
+    __syncwarp();
+    umma_commit_elect(smem_addr(&mi->acc_full));
+  } else {
     const int tid = threadIdx.x - kSumWarp0 * 32;
-    bool ok = true;
-    if (warp < kSumWarp0 + 4) {
-      // rows 16 s .. 16 s + 15 of the accumulator lie in lanes 32 s .. 32 s + 15
-      const int sp = warp & 3;
-      if (je > jb) {
-        ok = mbar_wait_warp(smem_addr(&mi->acc_full), 0, p.wait_limit_ns);
-        if (!ok && lane == 0) {
-          atomicOr(p.status, kDevTimeout);
-          mi->abort_flag = 1;
-        }
-        tc_fence_after_sync();
-        for (int c0 = 0; c0 < p.tile && ok; c0 += 16) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(sp * 32) << 16) + c0, v);
-          tmem_ld_wait();
-          if (lane < 16)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[(c0 + i) * kPitch + sp * 16 + lane] = __uint_as_float(v[i]);
-        }
-        tc_fence_before_sync();
-      } else {
-        for (int i = tid; i < p.tile * kPitch; i += 128) y[i] = 0.0f;
+    auto give_up = [&] {
+      if (lane == 0) {
+        atomicOr(p.status, kDevTimeout);
+        mi->abort_flag = 1;
       }
-    } else {
+    };
+    auto ready = [&] {
+      for (int i = tid; i < p.tile * kPitch / 4; i += kSumWarps * 32) reinterpret_cast<float4 *>(y)[i] = float4{};
       grid_dependency_wait();  // h; every block waits, so this kernel never ends before that one
       const float4 *src = reinterpret_cast<const float4 *>(p.H + static_cast<int64_t>(row0) * p.rank);
-      for (int i = tid - 128; i < rows * p.rank / 4; i += 128) reinterpret_cast<float4 *>(h)[i] = src[i];
+      for (int i = tid; i < rows * p.rank / 4; i += kSumWarps * 32) reinterpret_cast<float4 *>(h)[i] = src[i];
+      sum_warps_sync();
+    };
+    if (!mbar_wait_warp(smem_addr(&mi->listed), 0, p.wait_limit_ns)) {
+      give_up();
+      ready();
+    } else if (p.rank == 8) {
+      sum_adapters<BF16, 1>(p, mi, br, feats, part, h, y, ready);
+    } else if (p.rank == 16) {
+      sum_adapters<BF16, 2>(p, mi, br, feats, part, h, y, ready);
+    } else if (p.rank <= 32) {
+      sum_adapters<BF16, 4>(p, mi, br, feats, part, h, y, ready);
+    } else if (p.rank <= 64) {
+      sum_adapters<BF16, 8>(p, mi, br, feats, part, h, y, ready);
+    } else {
+      sum_adapters<BF16, 16>(p, mi, br, feats, part, h, y, ready);
     }
     sum_warps_sync();
-    ok = ok && mbar_wait_warp(smem_addr(&mi->listed), 0, p.wait_limit_ns);
-    const int32_t n_pieces = ok ? mi->n_pieces : 0;
-    const int sub = (warp - kSumWarp0) % subs;
-    for (int32_t i = (warp - kSumWarp0) / subs; i < n_pieces; i += groups) {
-      const int slot = i % p.qu;
-      const bool r = mbar_wait_warp(smem_addr(&mi->up_full[slot]), static_cast<uint32_t>(i / p.qu) & 1u, p.wait_limit_ns);
-      ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
-      if (!ok) break;
-      const TileSegment s = mi->pieces[i];
-      const uint4 *U = reinterpret_cast<const uint4 *>(ring + slot * slot_bytes);
-      if (p.rank == 8)
-        add_piece<BF16, 1>(s, U, h, y, p.rank, sub, subs);
-      else if (p.rank == 16)
-        add_piece<BF16, 2>(s, U, h, y, p.rank, sub, subs);
-      else if (p.rank <= 32)
-        add_piece<BF16, 4>(s, U, h, y, p.rank, sub, subs);
-      else if (p.rank <= 64)
-        add_piece<BF16, 8>(s, U, h, y, p.rank, sub, subs);
-      else
-        add_piece<BF16, 16>(s, U, h, y, p.rank, sub, subs);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&mi->up_empty[slot]));
+    if (je > jb) {
+      // Rows 16 s .. 16 s + 15 of the accumulator lie in lanes 32 s .. 32 s + 15.
+      // Two warps share them, each every other 16 columns (rows of X).
+      const int sp = warp & 3;
+      const bool ok = mbar_wait_warp(smem_addr(&mi->acc_full), 0, p.wait_limit_ns);
+      if (!ok) give_up();
+      tc_fence_after_sync();
+      for (int c0 = (warp - kSumWarp0) / 4 * 16; c0 < p.tile && ok; c0 += 32) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(sp * 32) << 16) + c0, v);
+        tmem_ld_wait();
+        if (lane < 16)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[(c0 + i) * kPitch + sp * 16 + lane] += __uint_as_float(v[i]);
+      }
     }
-    if (!ok && lane == 0) {
-      atomicOr(p.status, kDevTimeout);
-      mi->abort_flag = 1;
-    }
-    sum_warps_sync();
-    for (int i = tid; i < rows * (kBlk / 8); i += kSumWarps * 32) {
-      const int r = i / (kBlk / 8), f = i % (kBlk / 8) * 8;
+  }
+  tc_fence_before_sync();
+  if (p.split > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  {
+    const int32_t r0 = rows * part / p.split, r1 = rows * (part + 1) / p.split;
+    for (int i = threadIdx.x; i < (r1 - r0) * (kBlk / 8); i += kThreads) {
+      const int r = r0 + i / (kBlk / 8), f = i % (kBlk / 8) * 8;
       if (f >= feats) continue;  // M is a multiple of 8
-      const float4 a = *reinterpret_cast<const float4 *>(y + r * kPitch + f);
-      const float4 b = *reinterpret_cast<const float4 *>(y + r * kPitch + f + 4);
+      float4 a{}, b{};
+      if (p.split > 1) {
+        for (int c = 0; c < p.split; ++c) {
+          const uint32_t at = cluster_map(smem_addr(y + r * kPitch + f), c);
+          const float4 x = cluster_load_f4(at), z = cluster_load_f4(at + 16);
+          a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+          b.x += z.x, b.y += z.y, b.z += z.z, b.w += z.w;
+        }
+      } else {
+        a = *reinterpret_cast<const float4 *>(y + r * kPitch + f);
+        b = *reinterpret_cast<const float4 *>(y + r * kPitch + f + 4);
+      }
       const int64_t at = static_cast<int64_t>(row0 + r) * p.M + br * kBlk + f;
       if constexpr (OUT_BF16) {
         const __nv_bfloat162 v[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w),
@@ -354,8 +394,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   }
-  tc_fence_before_sync();
-  __syncthreads();
+  if (p.split > 1) cluster_sync();  // the others may still read this CTA's sums
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, tmem_cols);
@@ -364,34 +403,38 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 }  // namespace
 
-cudaError_t launch_adapter_decode(const CUtensorMap &tmA, const CUtensorMap &tmX, AdapterDecodeParams p, bool bf16,
-                                  bool out_bf16, cudaStream_t s) {
-  // the stages get what U's ring and h leave of half an SM; y takes their place at the end
-  const int slot = kBlk * p.rank * 2, stage = kBlkBytes + p.tile * 128;
-  p.qu = kMaxQU;  // a power of two
-  while (p.qu * slot > kUpRing) p.qu /= 2;
-  const int fixed = p.qu * slot + p.tile * p.rank * 4 + kMiscBytes + 1024;
+cudaError_t launch_adapter_decode(const CUtensorMap &tmA, const CUtensorMap &tmX, AdapterDecodeParams p, int num_sms,
+                                  bool bf16, bool out_bf16, cudaStream_t s) {
+  const int64_t tiles = (static_cast<int64_t>(p.M) + kBlk - 1) / kBlk * ((p.N + p.tile - 1) / p.tile);
+  p.split = 1;
+  while (p.split < 8 && tiles * p.split * 2 <= 2ll * num_sms) p.split *= 2;
+  // the stages get what h and y leave of half an SM
+  const int stage = kBlkBytes + p.tile * 128;
+  const int fixed = p.tile * (p.rank + kPitch) * 4 + kMiscBytes + 1024;
   p.q = (kSmemLimit - fixed) / stage;
-  if (p.q < 2) p.q = 2;
-  static_assert(2 * (kBlkBytes + 16 * 128) >= 16 * kPitch * 4 && 2 * (kBlkBytes + 64 * 128) >= 64 * kPitch * 4,
-                "y fits in two stages");
   if (p.q > kMaxQ) p.q = kMaxQ;
+  static_assert((kSmemLimit - kAdapterDecodeRows * (kMaxRank + kPitch) * 4 - kMiscBytes - 1024) / (kBlkBytes + 64 * 128) >= 3,
+                "at least three stages");
   const int smem = fixed + p.q * stage;
   auto kern = bf16 ? (out_bf16 ? adapter_decode_kernel<true, true> : adapter_decode_kernel<true, false>)
                    : (out_bf16 ? adapter_decode_kernel<false, true> : adapter_decode_kernel<false, false>);
   static std::atomic<uint64_t> smem_set[4];
-  cudaError_t e = set_smem_limit_once(kern, 160 * 1024, smem_set[(bf16 ? 2 : 0) + (out_bf16 ? 1 : 0)]);
+  cudaError_t e = set_smem_limit_once(kern, kSmemLimit, smem_set[(bf16 ? 2 : 0) + (out_bf16 ? 1 : 0)]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.M + kBlk - 1) / kBlk), static_cast<unsigned>((p.N + p.tile - 1) / p.tile));
+  cfg.gridDim = dim3(static_cast<unsigned>((p.M + kBlk - 1) / kBlk * p.split), static_cast<unsigned>((p.N + p.tile - 1) / p.tile));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, tmA, tmX, p);
 }
 

@@ -40,8 +40,8 @@ constexpr int kShrinkRows = 8;
 template <bool BF16, int ROWS>
 __device__ __forceinline__ void shrink_run(const uint4 *__restrict__ D, const uint4 *__restrict__ X, int32_t k8, int rows,
                                            float (&acc)[kShrinkRanks][ROWS]) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int32_t c = warp * 32 + lane; c < k8; c += kShrinkThreads) {
+#pragma unroll(ROWS == 1 ? 3 : 1)
+  for (int32_t c = threadIdx.x; c < k8; c += kShrinkThreads) {
     uint4 w[kShrinkRanks], x[ROWS];
 #pragma unroll
     for (int j = 0; j < kShrinkRanks; ++j) w[j] = D[static_cast<int64_t>(j) * k8 + c];

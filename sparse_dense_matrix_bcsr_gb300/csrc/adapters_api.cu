@@ -206,7 +206,7 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
   const spmm_status st = spmm::encode_2d(&tmX, p.X, bf16, p.N, p.K, p.K, d.tile, 64);
   if (st != SPMM_OK) return st;
   CUDA_TRY(spmm::launch_shrink(p, bf16, s), "adapter down projection launch");
-  CUDA_TRY(spmm::launch_adapter_decode(h->tm_vals, tmX, d, bf16, h->out_t == SPMM_BF16, s),
+  CUDA_TRY(spmm::launch_adapter_decode(h->tm_vals, tmX, d, p.num_sms, bf16, h->out_t == SPMM_BF16, s),
            "projection with adapters launch");
   return SPMM_OK;
 }

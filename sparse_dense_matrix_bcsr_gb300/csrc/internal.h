@@ -295,12 +295,12 @@ struct AdapterDecodeParams {
   const int32_t *seg_adapter;
   int32_t n_seg, n_adapters, rank, tile;
   int32_t M, N;
-  int32_t q, qu;                 // filled in by the launch: stages, slots of U
+  int32_t split, q;              // filled in by the launch: CTAs per tile, stages
   uint32_t *status;
   uint64_t wait_limit_ns;
 };
-cudaError_t launch_adapter_decode(const CUtensorMap &tmA, const CUtensorMap &tmX, AdapterDecodeParams p, bool bf16,
-                                  bool out_bf16, cudaStream_t s);
+cudaError_t launch_adapter_decode(const CUtensorMap &tmA, const CUtensorMap &tmX, AdapterDecodeParams p, int num_sms,
+                                  bool bf16, bool out_bf16, cudaStream_t s);
 
 // n matrices of rows x cols 16-bit elements, each transposed.
 cudaError_t launch_transpose(const void *in, void *out, int32_t n, int32_t rows, int32_t cols, cudaStream_t s);
