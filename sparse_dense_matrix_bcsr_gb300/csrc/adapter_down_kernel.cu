@@ -3,15 +3,17 @@
 // on the tensor cores, with H in the 16-bit type that the projection's MMAs
 // take it in.
 //
-// Work unit = 128 rows of X (the M operand) and all ranks (the N operand, D_a's
-// rows, both K-major as they lie in memory); one stage is 64 columns of both,
-// two TMA boxes.  A tile that several segments share runs its columns once per
-// segment, each time updating that segment's lanes only (the MMA's lane mask),
-// so every row meets its own adapter alone.  X is read once for tiles of one
-// segment; the product is 2 N r k FLOP against 2 N k bytes, far below the tensor
-// rate, so HBM bounds it for prompts.  Short batches have few tiles: a cluster
-// of up to 8 CTAs then splits a tile's columns and adds the fp32 sums through
-// distributed shared memory in CTA order (no atomics, no second launch).
+// Work unit = the part of a 128-row tile that lies in one segment: the tile's
+// rows of X are the M operand and the adapter's ranks the N operand (D_a's rows),
+// both K-major as they lie in memory; one stage is 64 columns of both, two TMA
+// boxes.  Rows of the tile outside the segment run along and are not stored, so
+// every row meets its own adapter alone; a tile that several segments share is
+// read once per segment, from L2.  2 N r k FLOP against 2 N k bytes are far below
+// the tensor rate, so HBM bounds it for prompts.  Few units leave SMs idle: a
+// cluster of up to 8 CTAs then splits a unit's columns and adds the fp32 sums
+// through distributed shared memory in CTA order (no atomics, no second launch).
+// One CTA per tile that walked the tile's segments one after another took 56
+// against 20 us for 777 rows in 40 segments (8192 columns, rank 64).
 //
 // Where the projection's output is fp32, H is kept as two 16-bit parts (the
 // value rounded, and the rest rounded), which holds 16 (bf16) or 22 (fp16) bits.
@@ -30,7 +32,7 @@ constexpr int kXBytes = kRows * 128;  // 128 rows x 64 columns
 constexpr int kMaxQ = 8;
 constexpr int kThreads = 192;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2;
-constexpr int kMiscBytes = 4096;
+constexpr int kMiscBytes = 1024;
 constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
 
 __host__ __device__ constexpr int rank16(int rank) { return (rank + 15) / 16 * 16; }
@@ -38,10 +40,8 @@ __host__ __device__ constexpr int d_bytes(int rank) { return (rank16(rank) * 128
 __host__ __device__ constexpr int part_pitch(int rank) { return rank16(rank) + 4; }  // floats per row of the CTA's sums
 
 struct Misc {
-  uint64_t full[kMaxQ], empty[kMaxQ], acc_full, drain;
-  TileSegment segs[kRows];
-  float scale[kRows];
-  int32_t n_segs;
+  uint64_t full[kMaxQ], empty[kMaxQ], acc_full;
+  RowPiece piece;
   uint32_t tmem;
   volatile int32_t abort_flag;
 };
@@ -87,8 +87,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int stage_bytes = kXBytes + d_bytes(p.rank);
   Misc *mi = reinterpret_cast<Misc *>(smem + p.q * stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t tile = blockIdx.x / p.split, part = blockIdx.x % p.split;  // part = rank in the cluster
-  const int64_t row0 = static_cast<int64_t>(tile) * kRows;
+  const int32_t unit = blockIdx.x / p.split, part = blockIdx.x % p.split;  // part = rank in the cluster
   const int n16 = rank16(p.rank);
   uint32_t tmem_cols = 32;
   while (static_cast<int>(tmem_cols) < n16) tmem_cols <<= 1;
@@ -100,67 +99,56 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_init(smem_addr(&mi->empty[q]), 1);
       }
       mbar_init(smem_addr(&mi->acc_full), 1);
-      mbar_init(smem_addr(&mi->drain), 1);
       mi->abort_flag = 0;
       fence_barrier_init();
       tma_prefetch_desc(&tmX);
       tma_prefetch_desc(&tmD);
     }
     __syncwarp();
-    const int32_t c = list_segments(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, row0,
-                                    min(row0 + kRows, static_cast<int64_t>(p.N)), mi->segs, kRows, p.status);
-    if (lane == 0) mi->n_segs = c;
-    for (int r = lane; r < kRows; r += 32) mi->scale[r] = 0.0f;
-    __syncwarp();
-    for (int i = 0; i < c; ++i) {
-      const TileSegment s = mi->segs[i];
-      const float f = p.scale[s.adapter];
-      for (int r = s.begin + lane; r < s.end; r += 32) mi->scale[r] = f;
-    }
+    const RowPiece r = find_piece(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, kRows, p.N, unit, p.status);
+    if (lane == 0) mi->piece = r;
   } else if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(&mi->tmem), tmem_cols);
     tmem_relinquish();
-  } else if (warp == kEpiWarp0 && part == 0 && tile % (kAdapterTileRows / kRows) == 0) {
+  } else if (warp == kEpiWarp0 && part == 0 && static_cast<int64_t>(unit) * kAdapterTileRows < p.N) {
     // the projection's own tiles: their segments, for its producers
-    const int32_t t = tile / (kAdapterTileRows / kRows);
+    const int64_t row0 = static_cast<int64_t>(unit) * kAdapterTileRows;
     const int32_t c = list_segments(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, row0,
-                                    min(row0 + kAdapterTileRows, static_cast<int64_t>(p.N)),
-                                    p.tile_segs + static_cast<int64_t>(t) * kAdapterTileRows, kAdapterTileRows, p.status);
-    if (lane == 0) p.tile_count[t] = c;
+                                    min(row0 + kAdapterTileRows, static_cast<int64_t>(p.N)), p.tile_segs + row0,
+                                    kAdapterTileRows, p.status);
+    if (lane == 0) p.tile_count[unit] = c;
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = mi->tmem;
-  const int32_t n_segs = mi->n_segs;
+  const RowPiece piece = mi->piece;
+  const int64_t row0 = static_cast<int64_t>(piece.tile) * kRows;
   const int32_t nk = (p.K + 63) / 64;
   const int32_t k_begin = static_cast<int32_t>(static_cast<int64_t>(nk) * part / p.split);
   const int32_t k_end = static_cast<int32_t>(static_cast<int64_t>(nk) * (part + 1) / p.split);
 
-  if (n_segs > 0) {
+  if (piece.adapter >= 0) {
     if (warp == kTmaWarp) {
       uint32_t stage = 0, phase = 0;
       int64_t seq = 0;
       bool ok = true;
-      for (int i = 0; i < n_segs && ok; ++i) {
-        const int32_t a = mi->segs[i].adapter;
-        for (int32_t c = k_begin; c < k_end; ++c) {
-          const bool r = mbar_wait_warp(smem_addr(&mi->empty[stage]), phase ^ 1u, p.wait_limit_ns);
-          ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
-          if (!ok) break;
-          if (lane == 0) {
-            const uint32_t fb = smem_addr(&mi->full[stage]);
-            const uint32_t st = smem_addr(smem + stage * stage_bytes);
-            mbar_arrive_expect_tx(fb, kXBytes + p.rank * 128);
-            tma_load_2d(st, &tmX, fb, c * 64, static_cast<int32_t>(row0));
-            tma_load_2d(st + kXBytes, &tmD, fb, c * 64, a * p.rank);
-          }
-          __syncwarp();
-          ++seq;
-          if (++stage == static_cast<uint32_t>(p.q)) {
-            stage = 0;
-            phase ^= 1u;
-          }
+      for (int32_t c = k_begin; c < k_end; ++c) {
+        const bool r = mbar_wait_warp(smem_addr(&mi->empty[stage]), phase ^ 1u, p.wait_limit_ns);
+        ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t fb = smem_addr(&mi->full[stage]);
+          const uint32_t st = smem_addr(smem + stage * stage_bytes);
+          mbar_arrive_expect_tx(fb, kXBytes + p.rank * 128);
+          tma_load_2d(st, &tmX, fb, c * 64, static_cast<int32_t>(row0));
+          tma_load_2d(st + kXBytes, &tmD, fb, c * 64, piece.adapter * p.rank);
+        }
+        __syncwarp();
+        ++seq;
+        if (++stage == static_cast<uint32_t>(p.q)) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
       if (!ok && lane == 0) {
@@ -174,39 +162,30 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t idesc = idesc_f16(BF16, false, false, kRows, static_cast<uint32_t>(n16));
       uint32_t stage = 0, phase = 0;
       bool ok = true;
-      for (int i = 0; i < n_segs && ok; ++i) {
-        const TileSegment s = mi->segs[i];
-        uint32_t off[4];
-        lanes_off(s.begin, s.end, off);
-        for (int32_t c = k_begin; c < k_end; ++c) {
-          const bool r = mbar_wait_warp(smem_addr(&mi->full[stage]), phase, p.wait_limit_ns);
-          ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
-          if (!ok) break;
-          if (lane == 0) {
-            tc_fence_after_sync();
-            const uint32_t st = smem_addr(smem + stage * stage_bytes);
-            const uint64_t x = smem_desc_sw128(st, 16, 1024);
-            const uint64_t d = smem_desc_sw128(st + kXBytes, 16, 1024);
+      for (int32_t c = k_begin; c < k_end; ++c) {
+        const bool r = mbar_wait_warp(smem_addr(&mi->full[stage]), phase, p.wait_limit_ns);
+        ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t st = smem_addr(smem + stage * stage_bytes);
+        const uint64_t x = smem_desc_sw128(st, 16, 1024);
+        const uint64_t d = smem_desc_sw128(st + kXBytes, 16, 1024);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f16_lanes(tmem, smem_desc_add(x, kk * 32), smem_desc_add(d, kk * 32), idesc,
-                             (c == k_begin && kk == 0) ? 0u : 1u, off);
-            umma_commit(smem_addr(&mi->empty[stage]));
-          }
-          __syncwarp();
-          if (++stage == static_cast<uint32_t>(p.q)) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16_elect(tmem, smem_desc_add(x, kk * 32), smem_desc_add(d, kk * 32), idesc,
+                         (c == k_begin && kk == 0) ? 0u : 1u);
+        umma_commit_elect(smem_addr(&mi->empty[stage]));
+        if (++stage == static_cast<uint32_t>(p.q)) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (lane == 0) {
-        if (!ok) {
-          atomicOr(p.status, kDevTimeout);
-          mi->abort_flag = 1;
-        }
-        umma_commit(smem_addr(&mi->acc_full));  // also waits for what was issued when giving up
+      if (!ok && lane == 0) {
+        atomicOr(p.status, kDevTimeout);
+        mi->abort_flag = 1;
       }
+      __syncwarp();
+      umma_commit_elect(smem_addr(&mi->acc_full));  // also waits for what was issued when giving up
     }
     if (warp >= kEpiWarp0) {
       const int sp = warp & 3;
@@ -218,9 +197,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       tc_fence_after_sync();
       float *sums = reinterpret_cast<float *>(smem);  // the stages are done with
-      const float f = mi->scale[r];
-      bool has = false;
-      for (int i = 0; i < n_segs; ++i) has |= r >= mi->segs[i].begin && r < mi->segs[i].end;
+      const float f = p.scale[piece.adapter];
+      const bool mine = row0 + r >= piece.begin && row0 + r < piece.end;
       for (int c0 = 0; c0 < n16 && ok; c0 += 16) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(sp * 32) << 16) + c0, v);
@@ -231,13 +209,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int i = 0; i < 4; ++i)
             dst[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
                                  __uint_as_float(v[4 * i + 3]));
-        } else if (row0 + r < p.N) {
+        } else if (mine) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (c0 + 8 * h >= p.rank) continue;
             float o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = has ? f * __uint_as_float(v[8 * h + i]) : 0.0f;
+            for (int i = 0; i < 8; ++i) o[i] = f * __uint_as_float(v[8 * h + i]);
             store_h<BF16>(p.H, row0 + r, p.N, p.rank, c0 + 8 * h, p.parts, o);
           }
         }
@@ -248,12 +226,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (p.split > 1) {
     // every CTA of the cluster comes here, whatever happened before
     cluster_sync();
-    if (n_segs > 0) {
-      const int rows = kRows / p.split, r0 = part * rows, units = p.rank / 8;
+    if (piece.adapter >= 0) {
+      // the segment's rows in equal shares
+      const int32_t begin = static_cast<int32_t>(piece.begin - row0), n = static_cast<int32_t>(piece.end - piece.begin);
+      const int32_t r0 = begin + n * part / p.split, r1 = begin + n * (part + 1) / p.split, units = p.rank / 8;
       const uint32_t base = smem_addr(smem);
-      for (int u = threadIdx.x; u < rows * units; u += kThreads) {
+      const float f = p.scale[piece.adapter];
+      for (int u = threadIdx.x; u < (r1 - r0) * units; u += kThreads) {
         const int r = r0 + u / units, j = (u % units) * 8;
-        if (row0 + r >= p.N) continue;
         float o[8] = {};
         for (int c = 0; c < p.split; ++c) {
           const uint32_t at = cluster_map(base + (r * part_pitch(p.rank) + j) * 4, c);
@@ -261,10 +241,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
           o[4] += y.x, o[5] += y.y, o[6] += y.z, o[7] += y.w;
         }
-        bool has = false;
-        for (int i = 0; i < n_segs; ++i) has |= r >= mi->segs[i].begin && r < mi->segs[i].end;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = has ? mi->scale[r] * o[i] : 0.0f;
+        for (int i = 0; i < 8; ++i) o[i] *= f;
         store_h<BF16>(p.H, row0 + r, p.N, p.rank, j, p.parts, o);
       }
     }
@@ -282,12 +260,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 cudaError_t launch_adapter_down(const CUtensorMap &tmX, const CUtensorMap &tmD, AdapterDownParams p, int num_sms, bool bf16,
                                 cudaStream_t s) {
-  const int64_t tiles = (static_cast<int64_t>(p.N) + kRows - 1) / kRows;
+  // units: see find_piece; about as many have rows
+  const int64_t units = (static_cast<int64_t>(p.N) + kRows - 1) / kRows + p.n_seg;
   const int nk = (p.K + 63) / 64;
-  // as many CTAs per tile (a cluster) as keep the grid within two per SM, with
+  // as many CTAs per unit (a cluster) as keep the grid within two per SM, with
   // at least four stages each
   p.split = 1;
-  while (p.split < 8 && tiles * p.split * 2 <= 2ll * num_sms && nk >= 8 * p.split) p.split *= 2;
+  while (p.split < 8 && units * p.split * 2 <= 2ll * num_sms && nk >= 8 * p.split) p.split *= 2;
   const int stage = kXBytes + d_bytes(p.rank);
   p.q = (kSmemLimit - kMiscBytes - 1024) / stage;
   if (p.q > kMaxQ) p.q = kMaxQ;
@@ -297,7 +276,7 @@ cudaError_t launch_adapter_down(const CUtensorMap &tmX, const CUtensorMap &tmD, 
   cudaError_t e = set_smem_limit_once(kern, kSmemLimit, smem_set[bf16 ? 1 : 0]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
+  cfg.gridDim = dim3(static_cast<unsigned>(units * p.split));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

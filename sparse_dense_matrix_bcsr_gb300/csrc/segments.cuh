@@ -63,6 +63,65 @@ struct FewSegments {
   }
 };
 
+// Row tiles of `rows` rows cut at the segments' ends: piece e is the part of tile
+// t that lies in segment s, with e = t + s.  From one piece to the next either
+// the tile or the segment moves on, so the sum is a number of its own for every
+// piece (numbers without one are left over where both move on or a segment is
+// empty), pieces number below tiles + n_seg, and one search finds piece e: the
+// last segment with s + tile(seg_ptr[s]) <= e.
+struct RowPiece {
+  int64_t begin, end;  // rows of the batch
+  int32_t tile, adapter;
+};
+__device__ __forceinline__ RowPiece find_piece(const int64_t *__restrict__ seg_ptr, const int32_t *__restrict__ seg_adapter,
+                                               int32_t n_seg, int32_t n_adapters, int32_t rows, int64_t N, int32_t e,
+                                               uint32_t *status) {
+  const int lane = threadIdx.x & 31;
+  RowPiece r{0, 0, 0, -1};
+  int32_t s = -1, adapter = -1;
+  int64_t b = 0, last = 0;
+  if (n_seg <= kFewSegments) {
+    const FewSegments few(seg_ptr, seg_adapter, n_seg);
+#pragma unroll
+    for (int g = 0; g < kFewGroups; ++g) {
+      const int32_t i = 32 * g + lane;
+      const int c = __popc(__ballot_sync(0xffffffffu, i < n_seg && i + few.begin[g] / rows <= e));
+      if (c > 0) {
+        s = 32 * g + c - 1;
+        b = __shfl_sync(0xffffffffu, few.begin[g], c - 1);
+        last = __shfl_sync(0xffffffffu, few.end[g], c - 1);
+        adapter = __shfl_sync(0xffffffffu, few.adapter[g], c - 1);
+      }
+    }
+    if (s < 0) return r;
+  } else {
+    int32_t lo = 0, hi = n_seg;
+    while (lo < hi) {
+      const int32_t stride = (hi - lo + 31) / 32;
+      const int64_t i = lo + static_cast<int64_t>(lane) * stride;
+      const bool below = i < hi && i + seg_ptr[i] / rows <= e;
+      const int c = __popc(__ballot_sync(0xffffffffu, below));
+      if (c == 0) break;
+      const int32_t at = lo + (c - 1) * stride;
+      if (stride == 1) {
+        s = at;
+        break;
+      }
+      hi = min(hi, at + stride);
+      lo = at;
+    }
+    if (s < 0) return r;
+    b = seg_ptr[s];
+    last = seg_ptr[s + 1];
+    adapter = seg_adapter[s];
+  }
+  r.tile = e - s;
+  r.begin = max(max(b, int64_t{0}), static_cast<int64_t>(r.tile) * rows);
+  r.end = min(min(last, N), static_cast<int64_t>(r.tile + 1) * rows);
+  if (r.begin < r.end) r.adapter = checked_adapter(adapter, n_adapters, status);
+  return r;
+}
+
 // The segment that holds row n, by one warp: its rows and adapter (-1 for none).
 struct RowSegment {
   int64_t begin, end;
