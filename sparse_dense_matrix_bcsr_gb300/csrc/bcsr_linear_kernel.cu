@@ -60,14 +60,19 @@ constexpr int kSmemBytes = kQ * kStageBytes + kStagingBytes + kMiscBytes + 1024;
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 static_assert(2 * kTmemCols <= 512, "TMEM of two CTAs");
 
-constexpr int32_t kRecFirst = 1, kRecLast = 2, kRecEmpty = 4, kRecEnd = 8;
+constexpr int32_t kRecEmpty = 1, kRecEnd = 2, kRecAdaptersShift = 8;
+// What the producer tells the MMA warp with a tile's first stage: the tile, how
+// many stages of blocks it has and (flags >> kRecAdaptersShift) how many of
+// adapters follow.  With a stage of an adapter: its steps of 16 ranks and its
+// rows of the tile, begin | end << 16.
 struct TileRec {
   int32_t br;
   int32_t nt;
   int32_t flags;
-  int32_t rows;  // adapter stage: its rows of the tile, begin | end << 16
+  int32_t stages;  // or steps
+  int32_t rows;
+  int32_t pad_[3];
 };
-constexpr int32_t kRecAdapter = 16, kRecStepsShift = 8;  // adapter stage, with its 16-rank steps
 
 constexpr int kGroupN = 8;
 __device__ __forceinline__ void tile_coords(int64_t t, int n_block_rows, int n_tiles_n, int &br, int &nt) {
@@ -136,15 +141,28 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
+  // A wait taken by a whole warp: one probe decides when the phase is there; the
+  // abort flag and the limit are looked at only while it is not.
+  auto wait_phase = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (__shfl_sync(0xffffffffu, mbar_try_wait(bar, parity) ? 1 : 0, 0)) return true;
+    const long long limit = static_cast<long long>(p.wait_limit_ns) * 21 / 10, t0 = clock64();
+    while (true) {
+      __nanosleep(32);
+      int state = mbar_try_wait(bar, parity) ? 1 : (*abort_flag || clock64() - t0 > limit) ? 2 : 0;
+      state = __shfl_sync(0xffffffffu, state, 0);
+      if (state != 0) return state == 1;
+    }
+  };
+
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ producer
+    // Tiles are looked up 32 at a time, one a lane (their coordinates take
+    // 64-bit divisions, their block rows' bounds a trip to L2), and a tile's
+    // block columns are loaded while the tile before it is issued.
     uint32_t stage = 0, phase = 0;
     int64_t seq = 0;
     bool ok = true;
-    auto claim = [&]() -> bool {
-      const bool r = mbar_wait_warp(empty0 + 8 * stage, phase ^ 1u, p.wait_limit_ns);
-      return __shfl_sync(0xffffffffu, r && !*abort_flag, 0);
-    };
+    auto claim = [&]() -> bool { return wait_phase(empty0 + 8 * stage, phase ^ 1u); };
     auto advance = [&]() {
       ++seq;
       if (++stage == kQ) {
@@ -153,80 +171,110 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     };
     if constexpr (kAdapt) grid_dependency_wait();  // the tile lists and H
-    for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-      int br, nt;
-      tile_coords(t, p.n_block_rows, n_tiles_n, br, nt);
-      const int64_t jb = p.block_row_ptr[br], je = p.block_row_ptr[br + 1];
-      int32_t segs = 0;  // segments with an adapter in the tile
-      if constexpr (kAdapt) segs = ad.tile_count[nt];
-      if (jb == je && segs > 0) {
-        // no block to start the sums with: a stage of zeros, read past the end of the blocks and of X
-        ok = claim();
-        if (!ok) break;
-        if (lane == 0) {
-          tile_rec[stage] = TileRec{br, nt, kRecFirst, 0};
-          const uint32_t fb = full0 + 8 * stage;
-          const uint32_t st = smem_addr(smem + stage * kStageBytes);
-          mbar_arrive_expect_tx(fb, kStageBytes);
-          tma_load_2d(st, &tmA, fb, kBlk, 0);
-          tma_load_2d(st + kBlkBytes, &tmX, fb, (p.K + kBlk - 1) / kBlk * kBlk, 0);
-        }
-        advance();
-      } else if (jb == je) {
-        ok = claim();
-        if (!ok) break;
-        if (lane == 0) {
-          tile_rec[stage] = TileRec{br, nt, kRecFirst | kRecLast | kRecEmpty, 0};
-          mbar_arrive(full0 + 8 * stage);
-        }
-        advance();
+    for (int64_t t0 = blockIdx.x; t0 < n_tiles && ok; t0 += 32ll * gridDim.x) {
+      const int64_t mine = t0 + static_cast<int64_t>(lane) * gridDim.x;
+      int my_br = 0, my_nt = 0, my_segs = 0;
+      int64_t my_jb = 0, my_je = 0;
+      if (mine < n_tiles) {
+        tile_coords(mine, p.n_block_rows, n_tiles_n, my_br, my_nt);
+        my_jb = p.block_row_ptr[my_br];
+        my_je = p.block_row_ptr[my_br + 1];
+        if constexpr (kAdapt) my_segs = ad.tile_count[my_nt];  // segments with an adapter in the tile
       }
-      for (int64_t jbase = jb; jbase < je && ok; jbase += 32) {
-        const int64_t jl = jbase + lane;
-        const int32_t my_col = jl < je ? p.block_col_idx[jl] : 0;
-        const int cnt = (je - jbase) < 32 ? static_cast<int>(je - jbase) : 32;
-        for (int i = 0; i < cnt; ++i) {
-          const int32_t bcol = __shfl_sync(0xffffffffu, my_col, i);
+      const int tiles = static_cast<int>(min((n_tiles - t0 + gridDim.x - 1) / gridDim.x, int64_t{32}));
+      auto first_cols = [&](int i) {  // lane l: column of the tile's l-th block
+        const int64_t b = __shfl_sync(0xffffffffu, my_jb, i), e = __shfl_sync(0xffffffffu, my_je, i);
+        return b + lane < e ? p.block_col_idx[b + lane] : 0;
+      };
+      auto first_segs = [&](int i) {
+        TileSegment s{};
+        if constexpr (kAdapt) {
+          const int nt = __shfl_sync(0xffffffffu, my_nt, i), n = __shfl_sync(0xffffffffu, my_segs, i);
+          if (lane < n) s = ad.tile_segs[static_cast<int64_t>(nt) * kAdapterTileRows + lane];
+        }
+        return s;
+      };
+      int32_t next_cols = first_cols(0);
+      TileSegment next_segs = first_segs(0);
+      for (int ti = 0; ti < tiles && ok; ++ti) {
+        const int br = __shfl_sync(0xffffffffu, my_br, ti), nt = __shfl_sync(0xffffffffu, my_nt, ti);
+        const int64_t jb = __shfl_sync(0xffffffffu, my_jb, ti), je = __shfl_sync(0xffffffffu, my_je, ti);
+        const int32_t segs = __shfl_sync(0xffffffffu, my_segs, ti);
+        const int32_t cols = next_cols;
+        const TileSegment tile_segs = next_segs;
+        if (ti + 1 < tiles) {
+          next_cols = first_cols(ti + 1);
+          next_segs = first_segs(ti + 1);
+        }
+        int32_t adapter_stages = 0;
+        if constexpr (kAdapt) adapter_stages = segs * ((ad.rank + kBlk - 1) / kBlk) * ad.parts;
+        if (jb == je && segs > 0) {
+          // no block to start the sums with: a stage of zeros, read past the end of the blocks and of X
           ok = claim();
           if (!ok) break;
           if (lane == 0) {
-            const int64_t j = jbase + i;
-            tile_rec[stage] =
-                TileRec{br, nt, (j == jb ? kRecFirst : 0) | (j == je - 1 && segs == 0 ? kRecLast : 0), 0};
+            tile_rec[stage] = TileRec{br, nt, adapter_stages << kRecAdaptersShift, 1, 0, {}};
             const uint32_t fb = full0 + 8 * stage;
             const uint32_t st = smem_addr(smem + stage * kStageBytes);
             mbar_arrive_expect_tx(fb, kStageBytes);
-            tma_load_2d(st, &tmA, fb, 0, static_cast<int32_t>(j * kBlk));
-            tma_load_2d(st + kBlkBytes, &tmX, fb, bcol * kBlk, nt * kTileN);
+            tma_load_2d(st, &tmA, fb, kBlk, 0);
+            tma_load_2d(st + kBlkBytes, &tmX, fb, (p.K + kBlk - 1) / kBlk * kBlk, 0);
+          }
+          advance();
+        } else if (jb == je) {
+          ok = claim();
+          if (!ok) break;
+          if (lane == 0) {
+            tile_rec[stage] = TileRec{br, nt, kRecEmpty, 0, 0, {}};
+            mbar_arrive(full0 + 8 * stage);
           }
           advance();
         }
-      }
-      if constexpr (kAdapt) {
-        const int chunks = (ad.rank + kBlk - 1) / kBlk;
-        for (int32_t base = 0; base < segs && ok; base += 32) {
-          TileSegment my{};
-          if (base + lane < segs) my = ad.tile_segs[static_cast<int64_t>(nt) * kAdapterTileRows + base + lane];
-          const int cnt = min(segs - base, 32);
-          for (int i = 0; i < cnt && ok; ++i) {
-            const int32_t a = __shfl_sync(0xffffffffu, my.adapter, i);
-            const int32_t rows = __shfl_sync(0xffffffffu, my.begin | my.end << 16, i);
-            for (int c = 0; c < chunks * ad.parts; ++c) {
-              ok = claim();
-              if (!ok) break;
-              if (lane == 0) {
-                const int part = c / chunks, r0 = (c - part * chunks) * kBlk;
-                const int steps = (min(ad.rank - r0, kBlk) + 15) / 16;
-                const bool last = base + i == segs - 1 && c == chunks * ad.parts - 1;
+        for (int64_t jbase = jb; jbase < je && ok; jbase += 32) {
+          const int32_t my_col = jbase == jb ? cols : jbase + lane < je ? p.block_col_idx[jbase + lane] : 0;
+          const int cnt = (je - jbase) < 32 ? static_cast<int>(je - jbase) : 32;
+          for (int i = 0; i < cnt; ++i) {
+            const int32_t bcol = __shfl_sync(0xffffffffu, my_col, i);
+            ok = claim();
+            if (!ok) break;
+            if (lane == 0) {
+              const int64_t j = jbase + i;
+              if (j == jb)
                 tile_rec[stage] =
-                    TileRec{br, nt, kRecAdapter | steps << kRecStepsShift | (last ? kRecLast : 0), rows};
-                const uint32_t fb = full0 + 8 * stage;
-                const uint32_t st = smem_addr(smem + stage * kStageBytes);
-                mbar_arrive_expect_tx(fb, kStageBytes);
-                tma_load_2d(st, &ad.tmU, fb, r0, a * p.M + br * kBlk);
-                tma_load_2d(st + kBlkBytes, &ad.tmH, fb, r0, part * p.N + nt * kTileN);
+                    TileRec{br, nt, adapter_stages << kRecAdaptersShift, static_cast<int32_t>(je - jb), 0, {}};
+              const uint32_t fb = full0 + 8 * stage;
+              const uint32_t st = smem_addr(smem + stage * kStageBytes);
+              mbar_arrive_expect_tx(fb, kStageBytes);
+              tma_load_2d(st, &tmA, fb, 0, static_cast<int32_t>(j * kBlk));
+              tma_load_2d(st + kBlkBytes, &tmX, fb, bcol * kBlk, nt * kTileN);
+            }
+            advance();
+          }
+        }
+        if constexpr (kAdapt) {
+          const int chunks = (ad.rank + kBlk - 1) / kBlk;
+          for (int32_t base = 0; base < segs && ok; base += 32) {
+            TileSegment my = tile_segs;
+            if (base > 0 && base + lane < segs) my = ad.tile_segs[static_cast<int64_t>(nt) * kAdapterTileRows + base + lane];
+            const int cnt = min(segs - base, 32);
+            for (int i = 0; i < cnt && ok; ++i) {
+              const int32_t a = __shfl_sync(0xffffffffu, my.adapter, i);
+              const int32_t rows = __shfl_sync(0xffffffffu, my.begin | my.end << 16, i);
+              for (int c = 0; c < chunks * ad.parts; ++c) {
+                ok = claim();
+                if (!ok) break;
+                if (lane == 0) {
+                  const int part = c / chunks, r0 = (c - part * chunks) * kBlk;
+                  const int steps = (min(ad.rank - r0, kBlk) + 15) / 16;
+                  tile_rec[stage] = TileRec{br, nt, 0, steps, rows, {}};
+                  const uint32_t fb = full0 + 8 * stage;
+                  const uint32_t st = smem_addr(smem + stage * kStageBytes);
+                  mbar_arrive_expect_tx(fb, kStageBytes);
+                  tma_load_2d(st, &ad.tmU, fb, r0, a * p.M + br * kBlk);
+                  tma_load_2d(st + kBlkBytes, &ad.tmH, fb, r0, part * p.N + nt * kTileN);
+                }
+                advance();
               }
-              advance();
             }
           }
         }
@@ -235,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (ok) {
       ok = claim();
       if (ok && lane == 0) {
-        tile_rec[stage] = TileRec{-1, -1, kRecEnd, 0};
+        tile_rec[stage] = TileRec{-1, -1, kRecEnd, 0, 0, {}};
         mbar_arrive(full0 + 8 * stage);
       }
     }
@@ -252,18 +300,25 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool leader = lane == 0;
     uint32_t stage = 0, phase = 0, tcount = 0, buf = 0;
     bool ok = true;
-    while (true) {
-      ok = mbar_wait_warp(full0 + 8 * stage, phase, p.wait_limit_ns);
-      ok = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
-      if (!ok) break;
-      const TileRec rec = tile_rec[stage];
-      if (rec.flags & (kRecFirst | kRecEnd)) {
-        buf = tcount % kNbuf;
-        const bool r = mbar_wait_warp(acce0 + 8 * buf, ((tcount / kNbuf) & 1u) ^ 1u, p.wait_limit_ns);
-        ok = __shfl_sync(0xffffffffu, r && !*abort_flag, 0);
-        if (!ok) break;
-        tc_fence_after_sync();
+    auto wait_full = [&]() -> bool { return wait_phase(full0 + 8 * stage, phase); };
+    auto release = [&]() {
+      umma_commit_elect(empty0 + 8 * stage);
+      if (++stage == kQ) {
+        stage = 0;
+        phase ^= 1u;
       }
+    };
+    // Operands of stage 0; the block is the N operand (64 rows of A x 64 k), X
+    // the M operand (256 rows x 64 k, half h its rows 128 h .. 128 h + 127).
+    const uint64_t blk_desc = smem_desc_sw128(smem_addr(smem), 16, 1024);
+    const uint64_t x_desc = smem_desc_sw128(smem_addr(smem) + kBlkBytes, 16, 1024);
+    while (true) {
+      ok = wait_full();
+      if (!ok) break;
+      const TileRec rec = tile_rec[stage];  // the tile's first stage tells how many follow
+      buf = tcount % kNbuf;
+      ok = wait_phase(acce0 + 8 * buf, ((tcount / kNbuf) & 1u) ^ 1u);
+      if (!ok) break;
       if (rec.flags & kRecEnd) {
         if (leader) {
           acc_rec[buf].flags = kRecEnd;
@@ -272,61 +327,69 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         break;
       }
-      if (leader) {
-        if (!(rec.flags & kRecEmpty)) {
+      const uint32_t acc = tmem + buf * kAccCols;
+      if (rec.flags & kRecEmpty) {
+        release();
+      } else {
+        for (int j = 0; j < rec.stages; ++j) {
+          if (j > 0) {
+            ok = wait_full();
+            if (!ok) break;
+          }
           tc_fence_after_sync();
-          const uint32_t blk = smem_addr(smem + stage * kStageBytes);  // N operand: 64 rows of A x 64 k
-          const uint32_t xt = blk + kBlkBytes;                         // M operand: 256 rows of X x 64 k
-          const uint32_t acc = tmem + buf * kAccCols;
-          const bool first = (rec.flags & kRecFirst) != 0;
-          // half h: rows 128h .. 128h + 127 of the tile
-          const uint64_t bdesc0 = smem_desc_sw128(blk, 16, 1024);
-          const uint64_t adesc0 = smem_desc_sw128(xt, 16, 1024);
-          if (kAdapt && (rec.flags & kRecAdapter)) {
-            const int steps = rec.flags >> kRecStepsShift;
-            const int begin = rec.rows & 0xffff, end = rec.rows >> 16;
+          const uint64_t bdesc0 = smem_desc_add(blk_desc, stage * kStageBytes);
+          const uint64_t adesc0 = smem_desc_add(x_desc, stage * kStageBytes);
+          const uint32_t accumulate = j > 0 ? 1u : 0u;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              umma_f16_elect(acc + h * kBlk, smem_desc_add(adesc0, h * (kXBytes / 2) + kk * 32),
+                             smem_desc_add(bdesc0, kk * 32), idesc, kk > 0 ? 1u : accumulate);
+          }
+          release();
+        }
+        if constexpr (kAdapt) {
+          const int adapter_stages = rec.flags >> kRecAdaptersShift;
+          for (int j = 0; j < adapter_stages && ok; ++j) {
+            ok = wait_full();
+            if (!ok) break;
+            tc_fence_after_sync();
+            const TileRec seg = tile_rec[stage];
+            const int steps = seg.stages, begin = seg.rows & 0xffff, end = seg.rows >> 16;
+            const uint64_t bdesc0 = smem_desc_add(blk_desc, stage * kStageBytes);
+            const uint64_t adesc0 = smem_desc_add(x_desc, stage * kStageBytes);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               if (end <= 128 * h || begin >= 128 * (h + 1)) continue;
               uint32_t off[4];
               lanes_off(begin - 128 * h, end - 128 * h, off);
               for (int kk = 0; kk < steps; ++kk)
-                umma_f16_lanes(acc + h * kBlk, smem_desc_add(adesc0, h * (kXBytes / 2) + kk * 32),
-                               smem_desc_add(bdesc0, kk * 32), idesc, 1u, off);
+                umma_f16_lanes_elect(acc + h * kBlk, smem_desc_add(adesc0, h * (kXBytes / 2) + kk * 32),
+                                     smem_desc_add(bdesc0, kk * 32), idesc, 1u, off);
             }
-          } else {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t bdesc = smem_desc_add(bdesc0, kk * 32);
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                umma_f16(acc + h * kBlk, smem_desc_add(adesc0, h * (kXBytes / 2) + kk * 32), bdesc, idesc,
-                         (first && kk == 0) ? 0u : 1u);
-            }
+            release();
           }
         }
-        umma_commit(empty0 + 8 * stage);
-        if (rec.flags & kRecLast) {
-          acc_rec[buf].br = rec.br;
-          acc_rec[buf].nt = rec.nt;
-          acc_rec[buf].flags = rec.flags & kRecEmpty;
-          mbar_arrive(accf0 + 8 * buf);
-          umma_commit(accf0 + 8 * buf);
-        }
+        if (!ok) break;
       }
-      if (rec.flags & kRecLast) ++tcount;
+      if (leader) {
+        acc_rec[buf].br = rec.br;
+        acc_rec[buf].nt = rec.nt;
+        acc_rec[buf].flags = rec.flags & kRecEmpty;
+        mbar_arrive(accf0 + 8 * buf);
+      }
       __syncwarp();
-      if (++stage == kQ) {
-        stage = 0;
-        phase ^= 1u;
-      }
+      umma_commit_elect(accf0 + 8 * buf);
+      ++tcount;
     }
     if (!ok) {
       if (leader) {
         atomicOr(p.status, kDevTimeout);
         *abort_flag = 1;
-        umma_commit(drain_bar);
       }
+      __syncwarp();
+      umma_commit_elect(drain_bar);
       mbar_wait_warp(drain_bar, 0, 1000000ull);
       if (leader)
         for (int b = 0; b < kNbuf; ++b) {

@@ -311,6 +311,18 @@ __device__ __forceinline__ void umma_f16_lanes(uint32_t d_tmem, uint64_t a_desc,
       : "memory");
 }
 
+// The same issued by a whole converged warp.
+__device__ __forceinline__ void umma_f16_lanes_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                     uint32_t accumulate, const uint32_t (&off)[4]) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
+      : "memory");
+}
+
 // Lanes [begin, end) of an M = 128 product enabled, as umma_f16_lanes takes them.
 __device__ __forceinline__ void lanes_off(int begin, int end, uint32_t (&off)[4]) {
 #pragma unroll
