@@ -133,12 +133,15 @@ spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams
   const bool bf16 = h->in_t == SPMM_BF16, out_bf16 = h->out_t == SPMM_BF16;
   CUtensorMap tmX, tmY;
   spmm::LinearAdapters ad;
+  ad.box = p.rank <= 16 ? 16 : p.rank <= 32 ? 32 : 64;
   spmm_status st = spmm::encode_x(&tmX, p.X, bf16, p.N, p.K);
   if (st == SPMM_OK) st = spmm::encode_y(&tmY, p.Y, out_bf16, p.N, p.M);
   if (st == SPMM_OK)
-    st = spmm::encode_2d(&ad.tmU, p.up, bf16, static_cast<uint64_t>(p.n_adapters) * p.M, p.rank, p.rank, 64, 64);
+    st = spmm::encode_2d(&ad.tmU, p.up, bf16, static_cast<uint64_t>(p.n_adapters) * p.M, p.rank, p.rank, 64, ad.box,
+                         ad.box * 2);
   if (st == SPMM_OK)
-    st = spmm::encode_2d(&ad.tmH, p.H, bf16, static_cast<uint64_t>(parts) * p.N, p.rank, p.rank, spmm::kAdapterTileRows, 64);
+    st = spmm::encode_2d(&ad.tmH, p.H, bf16, static_cast<uint64_t>(parts) * p.N, p.rank, p.rank, spmm::kAdapterTileRows,
+                         ad.box, ad.box * 2);
   if (st != SPMM_OK) return st;
   ad.tile_segs = a->d_tile_segs;
   ad.tile_count = a->d_tile_count;

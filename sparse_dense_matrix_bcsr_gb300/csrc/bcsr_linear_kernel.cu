@@ -47,7 +47,7 @@ constexpr int kBlkBytes = kBlk * kBlk * 2;
 constexpr int kTileN = kAdapterTileRows;       // rows of X per tile (256)
 constexpr int kXBytes = kTileN * kBlk * 2;     // one 256 x 64 box of X
 constexpr int kStageBytes = kBlkBytes + kXBytes;
-constexpr int kQ = 2;                          // stages per CTA
+constexpr int kQ = 5;                          // stages
 constexpr int kNbuf = 2;                       // TMEM accumulators per CTA
 constexpr int kAccCols = 2 * kBlk;             // two halves of 128 rows x 64 columns
 constexpr int kTmemCols = kNbuf * kAccCols;
@@ -57,8 +57,7 @@ constexpr int kPartBytes = 32 * 128;           // one store box: 32 rows of Y x 
 constexpr int kStagingBytes = kEpiWarps * kPartBytes;  // one staging buffer per warp
 constexpr int kMiscBytes = 1024;
 constexpr int kSmemBytes = kQ * kStageBytes + kStagingBytes + kMiscBytes + 1024;
-static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
-static_assert(2 * kTmemCols <= 512, "TMEM of two CTAs");
+static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
 
 constexpr int32_t kRecEmpty = 1, kRecEnd = 2, kRecAdaptersShift = 8;
 // What the producer tells the MMA warp with a tile's first stage: the tile, how
@@ -88,7 +87,7 @@ __device__ __forceinline__ void tile_coords(int64_t t, int n_block_rows, int n_t
 // each) x 64 output features, as 128-byte box rows: one box per half for bf16
 // Y, two (32 features each) for fp32.
 template <bool IN_BF16, bool OUT_BF16, class Adapters>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     bcsr_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ CUtensorMap tmY, const BcsrParams p,
                        const __grid_constant__ Adapters ad) {
@@ -207,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           next_segs = first_segs(ti + 1);
         }
         int32_t adapter_stages = 0;
-        if constexpr (kAdapt) adapter_stages = segs * ((ad.rank + kBlk - 1) / kBlk) * ad.parts;
+        if constexpr (kAdapt) adapter_stages = segs * ((ad.rank + ad.box - 1) / ad.box) * ad.parts;
         if (jb == je && segs > 0) {
           // no block to start the sums with: a stage of zeros, read past the end of the blocks and of X
           ok = claim();
@@ -252,7 +251,6 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         if constexpr (kAdapt) {
-          const int chunks = (ad.rank + kBlk - 1) / kBlk;
           for (int32_t base = 0; base < segs && ok; base += 32) {
             TileSegment my = tile_segs;
             if (base > 0 && base + lane < segs) my = ad.tile_segs[static_cast<int64_t>(nt) * kAdapterTileRows + base + lane];
@@ -260,20 +258,20 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int i = 0; i < cnt && ok; ++i) {
               const int32_t a = __shfl_sync(0xffffffffu, my.adapter, i);
               const int32_t rows = __shfl_sync(0xffffffffu, my.begin | my.end << 16, i);
-              for (int c = 0; c < chunks * ad.parts; ++c) {
-                ok = claim();
-                if (!ok) break;
-                if (lane == 0) {
-                  const int part = c / chunks, r0 = (c - part * chunks) * kBlk;
-                  const int steps = (min(ad.rank - r0, kBlk) + 15) / 16;
-                  tile_rec[stage] = TileRec{br, nt, 0, steps, rows, {}};
-                  const uint32_t fb = full0 + 8 * stage;
-                  const uint32_t st = smem_addr(smem + stage * kStageBytes);
-                  mbar_arrive_expect_tx(fb, kStageBytes);
-                  tma_load_2d(st, &ad.tmU, fb, r0, a * p.M + br * kBlk);
-                  tma_load_2d(st + kBlkBytes, &ad.tmH, fb, r0, part * p.N + nt * kTileN);
+              for (int part = 0; part < ad.parts && ok; ++part) {
+                for (int32_t r0 = 0; r0 < ad.rank; r0 += ad.box) {
+                  ok = claim();
+                  if (!ok) break;
+                  if (lane == 0) {
+                    tile_rec[stage] = TileRec{br, nt, 0, (min(ad.rank - r0, ad.box) + 15) / 16, rows, {}};
+                    const uint32_t fb = full0 + 8 * stage;
+                    const uint32_t st = smem_addr(smem + stage * kStageBytes);
+                    mbar_arrive_expect_tx(fb, (kBlk + kTileN) * ad.box * 2);
+                    tma_load_2d(st, &ad.tmU, fb, r0, a * p.M + br * kBlk);
+                    tma_load_2d(st + kBlkBytes, &ad.tmH, fb, r0, part * p.N + nt * kTileN);
+                  }
+                  advance();
                 }
-                advance();
               }
             }
           }
@@ -312,6 +310,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     // the M operand (256 rows x 64 k, half h its rows 128 h .. 128 h + 127).
     const uint64_t blk_desc = smem_desc_sw128(smem_addr(smem), 16, 1024);
     const uint64_t x_desc = smem_desc_sw128(smem_addr(smem) + kBlkBytes, 16, 1024);
+    // An adapter's operands lie in the same places, in rows of ad.box ranks.
+    uint64_t u_desc = 0, h_desc = 0;
+    uint32_t h_half = 0;
+    if constexpr (kAdapt) {
+      h_half = 128 * ad.box * 2;
+      u_desc = smem_desc_k_major(smem_addr(smem), ad.box * 2);
+      h_desc = smem_desc_k_major(smem_addr(smem) + kBlkBytes, ad.box * 2);
+    }
     while (true) {
       ok = wait_full();
       if (!ok) break;
@@ -357,16 +363,22 @@ __global__ void __launch_bounds__(kThreads, 2)
             tc_fence_after_sync();
             const TileRec seg = tile_rec[stage];
             const int steps = seg.stages, begin = seg.rows & 0xffff, end = seg.rows >> 16;
-            const uint64_t bdesc0 = smem_desc_add(blk_desc, stage * kStageBytes);
-            const uint64_t adesc0 = smem_desc_add(x_desc, stage * kStageBytes);
+            const uint64_t bdesc0 = smem_desc_add(u_desc, stage * kStageBytes);
+            const uint64_t adesc0 = smem_desc_add(h_desc, stage * kStageBytes);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               if (end <= 128 * h || begin >= 128 * (h + 1)) continue;
-              uint32_t off[4];
-              lanes_off(begin - 128 * h, end - 128 * h, off);
-              for (int kk = 0; kk < steps; ++kk)
-                umma_f16_lanes_elect(acc + h * kBlk, smem_desc_add(adesc0, h * (kXBytes / 2) + kk * 32),
-                                     smem_desc_add(bdesc0, kk * 32), idesc, 1u, off);
+              const uint64_t adesc = smem_desc_add(adesc0, h * h_half);
+              if (begin <= 128 * h && end >= 128 * (h + 1)) {  // the segment holds the half: no lanes to mask
+                for (int kk = 0; kk < steps; ++kk)
+                  umma_f16_elect(acc + h * kBlk, smem_desc_add(adesc, kk * 32), smem_desc_add(bdesc0, kk * 32), idesc, 1u);
+              } else {
+                uint32_t off[4];
+                lanes_off(begin - 128 * h, end - 128 * h, off);
+                for (int kk = 0; kk < steps; ++kk)
+                  umma_f16_lanes_elect(acc + h * kBlk, smem_desc_add(adesc, kk * 32), smem_desc_add(bdesc0, kk * 32),
+                                       idesc, 1u, off);
+              }
             }
             release();
           }
@@ -497,7 +509,7 @@ cudaError_t launch_linear_variant(const CUtensorMap &tmA, const CUtensorMap &tmX
   cudaError_t e = set_smem_limit_once(kern, kSmemBytes, smem_set);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(p.n_block_rows) * ((p.N + kTileN - 1) / kTileN);
-  const int64_t cap = p.max_ctas > 0 ? p.max_ctas : 2ll * p.num_sms;
+  const int64_t cap = p.max_ctas > 0 ? p.max_ctas : p.num_sms;
   const int64_t grid = tiles < cap ? tiles : cap;
   if constexpr (std::is_same_v<Adapters, LinearAdapters>) {
     // a dependent of the down projection: set up while it ends

@@ -106,14 +106,15 @@ struct TileSegment {
   int32_t adapter, begin, end, pad_;
 };
 // The adapters of the same product (launch_bcsr_linear_adapters): tmU covers
-// the up matrices as [n_adapters * M rows, rank cols] with 64 x 64 boxes, tmH
-// covers H as [parts * N rows, rank cols] with 256 x 64 boxes, both 128-byte
-// swizzle; parts > 1: H is the sum of its parts.
+// the up matrices as [n_adapters * M rows, rank cols] with 64 x box boxes, tmH
+// covers H as [parts * N rows, rank cols] with 256 x box boxes, both swizzled in
+// the width of a box row; box = 16, 32 or 64 ranks; parts > 1: H is the sum of
+// its parts.
 struct LinearAdapters {
   CUtensorMap tmU, tmH;
   const TileSegment *tile_segs;  // device, kAdapterTileRows per tile
   const int32_t *tile_count;     // device, per tile: its segments with an adapter
-  int32_t rank, parts;
+  int32_t rank, parts, box;
 };
 // Launched as a programmatic dependent of the kernel that writes H and the
 // tile lists.

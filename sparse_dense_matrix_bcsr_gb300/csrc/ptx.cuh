@@ -375,6 +375,18 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
   return d;
 }
 
+// K-major operand with rows of 32, 64 or 128 contiguous bytes and the swizzle of
+// that width (what a TMA box of that inner size writes with it).
+__device__ __forceinline__ uint64_t smem_desc_k_major(uint32_t saddr, uint32_t row_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(1) << 16;                       // lbo: unused
+  d |= static_cast<uint64_t>((8 * row_bytes) >> 4) << 32;    // sbo: a group of 8 rows
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(row_bytes == 128 ? 2 : row_bytes == 64 ? 4 : 6) << 61;
+  return d;
+}
+
 // The descriptor of the same layout `bytes` further on in shared memory
 // (bytes a multiple of 16): the start-address field (address / 16, bits
 // 0..13) grows by bytes / 16.  Shared-memory addresses stay below 256 KB, so

@@ -58,10 +58,10 @@ EncodeTiledFn encode_fn() {
 }
 
 // 2-D row-major tensor of 16-bit elements: `rows` x `cols`, row pitch
-// `pitch_elems`; boxes of box_rows x box_cols (box_cols * 2 <= 128 bytes),
-// 128-byte swizzle, out-of-bounds elements read as zero.
+// `pitch_elems`; boxes of box_rows x box_cols (box_cols * 2 <= swizzle_bytes),
+// the swizzle of 32, 64 or 128 bytes, out-of-bounds elements read as zero.
 spmm_status encode_2d(CUtensorMap *map, const void *base, bool bf16, uint64_t rows, uint64_t cols,
-                      uint64_t pitch_elems, uint32_t box_rows, uint32_t box_cols) {
+                      uint64_t pitch_elems, uint32_t box_rows, uint32_t box_cols, uint32_t swizzle_bytes) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(SPMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   cuuint64_t dims[2] = {cols, rows};
@@ -70,7 +70,10 @@ spmm_status encode_2d(CUtensorMap *map, const void *base, bool bf16, uint64_t ro
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                   const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  swizzle_bytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                  : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                        : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SPMM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
   return SPMM_OK;
 }
