@@ -168,8 +168,19 @@ spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams
   return SPMM_OK;
 }
 
-// Batches up to this many rows take the row kernels, longer ones the tiled ones.
-constexpr int64_t kRowsPath = 64;
+// Whether a batch takes the row kernels (adapter_decode_kernel.cu) or the tiled
+// ones.  The row kernels' time grows with the rows, N * (a + b * rank) (every row
+// meets its U on the CUDA cores), the tiled ones' with the segments (one more
+// stage in every tile a segment touches).  Fitted to GPU times through 18944 x
+// 3584 (us, rows / tiles), which it decides as the faster one does: 64 rows of
+// one adapter, rank 16: 15.6 / 18.4, rank 64: 28.2 / 19.7; 128 rows, rank 16, in
+// 1 segment: 23.6 / 18.9, in 16: 24.5 / 44.5, in 128: 32.8 / 295; 256 rows in 4:
+// 41.0 / 23.5, in 64: 44.1 / 94.8; 512 rows of rank 64 in 64: 192 / 70; 1024 rows
+// of rank 16 in 128: 156 / 132; 300 rows of rank 128 in 300 (3584 x 18944): 182 / 314.
+bool rows_path(int64_t N, int32_t rank, int64_t n_seg) {
+  constexpr int64_t kMostRows = 65535ll * spmm::kAdapterDecodeRows;  // the launch grid's second dimension
+  return N <= kMostRows && N * (rank + 24) < 2300 + 290 * n_seg;
+}
 
 // Y = X W^T + adapters, with D rank x K and U M x rank per adapter; tiled: by the
 // tensor-core kernels, which leave H in 16 bits.
@@ -291,7 +302,8 @@ spmm_status spmm_run_linear_adapters(spmm_handle h, spmm_adapters a, const void 
   if (N == 0) return SPMM_OK;
   if (!X || !Y) return fail(SPMM_ERR_INVALID_ARG, "X or Y is NULL");
   if (misaligned({X, Y, down, up})) return fail(SPMM_ERR_UNSUPPORTED, "X, Y, down and up must be 16-byte aligned");
-  return project(h, a, make_params(h, a, N, scale, seg_ptr, seg_adapter, n_seg), X, Y, down, up, a->d_h, N > kRowsPath,
+  return project(h, a, make_params(h, a, N, scale, seg_ptr, seg_adapter, n_seg), X, Y, down, up, a->d_h,
+                 !rows_path(N, a->rank, n_seg),
                  static_cast<cudaStream_t>(stream));
 }
 

@@ -323,7 +323,8 @@ struct AdapterWgradParams {
 cudaError_t launch_adapter_wgrad(AdapterWgradParams p, int num_sms, bool bf16, cudaStream_t s);
 
 // ---------------------------------------------------------------- expert routing (route.cu)
-constexpr int kRouteChunk = 8192;        // ids per block of the sort
+constexpr int kRouteOneChunk = 8192;     // ids that one block of the sort takes alone
+constexpr int kRouteChunk = 2048;        // ids per block of longer sorts
 constexpr int kRouteMaxExperts = 2048;   // the sort's counts of a block lie in shared memory
 constexpr int kRouteMaxTopk = 32;        // a warp holds a token's positions, one a lane
 

@@ -14,6 +14,7 @@
 #include <cuda_fp16.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace spmm {
 namespace {
@@ -21,32 +22,38 @@ namespace {
 // ---------------------------------------------------------------- sort
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-static_assert(kRouteChunk % kSortThreads == 0, "each warp walks whole groups of 32 ids");
 
-// Number of each expert's ids in every chunk of kRouteChunk: counts[chunk][expert].
+// Number of each expert's ids in every chunk: counts[chunk][expert].
+template <int STEPS>
 __global__ void __launch_bounds__(kSortThreads) route_count_kernel(const int32_t *__restrict__ ids, int64_t n, int32_t E,
                                                                    int32_t *__restrict__ counts) {
   extern __shared__ int32_t hist[];
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * (kSortThreads * STEPS);
+  int32_t id[STEPS];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int64_t q = base + i * kSortThreads + threadIdx.x;
+    id[i] = q < n ? ids[q] : -1;
+  }
   for (int e = threadIdx.x; e < E; e += kSortThreads) hist[e] = 0;
   __syncthreads();
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kRouteChunk;
 #pragma unroll
-  for (int i = 0; i < kRouteChunk / kSortThreads; ++i) {
-    const int64_t q = base + i * kSortThreads + threadIdx.x;
-    const int32_t id = q < n ? ids[q] : -1;
-    if (static_cast<uint32_t>(id) < static_cast<uint32_t>(E)) atomicAdd(&hist[id], 1);
-  }
+  for (int i = 0; i < STEPS; ++i)
+    if (static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(E)) atomicAdd(&hist[id[i]], 1);
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kSortThreads) counts[static_cast<int64_t>(blockIdx.x) * E + e] = hist[e];
+  grid_launch_dependents();
 }
 
-// Slots of one chunk's entries.  An entry's slot is its expert's offset (a scan
-// of all counts), plus the expert's entries in earlier chunks, in earlier
-// warps' parts of this chunk, and before it in its own warp's part; no atomic
-// decides an order, so the sort is stable and the same every time.  Each block
-// repeats the scan of the chunk counts (chunks x E words out of L2, under 4 us
-// for 512K ids and 256 experts) rather than waiting for a third kernel.
-// A single chunk needs no counts from a kernel before it.
+// Slots of one chunk's entries (STEPS * 32 consecutive ids per warp).  An
+// entry's slot is its expert's offset (a scan of all counts), plus the expert's
+// entries in earlier chunks, in earlier warps' parts of this chunk, and before
+// it in its own warp's part; no atomic decides an order, so the sort is stable
+// and the same every time.  Each block repeats the scan of the chunk counts
+// (chunks x E words out of L2) rather than waiting for a third kernel.  A single
+// chunk needs no counts from a kernel before it, which is what a decoding batch
+// takes: its length sets STEPS, so that 96 ids are one step and not sixteen.
+template <int STEPS>
 __global__ void __launch_bounds__(kSortThreads)
     route_place_kernel(const int32_t *__restrict__ ids, int64_t n, int32_t E, int32_t n_chunks,
                        const int32_t *__restrict__ counts, int64_t *__restrict__ offsets,
@@ -55,30 +62,32 @@ __global__ void __launch_bounds__(kSortThreads)
   int32_t *part = smem;                    // [kSortWarps][E]: entries of each expert in each warp's part
   int32_t *first = smem + kSortWarps * E;  // [E]: first slot of this chunk's entries of each expert
   __shared__ int64_t warp_sum[kSortWarps];
-  __shared__ int64_t carry;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunk = blockIdx.x;
-  constexpr int kPart = kRouteChunk / kSortWarps;  // ids per warp
-  const int64_t base = static_cast<int64_t>(chunk) * kRouteChunk + warp * kPart;
+  const int64_t base = static_cast<int64_t>(chunk) * (kSortThreads * STEPS) + warp * (32 * STEPS);
 
-  for (int e = threadIdx.x; e < kSortWarps * E; e += kSortThreads) part[e] = 0;
-  if (threadIdx.x == 0) carry = 0;
-  __syncthreads();
-  int32_t id[kPart / 32];
+  int32_t id[STEPS];
 #pragma unroll
-  for (int i = 0; i < kPart / 32; ++i) {
+  for (int i = 0; i < STEPS; ++i) {
     const int64_t q = base + i * 32 + lane;
     const int32_t v = q < n ? ids[q] : -1;
     id[i] = static_cast<uint32_t>(v) < static_cast<uint32_t>(E) ? v : -1;
-    if (id[i] >= 0) atomicAdd(&part[warp * E + id[i]], 1);
   }
+  for (int e = threadIdx.x; e < kSortWarps * E; e += kSortThreads) part[e] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i)
+    if (id[i] >= 0) atomicAdd(&part[warp * E + id[i]], 1);
+  grid_dependency_wait();  // the counts of a kernel before this one
   __syncthreads();
   // scan over experts, kSortThreads at a time
+  int64_t carry = 0;
   for (int e0 = 0; e0 < E; e0 += kSortThreads) {
     const int e = e0 + threadIdx.x;
     int64_t total = 0, before = 0;
-    int32_t mine = 0;
     if (e < E) {
+      int32_t mine = 0;
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {  // warps' parts -> exclusive prefix
         const int32_t c = part[w * E + e];
         part[w * E + e] = mine;
@@ -87,6 +96,7 @@ __global__ void __launch_bounds__(kSortThreads)
       if (n_chunks == 1) {
         total = mine;
       } else {
+#pragma unroll 8
         for (int c = 0; c < n_chunks; ++c) {
           const int32_t v = counts[static_cast<int64_t>(c) * E + e];
           total += v;
@@ -103,27 +113,32 @@ __global__ void __launch_bounds__(kSortThreads)
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
     int64_t pre = carry;
-    for (int w = 0; w < warp; ++w) pre += warp_sum[w];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int64_t s = warp_sum[w];
+      if (w < warp) pre += s;
+      carry += s;
+    }
     if (e < E) {
       first[e] = static_cast<int32_t>(pre + incl - total + before);
       if (chunk == 0) offsets[e] = pre + incl - total;
     }
     __syncthreads();
-    if (threadIdx.x == kSortThreads - 1) carry = pre + incl;
-    __syncthreads();
   }
   const int64_t kept = carry;
   if (chunk == 0 && threadIdx.x == 0) offsets[E] = kept;
 #pragma unroll
-  for (int i = 0; i < kPart / 32; ++i) {
+  for (int i = 0; i < STEPS; ++i) {
     const int64_t q = base + i * 32 + lane;
     const uint32_t same = __match_any_sync(0xffffffffu, id[i]);
     const int rank = __popc(same & ((1u << lane) - 1u));
     int32_t slot = -1;
     if (id[i] >= 0) slot = first[id[i]] + part[warp * E + id[i]] + rank;
-    __syncwarp();
-    if (id[i] >= 0 && rank == 0) part[warp * E + id[i]] += __popc(same);
-    __syncwarp();
+    if (i + 1 < STEPS) {
+      __syncwarp();
+      if (id[i] >= 0 && rank == 0) part[warp * E + id[i]] += __popc(same);
+      __syncwarp();
+    }
     if (q < n) {
       position[q] = slot;
       if (slot >= 0) order[slot] = static_cast<int32_t>(q);
@@ -223,49 +238,55 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // out[t] = sum over j (in order, fp32, one rounding) of w[t, j] * y[position[t, j]];
-// dropped entries are skipped, whatever their weight holds.
-constexpr int kCombineSteps = 2;
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kRowThreads)
+// dropped entries are skipped, whatever their weight holds.  A block takes a
+// part of one token's row, STEPS packs per thread, and has eight loads of y in
+// flight per thread (a warp per part that fetched its positions by lane and
+// branched on each entry had 4.9 TB/s for 32K tokens with six entries each).
+constexpr int kCombineThreads = 128;
+template <typename T, int VEC, int STEPS>
+__global__ void __launch_bounds__(kCombineThreads)
     route_combine_kernel(const T *__restrict__ y, const int32_t *__restrict__ position, const float *__restrict__ weights,
                          T *__restrict__ out, int64_t T_, int32_t topk, int64_t d, int32_t n_parts) {
   using P = RowWord<T, VEC>;
+  constexpr int kGroup = 8 / STEPS;  // entries at a time
   const int64_t packs = d / VEC;
-  const int lane = threadIdx.x & 31;
   const int64_t rows = T_ * topk;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = item / n_parts;
-  if (t >= T_) return;
-  const int64_t p0 = (item - t * n_parts) * (32 * kCombineSteps) + lane;
-  int32_t my_pos = lane < topk ? position[t * topk + lane] : -1;
-  if (my_pos >= rows) my_pos = -1;
-  const float my_w = lane < topk ? (weights ? weights[t * topk + lane] : 1.0f) : 0.0f;
-  float acc[kCombineSteps][VEC];
+  const int64_t t = blockIdx.x / n_parts;
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x - t * n_parts) * (kCombineThreads * STEPS) + threadIdx.x;
+  float acc[STEPS][VEC] = {};
+  for (int j0 = 0; j0 < topk; j0 += kGroup) {
+    int32_t pos[kGroup];
+    float w[kGroup];
 #pragma unroll
-  for (int i = 0; i < kCombineSteps; ++i)
+    for (int j = 0; j < kGroup; ++j) {
+      const bool in = j0 + j < topk;
+      pos[j] = in ? __ldg(position + t * topk + j0 + j) : -1;
+      w[j] = !in ? 0.0f : weights ? __ldg(weights + t * topk + j0 + j) : 1.0f;
+      if (pos[j] >= rows) pos[j] = -1;
+    }
+    P v[kGroup][STEPS];
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) acc[i][c] = 0.0f;
-#pragma unroll 4
-  for (int j = 0; j < topk; ++j) {
-    const int32_t pos = __shfl_sync(0xffffffffu, my_pos, j);
-    const float w = __shfl_sync(0xffffffffu, my_w, j);
-    if (pos < 0) continue;
-    const P *src = reinterpret_cast<const P *>(y) + static_cast<int64_t>(pos) * packs;
+    for (int j = 0; j < kGroup; ++j)
 #pragma unroll
-    for (int i = 0; i < kCombineSteps; ++i) {
-      if (p0 + 32 * i < packs) {
-        float v[VEC];
-        unpack<T, VEC>(src[p0 + 32 * i], v);
+      for (int i = 0; i < STEPS; ++i)
+        if (pos[j] >= 0 && p0 + kCombineThreads * i < packs)
+          v[j][i] = reinterpret_cast<const P *>(y)[pos[j] * packs + p0 + kCombineThreads * i];
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) acc[i][c] = fmaf(w, v[c], acc[i][c]);
+    for (int j = 0; j < kGroup; ++j) {
+      if (pos[j] < 0) continue;
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        float f[VEC];
+        unpack<T, VEC>(v[j][i], f);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) acc[i][c] = fmaf(w[j], f[c], acc[i][c]);
       }
     }
   }
   P *dst = reinterpret_cast<P *>(out) + t * packs;
 #pragma unroll
-  for (int i = 0; i < kCombineSteps; ++i) {
-    if (p0 + 32 * i < packs) dst[p0 + 32 * i] = pack<T, VEC>(acc[i]);
-  }
+  for (int i = 0; i < STEPS; ++i)
+    if (p0 + kCombineThreads * i < packs) dst[p0 + kCombineThreads * i] = pack<T, VEC>(acc[i]);
 }
 
 // One block per token: dout[t] is read once for all of its entries of a group
@@ -358,10 +379,13 @@ cudaError_t gather_rows(const RouteRows &r, cudaStream_t s) {
 template <typename T, int VEC>
 cudaError_t combine_rows(const RouteRows &r, cudaStream_t s) {
   const int64_t packs = r.d / VEC;
-  const int32_t parts = static_cast<int32_t>((packs + 32 * kCombineSteps - 1) / (32 * kCombineSteps));
-  const int64_t blocks = (r.T * parts + kRowThreads / 32 - 1) / (kRowThreads / 32);
-  if (blocks >= (1ll << 31)) return cudaErrorInvalidConfiguration;
-  route_combine_kernel<T, VEC><<<static_cast<unsigned>(blocks), kRowThreads, 0, s>>>(
+  // four packs a thread where tokens alone fill the GPU, one where a few tokens
+  // leave latency as the bound
+  const int steps = r.T >= 1024 ? 4 : 1;
+  const int32_t parts = static_cast<int32_t>((packs + kCombineThreads * steps - 1) / (kCombineThreads * steps));
+  if (r.T * parts >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+  auto kern = steps == 4 ? route_combine_kernel<T, VEC, 4> : route_combine_kernel<T, VEC, 1>;
+  kern<<<static_cast<unsigned>(r.T * parts), kCombineThreads, 0, s>>>(
       static_cast<const T *>(r.src), r.position, r.weights, static_cast<T *>(r.dst), r.T, r.topk, r.d, parts);
   return cudaGetLastError();
 }
@@ -384,23 +408,47 @@ bool wide_rows(const RouteRows &r, int esize) {
 
 }  // namespace
 
-int64_t route_chunks(int64_t n) { return n <= kRouteChunk ? 1 : (n + kRouteChunk - 1) / kRouteChunk; }
+// Up to kRouteOneChunk ids are one block's work, without counts in global memory;
+// longer lists are cut into chunks of kRouteChunk.
+int64_t route_chunks(int64_t n) { return n <= kRouteOneChunk ? 1 : (n + kRouteChunk - 1) / kRouteChunk; }
+
+namespace {
+
+template <int STEPS>
+cudaError_t sort_ids(const int32_t *ids, int64_t n, int32_t n_experts, int64_t *offsets, int32_t *order, int32_t *position,
+                     int32_t *counts, int64_t chunks, cudaStream_t s) {
+  static std::atomic<uint64_t> smem_set{0};
+  cudaError_t e = set_smem_limit_once(route_place_kernel<STEPS>, (kSortWarps + 1) * kRouteMaxExperts * 4, smem_set);
+  if (e != cudaSuccess) return e;
+  if (chunks > 1) {
+    route_count_kernel<STEPS><<<static_cast<unsigned>(chunks), kSortThreads, n_experts * 4, s>>>(ids, n, n_experts, counts);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(chunks));
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(kSortWarps + 1) * n_experts * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = chunks > 1 ? 1 : 0;  // a dependent of the counting kernel
+  return cudaLaunchKernelEx(&cfg, route_place_kernel<STEPS>, ids, n, n_experts, static_cast<int32_t>(chunks),
+                            static_cast<const int32_t *>(counts), offsets, order, position);
+}
+
+}  // namespace
 
 cudaError_t launch_route_sort(const int32_t *ids, int64_t n, int32_t n_experts, int64_t *offsets, int32_t *order,
                               int32_t *position, int32_t *counts, cudaStream_t s) {
   const int64_t chunks = route_chunks(n);
-  const size_t place_smem = static_cast<size_t>(kSortWarps + 1) * n_experts * 4;
-  static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = set_smem_limit_once(route_place_kernel, (kSortWarps + 1) * kRouteMaxExperts * 4, smem_set);
-  if (e != cudaSuccess) return e;
-  if (chunks > 1) {
-    route_count_kernel<<<static_cast<unsigned>(chunks), kSortThreads, n_experts * 4, s>>>(ids, n, n_experts, counts);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  route_place_kernel<<<static_cast<unsigned>(chunks), kSortThreads, place_smem, s>>>(
-      ids, n, n_experts, static_cast<int32_t>(chunks), counts, offsets, order, position);
-  return cudaGetLastError();
+  static_assert(kRouteChunk == 4 * kSortThreads && kRouteOneChunk == 16 * kSortThreads, "steps");
+  if (chunks > 1 || (n > kSortThreads && n <= kRouteChunk))
+    return sort_ids<4>(ids, n, n_experts, offsets, order, position, counts, chunks, s);
+  if (n <= kSortThreads) return sort_ids<1>(ids, n, n_experts, offsets, order, position, counts, 1, s);
+  return sort_ids<16>(ids, n, n_experts, offsets, order, position, counts, 1, s);
 }
 
 #define SPMM_ROUTE_ROWS(name)                                                                            \
