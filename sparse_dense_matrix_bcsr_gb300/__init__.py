@@ -430,11 +430,15 @@ def _load_torch():
     return torch
 
 
-def _tensor(t, name, dtype, shape):
-    """Address of t; raises ValueError unless it is a contiguous CUDA tensor of this dtype and shape."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous CUDA tensor {dtype} {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+def _refuse(what, t, dtype, shape):
+    raise ValueError(f"{what}: expected a contiguous tensor {dtype} {tuple(shape)} on the CUDA device of the others, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _tensor(t, what, dtype, shape, device):
+    """Address of t; raises ValueError unless it is a contiguous tensor of this dtype and shape on CUDA device `device`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or device < 0 or not t.is_contiguous():
+        _refuse(what, t, dtype, shape)
     return t.data_ptr()
 
 
@@ -458,34 +462,34 @@ class Adapters:
     def _out(self, layer):
         return _torch.bfloat16 if _dt(layer.out_t) == SPMM_BF16 else _torch.float32
 
+    def _batch(self, device, down, up, scale, seg_ptr, seg_adapter):
+        n_seg, dtype = seg_adapter.shape[0], self._dtype
+        return (_tensor(down, "down", dtype, self._down, device), _tensor(up, "up", dtype, self._up, device),
+                _tensor(scale, "scale", _torch.float32, self._scale, device),
+                _tensor(seg_ptr, "seg_ptr", _torch.int64, (n_seg + 1,), device),
+                _tensor(seg_adapter, "seg_adapter", _torch.int32, (n_seg,), device), n_seg)
+
     def linear(self, layer: SpMM, X, Y, down, up, scale, seg_ptr, seg_adapter, stream=None):
         """Y = X * A^T plus each row's adapter, for a BCSR layer A (m x k); returns Y."""
-        N, n_seg = X.shape[0], seg_adapter.shape[0]
-        x = _tensor(X, "X", self._dtype, (N, self.k))
+        N, device = X.shape[0], X.get_device()
         status = _lib.spmm_run_linear_adapters(
-            layer.h, self.a, x, _tensor(Y, "Y", self._out(layer), (N, self.m)), N,
-            _tensor(down, "down", self._dtype, self._down), _tensor(up, "up", self._dtype, self._up),
-            _tensor(scale, "scale", _torch.float32, self._scale),
-            _tensor(seg_ptr, "seg_ptr", _torch.int64, (n_seg + 1,)),
-            _tensor(seg_adapter, "seg_adapter", _torch.int32, (n_seg,)), n_seg,
-            (stream.cuda_stream if stream is not None else _raw_stream(X.get_device())) or None)
+            layer.h, self.a, _tensor(X, "X", self._dtype, (N, self.k), device),
+            _tensor(Y, "Y", self._out(layer), (N, self.m), device), N,
+            *self._batch(device, down, up, scale, seg_ptr, seg_adapter),
+            (stream.cuda_stream if stream is not None else _raw_stream(device)) or None)
         if status:
             _check(status, "spmm_run_linear_adapters")
         return Y
 
     def grad(self, layer_t: SpMM, X, dY, dX, d_down, d_up, down, up, scale, seg_ptr, seg_adapter, stream=None):
         """Gradients of `linear` into dX (None to leave it out), d_down and d_up; layer_t holds A^T (k x m)."""
-        N, n_seg = X.shape[0], seg_adapter.shape[0]
-        x = _tensor(X, "X", self._dtype, (N, self.k))
+        N, device, dtype = X.shape[0], X.get_device(), self._dtype
         status = _lib.spmm_adapters_grad(
-            layer_t.h, self.a, x, _tensor(dY, "dY", self._dtype, (N, self.m)),
-            None if dX is None else _tensor(dX, "dX", self._out(layer_t), (N, self.k)),
-            _tensor(d_down, "d_down", self._dtype, self._down), _tensor(d_up, "d_up", self._dtype, self._up), N,
-            _tensor(down, "down", self._dtype, self._down), _tensor(up, "up", self._dtype, self._up),
-            _tensor(scale, "scale", _torch.float32, self._scale),
-            _tensor(seg_ptr, "seg_ptr", _torch.int64, (n_seg + 1,)),
-            _tensor(seg_adapter, "seg_adapter", _torch.int32, (n_seg,)), n_seg,
-            (stream.cuda_stream if stream is not None else _raw_stream(X.get_device())) or None)
+            layer_t.h, self.a, _tensor(X, "X", dtype, (N, self.k), device), _tensor(dY, "dY", dtype, (N, self.m), device),
+            None if dX is None else _tensor(dX, "dX", self._out(layer_t), (N, self.k), device),
+            _tensor(d_down, "d_down", dtype, self._down, device), _tensor(d_up, "d_up", dtype, self._up, device), N,
+            *self._batch(device, down, up, scale, seg_ptr, seg_adapter),
+            (stream.cuda_stream if stream is not None else _raw_stream(device)) or None)
         if status:
             _check(status, "spmm_adapters_grad")
 
@@ -508,25 +512,20 @@ def _row_dtype(t):
     return dt
 
 
-def _kept_ptr(offsets):
-    """Address of offsets[n_experts], the number of kept entries."""
-    n = offsets.shape[0]
-    return _tensor(offsets, "offsets", _torch.int64, (n,)) + 8 * (n - 1)
-
-
 def route_sort(ids, n_experts: int):
     """(offsets [n_experts + 1] int64, order [T * topk] int32, position [T, topk] int32) of expert ids [T, topk]
     (int32; ids outside [0, n_experts) are dropped), on the current stream."""
     torch = _torch or _load_torch()
     T, topk = shape = ids.shape
-    p, device = _tensor(ids, "ids", torch.int32, shape), ids.device
-    offsets = torch.empty(n_experts + 1, dtype=torch.int64, device=device)
-    order = torch.empty(T * topk, dtype=torch.int32, device=device)
+    n, at, where = T * topk, ids.get_device(), ids.device
+    p = _tensor(ids, "ids", torch.int32, shape, at)
+    offsets = torch.empty(n_experts + 1, dtype=torch.int64, device=where)
+    order = torch.empty(n, dtype=torch.int32, device=where)
     position = torch.empty_like(ids)
-    size = _lib.spmm_route_workspace_bytes(T, topk, n_experts)
-    work = torch.empty(size, dtype=torch.uint8, device=device) if size else None
+    size = _lib.spmm_route_workspace_bytes(T, topk, n_experts) if n > 4096 else 0  # short lists need none
+    work = torch.empty(size, dtype=torch.uint8, device=where) if size else None
     status = _lib.spmm_route_sort(p, T, topk, n_experts, offsets.data_ptr(), order.data_ptr(), position.data_ptr(),
-                                  work.data_ptr() if size else None, _raw_stream(ids.get_device()) or None)
+                                  work.data_ptr() if size else None, _raw_stream(at) or None)
     if status:
         _check(status, "spmm_route_sort")
     return offsets, order, position
@@ -536,11 +535,12 @@ def route_gather(x, position, offsets):
     """Rows of x [T, d] in slot order [T * topk, d]; slots that no entry takes are 0.  Current stream."""
     torch = _torch or _load_torch()
     T, topk = shape = position.shape
-    d, dt = x.shape[1], x.dtype
-    out = torch.empty((T * topk, d), dtype=dt, device=x.device)
-    status = _lib.spmm_route_gather(_tensor(x, "x", dt, (T, d)), _tensor(position, "position", torch.int32, shape),
-                                    _kept_ptr(offsets), out.data_ptr(), T, topk, d, _row_dtype(x),
-                                    _raw_stream(x.get_device()) or None)
+    d, dtype, at, last = x.shape[1], x.dtype, x.get_device(), offsets.shape[0] - 1
+    out = torch.empty((T * topk, d), dtype=dtype, device=x.device)
+    status = _lib.spmm_route_gather(
+        _tensor(x, "x", dtype, (T, d), at), _tensor(position, "position", torch.int32, shape, at),
+        _tensor(offsets, "offsets", torch.int64, (last + 1,), at) + 8 * last, out.data_ptr(), T, topk, d, _row_dtype(x),
+        _raw_stream(at) or None)
     if status:
         _check(status, "spmm_route_gather")
     return out
@@ -550,11 +550,12 @@ def route_combine(y, position, weights=None):
     """out[t] = sum_j weights[t, j] * y[position[t, j]] (weights None: ones), fp32 sums.  Current stream."""
     torch = _torch or _load_torch()
     T, topk = shape = position.shape
-    d, dt = y.shape[1], y.dtype
-    out = torch.empty((T, d), dtype=dt, device=y.device)
-    status = _lib.spmm_route_combine(_tensor(y, "y", dt, (T * topk, d)), _tensor(position, "position", torch.int32, shape),
-                                     None if weights is None else _tensor(weights, "weights", torch.float32, shape),
-                                     out.data_ptr(), T, topk, d, _row_dtype(y), _raw_stream(y.get_device()) or None)
+    d, dtype, at = y.shape[1], y.dtype, y.get_device()
+    out = torch.empty((T, d), dtype=dtype, device=y.device)
+    status = _lib.spmm_route_combine(
+        _tensor(y, "y", dtype, (T * topk, d), at), _tensor(position, "position", torch.int32, shape, at),
+        None if weights is None else _tensor(weights, "weights", torch.float32, shape, at), out.data_ptr(), T, topk, d,
+        _row_dtype(y), _raw_stream(at) or None)
     if status:
         _check(status, "spmm_route_combine")
     return out
@@ -564,14 +565,15 @@ def route_combine_grad(dout, y, position, weights, offsets):
     """(dy [T * topk, d], dweights [T, topk] fp32) of route_combine.  Current stream."""
     torch = _torch or _load_torch()
     T, topk = shape = position.shape
-    d, dt = y.shape[1], y.dtype
+    d, dtype, at, last = y.shape[1], y.dtype, y.get_device(), offsets.shape[0] - 1
     dy = torch.empty_like(y)
     dw = torch.empty(shape, dtype=torch.float32, device=y.device)
     status = _lib.spmm_route_combine_grad(
-        _tensor(dout, "dout", dt, (T, d)), _tensor(y, "y", dt, (T * topk, d)),
-        _tensor(position, "position", torch.int32, shape),
-        None if weights is None else _tensor(weights, "weights", torch.float32, shape), _kept_ptr(offsets), dy.data_ptr(),
-        dw.data_ptr(), T, topk, d, _row_dtype(y), _raw_stream(y.get_device()) or None)
+        _tensor(dout, "dout", dtype, (T, d), at), _tensor(y, "y", dtype, (T * topk, d), at),
+        _tensor(position, "position", torch.int32, shape, at),
+        None if weights is None else _tensor(weights, "weights", torch.float32, shape, at),
+        _tensor(offsets, "offsets", torch.int64, (last + 1,), at) + 8 * last, dy.data_ptr(), dw.data_ptr(), T, topk, d,
+        _row_dtype(y), _raw_stream(at) or None)
     if status:
         _check(status, "spmm_route_combine_grad")
     return dy, dw
