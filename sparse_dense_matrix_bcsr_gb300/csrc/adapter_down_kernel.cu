@@ -110,12 +110,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(&mi->tmem), tmem_cols);
     tmem_relinquish();
-  } else if (warp == kEpiWarp0 && part == 0 && static_cast<int64_t>(unit) * kAdapterTileRows < p.N) {
+  } else if (warp == kEpiWarp0 && part == 0 && static_cast<int64_t>(unit) * p.tile_rows < p.N) {
     // the projection's own tiles: their segments, for its producers
-    const int64_t row0 = static_cast<int64_t>(unit) * kAdapterTileRows;
-    const int32_t c = list_segments(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, row0,
-                                    min(row0 + kAdapterTileRows, static_cast<int64_t>(p.N)), p.tile_segs + row0,
-                                    kAdapterTileRows, p.status);
+    const int64_t tile0 = static_cast<int64_t>(unit) * p.tile_rows;
+    const int32_t c = list_segments(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, tile0,
+                                    min(tile0 + p.tile_rows, static_cast<int64_t>(p.N)), p.tile_segs + tile0,
+                                    p.tile_rows, p.status);
     if (lane == 0) p.tile_count[unit] = c;
   }
   tc_fence_before_sync();

@@ -101,7 +101,7 @@ spmm::AdapterParams make_params(spmm_handle h, spmm_adapters a, int64_t N, const
 }
 
 // H = scale * X D^T in 16 bits (`parts` of them), with the projection's tile lists.
-spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, int parts, cudaStream_t s) {
+spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, int parts, int tile_rows, cudaStream_t s) {
   const bool bf16 = a->in_t == SPMM_BF16;
   CUtensorMap tmX, tmD;
   spmm_status st = spmm::encode_2d(&tmX, p.X, bf16, p.N, p.K, p.K, 128, 64);
@@ -122,6 +122,7 @@ spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, int part
   d.parts = parts;
   d.N = p.N;
   d.K = p.K;
+  d.tile_rows = tile_rows;
   d.status = p.status;
   d.wait_limit_ns = p.wait_limit_ns;
   CUDA_TRY(spmm::launch_adapter_down(tmX, tmD, d, p.num_sms, bf16, s), "adapter down projection launch");
@@ -129,24 +130,26 @@ spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, int part
 }
 
 // Y = X W^T + U H per row, H and the tile lists from down_project.
-spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams &p, int parts, cudaStream_t s) {
+spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams &p, int parts, spmm::LinearTile tile,
+                       cudaStream_t s) {
   const bool bf16 = h->in_t == SPMM_BF16, out_bf16 = h->out_t == SPMM_BF16;
   CUtensorMap tmX, tmY;
   spmm::LinearAdapters ad;
   ad.box = p.rank <= 16 ? 16 : p.rank <= 32 ? 32 : 64;
   spmm_status st = spmm::encode_x(&tmX, p.X, bf16, p.N, p.K);
-  if (st == SPMM_OK) st = spmm::encode_y(&tmY, p.Y, out_bf16, p.N, p.M);
+  if (st == SPMM_OK) st = spmm::encode_y(&tmY, p.Y, out_bf16, p.N, p.M, spmm::linear_tile_rows(tile));
   if (st == SPMM_OK)
     st = spmm::encode_2d(&ad.tmU, p.up, bf16, static_cast<uint64_t>(p.n_adapters) * p.M, p.rank, p.rank, 64, ad.box,
                          ad.box * 2);
   if (st == SPMM_OK)
-    st = spmm::encode_2d(&ad.tmH, p.H, bf16, static_cast<uint64_t>(parts) * p.N, p.rank, p.rank, spmm::kAdapterTileRows,
-                         ad.box, ad.box * 2);
+    st = spmm::encode_2d(&ad.tmH, p.H, bf16, static_cast<uint64_t>(parts) * p.N, p.rank, p.rank, 128, ad.box,
+                         ad.box * 2);
   if (st != SPMM_OK) return st;
   ad.tile_segs = a->d_tile_segs;
   ad.tile_count = a->d_tile_count;
   ad.rank = p.rank;
   ad.parts = parts;
+  ad.tile = tile;
   spmm::BcsrParams b;
   std::memset(&b, 0, sizeof b);
   b.block_row_ptr = p.block_row_ptr;
@@ -196,8 +199,9 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
   p.K = static_cast<int32_t>(h->k);
   if (tiled) {
     const int parts = h->out_t == SPMM_F32 ? 2 : 1;
-    const spmm_status st = down_project(a, p, parts, s);
-    return st != SPMM_OK ? st : up_project(h, a, p, parts, s);
+    const spmm::LinearTile tile = spmm::linear_adapters_tile(h->n_groups, h->n_units, p.N, p.n_seg, p.num_sms);
+    const spmm_status st = down_project(a, p, parts, spmm::linear_tile_rows(tile), s);
+    return st != SPMM_OK ? st : up_project(h, a, p, parts, tile, s);
   }
   spmm::AdapterDecodeParams d;
   std::memset(&d, 0, sizeof d);
@@ -264,10 +268,10 @@ spmm_status spmm_adapters_create(spmm_adapters *out, int64_t m, int64_t k, int32
     a->sm103 = major == 10 && minor == 3;
     const size_t h = static_cast<size_t>(std::max<int64_t>(max_rows, 1)) * rank * sizeof(float);
     CUDA_TRY(cudaMalloc(&a->d_h, h), "cudaMalloc(adapter activations)");
-    const size_t tiles = static_cast<size_t>(max_rows) / spmm::kAdapterTileRows + 1;
-    CUDA_TRY(cudaMalloc(&a->d_tile_segs, tiles * spmm::kAdapterTileRows * sizeof(spmm::TileSegment)),
-             "cudaMalloc(tile segments)");
-    CUDA_TRY(cudaMalloc(&a->d_tile_count, tiles * sizeof(int32_t)), "cudaMalloc(tile counts)");
+    // one entry per row of the tiles, one count per tile of the smallest
+    const size_t rows = (static_cast<size_t>(max_rows) / spmm::kMaxTileRows + 1) * spmm::kMaxTileRows;
+    CUDA_TRY(cudaMalloc(&a->d_tile_segs, rows * sizeof(spmm::TileSegment)), "cudaMalloc(tile segments)");
+    CUDA_TRY(cudaMalloc(&a->d_tile_count, rows / 256 * sizeof(int32_t)), "cudaMalloc(tile counts)");
     if (a->grad) {
       CUDA_TRY(cudaMalloc(&a->d_dh, h), "cudaMalloc(adapter gradients)");
       CUDA_TRY(cudaMalloc(&a->d_down_t, static_cast<size_t>(n_adapters) * k * rank * 2), "cudaMalloc(transposed down)");
@@ -334,7 +338,7 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
   p.K = k;
   p.down = down;
   p.H = a->d_h;
-  st = down_project(a, p, 1, s);
+  st = down_project(a, p, 1, spmm::kMaxTileRows, s);
   if (st != SPMM_OK) return st;
   if (dX) {
     st = project(h_t, a, p, dY, dX, a->d_up_t, a->d_down_t, a->d_dh, true, s);
@@ -343,7 +347,7 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
     p.K = m;
     p.down = a->d_up_t;
     p.H = a->d_dh;
-    st = down_project(a, p, 1, s);
+    st = down_project(a, p, 1, spmm::kMaxTileRows, s);
   }
   spmm::AdapterWgradParams w;
   if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dy, dY, bf16, N, m, m, 64, 64);

@@ -11,21 +11,32 @@
 // are the M operand and the 64 x 64 block is the N operand, both K-major as
 // they lie in memory, so TMEM holds Y's own layout (lane = row n of X,
 // columns = the block row's 64 output features) and the epilogue writes
-// contiguous 128-byte pieces of Y's rows.  One stage is the block (8 KB) and a
-// 256-row tile of X (one 32 KB TMA box); its MMAs are 4 k-steps x 2 halves of
-// M = 128, N = 64, K = 16.
+// contiguous pieces of Y's rows.  One stage is the block (8 KB) and a tile of 256
+// or 512 rows of X (one or two 32 KB TMA boxes); its MMAs are 4 k-steps x 2 or 4
+// parts of M = 128, N = 64, K = 16.
 //
-// Work unit ("tile") = one block row x 256 rows of X.  Persistent CTAs take
-// tiles t, t + G, ... in the order of tile_coords (kGroupN tiles of X of the
-// same block row in a row, so the CTAs running together read a few X slices,
-// which stay in L2); two TMEM accumulators alternate between tiles; two CTAs
-// per SM.  6 warps, as in bcsr_kernel.cu: a TMA producer, an MMA issuer and
-// four epilogue warps (warp w reads TMEM lanes 32 (w % 4) .. + 31, rows of X).
+// Work unit ("tile") = one block row x 256 or 512 rows of X.  Persistent CTAs,
+// one (or two) per SM, take tiles t, t + G, ... in the order of tile_coords (8 or 4 tiles
+// of X of the same block row in a row, so the CTAs running together read a few X
+// slices, which stay in L2); two TMEM accumulators alternate between tiles.
+// 6 warps, as in bcsr_kernel.cu: a TMA producer, an MMA issuer and four epilogue
+// warps (warp w reads TMEM lanes 32 (w % 4) .. + 31, rows of X).
+//
+// What bounds it is neither bytes nor MMAs but the roles' handshakes per stage
+// (18944 x 3584 with 90 % zero blocks, 65536 rows, 256-row tiles: 1066 us;
+// without X's copies 1043, with an eighth of the MMAs 1047, without stores 991):
+// the MMA warp spends ~30 cycles an MMA, ~85 on a stage's commit and ~120 on a
+// wait that has nothing to wait for.  Tiles of 512 rows (half the handshakes, but
+// three stages of 72 KB in place of five of 40) measured the same without
+// adapters (1057 us) and 8 % slower on long block rows (3584 x 18944, 30 blocks a
+// row); with adapters, see linear_adapters_tile.
 //
 // With adapters (spmm_run_linear_adapters) a tile has further stages after its
 // blocks: for every segment with an adapter among its rows, the block row's 64
 // rows of U_a as the N operand and the tile's rows of H as the M operand, 64
-// ranks a stage.  Their MMAs update the segment's lanes only (the MMA's lane
+// ranks a stage (H in one 16-bit part; in two parts, a stage takes both parts of
+// half the tile, so a segment within a half costs one stage either way).  Their
+// MMAs update the segment's lanes only (the MMA's lane
 // mask), so the other rows' sums do not see the product at all: no zeroed copy
 // of H, and an adapter with infinities cannot reach other rows as 0 * inf.  The
 // product with adapters reads X and writes Y once; a second pass over Y would
@@ -44,57 +55,67 @@ struct NoAdapters {};
 
 constexpr int kBlk = 64;
 constexpr int kBlkBytes = kBlk * kBlk * 2;
-constexpr int kTileN = kAdapterTileRows;       // rows of X per tile (256)
-constexpr int kXBytes = kTileN * kBlk * 2;     // one 256 x 64 box of X
-constexpr int kStageBytes = kBlkBytes + kXBytes;
-constexpr int kQ = 5;                          // stages
+constexpr int kBoxRows = 256;                  // rows of X per TMA box
 constexpr int kNbuf = 2;                       // TMEM accumulators per CTA
-constexpr int kAccCols = 2 * kBlk;             // two halves of 128 rows x 64 columns
-constexpr int kTmemCols = kNbuf * kAccCols;
 constexpr int kThreads = 192;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2, kEpiWarps = 4;
-constexpr int kPartBytes = 32 * 128;           // one store box: 32 rows of Y x 128 bytes
-constexpr int kStagingBytes = kEpiWarps * kPartBytes;  // one staging buffer per warp
 constexpr int kMiscBytes = 1024;
-constexpr int kSmemBytes = kQ * kStageBytes + kStagingBytes + kMiscBytes + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
 
-constexpr int32_t kRecEmpty = 1, kRecEnd = 2, kRecAdaptersShift = 8;
+// A tile of ROWS rows of X, CTAS CTAs per SM.
+template <int ROWS, int CTAS>
+struct Tile {
+  static constexpr int kRows = ROWS, kCtas = CTAS;
+  static constexpr int kParts = ROWS / 128;                    // M = 128 parts
+  static constexpr int kXBytes = ROWS * kBlk * 2;
+  static constexpr int kStageBytes = kBlkBytes + kXBytes;
+  static constexpr int kQ = CTAS == 2 ? 2 : ROWS == 256 ? 5 : 3;  // stages
+  static constexpr int kAccCols = kParts * kBlk;
+  static constexpr int kTmemCols = kNbuf * kAccCols;
+  static constexpr int kBoxBytes = ROWS == 256 ? 128 : 64;     // bytes of Y per row of a store box (32 rows)
+  static constexpr int kStagingBytes = kEpiWarps * 32 * kBoxBytes;  // one staging buffer per warp
+  static constexpr int kSmemBytes = kQ * kStageBytes + kStagingBytes + kMiscBytes + 1024;
+  static constexpr int kGroup = 2048 / ROWS;                   // tiles of X that a block row takes in a row
+  static_assert(CTAS * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of an SM");
+  static_assert(CTAS * kTmemCols <= 512, "TMEM");
+};
+
+constexpr int32_t kRecEmpty = 1, kRecEnd = 2, kRecAdapters = 4, kRecLast = 8;
 // What the producer tells the MMA warp with a tile's first stage: the tile, how
-// many stages of blocks it has and (flags >> kRecAdaptersShift) how many of
-// adapters follow.  With a stage of an adapter: its steps of 16 ranks and its
-// rows of the tile, begin | end << 16.
+// many stages of blocks it has and whether adapters follow.  With a stage of an
+// adapter: its steps of 16 ranks, its rows of the tile (begin | end << 16), the
+// first part that the stage holds and whether it is the tile's last.
 struct TileRec {
   int32_t br;
   int32_t nt;
   int32_t flags;
   int32_t stages;  // or steps
   int32_t rows;
-  int32_t pad_[3];
+  int32_t part;
+  int32_t pad_[2];
 };
 
-constexpr int kGroupN = 8;
+template <int GROUP>
 __device__ __forceinline__ void tile_coords(int64_t t, int n_block_rows, int n_tiles_n, int &br, int &nt) {
-  const int64_t span = static_cast<int64_t>(n_block_rows) * kGroupN;
+  const int64_t span = static_cast<int64_t>(n_block_rows) * GROUP;
   const int64_t g = t / span;
   const int64_t r = t - g * span;
-  const int gsz = min(kGroupN, n_tiles_n - static_cast<int>(g) * kGroupN);
+  const int gsz = min(GROUP, n_tiles_n - static_cast<int>(g) * GROUP);
   br = static_cast<int>(r / gsz);
-  nt = static_cast<int>(g) * kGroupN + static_cast<int>(r % gsz);
+  nt = static_cast<int>(g) * GROUP + static_cast<int>(r % gsz);
 }
 
-// Y's parts per tile and warp: 2 halves of 128 rows (the warp's 32 rows of
-// each) x 64 output features, as 128-byte box rows: one box per half for bf16
-// Y, two (32 features each) for fp32.
-template <bool IN_BF16, bool OUT_BF16, class Adapters>
-__global__ void __launch_bounds__(kThreads, 1)
+// Y's store boxes: 32 rows (a warp's lanes of one part) x 128 or 64 bytes.
+template <bool IN_BF16, bool OUT_BF16, class T, class Adapters>
+__global__ void __launch_bounds__(kThreads, T::kCtas)
     bcsr_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ CUtensorMap tmY, const BcsrParams p,
                        const __grid_constant__ Adapters ad) {
   constexpr bool kAdapt = std::is_same_v<Adapters, LinearAdapters>;
+  constexpr int kQ = T::kQ, kStageBytes = T::kStageBytes, kStagingBytes = T::kStagingBytes;
+  constexpr int kAccCols = T::kAccCols, kTmemCols = T::kTmemCols, kTileN = T::kRows;
   constexpr int kOutBytes = OUT_BF16 ? 2 : 4;
-  constexpr int kBoxCols = 128 / kOutBytes;      // features per box row
-  constexpr int kParts = 2 * (kBlk / kBoxCols);  // store boxes per warp and tile
+  constexpr int kBoxCols = T::kBoxBytes / kOutBytes;  // features per box row
+  constexpr int kBoxes = kBlk / kBoxCols;             // store boxes per warp and part
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *staging = smem + kQ * kStageBytes;
@@ -175,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int my_br = 0, my_nt = 0, my_segs = 0;
       int64_t my_jb = 0, my_je = 0;
       if (mine < n_tiles) {
-        tile_coords(mine, p.n_block_rows, n_tiles_n, my_br, my_nt);
+        tile_coords<T::kGroup>(mine, p.n_block_rows, n_tiles_n, my_br, my_nt);
         my_jb = p.block_row_ptr[my_br];
         my_je = p.block_row_ptr[my_br + 1];
         if constexpr (kAdapt) my_segs = ad.tile_count[my_nt];  // segments with an adapter in the tile
@@ -189,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         TileSegment s{};
         if constexpr (kAdapt) {
           const int nt = __shfl_sync(0xffffffffu, my_nt, i), n = __shfl_sync(0xffffffffu, my_segs, i);
-          if (lane < n) s = ad.tile_segs[static_cast<int64_t>(nt) * kAdapterTileRows + lane];
+          if (lane < n) s = ad.tile_segs[static_cast<int64_t>(nt) * kTileN + lane];
         }
         return s;
       };
@@ -205,26 +226,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           next_cols = first_cols(ti + 1);
           next_segs = first_segs(ti + 1);
         }
-        int32_t adapter_stages = 0;
-        if constexpr (kAdapt) adapter_stages = segs * ((ad.rank + ad.box - 1) / ad.box) * ad.parts;
+        const int32_t first_flags = segs > 0 ? kRecAdapters : 0;
+        auto copy_x = [&](uint32_t st, uint32_t fb, int32_t x) {
+#pragma unroll
+          for (int b = 0; b < kTileN / kBoxRows; ++b)
+            tma_load_2d(st + kBlkBytes + b * (kBoxRows * kBlk * 2), &tmX, fb, x, nt * kTileN + b * kBoxRows);
+        };
         if (jb == je && segs > 0) {
           // no block to start the sums with: a stage of zeros, read past the end of the blocks and of X
           ok = claim();
           if (!ok) break;
           if (lane == 0) {
-            tile_rec[stage] = TileRec{br, nt, adapter_stages << kRecAdaptersShift, 1, 0, {}};
+            tile_rec[stage] = TileRec{br, nt, first_flags, 1, 0, 0, {}};
             const uint32_t fb = full0 + 8 * stage;
             const uint32_t st = smem_addr(smem + stage * kStageBytes);
             mbar_arrive_expect_tx(fb, kStageBytes);
             tma_load_2d(st, &tmA, fb, kBlk, 0);
-            tma_load_2d(st + kBlkBytes, &tmX, fb, (p.K + kBlk - 1) / kBlk * kBlk, 0);
+            copy_x(st, fb, (p.K + kBlk - 1) / kBlk * kBlk);
           }
           advance();
         } else if (jb == je) {
           ok = claim();
           if (!ok) break;
           if (lane == 0) {
-            tile_rec[stage] = TileRec{br, nt, kRecEmpty, 0, 0, {}};
+            tile_rec[stage] = TileRec{br, nt, kRecEmpty, 0, 0, 0, {}};
             mbar_arrive(full0 + 8 * stage);
           }
           advance();
@@ -238,14 +263,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if (lane == 0) {
               const int64_t j = jbase + i;
-              if (j == jb)
-                tile_rec[stage] =
-                    TileRec{br, nt, adapter_stages << kRecAdaptersShift, static_cast<int32_t>(je - jb), 0, {}};
+              if (j == jb) tile_rec[stage] = TileRec{br, nt, first_flags, static_cast<int32_t>(je - jb), 0, 0, {}};
               const uint32_t fb = full0 + 8 * stage;
               const uint32_t st = smem_addr(smem + stage * kStageBytes);
               mbar_arrive_expect_tx(fb, kStageBytes);
               tma_load_2d(st, &tmA, fb, 0, static_cast<int32_t>(j * kBlk));
-              tma_load_2d(st + kBlkBytes, &tmX, fb, bcol * kBlk, nt * kTileN);
+              copy_x(st, fb, bcol * kBlk);
             }
             advance();
           }
@@ -253,22 +276,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kAdapt) {
           for (int32_t base = 0; base < segs && ok; base += 32) {
             TileSegment my = tile_segs;
-            if (base > 0 && base + lane < segs) my = ad.tile_segs[static_cast<int64_t>(nt) * kAdapterTileRows + base + lane];
+            if (base > 0 && base + lane < segs) my = ad.tile_segs[static_cast<int64_t>(nt) * kTileN + base + lane];
             const int cnt = min(segs - base, 32);
             for (int i = 0; i < cnt && ok; ++i) {
               const int32_t a = __shfl_sync(0xffffffffu, my.adapter, i);
-              const int32_t rows = __shfl_sync(0xffffffffu, my.begin | my.end << 16, i);
-              for (int part = 0; part < ad.parts && ok; ++part) {
+              const int32_t begin = __shfl_sync(0xffffffffu, my.begin, i), end = __shfl_sync(0xffffffffu, my.end, i);
+              const int group = T::kParts / ad.parts;  // parts of the tile that a stage holds
+              for (int g = begin / 128 / group * group; g * 128 < end && ok; g += group) {
+                const int h0 = max(begin / 128, g), h1 = min((end + 127) / 128, g + group);
                 for (int32_t r0 = 0; r0 < ad.rank; r0 += ad.box) {
                   ok = claim();
                   if (!ok) break;
                   if (lane == 0) {
-                    tile_rec[stage] = TileRec{br, nt, 0, (min(ad.rank - r0, ad.box) + 15) / 16, rows, {}};
+                    const bool last = base + i == segs - 1 && (g + group) * 128 >= end && r0 + ad.box >= ad.rank;
+                    tile_rec[stage] = TileRec{br, nt, last ? kRecLast : 0, (min(ad.rank - r0, ad.box) + 15) / 16,
+                                              begin | end << 16, g, {}};
                     const uint32_t fb = full0 + 8 * stage;
                     const uint32_t st = smem_addr(smem + stage * kStageBytes);
-                    mbar_arrive_expect_tx(fb, (kBlk + kTileN) * ad.box * 2);
+                    const uint32_t part_bytes = 128 * ad.box * 2;
+                    mbar_arrive_expect_tx(fb, kBlk * ad.box * 2 + (h1 - h0) * ad.parts * part_bytes);
                     tma_load_2d(st, &ad.tmU, fb, r0, a * p.M + br * kBlk);
-                    tma_load_2d(st + kBlkBytes, &ad.tmH, fb, r0, part * p.N + nt * kTileN);
+                    for (int q = 0; q < ad.parts; ++q)
+                      for (int h = h0; h < h1; ++h)
+                        tma_load_2d(st + kBlkBytes + (q * group + h - g) * part_bytes, &ad.tmH, fb, r0,
+                                    q * p.N + nt * kTileN + h * 128);
                   }
                   advance();
                 }
@@ -281,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       ok = claim();
       if (ok && lane == 0) {
-        tile_rec[stage] = TileRec{-1, -1, kRecEnd, 0, 0, {}};
+        tile_rec[stage] = TileRec{-1, -1, kRecEnd, 0, 0, 0, {}};
         mbar_arrive(full0 + 8 * stage);
       }
     }
@@ -307,14 +338,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     // Operands of stage 0; the block is the N operand (64 rows of A x 64 k), X
-    // the M operand (256 rows x 64 k, half h its rows 128 h .. 128 h + 127).
+    // the M operand (part h its rows 128 h .. 128 h + 127).
     const uint64_t blk_desc = smem_desc_sw128(smem_addr(smem), 16, 1024);
     const uint64_t x_desc = smem_desc_sw128(smem_addr(smem) + kBlkBytes, 16, 1024);
     // An adapter's operands lie in the same places, in rows of ad.box ranks.
     uint64_t u_desc = 0, h_desc = 0;
-    uint32_t h_half = 0;
+    uint32_t h_part = 0;
     if constexpr (kAdapt) {
-      h_half = 128 * ad.box * 2;
+      h_part = 128 * ad.box * 2;
       u_desc = smem_desc_k_major(smem_addr(smem), ad.box * 2);
       h_desc = smem_desc_k_major(smem_addr(smem) + kBlkBytes, ad.box * 2);
     }
@@ -349,35 +380,46 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              umma_f16_elect(acc + h * kBlk, smem_desc_add(adesc0, h * (kXBytes / 2) + kk * 32),
+            for (int h = 0; h < T::kParts; ++h)
+              umma_f16_elect(acc + h * kBlk, smem_desc_add(adesc0, h * (128 * kBlk * 2) + kk * 32),
                              smem_desc_add(bdesc0, kk * 32), idesc, kk > 0 ? 1u : accumulate);
           }
           release();
         }
         if constexpr (kAdapt) {
-          const int adapter_stages = rec.flags >> kRecAdaptersShift;
-          for (int j = 0; j < adapter_stages && ok; ++j) {
+          bool more = (rec.flags & kRecAdapters) != 0 && ok;
+          while (more) {
             ok = wait_full();
             if (!ok) break;
             tc_fence_after_sync();
             const TileRec seg = tile_rec[stage];
-            const int steps = seg.stages, begin = seg.rows & 0xffff, end = seg.rows >> 16;
+            more = (seg.flags & kRecLast) == 0;
+            const int begin = seg.rows & 0xffff, end = seg.rows >> 16, group = T::kParts / ad.parts;
             const uint64_t bdesc0 = smem_desc_add(u_desc, stage * kStageBytes);
             const uint64_t adesc0 = smem_desc_add(h_desc, stage * kStageBytes);
+            if (begin <= 128 * seg.part && end >= 128 * (seg.part + group)) {
+              // the segment holds all rows of the stage: no lanes to mask; as for the
+              // blocks, MMAs in a row go to different accumulators
+              for (int kk = 0; kk < seg.stages; ++kk) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (end <= 128 * h || begin >= 128 * (h + 1)) continue;
-              const uint64_t adesc = smem_desc_add(adesc0, h * h_half);
-              if (begin <= 128 * h && end >= 128 * (h + 1)) {  // the segment holds the half: no lanes to mask
-                for (int kk = 0; kk < steps; ++kk)
-                  umma_f16_elect(acc + h * kBlk, smem_desc_add(adesc, kk * 32), smem_desc_add(bdesc0, kk * 32), idesc, 1u);
-              } else {
+                for (int i = 0; i < T::kParts; ++i) {  // slot i: part i of H, or of its second 16 bits
+                  const int h = seg.part + (i < group ? i : i - group);
+                  umma_f16_elect(acc + h * kBlk, smem_desc_add(adesc0, i * h_part + kk * 32),
+                                 smem_desc_add(bdesc0, kk * 32), idesc, 1u);
+                }
+              }
+            } else {
+              for (int i = 0; i < group; ++i) {
+                const int h = seg.part + i;
+                if (end <= 128 * h || begin >= 128 * (h + 1)) continue;
                 uint32_t off[4];
                 lanes_off(begin - 128 * h, end - 128 * h, off);
-                for (int kk = 0; kk < steps; ++kk)
-                  umma_f16_lanes_elect(acc + h * kBlk, smem_desc_add(adesc, kk * 32), smem_desc_add(bdesc0, kk * 32),
-                                       idesc, 1u, off);
+                for (int q = 0; q < ad.parts; ++q) {
+                  const uint64_t adesc = smem_desc_add(adesc0, (q * group + i) * h_part);
+                  for (int kk = 0; kk < seg.stages; ++kk)
+                    umma_f16_lanes_elect(acc + h * kBlk, smem_desc_add(adesc, kk * 32), smem_desc_add(bdesc0, kk * 32),
+                                         idesc, 1u, off);
+                }
               }
             }
             release();
@@ -411,14 +453,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    // Warp w holds rows 32 (w % 4) + lane of each 128-row half (TMEM lanes)
-    // and the block row's 64 features (TMEM columns h * 64 ..).  Each part
-    // (one store box: 32 rows x 128 bytes) goes through the warp's staging
-    // buffer in the 128-byte swizzled layout of the store, reused once the
-    // previous store has read it.
+    // Warp w holds rows 32 (w % 4) + lane of each 128-row part (TMEM lanes)
+    // and the block row's 64 features (TMEM columns h * 64 ..).  Each store box
+    // goes through the warp's staging buffer in the swizzled layout of the
+    // store, reused once the previous store has read it.
     const int sp = warp & 3;
-    uint8_t *stg = staging + (warp - kEpiWarp0) * kPartBytes;
-    const uint32_t row_sw = static_cast<uint32_t>(lane & 7);
+    uint8_t *stg = staging + (warp - kEpiWarp0) * (32 * T::kBoxBytes);
+    const uint32_t row_sw = static_cast<uint32_t>(T::kBoxBytes == 128 ? lane & 7 : (lane >> 1) & 3);
     uint32_t tcount = 0;
     while (true) {
       const uint32_t buf = tcount % kNbuf;
@@ -438,9 +479,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after_sync();
       const uint32_t tbase = tmem + (static_cast<uint32_t>(sp * 32) << 16) + buf * kAccCols;
 #pragma unroll 1
-      for (int part = 0; part < kParts; ++part) {
-        const int h = part / (kParts / 2);             // half of the tile
-        const int c0 = (part % (kParts / 2)) * kBoxCols;  // first feature of the part
+      for (int box = 0; box < T::kParts * kBoxes; ++box) {
+        const int h = box / kBoxes;               // part of the tile
+        const int c0 = (box % kBoxes) * kBoxCols;  // first feature of the box
         uint8_t *pst = stg;
         if (lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
@@ -456,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!zero) tmem_ld_wait();
-        uint8_t *row = pst + lane * 128;
+        uint8_t *row = pst + lane * T::kBoxBytes;
 #pragma unroll
         for (int g = 0; g < kBoxCols / 16; ++g) {
           if constexpr (OUT_BF16) {
@@ -478,11 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_uint4(v[g][4 * q], v[g][4 * q + 1], v[g][4 * q + 2], v[g][4 * q + 3]);
           }
         }
-        if (part == kParts - 1) tc_fence_before_sync();
+        if (box == T::kParts * kBoxes - 1) tc_fence_before_sync();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (part == kParts - 1) mbar_arrive(acce0 + 8 * buf);
+          if (box == T::kParts * kBoxes - 1) mbar_arrive(acce0 + 8 * buf);
           const int y = n0 + h * 128;
           if (y < p.N && m0 + c0 < p.M) tma_store_2d(&tmY, smem_addr(pst), m0 + c0, y);
           bulk_commit_group();
@@ -501,15 +542,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool IN_BF16, bool OUT_BF16, class Adapters>
+template <bool IN_BF16, bool OUT_BF16, class T, class Adapters>
 cudaError_t launch_linear_variant(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,
                                   const BcsrParams &p, const Adapters &ad, cudaStream_t stream) {
-  auto kern = bcsr_linear_kernel<IN_BF16, OUT_BF16, Adapters>;
+  constexpr int kSmemBytes = T::kSmemBytes;
+  auto kern = bcsr_linear_kernel<IN_BF16, OUT_BF16, T, Adapters>;
   static std::atomic<uint64_t> smem_set{0};
   cudaError_t e = set_smem_limit_once(kern, kSmemBytes, smem_set);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>(p.n_block_rows) * ((p.N + kTileN - 1) / kTileN);
-  const int64_t cap = p.max_ctas > 0 ? p.max_ctas : p.num_sms;
+  const int64_t tiles = static_cast<int64_t>(p.n_block_rows) * ((p.N + T::kRows - 1) / T::kRows);
+  const int64_t cap = p.max_ctas > 0 ? p.max_ctas : static_cast<int64_t>(T::kCtas) * p.num_sms;
   const int64_t grid = tiles < cap ? tiles : cap;
   if constexpr (std::is_same_v<Adapters, LinearAdapters>) {
     // a dependent of the down projection: set up while it ends
@@ -530,28 +572,49 @@ cudaError_t launch_linear_variant(const CUtensorMap &tmA, const CUtensorMap &tmX
   }
 }
 
-template <class Adapters>
+template <class T, class Adapters>
 cudaError_t launch_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY, const BcsrParams &p,
-                          const Adapters &ad, bool in_bf16, bool out_bf16, cudaStream_t stream) {
+                               const Adapters &ad, bool in_bf16, bool out_bf16, cudaStream_t stream) {
   if (p.n_block_rows == 0 || p.N == 0) return cudaSuccess;
   if (in_bf16)
-    return out_bf16 ? launch_linear_variant<true, true>(tmA, tmX, tmY, p, ad, stream)
-                    : launch_linear_variant<true, false>(tmA, tmX, tmY, p, ad, stream);
-  return out_bf16 ? launch_linear_variant<false, true>(tmA, tmX, tmY, p, ad, stream)
-                  : launch_linear_variant<false, false>(tmA, tmX, tmY, p, ad, stream);
+    return out_bf16 ? launch_linear_variant<true, true, T>(tmA, tmX, tmY, p, ad, stream)
+                    : launch_linear_variant<true, false, T>(tmA, tmX, tmY, p, ad, stream);
+  return out_bf16 ? launch_linear_variant<false, true, T>(tmA, tmX, tmY, p, ad, stream)
+                  : launch_linear_variant<false, false, T>(tmA, tmX, tmY, p, ad, stream);
 }
 
 }  // namespace
 
+// The tile with adapters.  GPU times (us) of 256 rows by one CTA per SM / by two /
+// 512 rows:
+//   no more tiles than SMs (300 rows, 3584 x 18944):                    37 /   41 /   48
+//   more segments than row tiles, whose stages hide behind the other
+//   CTA's blocks (777 rows of 8192 x 8192 in 40):                      111 /   92 /  104
+//   (2048 rows, 18944 x 3584, in 128):                                 223 /  141 /  198
+//   fewer, short block rows, many tiles (65536 rows, 18944 x 3584, 9): 1477 / 1386 / 1218
+//   few tiles (2048 rows in 4):                                         83 /   70 /   71
+//   fewer, block rows of 16 blocks or more (16384 rows, 3584 x 18944):  380 /  411 /  390
+LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t N, int64_t n_seg, int num_sms) {
+  const int64_t row_tiles = (N + 255) / 256;
+  if (n_block_rows * row_tiles <= num_sms) return LinearTile::k256;
+  if (n_seg >= row_tiles) return LinearTile::k256x2;
+  if (n_blocks >= 16 * n_block_rows) return LinearTile::k256;
+  return n_block_rows * ((N + 511) / 512) >= 8ll * num_sms ? LinearTile::k512 : LinearTile::k256x2;
+}
+
 cudaError_t launch_bcsr_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,
                                const BcsrParams &p, bool in_bf16, bool out_bf16, cudaStream_t stream) {
-  return launch_linear(tmA, tmX, tmY, p, NoAdapters{}, in_bf16, out_bf16, stream);
+  return launch_linear<Tile<256, 1>>(tmA, tmX, tmY, p, NoAdapters{}, in_bf16, out_bf16, stream);
 }
 
 cudaError_t launch_bcsr_linear_adapters(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,
                                         const BcsrParams &p, const LinearAdapters &ad, bool in_bf16, bool out_bf16,
                                         cudaStream_t stream) {
-  return launch_linear(tmA, tmX, tmY, p, ad, in_bf16, out_bf16, stream);
+  switch (ad.tile) {
+    case LinearTile::k256x2: return launch_linear<Tile<256, 2>>(tmA, tmX, tmY, p, ad, in_bf16, out_bf16, stream);
+    case LinearTile::k512: return launch_linear<Tile<512, 1>>(tmA, tmX, tmY, p, ad, in_bf16, out_bf16, stream);
+    default: return launch_linear<Tile<256, 1>>(tmA, tmX, tmY, p, ad, in_bf16, out_bf16, stream);
+  }
 }
 
 }  // namespace spmm

@@ -95,26 +95,32 @@ cudaError_t launch_bcsr(const CUtensorMap &tmA, const CUtensorMap &tmB, const CU
 // p.B is X (N x K row-major), p.C is Y (N x M row-major).  tmA covers the
 // blocks as for launch_bcsr; tmX covers X as [N rows, K cols] with 256-row x
 // 64-column boxes, 128-byte swizzle; tmY covers Y as [N rows, M cols] with
-// 32-row x 128-byte boxes, 128-byte swizzle.
+// 32-row x 128-byte boxes, 128-byte swizzle (with adapters and tiles of 512 rows,
+// 32-row x 64-byte boxes, 64-byte swizzle).
 cudaError_t launch_bcsr_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,
                                const BcsrParams &p, bool in_bf16, bool out_bf16, cudaStream_t stream);
 
-// Rows of X per tile of that kernel.
-constexpr int kAdapterTileRows = 256;
+// The most rows of X per tile of that kernel; with adapters, its tiles: 256 rows
+// by one CTA per SM (as without adapters) or by two, or 512 rows by one.
+constexpr int kMaxTileRows = 512;
+enum class LinearTile : int32_t { k256, k256x2, k512 };
+LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t N, int64_t n_seg, int num_sms);
+inline int linear_tile_rows(LinearTile t) { return t == LinearTile::k512 ? 512 : 256; }
 // A segment with an adapter among a tile's rows: rows [begin, end) of the tile.
 struct TileSegment {
   int32_t adapter, begin, end, pad_;
 };
 // The adapters of the same product (launch_bcsr_linear_adapters): tmU covers
 // the up matrices as [n_adapters * M rows, rank cols] with 64 x box boxes, tmH
-// covers H as [parts * N rows, rank cols] with 256 x box boxes, both swizzled in
+// covers H as [parts * N rows, rank cols] with 128 x box boxes, both swizzled in
 // the width of a box row; box = 16, 32 or 64 ranks; parts > 1: H is the sum of
 // its parts.
 struct LinearAdapters {
   CUtensorMap tmU, tmH;
-  const TileSegment *tile_segs;  // device, kAdapterTileRows per tile
+  const TileSegment *tile_segs;  // device, the tile's rows per tile
   const int32_t *tile_count;     // device, per tile: its segments with an adapter
   int32_t rank, parts, box;
+  LinearTile tile;
 };
 // Launched as a programmatic dependent of the kernel that writes H and the
 // tile lists.
@@ -270,6 +276,7 @@ struct AdapterDownParams {
   const int32_t *seg_adapter;
   int32_t n_seg, n_adapters, rank, parts;
   int32_t N, K;
+  int32_t tile_rows;             // rows per tile of the lists
   int32_t split, q;              // filled in by the launch: CTAs per tile, stages
   uint32_t *status;
   uint64_t wait_limit_ns;

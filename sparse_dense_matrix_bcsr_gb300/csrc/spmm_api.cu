@@ -85,17 +85,19 @@ spmm_status encode_x(CUtensorMap *map, const void *base, bool bf16, uint64_t row
 }
 
 // Y of the linear-layer product as a TMA destination: N rows x m columns of
-// bf16 or fp32, 32-row x 128-byte boxes, 128-byte swizzle.
-spmm_status encode_y(CUtensorMap *map, void *base, bool bf16, uint64_t rows, uint64_t cols) {
+// bf16 or fp32, 32-row boxes of 128 bytes (tiles of 256 rows) or 64 bytes (tiles
+// of 512), swizzled in that width.
+spmm_status encode_y(CUtensorMap *map, void *base, bool bf16, uint64_t rows, uint64_t cols, int tile_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(SPMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const uint64_t esz = bf16 ? 2 : 4;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols * esz};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esz), 32u};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>((tile_rows == 512 ? 64 : 128) / esz), 32u};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims,
-                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  tile_rows == 512 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SPMM_ERR_CUDA, "cuTensorMapEncodeTiled (Y) failed (%d)", static_cast<int>(r));
   return SPMM_OK;
@@ -647,7 +649,7 @@ spmm_status spmm_run_linear(spmm_handle h, const void *X, void *Y, int64_t N, vo
     h->nx_cached = N;
   }
   if (h->y_cached != Y || h->ny_cached != N) {
-    st = encode_y(&h->tm_Y, Y, out_bf16, static_cast<uint64_t>(N), static_cast<uint64_t>(h->m));
+    st = encode_y(&h->tm_Y, Y, out_bf16, static_cast<uint64_t>(N), static_cast<uint64_t>(h->m), 256);
     if (st != SPMM_OK) return st;
     h->y_cached = Y;
     h->ny_cached = N;

@@ -195,6 +195,9 @@ SHAPES = [
     pytest.param(256, 256, 513, ([0, 255, 256, 257, 512, 513], [0, 1, 2, 0, 1]), 32, 3, "bf16", "bf16", id="tile-edges"),
     pytest.param(192, 8, 260, ragged(260, 4, 2), 16, 2, "bf16", "f32", id="k-8"),
     pytest.param(8, 192, 130, ragged(130, 4, 2), 16, 2, "bf16", "bf16", id="m-8"),
+    # enough block rows and rows for the projection's tiles of 512 rows
+    pytest.param(8200, 72, 5300, ragged(5300, 9, 4), 16, 4, "bf16", "bf16", id="tiles-of-512"),
+    pytest.param(8192, 72, 5300, ragged(5300, 40, 5, gaps=True), 72, 5, "f16", "f32", id="tiles-of-512-f32-rank-72"),
 ]
 
 
