@@ -5,8 +5,8 @@
 //
 // Work unit = the part of a 128-row tile that lies in one segment: the tile's
 // rows of X are the M operand and the adapter's ranks the N operand (D_a's rows),
-// both K-major as they lie in memory; one stage is 64 columns of both, two TMA
-// boxes.  Rows of the tile outside the segment run along and are not stored, so
+// both K-major as they lie in memory (the gradient's dY U_a takes U_a as it lies
+// too, MN-major); one stage is 64 columns of both.  Rows of the tile outside the segment run along and are not stored, so
 // every row meets its own adapter alone; a tile that several segments share is
 // read once per segment, from L2.  2 N r k FLOP against 2 N k bytes are far below
 // the tensor rate, so HBM bounds it for prompts.  Few units leave SMs idle: a
@@ -14,6 +14,9 @@
 // through distributed shared memory in CTA order (no atomics, no second launch).
 // One CTA per tile that walked the tile's segments one after another took 56
 // against 20 us for 777 rows in 40 segments (8192 columns, rank 64).
+//
+// The gradient wants two such products of a batch, of X and of dY: one launch
+// runs both, so that short batches fill the GPU with their sum.
 //
 // Where the projection's output is fp32, H is kept as two 16-bit parts (the
 // value rounded, and the rest rounded), which holds 16 (bf16) or 22 (fp16) bits.
@@ -36,7 +39,12 @@ constexpr int kMiscBytes = 1024;
 constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
 
 __host__ __device__ constexpr int rank16(int rank) { return (rank + 15) / 16 * 16; }
-__host__ __device__ constexpr int d_bytes(int rank) { return (rank16(rank) * 128 + 1023) / 1024 * 1024; }
+// D's part of a stage: rank rows of 64 columns, or (transposed, never less) 64
+// rows of 64 ranks per box.
+__host__ __device__ constexpr int d_boxes(int rank) { return (rank + 63) / 64; }
+__host__ __device__ constexpr int d_bytes(int rank, bool transposed) {
+  return transposed ? d_boxes(rank) * 8192 : (rank16(rank) * 128 + 1023) / 1024 * 1024;
+}
 __host__ __device__ constexpr int part_pitch(int rank) { return rank16(rank) + 4; }  // floats per row of the CTA's sums
 
 struct Misc {
@@ -79,15 +87,17 @@ __device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int64_t N, int
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 2)
-    adapter_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmD,
-                        const AdapterDownParams p) {
+__global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_constant__ AdapterDownParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int stage_bytes = kXBytes + d_bytes(p.rank);
+  const int32_t part = blockIdx.x % p.split;  // rank in the cluster
+  const bool second = static_cast<int32_t>(blockIdx.x / p.split) >= p.units;
+  const int32_t unit = blockIdx.x / p.split - (second ? p.units : 0);
+  const AdapterDownJob &job = p.job[second ? 1 : 0];
+  const bool transposed = job.transposed != 0;
+  const int stage_bytes = p.stage_bytes;
   Misc *mi = reinterpret_cast<Misc *>(smem + p.q * stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t unit = blockIdx.x / p.split, part = blockIdx.x % p.split;  // part = rank in the cluster
   const int n16 = rank16(p.rank);
   uint32_t tmem_cols = 32;
   while (static_cast<int>(tmem_cols) < n16) tmem_cols <<= 1;
@@ -101,8 +111,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(smem_addr(&mi->acc_full), 1);
       mi->abort_flag = 0;
       fence_barrier_init();
-      tma_prefetch_desc(&tmX);
-      tma_prefetch_desc(&tmD);
+      tma_prefetch_desc(&job.tmX);
+      tma_prefetch_desc(&job.tmD);
     }
     __syncwarp();
     const RowPiece r = find_piece(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, kRows, p.N, unit, p.status);
@@ -110,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(&mi->tmem), tmem_cols);
     tmem_relinquish();
-  } else if (warp == kEpiWarp0 && part == 0 && static_cast<int64_t>(unit) * p.tile_rows < p.N) {
+  } else if (warp == kEpiWarp0 && part == 0 && !second && static_cast<int64_t>(unit) * p.tile_rows < p.N) {
     // the projection's own tiles: their segments, for its producers
     const int64_t tile0 = static_cast<int64_t>(unit) * p.tile_rows;
     const int32_t c = list_segments(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, tile0,
@@ -124,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = mi->tmem;
   const RowPiece piece = mi->piece;
   const int64_t row0 = static_cast<int64_t>(piece.tile) * kRows;
-  const int32_t nk = (p.K + 63) / 64;
+  const int32_t nk = (job.K + 63) / 64;
   const int32_t k_begin = static_cast<int32_t>(static_cast<int64_t>(nk) * part / p.split);
   const int32_t k_end = static_cast<int32_t>(static_cast<int64_t>(nk) * (part + 1) / p.split);
 
@@ -140,9 +150,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) {
           const uint32_t fb = smem_addr(&mi->full[stage]);
           const uint32_t st = smem_addr(smem + stage * stage_bytes);
-          mbar_arrive_expect_tx(fb, kXBytes + p.rank * 128);
-          tma_load_2d(st, &tmX, fb, c * 64, static_cast<int32_t>(row0));
-          tma_load_2d(st + kXBytes, &tmD, fb, c * 64, piece.adapter * p.rank);
+          mbar_arrive_expect_tx(fb, kXBytes + (transposed ? d_boxes(p.rank) * 8192 : p.rank * 128));
+          tma_load_2d(st, &job.tmX, fb, c * 64, static_cast<int32_t>(row0));
+          if (transposed)
+            for (int b = 0; b < d_boxes(p.rank); ++b)
+              tma_load_3d(st + kXBytes + b * 8192, &job.tmD, fb, b * 64, c * 64, piece.adapter);
+          else
+            tma_load_2d(st + kXBytes, &job.tmD, fb, c * 64, piece.adapter * p.rank);
         }
         __syncwarp();
         ++seq;
@@ -159,7 +173,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           mbar_wait(smem_addr(&mi->full[i % p.q]), static_cast<uint32_t>((i / p.q) & 1), 1000000ull);
       }
     } else if (warp == kMmaWarp) {
-      const uint32_t idesc = idesc_f16(BF16, false, false, kRows, static_cast<uint32_t>(n16));
+      const uint32_t idesc = idesc_f16(BF16, false, transposed, kRows, static_cast<uint32_t>(n16));
+      const uint32_t lbo = transposed ? 8192 : 16, step = transposed ? 2048 : 32;  // D: groups of 64 ranks, 16 columns
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       for (int32_t c = k_begin; c < k_end; ++c) {
@@ -169,10 +184,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc_fence_after_sync();
         const uint32_t st = smem_addr(smem + stage * stage_bytes);
         const uint64_t x = smem_desc_sw128(st, 16, 1024);
-        const uint64_t d = smem_desc_sw128(st + kXBytes, 16, 1024);
+        const uint64_t d = smem_desc_sw128(st + kXBytes, lbo, 1024);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_f16_elect(tmem, smem_desc_add(x, kk * 32), smem_desc_add(d, kk * 32), idesc,
+          umma_f16_elect(tmem, smem_desc_add(x, kk * 32), smem_desc_add(d, kk * step), idesc,
                          (c == k_begin && kk == 0) ? 0u : 1u);
         umma_commit_elect(smem_addr(&mi->empty[stage]));
         if (++stage == static_cast<uint32_t>(p.q)) {
@@ -216,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             float o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = f * __uint_as_float(v[8 * h + i]);
-            store_h<BF16>(p.H, row0 + r, p.N, p.rank, c0 + 8 * h, p.parts, o);
+            store_h<BF16>(job.H, row0 + r, p.N, p.rank, c0 + 8 * h, job.parts, o);
           }
         }
       }
@@ -243,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] *= f;
-        store_h<BF16>(p.H, row0 + r, p.N, p.rank, j, p.parts, o);
+        store_h<BF16>(job.H, row0 + r, p.N, p.rank, j, job.parts, o);
       }
     }
     cluster_sync();  // the others may still read this CTA's sums
@@ -258,25 +273,31 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 }  // namespace
 
-cudaError_t launch_adapter_down(const CUtensorMap &tmX, const CUtensorMap &tmD, AdapterDownParams p, int num_sms, bool bf16,
-                                cudaStream_t s) {
+cudaError_t launch_adapter_down(AdapterDownParams p, int num_sms, bool bf16, cudaStream_t s) {
   // units: see find_piece; about as many have rows
   const int64_t units = (static_cast<int64_t>(p.N) + kRows - 1) / kRows + p.n_seg;
-  const int nk = (p.K + 63) / 64;
+  int32_t k = p.job[0].K;
+  bool transposed = p.job[0].transposed != 0;
+  if (p.jobs > 1) {
+    k = k < p.job[1].K ? k : p.job[1].K;
+    transposed = transposed || p.job[1].transposed != 0;
+  }
+  const int nk = (k + 63) / 64;
   // as many CTAs per unit (a cluster) as keep the grid within two per SM, with
   // at least four stages each
+  p.units = static_cast<int32_t>(units);
   p.split = 1;
-  while (p.split < 8 && units * p.split * 2 <= 2ll * num_sms && nk >= 8 * p.split) p.split *= 2;
-  const int stage = kXBytes + d_bytes(p.rank);
-  p.q = (kSmemLimit - kMiscBytes - 1024) / stage;
+  while (p.split < 8 && p.jobs * units * p.split * 2 <= 2ll * num_sms && nk >= 8 * p.split) p.split *= 2;
+  p.stage_bytes = kXBytes + d_bytes(p.rank, transposed);
+  p.q = (kSmemLimit - kMiscBytes - 1024) / p.stage_bytes;
   if (p.q > kMaxQ) p.q = kMaxQ;
-  const int smem = p.q * stage + kMiscBytes + 1024;
+  const int smem = p.q * p.stage_bytes + kMiscBytes + 1024;
   auto kern = bf16 ? adapter_down_kernel<true> : adapter_down_kernel<false>;
   static std::atomic<uint64_t> smem_set[2];
   cudaError_t e = set_smem_limit_once(kern, kSmemLimit, smem_set[bf16 ? 1 : 0]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * p.split));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.jobs * units * p.split));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -287,7 +308,7 @@ cudaError_t launch_adapter_down(const CUtensorMap &tmX, const CUtensorMap &tmD, 
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tmX, tmD, p);
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace spmm

@@ -110,22 +110,6 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_rows_kernel(const Adapt
   }
 }
 
-// ---------------------------------------------------------------- adapter weights, transposed
-// out[a][c][r] = in[a][r][c]: the gradient runs the forward kernels with the
-// roles of D and U exchanged, which want both in the other order.
-__global__ void __launch_bounds__(256) transpose_kernel(const uint16_t *__restrict__ in, uint16_t *__restrict__ out,
-                                                        int32_t rows, int32_t cols) {
-  __shared__ uint16_t tile[32][33];
-  const int64_t base = static_cast<int64_t>(blockIdx.z) * rows * cols;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int c0 = blockIdx.x * 32, r0 = blockIdx.y * 32;
-  for (int i = ty; i < 32; i += 8)
-    if (r0 + i < rows && c0 + tx < cols) tile[i][tx] = in[base + static_cast<int64_t>(r0 + i) * cols + c0 + tx];
-  __syncthreads();
-  for (int i = ty; i < 32; i += 8)
-    if (c0 + i < cols && r0 + tx < rows) out[base + static_cast<int64_t>(c0 + i) * rows + r0 + tx] = tile[tx][i];
-}
-
 }  // namespace
 
 cudaError_t launch_shrink(const AdapterParams &p, bool bf16, cudaStream_t s) {
@@ -134,12 +118,6 @@ cudaError_t launch_shrink(const AdapterParams &p, bool bf16, cudaStream_t s) {
     shrink_rows_kernel<true><<<grid, kShrinkThreads, 0, s>>>(p);
   else
     shrink_rows_kernel<false><<<grid, kShrinkThreads, 0, s>>>(p);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_transpose(const void *in, void *out, int32_t n, int32_t rows, int32_t cols, cudaStream_t s) {
-  const dim3 grid((cols + 31) / 32, (rows + 31) / 32, n);
-  transpose_kernel<<<grid, 256, 0, s>>>(static_cast<const uint16_t *>(in), static_cast<uint16_t *>(out), rows, cols);
   return cudaGetLastError();
 }
 

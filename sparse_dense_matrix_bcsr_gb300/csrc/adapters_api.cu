@@ -25,8 +25,6 @@ struct spmm_adapters_s {
 
   float *d_h = nullptr;        // max_rows x rank: scale * D x, or as many values in two 16-bit parts
   float *d_dh = nullptr;       // gradient: max_rows x rank: scale * U^T dy
-  uint16_t *d_down_t = nullptr;  // gradient: n_adapters x k x rank
-  uint16_t *d_up_t = nullptr;    // gradient: n_adapters x rank x m
   spmm::TileSegment *d_tile_segs = nullptr;  // the projection's row tiles: their segments with an adapter
   int32_t *d_tile_count = nullptr;
 };
@@ -37,8 +35,6 @@ void free_adapters(spmm_adapters a) {
   if (!a) return;
   cudaFree(a->d_h);
   cudaFree(a->d_dh);
-  cudaFree(a->d_down_t);
-  cudaFree(a->d_up_t);
   cudaFree(a->d_tile_segs);
   cudaFree(a->d_tile_count);
   delete a;
@@ -100,17 +96,34 @@ spmm::AdapterParams make_params(spmm_handle h, spmm_adapters a, int64_t N, const
   return p;
 }
 
-// H = scale * X D^T in 16 bits (`parts` of them), with the projection's tile lists.
-spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, int parts, int tile_rows, cudaStream_t s) {
+// One product of down_project: H = scale * X D^T in 16 bits (`parts` of them), D
+// n_adapters x rank x K, or transposed n_adapters x K x rank.
+struct DownJob {
+  const void *X, *D;
+  float *H;
+  int64_t K;
+  int parts;
+  bool transposed;
+};
+
+// One or two such products, with the lists of the projection's tiles.
+spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, std::initializer_list<DownJob> jobs, int tile_rows,
+                         cudaStream_t s) {
   const bool bf16 = a->in_t == SPMM_BF16;
-  CUtensorMap tmX, tmD;
-  spmm_status st = spmm::encode_2d(&tmX, p.X, bf16, p.N, p.K, p.K, 128, 64);
-  if (st != SPMM_OK) return st;
-  st = spmm::encode_2d(&tmD, p.down, bf16, static_cast<uint64_t>(p.n_adapters) * p.rank, p.K, p.K, p.rank, 64);
-  if (st != SPMM_OK) return st;
   spmm::AdapterDownParams d;
   std::memset(&d, 0, sizeof d);
-  d.H = reinterpret_cast<uint16_t *>(p.H);
+  for (const DownJob &j : jobs) {
+    spmm::AdapterDownJob &o = d.job[d.jobs++];
+    spmm_status st = spmm::encode_2d(&o.tmX, j.X, bf16, p.N, j.K, j.K, 128, 64);
+    if (st != SPMM_OK) return st;
+    st = j.transposed ? spmm::encode_3d(&o.tmD, j.D, bf16, p.n_adapters, j.K, p.rank, 64)
+                      : spmm::encode_2d(&o.tmD, j.D, bf16, static_cast<uint64_t>(p.n_adapters) * p.rank, j.K, j.K, p.rank, 64);
+    if (st != SPMM_OK) return st;
+    o.H = reinterpret_cast<uint16_t *>(j.H);
+    o.K = static_cast<int32_t>(j.K);
+    o.parts = j.parts;
+    o.transposed = j.transposed ? 1 : 0;
+  }
   d.tile_segs = a->d_tile_segs;
   d.tile_count = a->d_tile_count;
   d.scale = p.scale;
@@ -119,26 +132,26 @@ spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, int part
   d.n_seg = p.n_seg;
   d.n_adapters = p.n_adapters;
   d.rank = p.rank;
-  d.parts = parts;
   d.N = p.N;
-  d.K = p.K;
   d.tile_rows = tile_rows;
   d.status = p.status;
   d.wait_limit_ns = p.wait_limit_ns;
-  CUDA_TRY(spmm::launch_adapter_down(tmX, tmD, d, p.num_sms, bf16, s), "adapter down projection launch");
+  CUDA_TRY(spmm::launch_adapter_down(d, p.num_sms, bf16, s), "adapter down projection launch");
   return SPMM_OK;
 }
 
-// Y = X W^T + U H per row, H and the tile lists from down_project.
-spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams &p, int parts, spmm::LinearTile tile,
-                       cudaStream_t s) {
+// Y = X W^T + U H per row, H and the tile lists from down_project; U n_adapters x
+// M x rank, or transposed n_adapters x rank x M.
+spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams &p, int parts, bool transposed,
+                       spmm::LinearTile tile, cudaStream_t s) {
   const bool bf16 = h->in_t == SPMM_BF16, out_bf16 = h->out_t == SPMM_BF16;
   CUtensorMap tmX, tmY;
   spmm::LinearAdapters ad;
   ad.box = p.rank <= 16 ? 16 : p.rank <= 32 ? 32 : 64;
   spmm_status st = spmm::encode_x(&tmX, p.X, bf16, p.N, p.K);
   if (st == SPMM_OK) st = spmm::encode_y(&tmY, p.Y, out_bf16, p.N, p.M, spmm::linear_tile_rows(tile));
-  if (st == SPMM_OK)
+  if (st == SPMM_OK && transposed) st = spmm::encode_3d(&ad.tmU, p.up, bf16, p.n_adapters, p.rank, p.M, ad.box);
+  if (st == SPMM_OK && !transposed)
     st = spmm::encode_2d(&ad.tmU, p.up, bf16, static_cast<uint64_t>(p.n_adapters) * p.M, p.rank, p.rank, 64, ad.box,
                          ad.box * 2);
   if (st == SPMM_OK)
@@ -149,6 +162,7 @@ spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams
   ad.tile_count = a->d_tile_count;
   ad.rank = p.rank;
   ad.parts = parts;
+  ad.u_transposed = transposed ? 1 : 0;
   ad.tile = tile;
   spmm::BcsrParams b;
   std::memset(&b, 0, sizeof b);
@@ -185,23 +199,22 @@ bool rows_path(int64_t N, int32_t rank, int64_t n_seg) {
   return N <= kMostRows && N * (rank + 24) < 2300 + 290 * n_seg;
 }
 
-// Y = X W^T + adapters, with D rank x K and U M x rank per adapter; tiled: by the
-// tensor-core kernels, which leave H in 16 bits.
+// Y = X W^T + adapters.
 spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const void *X, void *Y, const void *down,
-                    const void *up, float *H, bool tiled, cudaStream_t s) {
+                    const void *up, cudaStream_t s) {
   const bool bf16 = h->in_t == SPMM_BF16;
   p.X = X;
   p.Y = Y;
-  p.H = H;
+  p.H = a->d_h;
   p.down = down;
   p.up = up;
   p.M = static_cast<int32_t>(h->m);
   p.K = static_cast<int32_t>(h->k);
-  if (tiled) {
+  if (!rows_path(p.N, p.rank, p.n_seg)) {
     const int parts = h->out_t == SPMM_F32 ? 2 : 1;
     const spmm::LinearTile tile = spmm::linear_adapters_tile(h->n_groups, h->n_units, p.N, p.n_seg, p.num_sms);
-    const spmm_status st = down_project(a, p, parts, spmm::linear_tile_rows(tile), s);
-    return st != SPMM_OK ? st : up_project(h, a, p, parts, tile, s);
+    const spmm_status st = down_project(a, p, {{X, down, a->d_h, p.K, parts, false}}, spmm::linear_tile_rows(tile), s);
+    return st != SPMM_OK ? st : up_project(h, a, p, parts, false, tile, s);
   }
   spmm::AdapterDecodeParams d;
   std::memset(&d, 0, sizeof d);
@@ -272,11 +285,7 @@ spmm_status spmm_adapters_create(spmm_adapters *out, int64_t m, int64_t k, int32
     const size_t rows = (static_cast<size_t>(max_rows) / spmm::kMaxTileRows + 1) * spmm::kMaxTileRows;
     CUDA_TRY(cudaMalloc(&a->d_tile_segs, rows * sizeof(spmm::TileSegment)), "cudaMalloc(tile segments)");
     CUDA_TRY(cudaMalloc(&a->d_tile_count, rows / 256 * sizeof(int32_t)), "cudaMalloc(tile counts)");
-    if (a->grad) {
-      CUDA_TRY(cudaMalloc(&a->d_dh, h), "cudaMalloc(adapter gradients)");
-      CUDA_TRY(cudaMalloc(&a->d_down_t, static_cast<size_t>(n_adapters) * k * rank * 2), "cudaMalloc(transposed down)");
-      CUDA_TRY(cudaMalloc(&a->d_up_t, static_cast<size_t>(n_adapters) * m * rank * 2), "cudaMalloc(transposed up)");
-    }
+    if (a->grad) CUDA_TRY(cudaMalloc(&a->d_dh, h), "cudaMalloc(adapter gradients)");
     return SPMM_OK;
   };
   const spmm_status st = setup();
@@ -306,8 +315,7 @@ spmm_status spmm_run_linear_adapters(spmm_handle h, spmm_adapters a, const void 
   if (N == 0) return SPMM_OK;
   if (!X || !Y) return fail(SPMM_ERR_INVALID_ARG, "X or Y is NULL");
   if (misaligned({X, Y, down, up})) return fail(SPMM_ERR_UNSUPPORTED, "X, Y, down and up must be 16-byte aligned");
-  return project(h, a, make_params(h, a, N, scale, seg_ptr, seg_adapter, n_seg), X, Y, down, up, a->d_h,
-                 !rows_path(N, a->rank, n_seg),
+  return project(h, a, make_params(h, a, N, scale, seg_ptr, seg_adapter, n_seg), X, Y, down, up,
                  static_cast<cudaStream_t>(stream));
 }
 
@@ -332,22 +340,20 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
     CUDA_TRY(cudaMemsetAsync(d_down, 0, bytes * k, s), "clear d_down");
     return SPMM_OK;
   }
-  CUDA_TRY(spmm::launch_transpose(up, a->d_up_t, a->n_adapters, m, a->rank, s), "adapter transpose launch");
-  CUDA_TRY(spmm::launch_transpose(down, a->d_down_t, a->n_adapters, a->rank, k, s), "adapter transpose launch");
-  p.X = X;
-  p.K = k;
-  p.down = down;
-  p.H = a->d_h;
-  st = down_project(a, p, 1, spmm::kMaxTileRows, s);
-  if (st != SPMM_OK) return st;
-  if (dX) {
-    st = project(h_t, a, p, dY, dX, a->d_up_t, a->d_down_t, a->d_dh, true, s);
-  } else {
+  // H and dH, then dX with the roles of the adapters' two matrices exchanged
+  const int parts = dX && h_t->out_t == SPMM_F32 ? 2 : 1;
+  const spmm::LinearTile tile = spmm::linear_adapters_tile(h_t->n_groups, h_t->n_units, p.N, p.n_seg, p.num_sms);
+  const DownJob of_x{X, down, a->d_h, k, 1, false}, of_dy{dY, up, a->d_dh, m, parts, true};
+  st = m > k ? down_project(a, p, {of_dy, of_x}, spmm::linear_tile_rows(tile), s)  // the longer first
+             : down_project(a, p, {of_x, of_dy}, spmm::linear_tile_rows(tile), s);
+  if (st == SPMM_OK && dX) {
     p.X = dY;
-    p.K = m;
-    p.down = a->d_up_t;
+    p.Y = dX;
     p.H = a->d_dh;
-    st = down_project(a, p, 1, spmm::kMaxTileRows, s);
+    p.up = down;
+    p.M = k;
+    p.K = m;
+    st = up_project(h_t, a, p, parts, true, tile, s);
   }
   spmm::AdapterWgradParams w;
   if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dy, dY, bf16, N, m, m, 64, 64);

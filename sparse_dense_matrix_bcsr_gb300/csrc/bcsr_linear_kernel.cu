@@ -36,11 +36,12 @@
 // rows of U_a as the N operand and the tile's rows of H as the M operand, 64
 // ranks a stage (H in one 16-bit part; in two parts, a stage takes both parts of
 // half the tile, so a segment within a half costs one stage either way).  Their
-// MMAs update the segment's lanes only (the MMA's lane
-// mask), so the other rows' sums do not see the product at all: no zeroed copy
-// of H, and an adapter with infinities cannot reach other rows as 0 * inf.  The
-// product with adapters reads X and writes Y once; a second pass over Y would
-// move 5 GB more for 64K tokens x 18944 features.
+// MMAs update the segment's lanes only (the MMA's lane mask), so the other rows'
+// sums do not see the product at all: no zeroed copy of H, and an adapter with
+// infinities cannot reach other rows as 0 * inf.  The product with adapters reads
+// X and writes Y once; a second pass over Y would move 5 GB more for 64K tokens x
+// 18944 features.  The gradient's dX takes D_a where the forward pass takes U_a,
+// as it lies (MN-major).
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -295,7 +296,10 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
                     const uint32_t st = smem_addr(smem + stage * kStageBytes);
                     const uint32_t part_bytes = 128 * ad.box * 2;
                     mbar_arrive_expect_tx(fb, kBlk * ad.box * 2 + (h1 - h0) * ad.parts * part_bytes);
-                    tma_load_2d(st, &ad.tmU, fb, r0, a * p.M + br * kBlk);
+                    if (ad.u_transposed)
+                      tma_load_3d(st, &ad.tmU, fb, br * kBlk, r0, a);
+                    else
+                      tma_load_2d(st, &ad.tmU, fb, r0, a * p.M + br * kBlk);
                     for (int q = 0; q < ad.parts; ++q)
                       for (int h = h0; h < h1; ++h)
                         tma_load_2d(st + kBlkBytes + (q * group + h - g) * part_bytes, &ad.tmH, fb, r0,
@@ -343,10 +347,15 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
     const uint64_t x_desc = smem_desc_sw128(smem_addr(smem) + kBlkBytes, 16, 1024);
     // An adapter's operands lie in the same places, in rows of ad.box ranks.
     uint64_t u_desc = 0, h_desc = 0;
-    uint32_t h_part = 0;
+    uint32_t h_part = 0, u_step = 32, u_idesc = idesc;
     if constexpr (kAdapt) {
       h_part = 128 * ad.box * 2;
       u_desc = smem_desc_k_major(smem_addr(smem), ad.box * 2);
+      if (ad.u_transposed) {  // rows of 64 features, one per rank
+        u_desc = smem_desc_sw128(smem_addr(smem), 16, 1024);
+        u_step = 16 * 128;
+        u_idesc = idesc_f16(IN_BF16, false, /*b_mn_major=*/true, 128, kBlk);
+      }
       h_desc = smem_desc_k_major(smem_addr(smem) + kBlkBytes, ad.box * 2);
     }
     while (true) {
@@ -405,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
                 for (int i = 0; i < T::kParts; ++i) {  // slot i: part i of H, or of its second 16 bits
                   const int h = seg.part + (i < group ? i : i - group);
                   umma_f16_elect(acc + h * kBlk, smem_desc_add(adesc0, i * h_part + kk * 32),
-                                 smem_desc_add(bdesc0, kk * 32), idesc, 1u);
+                                 smem_desc_add(bdesc0, kk * u_step), u_idesc, 1u);
                 }
               }
             } else {
@@ -417,8 +426,8 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
                 for (int q = 0; q < ad.parts; ++q) {
                   const uint64_t adesc = smem_desc_add(adesc0, (q * group + i) * h_part);
                   for (int kk = 0; kk < seg.stages; ++kk)
-                    umma_f16_lanes_elect(acc + h * kBlk, smem_desc_add(adesc, kk * 32), smem_desc_add(bdesc0, kk * 32),
-                                         idesc, 1u, off);
+                    umma_f16_lanes_elect(acc + h * kBlk, smem_desc_add(adesc, kk * 32), smem_desc_add(bdesc0, kk * u_step),
+                                         u_idesc, 1u, off);
                 }
               }
             }

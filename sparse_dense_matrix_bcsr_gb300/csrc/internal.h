@@ -111,7 +111,9 @@ struct TileSegment {
   int32_t adapter, begin, end, pad_;
 };
 // The adapters of the same product (launch_bcsr_linear_adapters): tmU covers
-// the up matrices as [n_adapters * M rows, rank cols] with 64 x box boxes, tmH
+// the up matrices as [n_adapters * M rows, rank cols] with 64 x box boxes (or,
+// u_transposed, matrices of [n_adapters, rank rows, M cols] with box x 64 boxes,
+// 128-byte swizzle), tmH
 // covers H as [parts * N rows, rank cols] with 128 x box boxes, both swizzled in
 // the width of a box row; box = 16, 32 or 64 ranks; parts > 1: H is the sum of
 // its parts.
@@ -120,6 +122,7 @@ struct LinearAdapters {
   const TileSegment *tile_segs;  // device, the tile's rows per tile
   const int32_t *tile_count;     // device, per tile: its segments with an adapter
   int32_t rank, parts, box;
+  int32_t u_transposed;          // the gradient's: the adapters' down matrices
   LinearTile tile;
 };
 // Launched as a programmatic dependent of the kernel that writes H and the
@@ -264,25 +267,29 @@ struct AdapterParams {
 };
 
 // H on the tensor cores (adapter_down_kernel.cu) and the projection's tile
-// lists.  tmX covers X as [N rows, K cols] with 128 x 64 boxes, tmD the down
-// matrices as [n_adapters * rank rows, K cols] with rank x 64 boxes, both
-// 128-byte swizzle.
-struct AdapterDownParams {
+// lists; up to two such products of the same batch in one launch.
+struct AdapterDownJob {
+  CUtensorMap tmX;               // X as [N rows, K cols], 128 x 64 boxes, 128-byte swizzle
+  CUtensorMap tmD;               // the down matrices as [n_adapters * rank rows, K cols], rank x 64 boxes, 128-byte
+                                 // swizzle; transposed: as [n_adapters, K rows, rank cols], 64 x 64 boxes
   uint16_t *H;                   // device, parts x N x rank: the rows of segments with an adapter
+  int32_t K, parts, transposed;
+};
+struct AdapterDownParams {
+  AdapterDownJob job[2];
   TileSegment *tile_segs;
   int32_t *tile_count;
   const float *scale;
   const int64_t *seg_ptr;
   const int32_t *seg_adapter;
-  int32_t n_seg, n_adapters, rank, parts;
-  int32_t N, K;
+  int32_t n_seg, n_adapters, rank, N;
   int32_t tile_rows;             // rows per tile of the lists
-  int32_t split, q;              // filled in by the launch: CTAs per tile, stages
+  int32_t jobs;
+  int32_t units, split, q, stage_bytes;  // filled in by the launch: units per job, CTAs per unit, stages
   uint32_t *status;
   uint64_t wait_limit_ns;
 };
-cudaError_t launch_adapter_down(const CUtensorMap &tmX, const CUtensorMap &tmD, AdapterDownParams p, int num_sms, bool bf16,
-                                cudaStream_t s);
+cudaError_t launch_adapter_down(AdapterDownParams p, int num_sms, bool bf16, cudaStream_t s);
 
 // H = scale * X D^T in fp32 of the rows with an adapter (other rows of H are
 // left alone), for few rows per adapter (adapters.cu).
@@ -309,9 +316,6 @@ struct AdapterDecodeParams {
 };
 cudaError_t launch_adapter_decode(const CUtensorMap &tmA, const CUtensorMap &tmX, AdapterDecodeParams p, int num_sms,
                                   bool bf16, bool out_bf16, cudaStream_t s);
-
-// n matrices of rows x cols 16-bit elements, each transposed.
-cudaError_t launch_transpose(const void *in, void *out, int32_t n, int32_t rows, int32_t cols, cudaStream_t s);
 
 // Gradients of the adapters' weights (adapter_wgrad_kernel.cu).  tm_dy and tm_x
 // cover dY [N rows, M cols] and X [N rows, K cols], tm_h and tm_dh H and dH
