@@ -112,34 +112,42 @@ struct Adders {
       u.w[i] = c < chunks && f < feats ? __ldg(U + f * chunks + c) : make_uint4(0, 0, 0, 0);
     }
   }
-  __device__ __forceinline__ void add(int32_t v, const Unit &u, const float *__restrict__ h, float *__restrict__ y) const {
-    const TileSegment s = piece(v);
-    float uf[kPasses][8];
+  // ROWS rows of the piece from row n on: U is unpacked once for them.
+  template <int ROWS>
+  __device__ __forceinline__ void add_rows(int32_t v, const Unit &u, const float *__restrict__ h, float *__restrict__ y,
+                                           int n) const {
+    float hv[ROWS][8] = {}, d[ROWS][kPasses];
+    if (c < chunks) {
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) unpack8<BF16>(u.w[i], uf[i]);
-    for (int n = s.begin; n < s.end; ++n) {
-      float hv[8] = {};
-      if (c < chunks) {
-        const float4 *src = reinterpret_cast<const float4 *>(h + n * p.rank) + c * 2;
+      for (int r = 0; r < ROWS; ++r) {
+        const float4 *src = reinterpret_cast<const float4 *>(h + (n + r) * p.rank) + c * 2;
         const float4 a = src[0], b = src[1];
-        hv[0] = a.x, hv[1] = a.y, hv[2] = a.z, hv[3] = a.w, hv[4] = b.x, hv[5] = b.y, hv[6] = b.z, hv[7] = b.w;
+        hv[r][0] = a.x, hv[r][1] = a.y, hv[r][2] = a.z, hv[r][3] = a.w;
+        hv[r][4] = b.x, hv[r][5] = b.y, hv[r][6] = b.z, hv[r][7] = b.w;
       }
-      float d[kPasses];
+    }
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        d[i] = uf[i][0] * hv[0];
+    for (int i = 0; i < kPasses; ++i) {
+      float uf[8];
+      unpack8<BF16>(u.w[i], uf);
 #pragma unroll
-        for (int e = 1; e < 8; ++e) d[i] = fmaf(uf[i][e], hv[e], d[i]);
+      for (int r = 0; r < ROWS; ++r) {
+        d[r][i] = uf[0] * hv[r][0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) d[r][i] = fmaf(uf[e], hv[r][e], d[r][i]);
       }
-      float *row = y + n * kPitch;
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      float *row = y + (n + r) * kPitch;
       if constexpr (SPAN == 1) {
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) row[feature(v, i)] += d[i];
+        for (int i = 0; i < kPasses; ++i) row[feature(v, i)] += d[r][i];
       } else {
         // the lanes of a feature add up and share the passes out between them
         const bool up = (c & (SPAN / 2)) != 0;
-        float e0 = (up ? d[2] : d[0]) + __shfl_xor_sync(0xffffffffu, up ? d[0] : d[2], SPAN / 2);
-        float e1 = (up ? d[3] : d[1]) + __shfl_xor_sync(0xffffffffu, up ? d[1] : d[3], SPAN / 2);
+        const float e0 = (up ? d[r][2] : d[r][0]) + __shfl_xor_sync(0xffffffffu, up ? d[r][0] : d[r][2], SPAN / 2);
+        const float e1 = (up ? d[r][3] : d[r][1]) + __shfl_xor_sync(0xffffffffu, up ? d[r][1] : d[r][3], SPAN / 2);
         if constexpr (SPAN == 2) {
           row[feature(v, up ? 2 : 0)] += e0;
           row[feature(v, up ? 3 : 1)] += e1;
@@ -153,6 +161,12 @@ struct Adders {
       }
     }
   }
+  __device__ __forceinline__ void add(int32_t v, const Unit &u, const float *__restrict__ h, float *__restrict__ y) const {
+    const TileSegment s = piece(v);
+    int n = s.begin;
+    for (; n + 1 < s.end; n += 2) add_rows<2>(v, u, h, y, n);
+    if (n < s.end) add_rows<1>(v, u, h, y, n);
+  }
 };
 
 // The summing warps' part, from the list of pieces to y complete in shared memory.
@@ -161,16 +175,21 @@ template <bool BF16, int SPAN, class Ready>
 __device__ __forceinline__ void sum_adapters(const AdapterDecodeParams &p, const Misc *mi, int32_t br, int32_t feats,
                                              int32_t part, const float *h, float *y, Ready &&ready) {
   const Adders<BF16, SPAN> a(p, mi, br, feats, part);
-  typename Adders<BF16, SPAN>::Unit cur, next;
+  // Two units in flight, in registers of their own: handing one set to the other
+  // would wait for the load that is to run ahead.
+  typename Adders<BF16, SPAN>::Unit even, odd;
   int32_t v = (threadIdx.x >> 5) - kSumWarp0;
-  a.load(v, cur);
-  a.load(v + kSumWarps, next);
+  a.load(v, even);
+  a.load(v + kSumWarps, odd);
   ready();
-  for (; v < a.n_units; v += kSumWarps) {
-    const typename Adders<BF16, SPAN>::Unit u = cur;
-    cur = next;
-    a.load(v + 2 * kSumWarps, next);
-    a.add(v, u, h, y);
+  while (v < a.n_units) {
+    a.add(v, even, h, y);
+    a.load(v + 2 * kSumWarps, even);
+    v += kSumWarps;
+    if (v >= a.n_units) break;
+    a.add(v, odd, h, y);
+    a.load(v + 2 * kSumWarps, odd);
+    v += kSumWarps;
   }
 }
 

@@ -28,14 +28,14 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float (&f)[8]) {
 
 // ---------------------------------------------------------------- down projection, a few rows per segment
 // h[n][j] = scale * <D_a[j], x[n]> in fp32.  One block per (row that starts a
-// run, group of kShrinkRanks ranks): a run is the rows of one segment within 8
-// consecutive rows, so a row of D is read once for up to 8 rows of X and every
+// run, group of kShrinkRanks ranks): a run is the rows of one segment within 4
+// consecutive rows, so a row of D is read once for up to 4 rows of X and every
 // single-row request still has its own block.  The block's warps take 256-column
 // pieces of k in turn and add their sums in warp order.
 constexpr int kShrinkThreads = 256;
 constexpr int kShrinkWarps = kShrinkThreads / 32;
 constexpr int kShrinkRanks = 4;
-constexpr int kShrinkRows = 8;
+constexpr int kShrinkRows = 4;
 
 template <bool BF16, int ROWS>
 __device__ __forceinline__ void shrink_run(const uint4 *__restrict__ D, const uint4 *__restrict__ X, int32_t k8, int rows,
@@ -65,7 +65,7 @@ __device__ __forceinline__ void shrink_run(const uint4 *__restrict__ D, const ui
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kShrinkThreads) shrink_rows_kernel(const AdapterParams p) {
+__global__ void __launch_bounds__(kShrinkThreads, 3) shrink_rows_kernel(const AdapterParams p) {
   grid_launch_dependents();  // the projection may set up and run its shared product beside this
   const int64_t n = blockIdx.x;
   const RowSegment seg = find_row(p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, n, p.status);

@@ -323,6 +323,22 @@ def test_a_broken_row_reaches_its_own_adapter_only(S):
         assert torch.isnan(got[name][1].float()).any()
 
 
+@pytest.mark.parametrize("rank", [8, 72])
+def test_a_broken_adapter_spoils_its_own_gradients_only(S, rank):
+    """Infinities and NaN in adapter 1's weights: rows and gradients of the adapters beside it in memory are as without."""
+    import torch
+    c = Case(136, 200, 300, [0, 120, 121, 260, 300], [0, 1, 2, 0], rank, 3)
+    ref = c.reference_grad()
+    c.down[1, 0], c.up[1, 0] = float("inf"), float("nan")
+    got = run_grad(S, c)
+    others = torch.ones(c.n, dtype=torch.bool)
+    others[120] = False
+    close(got["dX"][others], ref["dX"][0][others], ref["dX"][1][others], "dX")
+    for name in ("d_down", "d_up"):
+        for a in (0, 2):
+            close(got[name][a], ref[name][0][a], ref[name][1][a], f"{name}[{a}]")
+
+
 def test_other_streams_and_graphs(S):
     """A call on a side stream and a captured call replayed on new data give what a plain call gives."""
     import torch
