@@ -22,14 +22,19 @@
 // 6 warps, as in bcsr_kernel.cu: a TMA producer, an MMA issuer and four epilogue
 // warps (warp w reads TMEM lanes 32 (w % 4) .. + 31, rows of X).
 //
-// What bounds it is neither bytes nor MMAs but the roles' handshakes per stage
-// (18944 x 3584 with 90 % zero blocks, 65536 rows, 256-row tiles: 1066 us;
-// without X's copies 1043, with an eighth of the MMAs 1047, without stores 991):
-// the MMA warp spends ~30 cycles an MMA, ~85 on a stage's commit and ~120 on a
-// wait that has nothing to wait for.  Tiles of 512 rows (half the handshakes, but
-// three stages of 72 KB in place of five of 40) measured the same without
-// adapters (1057 us) and 8 % slower on long block rows (3584 x 18944, 30 blocks a
-// row); with adapters, see linear_adapters_tile.
+// What bounds it is shared memory.  A stage of 256 rows writes 40 KB there (TMA)
+// and its eight MMAs read 6 KB each (4 KB of X, 2 KB of the block for 16 deep in
+// K), and a tile's epilogue passes 32 KB through the staging area twice: ~99 KB per
+// stage of a block row of 5.6 blocks, 780 cycles at 128 bytes a cycle, where 745
+// were measured (18944 x 3584 with 90 % zero blocks, 65536 rows: 1066 us).  Taking
+// one user out helps little, taking several out does: without X's copies 1043
+// us, without 7/8 of the MMAs 1047, without stores 991, without the epilogue's
+// memory work 869, without both operands' copies 860, without copies and MMAs 656
+// (the roles' handshakes).  X is used once per block, as random blocks share no
+// columns with the row above, so there is no reuse to gain.  Tiles of 512 rows
+// (the block read and the handshakes shared by twice the rows, three stages of 72
+// KB in place of five of 40) measured 1057 us, and 8 % more on long block rows
+// (3584 x 18944, 30 blocks a row); with adapters, see linear_adapters_tile.
 //
 // With adapters (spmm_run_linear_adapters) a tile has further stages after its
 // blocks: for every segment with an adapter among its rows, the block row's 64
