@@ -214,24 +214,28 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   const int64_t jb = row_begin + blocks * part / p.split;
   const int64_t je = row_begin + blocks * (part + 1) / p.split;
-  int32_t ahead = static_cast<int32_t>(min(je - jb, static_cast<int64_t>(p.q)));
-
-  if (threadIdx.x == 0) {
-    for (int q = 0; q < p.q; ++q) {
-      mbar_init(smem_addr(&mi->full[q]), 1);
-      mbar_init(smem_addr(&mi->empty[q]), 1);
+  // The first stages, a lane each: their blocks at once, their rows of X as soon
+  // as their columns are known.
+  const int32_t ahead = static_cast<int32_t>(min(je - jb, static_cast<int64_t>(p.q)));
+  int32_t first_col = 0;
+  if (warp == kTmaWarp) {
+    if (lane < ahead) first_col = p.block_col_idx[jb + lane];
+    if (lane == 0) {
+      for (int q = 0; q < p.q; ++q) {
+        mbar_init(smem_addr(&mi->full[q]), 1);
+        mbar_init(smem_addr(&mi->empty[q]), 1);
+      }
+      mbar_init(smem_addr(&mi->acc_full), 1);
+      mbar_init(smem_addr(&mi->listed), 1);
+      mi->abort_flag = 0;
+      fence_barrier_init();
     }
-    mbar_init(smem_addr(&mi->acc_full), 1);
-    mbar_init(smem_addr(&mi->listed), 1);
-    mi->abort_flag = 0;
-    fence_barrier_init();
-    // the blocks of the first stages, before their columns have arrived
-    for (int q = 0; q < ahead; ++q) {
-      const uint32_t fb = smem_addr(&mi->full[q]);
+    __syncwarp();
+    if (lane < ahead) {
+      const uint32_t fb = smem_addr(&mi->full[lane]);
       mbar_arrive_expect_tx(fb, stage_bytes);
-      tma_load_2d(smem_addr(smem + q * stage_bytes), &tmA, fb, 0, static_cast<int32_t>((jb + q) * kBlk));
+      tma_load_2d(smem_addr(smem + lane * stage_bytes), &tmA, fb, 0, static_cast<int32_t>((jb + lane) * kBlk));
     }
-    tma_prefetch_desc(&tmX);
   }
   if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(&mi->tmem), tmem_cols);
@@ -243,30 +247,28 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = mi->tmem;
 
   if (warp == kTmaWarp) {
-    uint32_t stage = 0, phase = 0;
-    int64_t seq = 0;
+    if (lane < ahead)
+      tma_load_2d(smem_addr(smem + lane * stage_bytes) + kBlkBytes, &tmX, smem_addr(&mi->full[lane]), first_col * kBlk, row0);
+    __syncwarp();
+    uint32_t stage = 0, phase = 1;
+    int64_t seq = ahead;
     bool ok = true;
-    for (int64_t jbase = jb; jbase < je && ok; jbase += 32) {
+    for (int64_t jbase = jb + ahead; jbase < je && ok; jbase += 32) {
       const int32_t my_col = jbase + lane < je ? p.block_col_idx[jbase + lane] : 0;
       const int cnt = static_cast<int>(min(je - jbase, int64_t{32}));
       for (int i = 0; i < cnt; ++i) {
         const int32_t bcol = __shfl_sync(0xffffffffu, my_col, i);
-        if (ahead <= 0) {
-          const bool r = mbar_wait_warp(smem_addr(&mi->empty[stage]), phase ^ 1u, p.wait_limit_ns);
-          ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
-          if (!ok) break;
-        }
+        const bool r = mbar_wait_warp(smem_addr(&mi->empty[stage]), phase ^ 1u, p.wait_limit_ns);
+        ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
+        if (!ok) break;
         if (lane == 0) {
           const uint32_t fb = smem_addr(&mi->full[stage]);
           const uint32_t st = smem_addr(smem + stage * stage_bytes);
-          if (ahead <= 0) {
-            mbar_arrive_expect_tx(fb, stage_bytes);
-            tma_load_2d(st, &tmA, fb, 0, static_cast<int32_t>((jbase + i) * kBlk));
-          }
+          mbar_arrive_expect_tx(fb, stage_bytes);
+          tma_load_2d(st, &tmA, fb, 0, static_cast<int32_t>((jbase + i) * kBlk));
           tma_load_2d(st + kBlkBytes, &tmX, fb, bcol * kBlk, row0);
         }
         __syncwarp();
-        --ahead;
         ++seq;
         if (++stage == static_cast<uint32_t>(p.q)) {
           stage = 0;
@@ -311,20 +313,31 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t idesc = idesc_f16(BF16, false, false, kBlk, static_cast<uint32_t>(p.tile));
     uint32_t stage = 0, phase = 0;
     bool ok = true;
-    for (int64_t j = jb; j < je; ++j) {
-      const bool r = mbar_wait_warp(smem_addr(&mi->full[stage]), phase, p.wait_limit_ns);
-      ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
-      if (!ok) break;
+    for (int64_t j = jb; j < je;) {
+      // how many stages in a row are there, a lane each; one wait for all of them
+      const int32_t left = static_cast<int32_t>(min(je - j, static_cast<int64_t>(p.q)));
+      const bool wrap = stage + lane >= static_cast<uint32_t>(p.q);
+      const bool there = lane < left && mbar_test_wait(smem_addr(&mi->full[stage + lane - (wrap ? p.q : 0)]),
+                                                       phase ^ (wrap ? 1u : 0u));
+      int32_t ready = __ffs(~__ballot_sync(0xffffffffu, there)) - 1;
+      if (ready == 0) {
+        const bool r = mbar_wait_warp(smem_addr(&mi->full[stage]), phase, p.wait_limit_ns);
+        ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
+        if (!ok) break;
+        ready = 1;
+      }
       tc_fence_after_sync();
-      const uint32_t st = smem_addr(smem + stage * stage_bytes);
-      const uint64_t a = smem_desc_sw128(st, 16, 1024), b = smem_desc_sw128(st + kBlkBytes, 16, 1024);
+      for (; ready > 0; --ready, ++j) {
+        const uint32_t st = smem_addr(smem + stage * stage_bytes);
+        const uint64_t a = smem_desc_sw128(st, 16, 1024), b = smem_desc_sw128(st + kBlkBytes, 16, 1024);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        umma_f16_elect(tmem, smem_desc_add(a, kk * 32), smem_desc_add(b, kk * 32), idesc, (j > jb || kk > 0) ? 1u : 0u);
-      umma_commit_elect(smem_addr(&mi->empty[stage]));
-      if (++stage == static_cast<uint32_t>(p.q)) {
-        stage = 0;
-        phase ^= 1u;
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16_elect(tmem, smem_desc_add(a, kk * 32), smem_desc_add(b, kk * 32), idesc, (j > jb || kk > 0) ? 1u : 0u);
+        if (j + p.q < je) umma_commit_elect(smem_addr(&mi->empty[stage]));  // the stage is filled once more
+        if (++stage == static_cast<uint32_t>(p.q)) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
     if (!ok && lane == 0) {
