@@ -8,12 +8,15 @@
 // 2-8 KB of X per block instead of a 256-row tile.  The adapters follow on the
 // CUDA cores in fp32, since every row has its own U_a and an MMA would run for one
 // row: the 64 rows of U_a that the block row needs are contiguous (64 * rank
-// values), and the summing warps read them straight into registers, 2 KB at a
-// time with the next 2 KB in flight, and multiply them with h, kept in fp32.  (A
-// ring of bulk copies through shared memory in their place took 26 us for 64
-// single-row requests of rank 16 through 18944 features whatever the bytes: an
-// SM's copy engine starts one copy per ~110 cycles.)  A row meets its own adapter
-// alone.
+// values); every lane of the summing warps copies its own 16-byte words of them to
+// shared memory (cp.async, two units of 2 KB in flight per warp), so nothing but
+// the lane waits for them, and multiplies them with h, kept in fp32.  64
+// single-row requests with 64 adapters through 18944 features take 16.5 us at rank
+// 16 (46 MB of U), 37 at rank 64 (30 at the HBM rate).  In its place, a ring of
+// bulk copies took 26 us at rank 16 whatever the bytes (an SM's copy engine starts
+// one copy per ~110 cycles), loads into two sets of registers 19 and 46 us (they
+// spill, and a spilled load is waited for), three units per warp 18 us (a stage of
+// blocks less).  A row meets its own adapter alone.
 //
 // HBM bounds large batches of adapters (the blocks once, 2 nnz bytes, and each
 // adapter's U once), the chain of dependent loads the small ones: block row
@@ -42,6 +45,7 @@ constexpr int kMaxQ = 8;
 constexpr int kPiece = 8;               // rows of a segment that one warp takes
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kSumWarp0 = 2, kSumWarps = 8;
 constexpr int kThreads = (kSumWarp0 + kSumWarps) * 32;
+constexpr int kUnitDepth = 2;           // units of U (2 KB) in flight per summing warp
 constexpr int kPitch = kBlk + 4;        // floats per row of y in shared memory
 constexpr int kMiscBytes = 2560;
 constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
@@ -83,17 +87,17 @@ struct Adders {
   static constexpr int kPasses = SPAN == 1 ? 2 : 4;              // per unit
   static constexpr int kUnits = kBlk * SPAN / 32 / kPasses;      // per piece
   static constexpr int kFeats = 32 / SPAN;                       // per pass
-  struct Unit {
-    uint4 w[kPasses];
-  };
   const AdapterDecodeParams &p;
   const Misc *mi;
+  uint32_t ring;  // the lane's words: kDepth units of kPasses words, 512 bytes apart
   int32_t br, feats, part, n_units;
   int c, f0, chunks;
 
-  __device__ __forceinline__ Adders(const AdapterDecodeParams &p_, const Misc *mi_, int32_t br_, int32_t feats_, int32_t part_)
+  __device__ __forceinline__ Adders(const AdapterDecodeParams &p_, const Misc *mi_, int32_t br_, int32_t feats_, int32_t part_,
+                                  uint32_t ring_)
       : p(p_), mi(mi_), br(br_), feats(feats_), part(part_) {
     const int lane = threadIdx.x & 31;
+    ring = ring_ + ((threadIdx.x >> 5) - kSumWarp0) * (kUnitDepth * 2048) + lane * 16;
     c = lane % SPAN;
     f0 = lane / SPAN;
     chunks = p.rank / 8;
@@ -102,19 +106,21 @@ struct Adders {
   }
   __device__ __forceinline__ TileSegment piece(int32_t v) const { return mi->pieces[part + v / kUnits * p.split]; }
   __device__ __forceinline__ int feature(int32_t v, int pass) const { return (v % kUnits * kPasses + pass) * kFeats + f0; }
-  __device__ __forceinline__ void load(int32_t v, Unit &u) const {
-    if (v >= n_units) return;
-    const uint4 *U = static_cast<const uint4 *>(p.up) +
-                     (static_cast<int64_t>(piece(v).adapter) * p.M + br * kBlk) * chunks;
+  __device__ __forceinline__ void load(int32_t v, int slot) const {
+    if (v < n_units) {
+      const uint4 *U = static_cast<const uint4 *>(p.up) +
+                       (static_cast<int64_t>(piece(v).adapter) * p.M + br * kBlk) * chunks;
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int f = feature(v, i);
-      u.w[i] = c < chunks && f < feats ? __ldg(U + f * chunks + c) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kPasses; ++i) {
+        const int f = feature(v, i);
+        cp_async_16(ring + slot * 2048 + i * 512, U + f * chunks + c, c < chunks && f < feats ? 16 : 0);
+      }
     }
+    cp_async_commit();
   }
   // ROWS rows of the piece from row n on: U is unpacked once for them.
   template <int ROWS>
-  __device__ __forceinline__ void add_rows(int32_t v, const Unit &u, const float *__restrict__ h, float *__restrict__ y,
+  __device__ __forceinline__ void add_rows(int32_t v, int slot, const float *__restrict__ h, float *__restrict__ y,
                                            int n) const {
     float hv[ROWS][8] = {}, d[ROWS][kPasses];
     if (c < chunks) {
@@ -129,7 +135,7 @@ struct Adders {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       float uf[8];
-      unpack8<BF16>(u.w[i], uf);
+      unpack8<BF16>(ld_shared_16(ring + slot * 2048 + i * 512), uf);
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
         d[r][i] = uf[0] * hv[r][0];
@@ -161,11 +167,11 @@ struct Adders {
       }
     }
   }
-  __device__ __forceinline__ void add(int32_t v, const Unit &u, const float *__restrict__ h, float *__restrict__ y) const {
+  __device__ __forceinline__ void add(int32_t v, int slot, const float *__restrict__ h, float *__restrict__ y) const {
     const TileSegment s = piece(v);
     int n = s.begin;
-    for (; n + 1 < s.end; n += 2) add_rows<2>(v, u, h, y, n);
-    if (n < s.end) add_rows<1>(v, u, h, y, n);
+    for (; n + 1 < s.end; n += 2) add_rows<2>(v, slot, h, y, n);
+    if (n < s.end) add_rows<1>(v, slot, h, y, n);
   }
 };
 
@@ -173,24 +179,18 @@ struct Adders {
 // ready() returns once y is cleared and h is there.
 template <bool BF16, int SPAN, class Ready>
 __device__ __forceinline__ void sum_adapters(const AdapterDecodeParams &p, const Misc *mi, int32_t br, int32_t feats,
-                                             int32_t part, const float *h, float *y, Ready &&ready) {
-  const Adders<BF16, SPAN> a(p, mi, br, feats, part);
-  // Two units in flight, in registers of their own: handing one set to the other
-  // would wait for the load that is to run ahead.
-  typename Adders<BF16, SPAN>::Unit even, odd;
+                                             int32_t part, uint32_t ring, const float *h, float *y, Ready &&ready) {
+  const Adders<BF16, SPAN> a(p, mi, br, feats, part, ring);
   int32_t v = (threadIdx.x >> 5) - kSumWarp0;
-  a.load(v, even);
-  a.load(v + kSumWarps, odd);
+  for (int i = 0; i < kUnitDepth; ++i) a.load(v + i * kSumWarps, i);
   ready();
-  while (v < a.n_units) {
-    a.add(v, even, h, y);
-    a.load(v + 2 * kSumWarps, even);
-    v += kSumWarps;
-    if (v >= a.n_units) break;
-    a.add(v, odd, h, y);
-    a.load(v + 2 * kSumWarps, odd);
-    v += kSumWarps;
+  for (int slot = 0; v < a.n_units; v += kSumWarps) {
+    cp_async_wait_group<kUnitDepth - 1>();
+    a.add(v, slot, h, y);
+    a.load(v + kUnitDepth * kSumWarps, slot);
+    if (++slot == kUnitDepth) slot = 0;
   }
+  cp_async_wait_group<0>();
 }
 
 template <bool BF16, bool OUT_BF16>
@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int stage_bytes = kBlkBytes + p.tile * 128;
-  float *h = reinterpret_cast<float *>(smem + p.q * stage_bytes);  // [tile][rank]
+  uint8_t *ring = smem + p.q * stage_bytes;                        // U
+  float *h = reinterpret_cast<float *>(ring + kSumWarps * kUnitDepth * 2048);  // [tile][rank]
   float *y = h + p.tile * p.rank;                                  // [tile][kPitch]
   Misc *mi = reinterpret_cast<Misc *>(y + p.tile * kPitch);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -365,15 +366,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       give_up();
       ready();
     } else if (p.rank == 8) {
-      sum_adapters<BF16, 1>(p, mi, br, feats, part, h, y, ready);
+      sum_adapters<BF16, 1>(p, mi, br, feats, part, smem_addr(ring), h, y, ready);
     } else if (p.rank == 16) {
-      sum_adapters<BF16, 2>(p, mi, br, feats, part, h, y, ready);
+      sum_adapters<BF16, 2>(p, mi, br, feats, part, smem_addr(ring), h, y, ready);
     } else if (p.rank <= 32) {
-      sum_adapters<BF16, 4>(p, mi, br, feats, part, h, y, ready);
+      sum_adapters<BF16, 4>(p, mi, br, feats, part, smem_addr(ring), h, y, ready);
     } else if (p.rank <= 64) {
-      sum_adapters<BF16, 8>(p, mi, br, feats, part, h, y, ready);
+      sum_adapters<BF16, 8>(p, mi, br, feats, part, smem_addr(ring), h, y, ready);
     } else {
-      sum_adapters<BF16, 16>(p, mi, br, feats, part, h, y, ready);
+      sum_adapters<BF16, 16>(p, mi, br, feats, part, smem_addr(ring), h, y, ready);
     }
     sum_warps_sync();
     if (je > jb) {
@@ -442,11 +443,12 @@ cudaError_t launch_adapter_decode(const CUtensorMap &tmA, const CUtensorMap &tmX
   while (p.split < 8 && tiles * p.split * 2 <= 2ll * num_sms) p.split *= 2;
   // the stages get what h and y leave of half an SM
   const int stage = kBlkBytes + p.tile * 128;
-  const int fixed = p.tile * (p.rank + kPitch) * 4 + kMiscBytes + 1024;
+  const int fixed = kSumWarps * kUnitDepth * 2048 + p.tile * (p.rank + kPitch) * 4 + kMiscBytes + 1024;
   p.q = (kSmemLimit - fixed) / stage;
   if (p.q > kMaxQ) p.q = kMaxQ;
-  static_assert((kSmemLimit - kAdapterDecodeRows * (kMaxRank + kPitch) * 4 - kMiscBytes - 1024) / (kBlkBytes + 64 * 128) >= 3,
-                "at least three stages");
+  static_assert((kSmemLimit - kSumWarps * kUnitDepth * 2048 - 64 * (64 + kPitch) * 4 - kMiscBytes - 1024) / (kBlkBytes + 64 * 128) >= 2 &&
+                    (kSmemLimit - kSumWarps * kUnitDepth * 2048 - 32 * (kMaxRank + kPitch) * 4 - kMiscBytes - 1024) / (kBlkBytes + 32 * 128) >= 2,
+                "at least two stages: 64 rows up to rank 64, 32 above");
   const int smem = fixed + p.q * stage;
   auto kern = bf16 ? (out_bf16 ? adapter_decode_kernel<true, true> : adapter_decode_kernel<true, false>)
                    : (out_bf16 ? adapter_decode_kernel<false, true> : adapter_decode_kernel<false, false>);

@@ -228,7 +228,7 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
   d.n_seg = p.n_seg;
   d.n_adapters = p.n_adapters;
   d.rank = p.rank;
-  d.tile = p.N <= 16 ? 16 : p.N <= 32 ? 32 : spmm::kAdapterDecodeRows;
+  d.tile = p.N <= 16 ? 16 : p.N <= 32 || p.rank > 64 ? 32 : spmm::kAdapterDecodeRows;
   d.M = p.M;
   d.N = p.N;
   d.status = p.status;

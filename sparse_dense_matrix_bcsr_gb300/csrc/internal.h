@@ -296,7 +296,7 @@ cudaError_t launch_adapter_down(AdapterDownParams p, int num_sms, bool bf16, cud
 cudaError_t launch_shrink(const AdapterParams &p, bool bf16, cudaStream_t s);
 
 // Y = X W^T + U H per row for such batches (adapter_decode_kernel.cu): tiles of
-// `tile` (16, 32 or 64) rows.  tmA as for launch_bcsr, tmX covers X as
+// `tile` (16, 32 or, up to rank 64, 64) rows.  tmA as for launch_bcsr, tmX covers X as
 // [N rows, K cols] with tile x 64 boxes, 128-byte swizzle.  Launched as a
 // programmatic dependent of launch_shrink's kernel.
 constexpr int kAdapterDecodeRows = 64;
