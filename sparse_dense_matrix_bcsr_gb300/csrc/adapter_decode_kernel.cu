@@ -213,32 +213,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int64_t row_begin = p.block_row_ptr[br];
   const int64_t blocks = p.block_row_ptr[br + 1] - row_begin;
 
-  const int64_t jb = row_begin + blocks * part / p.split;
-  const int64_t je = row_begin + blocks * (part + 1) / p.split;
-  // The first stages, a lane each: their blocks at once, their rows of X as soon
-  // as their columns are known.
-  const int32_t ahead = static_cast<int32_t>(min(je - jb, static_cast<int64_t>(p.q)));
-  int32_t first_col = 0;
-  if (warp == kTmaWarp) {
-    if (lane < ahead) first_col = p.block_col_idx[jb + lane];
+  if (warp == kMmaWarp) {
+    if (lane < p.q) {
+      mbar_init(smem_addr(&mi->full[lane]), 1);
+      mbar_init(smem_addr(&mi->empty[lane]), 1);
+    }
     if (lane == 0) {
-      for (int q = 0; q < p.q; ++q) {
-        mbar_init(smem_addr(&mi->full[q]), 1);
-        mbar_init(smem_addr(&mi->empty[q]), 1);
-      }
       mbar_init(smem_addr(&mi->acc_full), 1);
       mbar_init(smem_addr(&mi->listed), 1);
       mi->abort_flag = 0;
-      fence_barrier_init();
     }
+    fence_barrier_init();
     __syncwarp();
-    if (lane < ahead) {
-      const uint32_t fb = smem_addr(&mi->full[lane]);
-      mbar_arrive_expect_tx(fb, stage_bytes);
-      tma_load_2d(smem_addr(smem + lane * stage_bytes), &tmA, fb, 0, static_cast<int32_t>((jb + lane) * kBlk));
-    }
-  }
-  if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(&mi->tmem), tmem_cols);
     tmem_relinquish();
   }
@@ -246,10 +232,20 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = mi->tmem;
+  const int64_t jb = row_begin + blocks * part / p.split;  // the block row's bounds are waited for only here
+  const int64_t je = row_begin + blocks * (part + 1) / p.split;
 
   if (warp == kTmaWarp) {
-    if (lane < ahead)
-      tma_load_2d(smem_addr(smem + lane * stage_bytes) + kBlkBytes, &tmX, smem_addr(&mi->full[lane]), first_col * kBlk, row0);
+    // The first stages, a lane each: their blocks at once, their rows of X as soon
+    // as their columns are known.
+    const int32_t ahead = static_cast<int32_t>(min(je - jb, static_cast<int64_t>(p.q)));
+    if (lane < ahead) {
+      const int32_t first_col = p.block_col_idx[jb + lane];
+      const uint32_t fb = smem_addr(&mi->full[lane]), st = smem_addr(smem + lane * stage_bytes);
+      mbar_arrive_expect_tx(fb, stage_bytes);
+      tma_load_2d(st, &tmA, fb, 0, static_cast<int32_t>((jb + lane) * kBlk));
+      tma_load_2d(st + kBlkBytes, &tmX, fb, first_col * kBlk, row0);
+    }
     __syncwarp();
     uint32_t stage = 0, phase = 1;
     int64_t seq = ahead;
