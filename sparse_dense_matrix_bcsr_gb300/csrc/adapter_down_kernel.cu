@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
   const int32_t unit = blockIdx.x / p.split - (second ? p.units : 0);
   const AdapterDownJob &job = p.job[second ? 1 : 0];
   const bool transposed = job.transposed != 0;
+  grid_launch_dependents();  // the projection may set up and start on its blocks beside this
   const int stage_bytes = p.stage_bytes;
   Misc *mi = reinterpret_cast<Misc *>(smem + p.q * stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -264,7 +265,6 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
     cluster_sync();  // the others may still read this CTA's sums
   }
   __syncthreads();
-  grid_launch_dependents();
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, tmem_cols);

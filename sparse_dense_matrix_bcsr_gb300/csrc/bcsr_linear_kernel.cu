@@ -196,7 +196,10 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
         phase ^= 1u;
       }
     };
-    if constexpr (kAdapt) grid_dependency_wait();  // the tile lists and H
+    // With adapters the first tile's blocks are issued before the lists of segments
+    // and H are there (the kernel that writes them may still run): that tile is
+    // announced with adapters to come, and an empty stage follows if it has none.
+    bool listed = !kAdapt;
     for (int64_t t0 = blockIdx.x; t0 < n_tiles && ok; t0 += 32ll * gridDim.x) {
       const int64_t mine = t0 + static_cast<int64_t>(lane) * gridDim.x;
       int my_br = 0, my_nt = 0, my_segs = 0;
@@ -205,14 +208,15 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
         tile_coords<T::kGroup>(mine, p.n_block_rows, n_tiles_n, my_br, my_nt);
         my_jb = p.block_row_ptr[my_br];
         my_je = p.block_row_ptr[my_br + 1];
-        if constexpr (kAdapt) my_segs = ad.tile_count[my_nt];  // segments with an adapter in the tile
+        if constexpr (kAdapt)
+          if (listed) my_segs = ad.tile_count[my_nt];  // segments with an adapter in the tile
       }
       const int tiles = static_cast<int>(min((n_tiles - t0 + gridDim.x - 1) / gridDim.x, int64_t{32}));
       auto first_cols = [&](int i) {  // lane l: column of the tile's l-th block
         const int64_t b = __shfl_sync(0xffffffffu, my_jb, i), e = __shfl_sync(0xffffffffu, my_je, i);
         return b + lane < e ? p.block_col_idx[b + lane] : 0;
       };
-      auto first_segs = [&](int i) {
+      auto first_segs = [&](int i) {  // lane l: the tile's l-th segment
         TileSegment s{};
         if constexpr (kAdapt) {
           const int nt = __shfl_sync(0xffffffffu, my_nt, i), n = __shfl_sync(0xffffffffu, my_segs, i);
@@ -221,24 +225,26 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
         return s;
       };
       int32_t next_cols = first_cols(0);
-      TileSegment next_segs = first_segs(0);
+      TileSegment next_segs{};
+      if (listed) next_segs = first_segs(0);
       for (int ti = 0; ti < tiles && ok; ++ti) {
         const int br = __shfl_sync(0xffffffffu, my_br, ti), nt = __shfl_sync(0xffffffffu, my_nt, ti);
         const int64_t jb = __shfl_sync(0xffffffffu, my_jb, ti), je = __shfl_sync(0xffffffffu, my_je, ti);
-        const int32_t segs = __shfl_sync(0xffffffffu, my_segs, ti);
+        int32_t segs = __shfl_sync(0xffffffffu, my_segs, ti);
         const int32_t cols = next_cols;
-        const TileSegment tile_segs = next_segs;
+        TileSegment tile_segs = next_segs;
         if (ti + 1 < tiles) {
           next_cols = first_cols(ti + 1);
-          next_segs = first_segs(ti + 1);
+          if (listed) next_segs = first_segs(ti + 1);
         }
-        const int32_t first_flags = segs > 0 ? kRecAdapters : 0;
+        const bool adapters = segs > 0 || !listed;
+        const int32_t first_flags = adapters ? kRecAdapters : 0;
         auto copy_x = [&](uint32_t st, uint32_t fb, int32_t x) {
 #pragma unroll
           for (int b = 0; b < kTileN / kBoxRows; ++b)
             tma_load_2d(st + kBlkBytes + b * (kBoxRows * kBlk * 2), &tmX, fb, x, nt * kTileN + b * kBoxRows);
         };
-        if (jb == je && segs > 0) {
+        if (jb == je && adapters) {
           // no block to start the sums with: a stage of zeros, read past the end of the blocks and of X
           ok = claim();
           if (!ok) break;
@@ -280,6 +286,23 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
           }
         }
         if constexpr (kAdapt) {
+          if (!listed) {
+            grid_dependency_wait();
+            listed = true;
+            if (mine < n_tiles) my_segs = ad.tile_count[my_nt];
+            segs = __shfl_sync(0xffffffffu, my_segs, ti);
+            tile_segs = first_segs(ti);
+            if (ti + 1 < tiles) next_segs = first_segs(ti + 1);
+            if (segs == 0 && ok) {
+              ok = claim();
+              if (!ok) break;
+              if (lane == 0) {
+                tile_rec[stage] = TileRec{br, nt, kRecLast, 0, 0, 0, {}};
+                mbar_arrive(full0 + 8 * stage);
+              }
+              advance();
+            }
+          }
           for (int32_t base = 0; base < segs && ok; base += 32) {
             TileSegment my = tile_segs;
             if (base > 0 && base + lane < segs) my = ad.tile_segs[static_cast<int64_t>(nt) * kTileN + base + lane];
