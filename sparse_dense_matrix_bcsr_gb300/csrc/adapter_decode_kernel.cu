@@ -400,14 +400,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = threadIdx.x; i < (r1 - r0) * (kBlk / 8); i += kThreads) {
       const int r = r0 + i / (kBlk / 8), f = i % (kBlk / 8) * 8;
       if (f >= feats) continue;  // M is a multiple of 8
-      float4 a{}, b{};
+      float4 a, b;
       if (p.split > 1) {
-        for (int c = 0; c < p.split; ++c) {
-          const uint32_t at = cluster_map(smem_addr(y + r * kPitch + f), c);
-          const float4 x = cluster_load_f4(at), z = cluster_load_f4(at + 16);
-          a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
-          b.x += z.x, b.y += z.y, b.z += z.z, b.w += z.w;
-        }
+        float o[8];
+        cluster_sum8(smem_addr(y + r * kPitch + f), p.split, o);
+        a = make_float4(o[0], o[1], o[2], o[3]);
+        b = make_float4(o[4], o[5], o[6], o[7]);
       } else {
         a = *reinterpret_cast<const float4 *>(y + r * kPitch + f);
         b = *reinterpret_cast<const float4 *>(y + r * kPitch + f + 4);

@@ -10,7 +10,7 @@
 // every row meets its own adapter alone; a tile that several segments share is
 // read once per segment, from L2.  2 N r k FLOP against 2 N k bytes are far below
 // the tensor rate, so HBM bounds it for prompts.  Few units leave SMs idle: a
-// cluster of up to 8 CTAs then splits a unit's columns and adds the fp32 sums
+// cluster of up to 16 CTAs then splits a unit's columns and adds the fp32 sums
 // through distributed shared memory in CTA order (no atomics, no second launch).
 // One CTA per tile that walked the tile's segments one after another took 56
 // against 20 us for 777 rows in 40 segments (8192 columns, rank 64).
@@ -33,6 +33,7 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kXBytes = kRows * 128;  // 128 rows x 64 columns
 constexpr int kMaxQ = 8;
+constexpr int kMaxSplit = 16;           // CTAs of a cluster (above 8 a kernel has to ask for it)
 constexpr int kThreads = 192;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2;
 constexpr int kMiscBytes = 1024;
@@ -250,13 +251,8 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
       const float f = p.scale[piece.adapter];
       for (int u = threadIdx.x; u < (r1 - r0) * units; u += kThreads) {
         const int r = r0 + u / units, j = (u % units) * 8;
-        float o[8] = {};
-        for (int c = 0; c < p.split; ++c) {
-          const uint32_t at = cluster_map(base + (r * part_pitch(p.rank) + j) * 4, c);
-          const float4 x = cluster_load_f4(at), y = cluster_load_f4(at + 16);
-          o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
-          o[4] += y.x, o[5] += y.y, o[6] += y.z, o[7] += y.w;
-        }
+        float o[8];
+        cluster_sum8(base + (r * part_pitch(p.rank) + j) * 4, p.split, o);
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] *= f;
         store_h<BF16>(job.H, row0 + r, p.N, p.rank, j, job.parts, o);
@@ -287,7 +283,7 @@ cudaError_t launch_adapter_down(AdapterDownParams p, int num_sms, bool bf16, cud
   // at least four stages each
   p.units = static_cast<int32_t>(units);
   p.split = 1;
-  while (p.split < 8 && p.jobs * units * p.split * 2 <= 2ll * num_sms && nk >= 8 * p.split) p.split *= 2;
+  while (p.split < kMaxSplit && p.jobs * units * p.split * 2 <= 2ll * num_sms && nk >= 8 * p.split) p.split *= 2;
   p.stage_bytes = kXBytes + d_bytes(p.rank, transposed);
   p.q = (kSmemLimit - kMiscBytes - 1024) / p.stage_bytes;
   if (p.q > kMaxQ) p.q = kMaxQ;
@@ -295,6 +291,9 @@ cudaError_t launch_adapter_down(AdapterDownParams p, int num_sms, bool bf16, cud
   auto kern = bf16 ? adapter_down_kernel<true> : adapter_down_kernel<false>;
   static std::atomic<uint64_t> smem_set[2];
   cudaError_t e = set_smem_limit_once(kern, kSmemLimit, smem_set[bf16 ? 1 : 0]);
+  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> cluster_set[2];
+  e = allow_large_clusters_once(kern, cluster_set[bf16 ? 1 : 0]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.jobs * units * p.split));

@@ -234,23 +234,13 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
   {
     const int feats = kFeat / p.split, r0 = part * feats;
     const uint32_t base = smem_addr(smem);
-    auto sum8 = [&](int r, int j, float (&o)[8]) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = 0.0f;
-      for (int c = 0; c < p.split; ++c) {
-        const uint32_t at = cluster_map(base + (r * part_pitch(p.rank) + j) * 4, c);
-        const float4 x = cluster_load_f4(at), y = cluster_load_f4(at + 16);
-        o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w;
-        o[4] += y.x, o[5] += y.y, o[6] += y.z, o[7] += y.w;
-      }
-    };
     const int units = p.rank / 8;
     for (int u = threadIdx.x; u < feats * units; u += kThreads) {
       // d_up: a feature's ranks are contiguous; d_down: a rank's features are
       const int r = r0 + (up ? u / units : u % feats), j = (up ? u % units : u / feats) * 8;
       if (f0 + r >= F) continue;
       float o[8];
-      sum8(r, j, o);
+      cluster_sum8(base + (r * part_pitch(p.rank) + j) * 4, p.split, o);
       if (up) {
         uint32_t w[4];
 #pragma unroll

@@ -26,6 +26,19 @@ cudaError_t set_smem_limit_once(Kernel kern, int bytes, std::atomic<uint64_t> &d
   return e;
 }
 
+// The same for clusters of more than 8 CTAs.
+template <typename Kernel>
+cudaError_t allow_large_clusters_once(Kernel kern, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = (dev >= 0 && dev < 64) ? (uint64_t{1} << dev) : 0;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 // Flags of a stage / segment: it holds the first and/or the last stage of its
 // group (a WCSR window, or a BCSR block row x column tile).
 constexpr int32_t kStageFirst = 1;

@@ -272,6 +272,36 @@ __device__ __forceinline__ float4 cluster_load_f4(uint32_t addr) {
   return v;
 }
 
+// o[0..7] = the sum over the cluster's first `ctas` CTAs (1, 2, 4, 8 or 16), in
+// their order, of the eight floats at shared-memory address `saddr` of each; the
+// loads of up to eight CTAs are in flight together.
+template <int N>
+__device__ __forceinline__ void cluster_add8(uint32_t saddr, uint32_t first, float (&o)[8]) {
+  float4 x[N], y[N];
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const uint32_t at = cluster_map(saddr, first + c);
+    x[c] = cluster_load_f4(at);
+    y[c] = cluster_load_f4(at + 16);
+  }
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    o[0] += x[c].x, o[1] += x[c].y, o[2] += x[c].z, o[3] += x[c].w;
+    o[4] += y[c].x, o[5] += y[c].y, o[6] += y[c].z, o[7] += y[c].w;
+  }
+}
+__device__ __forceinline__ void cluster_sum8(uint32_t saddr, int ctas, float (&o)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+  switch (ctas) {
+    case 1: return cluster_add8<1>(saddr, 0, o);
+    case 2: return cluster_add8<2>(saddr, 0, o);
+    case 4: return cluster_add8<4>(saddr, 0, o);
+    default:
+      for (int c = 0; c < ctas; c += 8) cluster_add8<8>(saddr, c, o);
+  }
+}
+
 // ---------------------------------------------------------------- cluster launch control
 // Asks the hardware to cancel the launch of one CTA of this grid that has not
 // started yet; the 16-byte answer is written to `resp` (16-byte aligned
