@@ -361,7 +361,8 @@ spmm_status spmm_wcsr_noalloc_check(void *stream);
  *   rank          of every adapter in the pool, a multiple of 8 up to 128
  *                 (adapters of lower rank are padded with zeros).
  *   in_t          SPMM_F16 or SPMM_BF16, the type of X and of the adapters.
- *   max_rows, max_segments   the largest batch that calls will bring.
+ *   max_rows, max_segments   the largest batch that calls will bring (below 2^30
+ *                 rows, 2^27 segments).
  *   grad          nonzero to hold the workspace of spmm_adapters_grad too.
  * Errors: INVALID_ARG, UNSUPPORTED (m, k or rank not a multiple of 8, rank
  * above 128), OOM, CUDA.  spmm_adapters_destroy waits for the device and frees
@@ -384,8 +385,10 @@ spmm_status spmm_adapters_destroy(spmm_adapters a);
  * The segments are read on the device only, so a batch can be described by
  * arrays that earlier work on the stream writes (spmm_route_sort's offsets).
  * An index outside the pool counts as -1 and is reported by spmm_check(h) as
- * SPMM_ERR_DEVICE_CHECK.  fp32 sums throughout; asynchronous; results are
- * bitwise reproducible run to run.
+ * SPMM_ERR_DEVICE_CHECK.  Sums are fp32.  Batches with few rows per adapter keep
+ * h in fp32; longer ones take it as a matrix operand, rounded to in_t (to two
+ * in_t parts where Y is fp32), so fp16 values of h above 65504 become infinite
+ * there.  Asynchronous; results are bitwise reproducible run to run.
  * Errors: as spmm_run_linear, plus INVALID_ARG for shapes, types or devices
  * that do not match and batches above the set's limits.
  */
@@ -399,7 +402,8 @@ spmm_status spmm_run_linear_adapters(spmm_handle h, spmm_adapters a, const void 
  *     dh[n] = scale[a] * U_a^T dY[n]
  *     dX[n] = A^T dY[n] + D_a^T dh[n]
  *     d_up_a = sum_n dY[n] h[n]^T       d_down_a = sum_n dh[n] X[n]^T
- * the sums over the rows of adapter a, in a fixed order.
+ * the sums over the rows of adapter a, in a fixed order; h and dh are rounded to
+ * in_t on the way (two parts of dh for an fp32 dX).
  *   h_t      a BCSR handle of A^T (k x m), of the set's in_t; dX has its out_t.
  *   X, dY    N x k and N x m row-major, in_t, 16-byte aligned.
  *   dX       N x k, or NULL where no gradient of the input is wanted.

@@ -40,10 +40,10 @@ void free_adapters(spmm_adapters a) {
   delete a;
 }
 
-bool misaligned(std::initializer_list<const void *> ps) {
+bool misaligned(std::initializer_list<const void *> ps, uintptr_t bytes = 16) {
   uintptr_t bits = 0;
   for (const void *p : ps) bits |= reinterpret_cast<uintptr_t>(p);
-  return (bits & 15) != 0;
+  return (bits & (bytes - 1)) != 0;
 }
 
 // What both directions check of the layer's handle, the batch and the pool.
@@ -70,6 +70,8 @@ spmm_status check_batch(spmm_handle h, spmm_adapters a, int64_t rows, int64_t co
                 static_cast<long long>(a->max_segments));
   if (!down || !up || !scale) return fail(SPMM_ERR_INVALID_ARG, "down, up or scale is NULL");
   if (n_seg > 0 && (!seg_ptr || !seg_adapter)) return fail(SPMM_ERR_INVALID_ARG, "seg_ptr or seg_adapter is NULL");
+  if (misaligned({scale, seg_adapter}, 4) || misaligned({seg_ptr}, 8))
+    return fail(SPMM_ERR_UNSUPPORTED, "scale, seg_ptr or seg_adapter is not aligned to its type");
   if (!a->sm103) return fail(SPMM_ERR_UNSUPPORTED, "the kernels need an sm_103 (GB300) device");
   return SPMM_OK;
 }
@@ -254,8 +256,8 @@ spmm_status spmm_adapters_create(spmm_adapters *out, int64_t m, int64_t k, int32
   if (n_adapters < 1 || n_adapters > 65535) return fail(SPMM_ERR_INVALID_ARG, "n_adapters must be in [1, 65535]");
   if (rank < 1) return fail(SPMM_ERR_INVALID_ARG, "rank must be positive");
   if (in_t != SPMM_F16 && in_t != SPMM_BF16) return fail(SPMM_ERR_INVALID_ARG, "in_t must be F16 or BF16");
-  if (max_rows < 0 || max_rows >= (1ll << 31) || max_segments < 0 || max_segments >= (1ll << 31))
-    return fail(SPMM_ERR_INVALID_ARG, "max_rows and max_segments must be in [0, 2^31)");
+  if (max_rows < 0 || max_rows >= (1ll << 30) || max_segments < 0 || max_segments >= (1ll << 27))
+    return fail(SPMM_ERR_INVALID_ARG, "max_rows must be in [0, 2^30), max_segments in [0, 2^27)");
   if (m % 8 != 0 || k % 8 != 0) return fail(SPMM_ERR_UNSUPPORTED, "m and k must be multiples of 8 (16-byte rows)");
   if (rank % 8 != 0 || rank > spmm::kMaxRank)
     return fail(SPMM_ERR_UNSUPPORTED, "rank must be a multiple of 8, at most %d (pad smaller adapters with zeros)",
@@ -419,6 +421,8 @@ spmm_status spmm_route_sort(const int32_t *ids, int64_t T, int32_t topk, int32_t
   if (n_experts > spmm::kRouteMaxExperts)
     return fail(SPMM_ERR_UNSUPPORTED, "n_experts must be at most %d", spmm::kRouteMaxExperts);
   if (!offsets || (T > 0 && (!ids || !order || !position))) return fail(SPMM_ERR_INVALID_ARG, "a pointer is NULL");
+  if (misaligned({ids, order, position, workspace}, 4) || misaligned({offsets}, 8))
+    return fail(SPMM_ERR_UNSUPPORTED, "a pointer is not aligned to its type");
   if (!workspace && spmm_route_workspace_bytes(T, topk, n_experts) > 0)
     return fail(SPMM_ERR_INVALID_ARG, "workspace is NULL; spmm_route_workspace_bytes gives its size");
   CUDA_TRY(spmm::launch_route_sort(ids, T * topk, n_experts, offsets, order, position, static_cast<int32_t *>(workspace),
@@ -432,6 +436,8 @@ spmm_status spmm_route_gather(const void *x, const int32_t *position, const int6
   spmm_status st = check_routing(T, topk, d, dtype);
   if (st != SPMM_OK || T == 0) return st;
   if (!position || !n_kept) return fail(SPMM_ERR_INVALID_ARG, "position or n_kept is NULL");
+  if (misaligned({position}, 4) || misaligned({n_kept}, 8))
+    return fail(SPMM_ERR_UNSUPPORTED, "a pointer is not aligned to its type");
   st = check_rows({x, out}, dtype);
   if (st != SPMM_OK) return st;
   spmm::RouteRows r{x, nullptr, out, position, nullptr, n_kept, nullptr, T, d, topk};
@@ -444,6 +450,7 @@ spmm_status spmm_route_combine(const void *y, const int32_t *position, const flo
   spmm_status st = check_routing(T, topk, d, dtype);
   if (st != SPMM_OK || T == 0) return st;
   if (!position) return fail(SPMM_ERR_INVALID_ARG, "position is NULL");
+  if (misaligned({position, weights}, 4)) return fail(SPMM_ERR_UNSUPPORTED, "a pointer is not aligned to its type");
   st = check_rows({y, out}, dtype);
   if (st != SPMM_OK) return st;
   spmm::RouteRows r{y, nullptr, out, position, weights, nullptr, nullptr, T, d, topk};
@@ -457,6 +464,8 @@ spmm_status spmm_route_combine_grad(const void *dout, const void *y, const int32
   spmm_status st = check_routing(T, topk, d, dtype);
   if (st != SPMM_OK || T == 0) return st;
   if (!position || !n_kept || !dweights) return fail(SPMM_ERR_INVALID_ARG, "position, n_kept or dweights is NULL");
+  if (misaligned({position, weights, dweights}, 4) || misaligned({n_kept}, 8))
+    return fail(SPMM_ERR_UNSUPPORTED, "a pointer is not aligned to its type");
   st = check_rows({dout, y, dy}, dtype);
   if (st != SPMM_OK) return st;
   spmm::RouteRows r{y, dout, dy, position, weights, n_kept, dweights, T, d, topk};

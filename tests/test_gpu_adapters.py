@@ -195,6 +195,9 @@ SHAPES = [
     pytest.param(256, 256, 513, ([0, 255, 256, 257, 512, 513], [0, 1, 2, 0, 1]), 32, 3, "bf16", "bf16", id="tile-edges"),
     pytest.param(192, 8, 260, ragged(260, 4, 2), 16, 2, "bf16", "f32", id="k-8"),
     pytest.param(8, 192, 130, ragged(130, 4, 2), 16, 2, "bf16", "bf16", id="m-8"),
+    pytest.param(192, 128, 3000, ragged(3000, 150, 9, gaps=True), 128, 9, "bf16", "bf16", id="150-segments-rank-128"),
+    pytest.param(72, 8200, 130, ragged(130, 2, 2, none=0.0), 64, 2, "f16", "f32", id="long-k-split"),
+    pytest.param(72, 8200, 130, singles(130, 3), 32, 3, "bf16", "f32", id="long-k-single-rows"),
     # enough block rows and rows for the projection's tiles of 512 rows
     pytest.param(8200, 72, 5300, ragged(5300, 9, 4), 16, 4, "bf16", "bf16", id="tiles-of-512"),
     pytest.param(8192, 72, 5300, ragged(5300, 40, 5, gaps=True), 72, 5, "f16", "f32", id="tiles-of-512-f32-rank-72"),
@@ -386,6 +389,7 @@ def test_refusals(S):
     refused(S.SPMM_ERR_INVALID_ARG, *ok[:10], 2)                        # more segments
     refused(S.SPMM_ERR_INVALID_ARG, *ok[:5], 0, *ok[6:])                # no weights
     refused(S.SPMM_ERR_UNSUPPORTED, *ok[:2], ok[2] + 8, *ok[3:])        # X not on 16 bytes
+    refused(S.SPMM_ERR_UNSUPPORTED, *ok[:8], ok[8] + 4, *ok[9:])        # seg_ptr not on 8
     w = S.SpMM("wcsr", 128, 192, c.rp, c.ci, c.vals, "bf16", "bf16")
     refused(S.SPMM_ERR_UNSUPPORTED, w.h, *ok[1:])
     half = S.SpMM("bcsr", 128, 192, c.rp, c.ci, c.vals, "f16", "bf16")
