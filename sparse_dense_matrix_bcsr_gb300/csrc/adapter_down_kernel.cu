@@ -272,18 +272,23 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
 cudaError_t launch_adapter_down(AdapterDownParams p, int num_sms, bool bf16, cudaStream_t s) {
   // units: see find_piece; about as many have rows
   const int64_t units = (static_cast<int64_t>(p.N) + kRows - 1) / kRows + p.n_seg;
-  int32_t k = p.job[0].K;
+  int32_t k = p.job[0].K, longest = k;
   bool transposed = p.job[0].transposed != 0;
   if (p.jobs > 1) {
     k = k < p.job[1].K ? k : p.job[1].K;
+    longest = longest > p.job[1].K ? longest : p.job[1].K;
     transposed = transposed || p.job[1].transposed != 0;
   }
   const int nk = (k + 63) / 64;
-  // as many CTAs per unit (a cluster) as keep the grid within two per SM, with
-  // at least four stages each
+  // As many CTAs per unit (a cluster) as keep the grid within two per SM, what an
+  // SM holds, with at least four stages each; within four where one product's
+  // CTAs are far longer than the other's and would run on alone (gradient of 4096
+  // rows through 18944 x 3584: 195 -> 172 us; with four throughout, 16384 rows
+  // through 3584 x 18944 take 383 in place of 371 us).
+  const int64_t most = (longest >= 2 * k ? 4ll : 2ll) * num_sms;
   p.units = static_cast<int32_t>(units);
   p.split = 1;
-  while (p.split < kMaxSplit && p.jobs * units * p.split * 2 <= 2ll * num_sms && nk >= 8 * p.split) p.split *= 2;
+  while (p.split < kMaxSplit && p.jobs * units * p.split * 2 <= most && nk >= 8 * p.split) p.split *= 2;
   p.stage_bytes = kXBytes + d_bytes(p.rank, transposed);
   p.q = (kSmemLimit - kMiscBytes - 1024) / p.stage_bytes;
   if (p.q > kMaxQ) p.q = kMaxQ;

@@ -19,6 +19,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "segments.cuh"
 
 namespace spmm {
 namespace {
@@ -105,20 +106,16 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
         phase ^= 1u;
       }
     };
-    for (int32_t base = 0; base < p.n_seg && ok; base += 32) {
-      int64_t b = 0, e = 0;
-      bool mine = false;
-      if (base + lane < p.n_seg) {
-        b = max(p.seg_ptr[base + lane], int64_t{0});
-        e = min(p.seg_ptr[base + lane + 1], static_cast<int64_t>(p.N));
-        mine = b < e && p.seg_adapter[base + lane] == a;
-      }
-      uint32_t todo = __ballot_sync(0xffffffffu, mine);
+    // the adapter's segments among 32, one a lane
+    auto walk = [&](int64_t begin, int64_t end, int32_t adapter) {
+      begin = max(begin, int64_t{0});
+      end = min(end, static_cast<int64_t>(p.N));
+      uint32_t todo = __ballot_sync(0xffffffffu, begin < end && adapter == a);
       while (todo && ok) {
         const int i = __ffs(todo) - 1;
         todo &= todo - 1;
-        const int32_t sb = __shfl_sync(0xffffffffu, static_cast<int32_t>(b), i);
-        const int32_t se = __shfl_sync(0xffffffffu, static_cast<int32_t>(e), i);
+        const int32_t sb = __shfl_sync(0xffffffffu, static_cast<int32_t>(begin), i);
+        const int32_t se = __shfl_sync(0xffffffffu, static_cast<int32_t>(end), i);
         for (int32_t n = sb; n < se; n = se - n > kK ? n + kK : se) {
           const bool take = turn == part;
           if (++turn == p.split) turn = 0;
@@ -137,6 +134,17 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
           __syncwarp();
           advance();
         }
+      }
+    };
+    if (p.n_seg <= kFewSegments) {
+      const FewSegments few(p.seg_ptr, p.seg_adapter, p.n_seg);
+#pragma unroll
+      for (int g = 0; g < kFewGroups; ++g) walk(few.begin[g], few.end[g], few.adapter[g]);
+    } else {
+      for (int32_t base = 0; base < p.n_seg && ok; base += 32) {
+        const int32_t s = base + lane;
+        const bool in = s < p.n_seg;
+        walk(in ? p.seg_ptr[s] : 0, in ? p.seg_ptr[s + 1] : 0, in ? p.seg_adapter[s] : -1);
       }
     }
     if (ok) {
