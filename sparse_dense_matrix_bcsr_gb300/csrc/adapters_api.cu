@@ -373,7 +373,7 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
   w.M = m;
   w.N = p.N;
   w.K = k;
-  w.up_tiles = w.split = w.q = 0;
+  w.tiles = w.up_tiles = w.split = w.q = 0;
   w.status = p.status;
   w.wait_limit_ns = p.wait_limit_ns;
   CUDA_TRY(spmm::launch_adapter_wgrad(w, p.num_sms, bf16, s), "adapter weight gradient launch");

@@ -340,7 +340,7 @@ struct AdapterWgradParams {
   const int32_t *seg_adapter;
   int32_t n_seg, n_adapters, rank;
   int32_t M, N, K;
-  int32_t up_tiles, split, q;    // filled in by the launch
+  int32_t tiles, up_tiles, split, q;  // filled in by the launch
   uint32_t *status;
   uint64_t wait_limit_ns;
 };

@@ -44,17 +44,17 @@ __device__ __forceinline__ int32_t checked_adapter(int32_t a, int32_t n_adapters
 constexpr int kFewGroups = 4;
 constexpr int32_t kFewSegments = 32 * kFewGroups;
 
-// Lane l holds segments l, l + 32, ... of such a batch; segments that do not
+// Lane l holds segments first + l, first + l + 32, ...; segments that do not
 // exist are empty.
 struct FewSegments {
   int64_t begin[kFewGroups], end[kFewGroups];
   int32_t adapter[kFewGroups];
   __device__ __forceinline__ FewSegments(const int64_t *__restrict__ seg_ptr, const int32_t *__restrict__ seg_adapter,
-                                         int32_t n_seg) {
+                                         int32_t n_seg, int32_t first = 0) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int g = 0; g < kFewGroups; ++g) {
-      const int32_t s = 32 * g + lane;
+      const int32_t s = first + 32 * g + lane;
       const bool in = s < n_seg;
       begin[g] = in ? seg_ptr[s] : 0;
       end[g] = in ? seg_ptr[s + 1] : 0;
