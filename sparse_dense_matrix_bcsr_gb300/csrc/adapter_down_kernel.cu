@@ -11,10 +11,10 @@
 // tile that several segments share is read once per segment, from L2.  (Loading a
 // segment's rows alone, in boxes of 32, 16 or 8 rows, is slower: 22, 28 and 35 us for
 // 20 with 777 rows in 40 segments, 61, 72 and 89 for 46 with 8192 rows in 500 segments
-// of 4096 columns.)  2 N r k FLOP against 2 N k bytes are far below
 // of 4096 columns.)  2 N r k FLOP against 2 N k bytes are far below the tensor
-// rate, so HBM bounds it for prompts.  Few units leave SMs idle: a
-// through distributed shared memory in CTA order (no atomics, no second launch).
+// rate, so HBM bounds it for prompts.  Few units leave SMs idle: a cluster of up to
+// 16 CTAs then splits a unit's columns and adds the fp32 sums through distributed
+// shared memory in CTA order (no atomics, no second launch).
 // One CTA per tile that walked the tile's segments one after another took 56
 // against 20 us for 777 rows in 40 segments (8192 columns, rank 64).
 //
