@@ -29,6 +29,11 @@
 // split over a cluster of up to 8 CTAs, each with a share of the blocks and of
 // the adapters, whose fp32 sums are added through distributed shared memory in
 // CTA order.
+//
+// The tensor cores cut what their fp32 sums shift out instead of rounding it, ~1e-9
+// of the result for every term of a chain.  Where y is bf16 its rounding hides that;
+// where it is fp32, blocks go to 8 accumulators in turn (4 with 64 rows), which are
+// added with rounding.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -47,6 +52,7 @@ constexpr int kTmaWarp = 0, kMmaWarp = 1, kSumWarp0 = 2, kSumWarps = 8;
 constexpr int kThreads = (kSumWarp0 + kSumWarps) * 32;
 constexpr int kUnitDepth = 2;           // units of U (2 KB) in flight per summing warp
 constexpr int kPitch = kBlk + 4;        // floats per row of y in shared memory
+constexpr int kAccCols = 256;           // TMEM columns of the accumulators where the output is fp32, half an SM's
 constexpr int kMiscBytes = 2560;
 constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
 
@@ -209,7 +215,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int32_t row0 = blockIdx.y * p.tile;
   const int32_t rows = min(p.N - row0, p.tile);
   const int32_t feats = min(p.M - br * kBlk, kBlk);
-  const uint32_t tmem_cols = p.tile < 32 ? 32 : p.tile;
+  const uint32_t acc_cols = p.tile < 32 ? 32 : p.tile;
+  const uint32_t n_acc = OUT_BF16 ? 1 : kAccCols / acc_cols;
+  const uint32_t tmem_cols = OUT_BF16 ? acc_cols : kAccCols;
   const int64_t row_begin = p.block_row_ptr[br];
   const int64_t blocks = p.block_row_ptr[br + 1] - row_begin;
 
@@ -308,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) mbar_arrive(smem_addr(&mi->listed));
 
     const uint32_t idesc = idesc_f16(BF16, false, false, kBlk, static_cast<uint32_t>(p.tile));
-    uint32_t stage = 0, phase = 0;
+    uint32_t stage = 0, phase = 0, acc = 0, accumulate = 0;
     bool ok = true;
     for (int64_t j = jb; j < je;) {
       // how many stages in a row are there, a lane each; one wait for all of them
@@ -329,7 +337,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint64_t a = smem_desc_sw128(st, 16, 1024), b = smem_desc_sw128(st + kBlkBytes, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_f16_elect(tmem, smem_desc_add(a, kk * 32), smem_desc_add(b, kk * 32), idesc, (j > jb || kk > 0) ? 1u : 0u);
+          umma_f16_elect(tmem + acc * acc_cols, smem_desc_add(a, kk * 32), smem_desc_add(b, kk * 32), idesc,
+                         kk > 0 ? 1u : accumulate);
+        if (++acc == n_acc) {
+          acc = 0;
+          accumulate = 1;
+        }
         if (j + p.q < je) umma_commit_elect(smem_addr(&mi->empty[stage]));  // the stage is filled once more
         if (++stage == static_cast<uint32_t>(p.q)) {
           stage = 0;
@@ -380,13 +393,19 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool ok = mbar_wait_warp(smem_addr(&mi->acc_full), 0, p.wait_limit_ns);
       if (!ok) give_up();
       tc_fence_after_sync();
+      const uint32_t used = static_cast<uint32_t>(min(je - jb, static_cast<int64_t>(n_acc)));
       for (int c0 = (warp - kSumWarp0) / 4 * 16; c0 < p.tile && ok; c0 += 32) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(sp * 32) << 16) + c0, v);
-        tmem_ld_wait();
+        float sum[16] = {};
+        for (uint32_t i = 0; i < used; ++i) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(sp * 32) << 16) + i * acc_cols + c0, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum[e] += __uint_as_float(v[e]);
+        }
         if (lane < 16)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) y[(c0 + i) * kPitch + sp * 16 + lane] += __uint_as_float(v[i]);
+          for (int e = 0; e < 16; ++e) y[(c0 + e) * kPitch + sp * 16 + lane] += sum[e];
       }
     }
   }

@@ -21,8 +21,13 @@
 // The gradient wants two such products of a batch, of X and of dY: one launch
 // runs both, so that short batches fill the GPU with their sum.
 //
-// Where the projection's output is fp32, H is kept as two 16-bit parts (the
-// value rounded, and the rest rounded), which holds 16 (bf16) or 22 (fp16) bits.
+// Where the projection's output is fp32, H is kept in 16-bit parts (the value
+// rounded, the rest rounded, ...): two of fp16 hold 22 bits, three of bf16 24 (two
+// of bf16, 16 bits, left 1.2e-6 of Y off where the adapters are most of it, three
+// 0.6e-6; 777 rows of 8192 columns in 40 segments, rank 64, take 112 for 90 us).  The
+// sums then leave the tensor cores, which cut what an fp32 sum shifts out instead of
+// rounding it (~1e-9 of the sum for every term), every kTurn stages and are added
+// in registers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -39,6 +44,8 @@ constexpr int kMaxQ = 8;
 constexpr int kMaxSplit = 16;           // CTAs of a cluster (above 8 a kernel has to ask for it)
 constexpr int kThreads = 192;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2;
+constexpr int kNbuf = 2;                // accumulators
+constexpr int kTurn = 8;                // stages between two drains of the accumulator (TURNS)
 constexpr int kMiscBytes = 1024;
 constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
 
@@ -52,7 +59,7 @@ __host__ __device__ constexpr int d_bytes(int rank, bool transposed) {
 __host__ __device__ constexpr int part_pitch(int rank) { return rank16(rank) + 4; }  // floats per row of the CTA's sums
 
 struct Misc {
-  uint64_t full[kMaxQ], empty[kMaxQ], acc_full;
+  uint64_t full[kMaxQ], empty[kMaxQ], acc_full[kNbuf], acc_empty[kNbuf], drained;
   RowPiece piece;
   uint32_t tmem;
   volatile int32_t abort_flag;
@@ -75,22 +82,25 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
-// Eight ranks of one row of H, rounded; with two parts also what the rounding left.
+// Eight ranks of one row of H, rounded; a further part holds what the roundings
+// before it left (nothing of what is infinite in 16 bits).
 template <bool BF16>
-__device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int64_t N, int32_t rank, int32_t j, int parts,
-                                        const float (&v)[8]) {
-  uint32_t hi[4], lo[4];
+__device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int64_t N, int32_t rank, int32_t j, int parts, float (&v)[8]) {
+  for (int q = 0; q < parts; ++q) {
+    uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    hi[i] = pack2<BF16>(v[2 * i], v[2 * i + 1]);
-    const float2 f = unpack2<BF16>(hi[i]);
-    lo[i] = pack2<BF16>(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+    for (int i = 0; i < 4; ++i) {
+      w[i] = pack2<BF16>(v[2 * i], v[2 * i + 1]);
+      const float2 f = unpack2<BF16>(w[i]);
+      v[2 * i] = isinf(f.x) ? 0.0f : v[2 * i] - f.x;
+      v[2 * i + 1] = isinf(f.y) ? 0.0f : v[2 * i + 1] - f.y;
+    }
+    *reinterpret_cast<uint4 *>(H + (q * N + row) * rank + j) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  *reinterpret_cast<uint4 *>(H + row * rank + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  if (parts == 2) *reinterpret_cast<uint4 *>(H + (N + row) * rank + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
-template <bool BF16>
+// TURNS: the sums leave the tensor cores every kTurn stages.
+template <bool BF16, bool TURNS>
 __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_constant__ AdapterDownParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -104,8 +114,9 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
   Misc *mi = reinterpret_cast<Misc *>(smem + p.q * stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n16 = rank16(p.rank);
-  uint32_t tmem_cols = 32;
-  while (static_cast<int>(tmem_cols) < n16) tmem_cols <<= 1;
+  uint32_t acc_cols = 32;
+  while (static_cast<int>(acc_cols) < n16) acc_cols <<= 1;
+  const uint32_t tmem_cols = TURNS ? kNbuf * acc_cols : acc_cols;
 
   if (warp == kTmaWarp) {
     if (lane == 0) {
@@ -113,7 +124,11 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
         mbar_init(smem_addr(&mi->full[q]), 1);
         mbar_init(smem_addr(&mi->empty[q]), 1);
       }
-      mbar_init(smem_addr(&mi->acc_full), 1);
+      for (int b = 0; b < kNbuf; ++b) {
+        mbar_init(smem_addr(&mi->acc_full[b]), 1);
+        mbar_init(smem_addr(&mi->acc_empty[b]), 4);
+      }
+      mbar_init(smem_addr(&mi->drained), 1);
       mi->abort_flag = 0;
       fence_barrier_init();
       tma_prefetch_desc(&job.tmX);
@@ -183,6 +198,14 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       for (int32_t c = k_begin; c < k_end; ++c) {
+        const int32_t i = c - k_begin;
+        const uint32_t turn = TURNS ? i / kTurn : 0, buf = turn % kNbuf, acc = tmem + buf * acc_cols;
+        const bool first = TURNS ? i % kTurn == 0 : i == 0;
+        if (TURNS && first) {
+          const bool r = mbar_wait_warp(smem_addr(&mi->acc_empty[buf]), ((turn / kNbuf) & 1u) ^ 1u, p.wait_limit_ns);
+          ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
+          if (!ok) break;
+        }
         const bool r = mbar_wait_warp(smem_addr(&mi->full[stage]), phase, p.wait_limit_ns);
         ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
         if (!ok) break;
@@ -192,55 +215,98 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
         const uint64_t d = smem_desc_sw128(st + kXBytes, lbo, 1024);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_f16_elect(tmem, smem_desc_add(x, kk * 32), smem_desc_add(d, kk * step), idesc,
-                         (c == k_begin && kk == 0) ? 0u : 1u);
+          umma_f16_elect(acc, smem_desc_add(x, kk * 32), smem_desc_add(d, kk * step), idesc, (first && kk == 0) ? 0u : 1u);
         umma_commit_elect(smem_addr(&mi->empty[stage]));
+        if (c == k_end - 1 || (TURNS && i % kTurn == kTurn - 1)) umma_commit_elect(smem_addr(&mi->acc_full[buf]));
         if (++stage == static_cast<uint32_t>(p.q)) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      if (!ok && lane == 0) {
-        atomicOr(p.status, kDevTimeout);
-        mi->abort_flag = 1;
+      if (!ok) {
+        if (lane == 0) {
+          atomicOr(p.status, kDevTimeout);
+          mi->abort_flag = 1;
+        }
+        __syncwarp();
+        // nothing may be in flight when the block ends
+        umma_commit_elect(smem_addr(&mi->drained));
+        mbar_wait_warp(smem_addr(&mi->drained), 0, 1000000ull);
+        if (lane == 0)
+          for (int b = 0; b < kNbuf; ++b) mbar_arrive(smem_addr(&mi->acc_full[b]));
       }
-      __syncwarp();
-      umma_commit_elect(smem_addr(&mi->acc_full));  // also waits for what was issued when giving up
     }
     if (warp >= kEpiWarp0) {
       const int sp = warp & 3;
       const int r = sp * 32 + lane;
-      const bool ok = mbar_wait_warp(smem_addr(&mi->acc_full), 0, p.wait_limit_ns);
-      if (!ok && lane == 0) {
-        atomicOr(p.status, kDevTimeout);
-        mi->abort_flag = 1;
-      }
-      tc_fence_after_sync();
-      float *sums = reinterpret_cast<float *>(smem);  // the stages are done with
+      float *sums = reinterpret_cast<float *>(smem);  // the stages are done with by then
       const float f = p.scale[piece.adapter];
       const bool mine = row0 + r >= piece.begin && row0 + r < piece.end;
-      for (int c0 = 0; c0 < n16 && ok; c0 += 16) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(sp * 32) << 16) + c0, v);
+      bool ok = true;
+      auto wait_acc = [&](uint32_t turn) {
+        const bool there = mbar_wait_warp(smem_addr(&mi->acc_full[turn % kNbuf]), (turn / kNbuf) & 1u, p.wait_limit_ns);
+        ok = __shfl_sync(0xffffffffu, there && !mi->abort_flag, 0);
+        if (!ok && lane == 0) {
+          atomicOr(p.status, kDevTimeout);
+          mi->abort_flag = 1;
+        }
+        tc_fence_after_sync();
+      };
+      auto load16 = [&](uint32_t buf, int c0, uint32_t (&v)[16]) {
+        tmem_ld_32x32b_x16(tmem + buf * acc_cols + (static_cast<uint32_t>(sp * 32) << 16) + c0, v);
         tmem_ld_wait();
+      };
+      // ranks c0 .. c0 + 15 of row r
+      auto put16 = [&](int c0, const float *v) {
         if (p.split > 1) {
           float4 *dst = reinterpret_cast<float4 *>(sums + r * part_pitch(p.rank) + c0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
-                                 __uint_as_float(v[4 * i + 3]));
+          for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         } else if (mine) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (c0 + 8 * h >= p.rank) continue;
             float o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = f * __uint_as_float(v[8 * h + i]);
+            for (int i = 0; i < 8; ++i) o[i] = f * v[8 * h + i];
             store_h<BF16>(job.H, row0 + r, p.N, p.rank, c0 + 8 * h, job.parts, o);
           }
         }
+      };
+      if constexpr (TURNS) {
+        float sum[kMaxRank] = {};
+        const int32_t turns = (k_end - k_begin + kTurn - 1) / kTurn;
+        for (int32_t t = 0; t < turns && ok; ++t) {
+          wait_acc(t);
+          if (!ok) break;
+#pragma unroll
+          for (int c0 = 0; c0 < kMaxRank; c0 += 16) {
+            if (c0 < n16) {
+              uint32_t v[16];
+              load16(t % kNbuf, c0, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum[c0 + i] += __uint_as_float(v[i]);
+            }
+          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&mi->acc_empty[t % kNbuf]));
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < kMaxRank; c0 += 16)
+          if (c0 < n16 && ok) put16(c0, sum + c0);
+      } else {
+        wait_acc(0);
+        for (int c0 = 0; c0 < n16 && ok; c0 += 16) {
+          uint32_t v[16];
+          load16(0, c0, v);
+          float o[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(v[i]);
+          put16(c0, o);
+        }
+        tc_fence_before_sync();
       }
-      tc_fence_before_sync();
     }
   }
   if (p.split > 1) {
@@ -296,12 +362,15 @@ cudaError_t launch_adapter_down(AdapterDownParams p, int num_sms, bool bf16, cud
   p.q = (kSmemLimit - kMiscBytes - 1024) / p.stage_bytes;
   if (p.q > kMaxQ) p.q = kMaxQ;
   const int smem = p.q * p.stage_bytes + kMiscBytes + 1024;
-  auto kern = bf16 ? adapter_down_kernel<true> : adapter_down_kernel<false>;
-  static std::atomic<uint64_t> smem_set[2];
-  cudaError_t e = set_smem_limit_once(kern, kSmemLimit, smem_set[bf16 ? 1 : 0]);
+  const bool turns = p.exact != 0;
+  auto kern = bf16 ? (turns ? adapter_down_kernel<true, true> : adapter_down_kernel<true, false>)
+                   : (turns ? adapter_down_kernel<false, true> : adapter_down_kernel<false, false>);
+  const int variant = (bf16 ? 2 : 0) + (turns ? 1 : 0);
+  static std::atomic<uint64_t> smem_set[4];
+  cudaError_t e = set_smem_limit_once(kern, kSmemLimit, smem_set[variant]);
   if (e != cudaSuccess) return e;
-  static std::atomic<uint64_t> cluster_set[2];
-  e = allow_large_clusters_once(kern, cluster_set[bf16 ? 1 : 0]);
+  static std::atomic<uint64_t> cluster_set[4];
+  e = allow_large_clusters_once(kern, cluster_set[variant]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.jobs * units * p.split));

@@ -23,13 +23,17 @@ struct spmm_adapters_s {
   int num_sms = 0;
   bool sm103 = false;
 
-  float *d_h = nullptr;        // max_rows x rank: scale * D x, or as many values in two 16-bit parts
+  float *d_h = nullptr;        // max_rows x rank: scale * D x, in fp32 or in up to three 16-bit parts
   float *d_dh = nullptr;       // gradient: max_rows x rank: scale * U^T dy
   spmm::TileSegment *d_tile_segs = nullptr;  // the projection's row tiles: their segments with an adapter
   int32_t *d_tile_count = nullptr;
 };
 
 namespace {
+
+// 16-bit parts of H (fp16: 22 bits, bf16: 24) in the products whose result is h's output.
+constexpr int kMaxHParts = 3;
+int h_parts(spmm_handle h) { return h->out_t != SPMM_F32 ? 1 : h->in_t == SPMM_BF16 ? kMaxHParts : 2; }
 
 void free_adapters(spmm_adapters a) {
   if (!a) return;
@@ -109,8 +113,8 @@ struct DownJob {
 };
 
 // One or two such products, with the lists of the projection's tiles.
-spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, std::initializer_list<DownJob> jobs, int tile_rows,
-                         cudaStream_t s) {
+spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, std::initializer_list<DownJob> jobs, bool exact,
+                         int tile_rows, cudaStream_t s) {
   const bool bf16 = a->in_t == SPMM_BF16;
   spmm::AdapterDownParams d;
   std::memset(&d, 0, sizeof d);
@@ -126,6 +130,7 @@ spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, std::ini
     o.parts = j.parts;
     o.transposed = j.transposed ? 1 : 0;
   }
+  d.exact = exact ? 1 : 0;
   d.tile_segs = a->d_tile_segs;
   d.tile_count = a->d_tile_count;
   d.scale = p.scale;
@@ -149,7 +154,7 @@ spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams
   const bool bf16 = h->in_t == SPMM_BF16, out_bf16 = h->out_t == SPMM_BF16;
   CUtensorMap tmX, tmY;
   spmm::LinearAdapters ad;
-  ad.box = p.rank <= 16 ? 16 : p.rank <= 32 ? 32 : 64;
+  ad.box = p.rank <= 16 ? 16 : p.rank <= 32 || parts > 2 ? 32 : 64;
   spmm_status st = spmm::encode_x(&tmX, p.X, bf16, p.N, p.K);
   if (st == SPMM_OK) st = spmm::encode_y(&tmY, p.Y, out_bf16, p.N, p.M, spmm::linear_tile_rows(tile));
   if (st == SPMM_OK && transposed) st = spmm::encode_3d(&ad.tmU, p.up, bf16, p.n_adapters, p.rank, p.M, ad.box);
@@ -213,9 +218,11 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
   p.M = static_cast<int32_t>(h->m);
   p.K = static_cast<int32_t>(h->k);
   if (!rows_path(p.N, p.rank, p.n_seg)) {
-    const int parts = h->out_t == SPMM_F32 ? 2 : 1;
-    const spmm::LinearTile tile = spmm::linear_adapters_tile(h->n_groups, h->n_units, p.N, p.n_seg, p.num_sms);
-    const spmm_status st = down_project(a, p, {{X, down, a->d_h, p.K, parts, false}}, spmm::linear_tile_rows(tile), s);
+    const int parts = h_parts(h);
+    const spmm::LinearTile tile = spmm::linear_adapters_tile(h->n_groups, h->n_units, p.N, p.n_seg, h->out_t == SPMM_BF16,
+                                                               p.num_sms);
+    const spmm_status st = down_project(a, p, {{X, down, a->d_h, p.K, parts, false}}, parts > 1,
+                                        spmm::linear_tile_rows(tile), s);
     return st != SPMM_OK ? st : up_project(h, a, p, parts, false, tile, s);
   }
   spmm::AdapterDecodeParams d;
@@ -281,7 +288,8 @@ spmm_status spmm_adapters_create(spmm_adapters *out, int64_t m, int64_t k, int32
     CUDA_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, a->device), "device attribute");
     CUDA_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, a->device), "device attribute");
     a->sm103 = major == 10 && minor == 3;
-    const size_t h = static_cast<size_t>(std::max<int64_t>(max_rows, 1)) * rank * sizeof(float);
+    const size_t h = static_cast<size_t>(std::max<int64_t>(max_rows, 1)) * rank *
+                     std::max(sizeof(float), in_t == SPMM_BF16 ? kMaxHParts * sizeof(uint16_t) : 0);
     CUDA_TRY(cudaMalloc(&a->d_h, h), "cudaMalloc(adapter activations)");
     // one entry per row of the tiles, one count per tile of the smallest
     const size_t rows = (static_cast<size_t>(max_rows) / spmm::kMaxTileRows + 1) * spmm::kMaxTileRows;
@@ -343,11 +351,13 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
     return SPMM_OK;
   }
   // H and dH, then dX with the roles of the adapters' two matrices exchanged
-  const int parts = dX && h_t->out_t == SPMM_F32 ? 2 : 1;
-  const spmm::LinearTile tile = spmm::linear_adapters_tile(h_t->n_groups, h_t->n_units, p.N, p.n_seg, p.num_sms);
+  const int parts = dX ? h_parts(h_t) : 1;
+  const spmm::LinearTile tile = spmm::linear_adapters_tile(h_t->n_groups, h_t->n_units, p.N, p.n_seg, h_t->out_t == SPMM_BF16,
+                                                               p.num_sms);
   const DownJob of_x{X, down, a->d_h, k, 1, false}, of_dy{dY, up, a->d_dh, m, parts, true};
-  st = m > k ? down_project(a, p, {of_dy, of_x}, spmm::linear_tile_rows(tile), s)  // the longer first
-             : down_project(a, p, {of_x, of_dy}, spmm::linear_tile_rows(tile), s);
+  const bool exact = h_t->out_t == SPMM_F32;  // with or without dX: the same d_up and d_down
+  st = m > k ? down_project(a, p, {of_dy, of_x}, exact, spmm::linear_tile_rows(tile), s)  // the longer first
+             : down_project(a, p, {of_x, of_dy}, exact, spmm::linear_tile_rows(tile), s);
   if (st == SPMM_OK && dX) {
     p.X = dY;
     p.Y = dX;

@@ -47,6 +47,16 @@
 // X and writes Y once; a second pass over Y would move 5 GB more for 64K tokens x
 // 18944 features.  The gradient's dX takes D_a where the forward pass takes U_a,
 // as it lies (MN-major).
+//
+// The tensor cores cut what their fp32 sums shift out instead of rounding it, ~1e-9
+// of the result for every term.  Where Y is bf16 its rounding hides that.  An fp32 Y
+// with adapters has its accumulator handed to the epilogue every kTurn blocks (512
+// terms), whose warps keep a 256-row tile's sums in registers and add with rounding:
+// 6.6e-7 off in place of 2.7e-6 with 777 rows of 8192 x 8192, 75 % zero blocks (90 us
+// either way), and in place of 2.2e-5 with 18944 dense columns; 3584 x 18944, 16384
+// rows, 409 for 398 us.  Every 4 blocks: 3.8e-7, and up to 4 % slower; every 16:
+// 1.2e-6 and as fast as 8.  Tiles of 512 rows, whose sums the registers cannot hold,
+// are for fp32 only where block rows average less than a turn.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -66,6 +76,7 @@ constexpr int kNbuf = 2;                       // TMEM accumulators per CTA
 constexpr int kThreads = 192;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2, kEpiWarps = 4;
 constexpr int kMiscBytes = 1024;
+constexpr int kTurn = 8;                       // blocks between two drains (fp32 outputs with adapters)
 
 // A tile of ROWS rows of X, CTAS CTAs per SM.
 template <int ROWS, int CTAS>
@@ -85,7 +96,7 @@ struct Tile {
   static_assert(CTAS * kTmemCols <= 512, "TMEM");
 };
 
-constexpr int32_t kRecEmpty = 1, kRecEnd = 2, kRecAdapters = 4, kRecLast = 8;
+constexpr int32_t kRecEmpty = 1, kRecEnd = 2, kRecAdapters = 4, kRecLast = 8, kRecMore = 16;
 // What the producer tells the MMA warp with a tile's first stage: the tile, how
 // many stages of blocks it has and whether adapters follow.  With a stage of an
 // adapter: its steps of 16 ranks, its rows of the tile (begin | end << 16), the
@@ -110,6 +121,14 @@ __device__ __forceinline__ void tile_coords(int64_t t, int n_block_rows, int n_t
   nt = static_cast<int>(g) * GROUP + static_cast<int>(r % gsz);
 }
 
+// Parts (128 rows) of the tile that a stage of an adapter holds: all of them, or as
+// many as leave room for H's 16-bit parts.
+template <int PARTS, bool OUT_BF16>
+__device__ __forceinline__ int stage_parts(const LinearAdapters &ad) {
+  if constexpr (OUT_BF16) return PARTS;
+  return PARTS > ad.parts ? PARTS / ad.parts : 1;
+}
+
 // Y's store boxes: 32 rows (a warp's lanes of one part) x 128 or 64 bytes.
 template <bool IN_BF16, bool OUT_BF16, class T, class Adapters>
 __global__ void __launch_bounds__(kThreads, T::kCtas)
@@ -119,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
   constexpr bool kAdapt = std::is_same_v<Adapters, LinearAdapters>;
   constexpr int kQ = T::kQ, kStageBytes = T::kStageBytes, kStagingBytes = T::kStagingBytes;
   constexpr int kAccCols = T::kAccCols, kTmemCols = T::kTmemCols, kTileN = T::kRows;
+  constexpr bool kTurns = kAdapt && !OUT_BF16 && T::kRows == 256;
   constexpr int kOutBytes = OUT_BF16 ? 2 : 4;
   constexpr int kBoxCols = T::kBoxBytes / kOutBytes;  // features per box row
   constexpr int kBoxes = kBlk / kBoxCols;             // store boxes per warp and part
@@ -310,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
             for (int i = 0; i < cnt && ok; ++i) {
               const int32_t a = __shfl_sync(0xffffffffu, my.adapter, i);
               const int32_t begin = __shfl_sync(0xffffffffu, my.begin, i), end = __shfl_sync(0xffffffffu, my.end, i);
-              const int group = T::kParts / ad.parts;  // parts of the tile that a stage holds
+              const int group = stage_parts<T::kParts, OUT_BF16>(ad);
               for (int g = begin / 128 / group * group; g * 128 < end && ok; g += group) {
                 const int h0 = max(begin / 128, g), h1 = min((end + 127) / 128, g + group);
                 for (int32_t r0 = 0; r0 < ad.rank; r0 += ad.box) {
@@ -401,11 +421,32 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
         }
         break;
       }
-      const uint32_t acc = tmem + buf * kAccCols;
+      uint32_t acc = tmem + buf * kAccCols;
+      // the accumulator to the epilogue
+      auto hand_over = [&](int32_t flags) {
+        if (leader) {
+          acc_rec[buf].br = rec.br;
+          acc_rec[buf].nt = rec.nt;
+          acc_rec[buf].flags = flags;
+          mbar_arrive(accf0 + 8 * buf);
+        }
+        __syncwarp();
+        umma_commit_elect(accf0 + 8 * buf);
+        ++tcount;
+      };
       if (rec.flags & kRecEmpty) {
         release();
       } else {
         for (int j = 0; j < rec.stages; ++j) {
+          if constexpr (kTurns) {
+            if (j > 0 && j % kTurn == 0) {
+              hand_over(kRecMore);
+              buf = tcount % kNbuf;
+              ok = wait_phase(acce0 + 8 * buf, ((tcount / kNbuf) & 1u) ^ 1u);
+              if (!ok) break;
+              acc = tmem + buf * kAccCols;
+            }
+          }
           if (j > 0) {
             ok = wait_full();
             if (!ok) break;
@@ -413,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
           tc_fence_after_sync();
           const uint64_t bdesc0 = smem_desc_add(blk_desc, stage * kStageBytes);
           const uint64_t adesc0 = smem_desc_add(x_desc, stage * kStageBytes);
-          const uint32_t accumulate = j > 0 ? 1u : 0u;
+          const uint32_t accumulate = (kTurns ? j % kTurn : j) > 0 ? 1u : 0u;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
@@ -431,18 +472,19 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
             tc_fence_after_sync();
             const TileRec seg = tile_rec[stage];
             more = (seg.flags & kRecLast) == 0;
-            const int begin = seg.rows & 0xffff, end = seg.rows >> 16, group = T::kParts / ad.parts;
+            const int begin = seg.rows & 0xffff, end = seg.rows >> 16;
+            const int parts = OUT_BF16 ? 1 : ad.parts, group = stage_parts<T::kParts, OUT_BF16>(ad);
             const uint64_t bdesc0 = smem_desc_add(u_desc, stage * kStageBytes);
             const uint64_t adesc0 = smem_desc_add(h_desc, stage * kStageBytes);
             if (begin <= 128 * seg.part && end >= 128 * (seg.part + group)) {
               // the segment holds all rows of the stage: no lanes to mask; as for the
               // blocks, MMAs in a row go to different accumulators
               for (int kk = 0; kk < seg.stages; ++kk) {
+                for (int q = 0; q < parts; ++q) {
 #pragma unroll
-                for (int i = 0; i < T::kParts; ++i) {  // slot i: part i of H, or of its second 16 bits
-                  const int h = seg.part + (i < group ? i : i - group);
-                  umma_f16_elect(acc + h * kBlk, smem_desc_add(adesc0, i * h_part + kk * 32),
-                                 smem_desc_add(bdesc0, kk * u_step), u_idesc, 1u);
+                  for (int i = 0; i < group; ++i)
+                    umma_f16_elect(acc + (seg.part + i) * kBlk, smem_desc_add(adesc0, (q * group + i) * h_part + kk * 32),
+                                   smem_desc_add(bdesc0, kk * u_step), u_idesc, 1u);
                 }
               }
             } else {
@@ -451,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
                 if (end <= 128 * h || begin >= 128 * (h + 1)) continue;
                 uint32_t off[4];
                 lanes_off(begin - 128 * h, end - 128 * h, off);
-                for (int q = 0; q < ad.parts; ++q) {
+                for (int q = 0; q < parts; ++q) {
                   const uint64_t adesc = smem_desc_add(adesc0, (q * group + i) * h_part);
                   for (int kk = 0; kk < seg.stages; ++kk)
                     umma_f16_lanes_elect(acc + h * kBlk, smem_desc_add(adesc, kk * 32), smem_desc_add(bdesc0, kk * u_step),
@@ -464,15 +506,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
         }
         if (!ok) break;
       }
-      if (leader) {
-        acc_rec[buf].br = rec.br;
-        acc_rec[buf].nt = rec.nt;
-        acc_rec[buf].flags = rec.flags & kRecEmpty;
-        mbar_arrive(accf0 + 8 * buf);
-      }
-      __syncwarp();
-      umma_commit_elect(accf0 + 8 * buf);
-      ++tcount;
+      hand_over(rec.flags & kRecEmpty);
     }
     if (!ok) {
       if (leader) {
@@ -498,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
     uint8_t *stg = staging + (warp - kEpiWarp0) * (32 * T::kBoxBytes);
     const uint32_t row_sw = static_cast<uint32_t>(T::kBoxBytes == 128 ? lane & 7 : (lane >> 1) & 3);
     uint32_t tcount = 0;
+    float sum[kTurns ? kAccCols : 1] = {};  // fp32 with adapters: the tile's sums so far
     while (true) {
       const uint32_t buf = tcount % kNbuf;
       const bool r = mbar_wait_warp(accf0 + 8 * buf, (tcount / kNbuf) & 1u, p.wait_limit_ns);
@@ -515,6 +550,43 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
       const int n0 = acc_rec[buf].nt * kTileN + sp * 32;
       tc_fence_after_sync();
       const uint32_t tbase = tmem + (static_cast<uint32_t>(sp * 32) << 16) + buf * kAccCols;
+      if constexpr (kTurns) {
+        if (!zero) {
+#pragma unroll
+          for (int c = 0; c < kAccCols; c += 16) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(tbase + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
+          }
+          tc_fence_before_sync();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acce0 + 8 * buf);
+        ++tcount;
+        if (flags & kRecMore) continue;
+#pragma unroll
+        for (int c = 0; c < kAccCols; c += kBoxCols) {  // a box: kBoxCols features of part c / kBlk
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+          uint8_t *row = stg + lane * T::kBoxBytes;
+#pragma unroll
+          for (int q = 0; q < kBoxCols / 4; ++q)
+            *reinterpret_cast<float4 *>(row + ((static_cast<uint32_t>(q) ^ row_sw) << 4)) =
+                make_float4(sum[c + 4 * q], sum[c + 4 * q + 1], sum[c + 4 * q + 2], sum[c + 4 * q + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int y = n0 + c / kBlk * 128, m = m0 + c % kBlk;
+            if (y < p.N && m < p.M) tma_store_2d(&tmY, smem_addr(stg), m, y);
+            bulk_commit_group();
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kAccCols; ++c) sum[c] = 0.0f;
+        continue;
+      }
 #pragma unroll 1
       for (int box = 0; box < T::kParts * kBoxes; ++box) {
         const int h = box / kBoxes;               // part of the tile
@@ -613,11 +685,11 @@ template <class T, class Adapters>
 cudaError_t launch_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY, const BcsrParams &p,
                                const Adapters &ad, bool in_bf16, bool out_bf16, cudaStream_t stream) {
   if (p.n_block_rows == 0 || p.N == 0) return cudaSuccess;
-  if (in_bf16)
-    return out_bf16 ? launch_linear_variant<true, true, T>(tmA, tmX, tmY, p, ad, stream)
-                    : launch_linear_variant<true, false, T>(tmA, tmX, tmY, p, ad, stream);
-  return out_bf16 ? launch_linear_variant<false, true, T>(tmA, tmX, tmY, p, ad, stream)
-                  : launch_linear_variant<false, false, T>(tmA, tmX, tmY, p, ad, stream);
+  if (out_bf16)
+    return in_bf16 ? launch_linear_variant<true, true, T>(tmA, tmX, tmY, p, ad, stream)
+                   : launch_linear_variant<false, true, T>(tmA, tmX, tmY, p, ad, stream);
+  return in_bf16 ? launch_linear_variant<true, false, T>(tmA, tmX, tmY, p, ad, stream)
+                 : launch_linear_variant<false, false, T>(tmA, tmX, tmY, p, ad, stream);
 }
 
 }  // namespace
@@ -631,12 +703,15 @@ cudaError_t launch_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const 
 //   fewer, short block rows, many tiles (65536 rows, 18944 x 3584, 9): 1477 / 1386 / 1218
 //   few tiles (2048 rows in 4):                                         83 /   70 /   71
 //   fewer, block rows of 16 blocks or more (16384 rows, 3584 x 18944):  380 /  411 /  390
-LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t N, int64_t n_seg, int num_sms) {
+// (bf16 outputs; an fp32 Y of 512-row tiles needs short block rows, see the top.)
+LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t N, int64_t n_seg, bool out_bf16,
+                                int num_sms) {
   const int64_t row_tiles = (N + 255) / 256;
   if (n_block_rows * row_tiles <= num_sms) return LinearTile::k256;
   if (n_seg >= row_tiles) return LinearTile::k256x2;
   if (n_blocks >= 16 * n_block_rows) return LinearTile::k256;
-  return n_block_rows * ((N + 511) / 512) >= 8ll * num_sms ? LinearTile::k512 : LinearTile::k256x2;
+  if (n_block_rows * ((N + 511) / 512) < 8ll * num_sms) return LinearTile::k256x2;
+  return out_bf16 || n_blocks < kTurn * n_block_rows ? LinearTile::k512 : LinearTile::k256x2;
 }
 
 cudaError_t launch_bcsr_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,
