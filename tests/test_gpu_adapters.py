@@ -409,3 +409,34 @@ def test_refusals(S):
         with pytest.raises(S.SpmmError) as e:
             S.spmm_adapters_create(m, k, n_adapters, rank)
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("n,in_t", [(3, "f16"), (300, "f16"), (300, "bf16")])
+def test_long_fp32_sums_are_rounded(S, n, in_t):
+    """Sums of 16384 positive terms into fp32.  The tensor cores cut up to two units of
+    2^-23 of an accumulator per step of 16 terms; a chain of 512 terms and an adapter's
+    48 has 35 such steps, one of h 32, and the chains are added with rounding.  Left in
+    one accumulator, the 1024 steps would lose several times as much."""
+    import torch
+    c = Case(128, 16384, n, [0, n // 2, n], [1, 0], 16, 2, in_t, "f32", keep=1.0)
+    c.vals &= np.uint16(0x7FFF)
+    for name in ("W", "X", "down", "up"):
+        setattr(c, name, getattr(c, name).abs())
+    y = c.X.double() @ c.W.t()
+    sums = 2 * 35 * 2.0 ** -23 + (16384 // 512 + 8) * 2.0 ** -24
+    bound = sums * y
+    for b, e, a in c.spans():
+        h = float(c.scale[a]) * (c.X[b:e].double() @ c.down[a].double().t())
+        uh = h @ c.up[a].double().t()
+        y[b:e] += uh
+        bound[b:e] += (2 * sums + TWO_PARTS["f16"]) * uh
+    close(run(S, c)[0], y, bound, "Y")
+
+
+def test_infinite_in_16_bits_is_not_nan(S):
+    """An h above fp16's range counts as infinite where it is a matrix operand, in every part."""
+    import torch
+    c = Case(64, 64, 300, [0, 300], [0], 8, 1, "f16", "f32", keep=1.0)
+    c.X, c.down, c.up = torch.full_like(c.X, 60.0), torch.full_like(c.down, 60.0), torch.full_like(c.up, 1.0)
+    y = run(S, c)[0]
+    assert (y == float("inf")).all()
