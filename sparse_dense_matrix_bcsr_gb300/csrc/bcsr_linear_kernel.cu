@@ -30,7 +30,8 @@
 // one user out helps little, taking several out does: without X's copies 1043
 // us, without 7/8 of the MMAs 1047, without stores 991, without the epilogue's
 // memory work 869, without both operands' copies 860, without copies and MMAs 656
-// (the roles' handshakes).  X is used once per block, as random blocks share no
+// (the roles' handshakes).  Storing from registers in 32-byte pieces instead of
+// through the staging area takes 1235.  X is used once per block, as random blocks share no
 // columns with the row above, so there is no reuse to gain.  Tiles of 512 rows
 // (the block read and the handshakes shared by twice the rows, three stages of 72
 // KB in place of five of 40) measured 1057 us, and 8 % more on long block rows
