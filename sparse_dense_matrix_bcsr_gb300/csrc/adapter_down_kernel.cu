@@ -85,7 +85,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
 // Eight ranks of one row of H, rounded; a further part holds what the roundings
 // before it left (nothing of what is infinite in 16 bits).
 template <bool BF16>
-__device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int64_t N, int32_t rank, int32_t j, int parts, float (&v)[8]) {
+__device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int32_t rank, int32_t j, int parts, float (&v)[8]) {
   for (int q = 0; q < parts; ++q) {
     uint32_t w[4];
 #pragma unroll
@@ -95,7 +95,7 @@ __device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int64_t N, int
       v[2 * i] = isinf(f.x) ? 0.0f : v[2 * i] - f.x;
       v[2 * i + 1] = isinf(f.y) ? 0.0f : v[2 * i + 1] - f.y;
     }
-    *reinterpret_cast<uint4 *>(H + (q * N + row) * rank + j) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(H + (row * parts + q) * rank + j) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
             float o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = f * v[8 * h + i];
-            store_h<BF16>(job.H, row0 + r, p.N, p.rank, c0 + 8 * h, job.parts, o);
+            store_h<BF16>(job.H, row0 + r, p.rank, c0 + 8 * h, job.parts, o);
           }
         }
       };
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
         cluster_sum8(base + (r * part_pitch(p.rank) + j) * 4, p.split, o);
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] *= f;
-        store_h<BF16>(job.H, row0 + r, p.N, p.rank, j, job.parts, o);
+        store_h<BF16>(job.H, row0 + r, p.rank, j, job.parts, o);
       }
     }
     cluster_sync();  // the others may still read this CTA's sums

@@ -12,13 +12,19 @@
 // operands before the MMA, as neither operand may hold another request's
 // infinities.  Every element of dY and X is read once, so HBM bounds the kernel;
 // S is read again by every feature tile, from L2.  16384 rows of 4 adapters of rank
-// 64, 18944 + 3584 features: 118 us, 6.3 TB/s of activations.
+// 64, 18944 + 3584 features: 117 us, 6.3 TB/s of activations.
+//
+// S comes in two 16-bit parts (the value rounded, and the rest rounded), whose sums
+// are added at the end: rounded once, h and dh alone would put the gradients'
+// error at 1.4 times what rounding the result to 16 bits does (up to 1.6 with few rows).
+// Up to rank 64 the parts lie side by side and one MMA of N = 2 rank takes both; one
+// MMA for each takes 121 us in place of 117, and a single part 102.
 //
 // With items enough for every SM, CTAs (two per SM) are persistent and take items
 // in turn, two TMEM accumulators alternating, so one item's sums are stored while
 // the next one's rows arrive.  A CTA per item instead, each with a start and an end
-// of its own: 37 us for this kernel's 24 with 100 segments of 20 rows (20 adapters of rank
-// 32, 4096 + 4096 features), 52 for 39 with 4096 rows of 4 adapters of rank 64
+// of its own, with one part of S: 37 us for 24 with 100 segments of 20 rows (20 adapters of
+// rank 32, 4096 + 4096 features), 52 for 39 with 4096 rows of 4 adapters of rank 64
 // (18944 + 3584 features), 109 for 75 with 500 segments of 16 rows.  With fewer
 // items a cluster of up to 8 CTAs shares one: an adapter's stages are dealt to it
 // in turn and it adds its fp32 sums through distributed shared memory in CTA order.
@@ -36,18 +42,26 @@ constexpr int kFeat = 128;            // features per CTA
 constexpr int kK = 64;                // rows per stage
 constexpr int kBox = kK * 128;        // one box: 64 rows x 64 columns
 constexpr int kVBytes = kFeat / 64 * kBox;
+constexpr int kSParts = kWgradParts;
+constexpr int kJointRank = 64;        // up to this rank one MMA takes both parts
+static_assert(kSParts == 2, "the MMA loop");
 constexpr int kMaxQ = 4;
 constexpr int kThreads = 192;
-constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2;
+constexpr int kTmaWarp = 0, kMmaWarp = 1;
 constexpr int kMiscBytes = 1024;
 constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
 
 __host__ __device__ constexpr int rank16(int rank) { return (rank + 15) / 16 * 16; }
 __host__ __device__ constexpr int rank_boxes(int rank) { return (rank + 63) / 64; }
+// Boxes of S in a stage: its parts side by side, or (too wide for an accumulator) each
+// by itself.
+__host__ __device__ constexpr int s_boxes(int rank) {
+  return rank <= kJointRank ? rank_boxes(kSParts * rank) : kSParts * rank_boxes(rank);
+}
 __host__ __device__ constexpr int part_pitch(int rank) { return rank16(rank) + 4; }
 
-constexpr int kNbuf = 2;              // accumulators: 2 x kMaxRank columns, twice an SM
-static_assert(2 * kNbuf * kMaxRank <= 512, "TMEM columns");
+constexpr int kNbuf = 2;              // accumulators
+static_assert(2 * kNbuf * kMaxRank <= 512 && 2 * kNbuf * kSParts * kJointRank <= 512, "TMEM columns of two CTAs");
 
 struct Misc {
   uint64_t full[kMaxQ], empty[kMaxQ], acc_full[kNbuf], acc_empty[kNbuf], drained;
@@ -98,16 +112,18 @@ template <bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid_constant__ AdapterWgradParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int boxes = rank_boxes(p.rank);
+  const bool joint = p.rank <= kJointRank;
+  const int rb = rank_boxes(p.rank), boxes = s_boxes(p.rank);
   const int stage_bytes = kVBytes + boxes * kBox;
   Misc *mi = reinterpret_cast<Misc *>(smem + p.q * stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t part = SPLIT ? blockIdx.x % p.split : 0, split = SPLIT ? p.split : 1;
   const int64_t first = blockIdx.x / split, step = gridDim.x / split;  // this CTA's items
   const int64_t items = SPLIT ? first + 1 : static_cast<int64_t>(p.tiles) * p.n_adapters;
-  const int n16 = rank16(p.rank);
+  const int n16 = rank16(p.rank);                  // ranks of an accumulator
+  const int mma_n = joint ? kSParts * p.rank : n16;
   uint32_t acc_cols = 32;
-  while (static_cast<int>(acc_cols) < n16) acc_cols <<= 1;
+  while (static_cast<int>(acc_cols) < mma_n) acc_cols <<= 1;
 
   if (threadIdx.x == 0) {
     for (int q = 0; q < p.q; ++q) {
@@ -183,7 +199,10 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
               mbar_arrive_expect_tx(fb, stage_bytes);
               tma_load_2d(st, tmV, fb, item.f0, n);
               tma_load_2d(st + kBox, tmV, fb, item.f0 + 64, n);
-              for (int c = 0; c < boxes; ++c) tma_load_2d(st + kVBytes + c * kBox, tmS, fb, c * 64, n);
+              for (int c = 0; c < boxes; ++c) {
+                const int32_t col = joint ? c * 64 : c / rb * p.rank + c % rb * 64;
+                tma_load_2d(st + kVBytes + c * kBox, tmS, fb, col, n);
+              }
             }
             __syncwarp();
             advance();
@@ -214,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
           mbar_wait(smem_addr(&mi->full[i % p.q]), static_cast<uint32_t>((i / p.q) & 1), 1000000ull);
     }
   } else if (warp == kMmaWarp) {
-    const uint32_t idesc = idesc_f16(BF16, /*a_mn_major=*/true, /*b_mn_major=*/true, kFeat, static_cast<uint32_t>(n16));
+    const uint32_t idesc = idesc_f16(BF16, /*a_mn_major=*/true, /*b_mn_major=*/true, kFeat, static_cast<uint32_t>(mma_n));
     uint32_t stage = 0, phase = 0, count = 0;
     bool ok = true;
     for (int64_t it = first; it < items && ok; it += step, ++count) {
@@ -244,8 +263,10 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
           const uint32_t st = smem_addr(smem + stage * stage_bytes);
           const uint64_t v = smem_desc_sw128(st, kBox, 1024);
           const uint64_t s = smem_desc_sw128(st + kVBytes, kBox, 1024);
-          for (int kk = 0; kk < steps; ++kk)
+          for (int kk = 0; kk < steps; ++kk) {
             umma_f16_elect(acc, smem_desc_add(v, kk * 2048), smem_desc_add(s, kk * 2048), idesc, (any || kk > 0) ? 1u : 0u);
+            if (!joint) umma_f16_elect(acc, smem_desc_add(v, kk * 2048), smem_desc_add(s, rb * kBox + kk * 2048), idesc, 1u);
+          }
           any = true;
         }
         umma_commit_elect(smem_addr(&mi->empty[stage]));
@@ -283,27 +304,28 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
       const Item item(p, it);
       const bool any = mi->any[buf];
       for (int c0 = 0; c0 < n16; c0 += 16) {
-        uint32_t v[16];
+        float v[16] = {};
         if (any) {
-          tmem_ld_32x32b_x16(tmem + buf * acc_cols + (static_cast<uint32_t>(sp * 32) << 16) + c0, v);
+          uint32_t hi[16], lo[16];
+          const uint32_t at = tmem + buf * acc_cols + (static_cast<uint32_t>(sp * 32) << 16) + c0;
+          tmem_ld_32x32b_x16(at, hi);
+          if (joint) tmem_ld_32x32b_x16(at + p.rank, lo);
           tmem_ld_wait();
-        } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = 0u;
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(hi[i]) + (joint ? __uint_as_float(lo[i]) : 0.0f);
         }
         if constexpr (SPLIT) {
           float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(smem) + r * part_pitch(p.rank) + c0);  // the stages are done with
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            dst[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
-                                 __uint_as_float(v[4 * i + 3]));
+            dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         } else if (item.f0 + r < item.F) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (c0 + 8 * h >= p.rank) continue;
             float o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(v[8 * h + i]);
+            for (int i = 0; i < 8; ++i) o[i] = v[8 * h + i];
             store_grad<BF16>(p, item, r, c0 + 8 * h, o);
           }
         }
@@ -343,7 +365,7 @@ cudaError_t launch_adapter_wgrad(AdapterWgradParams p, int num_sms, bool bf16, c
   p.tiles = p.up_tiles + (p.K + kFeat - 1) / kFeat;
   // Items of adapters that can have rows.  While clusters of twice the size still fit
   // beside each other and leave each CTA at least four stages, they are the faster
-  // (us with 1 / 2 / 4 / 8 CTAs an item, 16384 rows; 16 items, rank 64: 96 / 60 / 43 /
+  // (us with 1 / 2 / 4 / 8 CTAs an item and one part of S, 16384 rows; 16 items, rank 64: 96 / 60 / 43 /
   // 36; 64 items, rank 16: 69 / 46 / 41 / 49; 128 items, rank 64: 67 / 53 / 63 / 95); with
   // more items they only wait for one another (176: 119 / 153 / 150 / 179; 256: 61 / 58 /
   // 79 / 135, and 30 / 34 / 48 / 76 for 4096 rows).
@@ -351,7 +373,7 @@ cudaError_t launch_adapter_wgrad(AdapterWgradParams p, int num_sms, bool bf16, c
   p.split = 1;
   while (p.split < 8 && p.tiles * active * p.split * 2 <= 2ll * num_sms && p.N >= 8ll * kK * active * p.split) p.split *= 2;
   const bool split = p.split > 1;
-  const int stage = kVBytes + rank_boxes(p.rank) * kBox;
+  const int stage = kVBytes + s_boxes(p.rank) * kBox;
   p.q = (kSmemLimit - kMiscBytes - 1024) / stage;
   if (p.q > kMaxQ) p.q = kMaxQ;
   const int smem = p.q * stage + kMiscBytes + 1024;

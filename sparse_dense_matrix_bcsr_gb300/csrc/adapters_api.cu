@@ -122,7 +122,7 @@ spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, std::ini
     spmm::AdapterDownJob &o = d.job[d.jobs++];
     spmm_status st = spmm::encode_2d(&o.tmX, j.X, bf16, p.N, j.K, j.K, 128, 64);
     if (st != SPMM_OK) return st;
-    st = j.transposed ? spmm::encode_3d(&o.tmD, j.D, bf16, p.n_adapters, j.K, p.rank, 64)
+    st = j.transposed ? spmm::encode_3d(&o.tmD, j.D, bf16, p.n_adapters, j.K, p.rank, 1, 64)
                       : spmm::encode_2d(&o.tmD, j.D, bf16, static_cast<uint64_t>(p.n_adapters) * p.rank, j.K, j.K, p.rank, 64);
     if (st != SPMM_OK) return st;
     o.H = reinterpret_cast<uint16_t *>(j.H);
@@ -148,8 +148,8 @@ spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, std::ini
 }
 
 // Y = X W^T + U H per row, H and the tile lists from down_project; U n_adapters x
-// M x rank, or transposed n_adapters x rank x M.
-spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams &p, int parts, bool transposed,
+// M x rank, or transposed n_adapters x rank x M; the first `parts` of H's `stored` parts.
+spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams &p, int parts, int stored, bool transposed,
                        spmm::LinearTile tile, cudaStream_t s) {
   const bool bf16 = h->in_t == SPMM_BF16, out_bf16 = h->out_t == SPMM_BF16;
   CUtensorMap tmX, tmY;
@@ -157,13 +157,12 @@ spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams
   ad.box = p.rank <= 16 ? 16 : p.rank <= 32 || parts > 2 ? 32 : 64;
   spmm_status st = spmm::encode_x(&tmX, p.X, bf16, p.N, p.K);
   if (st == SPMM_OK) st = spmm::encode_y(&tmY, p.Y, out_bf16, p.N, p.M, spmm::linear_tile_rows(tile));
-  if (st == SPMM_OK && transposed) st = spmm::encode_3d(&ad.tmU, p.up, bf16, p.n_adapters, p.rank, p.M, ad.box);
+  if (st == SPMM_OK && transposed) st = spmm::encode_3d(&ad.tmU, p.up, bf16, p.n_adapters, p.rank, p.M, 1, ad.box);
   if (st == SPMM_OK && !transposed)
     st = spmm::encode_2d(&ad.tmU, p.up, bf16, static_cast<uint64_t>(p.n_adapters) * p.M, p.rank, p.rank, 64, ad.box,
                          ad.box * 2);
   if (st == SPMM_OK)
-    st = spmm::encode_2d(&ad.tmH, p.H, bf16, static_cast<uint64_t>(parts) * p.N, p.rank, p.rank, 128, ad.box,
-                         ad.box * 2);
+    st = spmm::encode_3d(&ad.tmH, p.H, bf16, p.N, stored, p.rank, 128, 1, ad.box, ad.box * 2);
   if (st != SPMM_OK) return st;
   ad.tile_segs = a->d_tile_segs;
   ad.tile_count = a->d_tile_count;
@@ -223,7 +222,7 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
                                                                p.num_sms);
     const spmm_status st = down_project(a, p, {{X, down, a->d_h, p.K, parts, false}}, parts > 1,
                                         spmm::linear_tile_rows(tile), s);
-    return st != SPMM_OK ? st : up_project(h, a, p, parts, false, tile, s);
+    return st != SPMM_OK ? st : up_project(h, a, p, parts, parts, false, tile, s);
   }
   spmm::AdapterDecodeParams d;
   std::memset(&d, 0, sizeof d);
@@ -354,7 +353,9 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
   const int parts = dX ? h_parts(h_t) : 1;
   const spmm::LinearTile tile = spmm::linear_adapters_tile(h_t->n_groups, h_t->n_units, p.N, p.n_seg, h_t->out_t == SPMM_BF16,
                                                                p.num_sms);
-  const DownJob of_x{X, down, a->d_h, k, 1, false}, of_dy{dY, up, a->d_dh, m, parts, true};
+  const int stored = std::max(parts, spmm::kWgradParts);
+  const DownJob of_x{X, down, a->d_h, k, spmm::kWgradParts, false},
+      of_dy{dY, up, a->d_dh, m, stored, true};
   const bool exact = h_t->out_t == SPMM_F32;  // with or without dX: the same d_up and d_down
   st = m > k ? down_project(a, p, {of_dy, of_x}, exact, spmm::linear_tile_rows(tile), s)  // the longer first
              : down_project(a, p, {of_x, of_dy}, exact, spmm::linear_tile_rows(tile), s);
@@ -365,13 +366,13 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
     p.up = down;
     p.M = k;
     p.K = m;
-    st = up_project(h_t, a, p, parts, true, tile, s);
+    st = up_project(h_t, a, p, parts, stored, true, tile, s);
   }
   spmm::AdapterWgradParams w;
   if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dy, dY, bf16, N, m, m, 64, 64);
   if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_x, X, bf16, N, k, k, 64, 64);
-  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_h, a->d_h, bf16, N, a->rank, a->rank, 64, 64);
-  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dh, a->d_dh, bf16, N, a->rank, a->rank, 64, 64);
+  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_h, a->d_h, bf16, N, spmm::kWgradParts * a->rank, spmm::kWgradParts * a->rank, 64, 64);
+  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dh, a->d_dh, bf16, N, spmm::kWgradParts * a->rank, stored * a->rank, 64, 64);
   if (st != SPMM_OK) return st;
   w.d_up = static_cast<uint16_t *>(d_up);
   w.d_down = static_cast<uint16_t *>(d_down);

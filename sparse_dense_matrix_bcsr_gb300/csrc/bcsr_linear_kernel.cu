@@ -351,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
                       tma_load_2d(st, &ad.tmU, fb, r0, a * p.M + br * kBlk);
                     for (int q = 0; q < ad.parts; ++q)
                       for (int h = h0; h < h1; ++h)
-                        tma_load_2d(st + kBlkBytes + (q * group + h - g) * part_bytes, &ad.tmH, fb, r0,
-                                    q * p.N + nt * kTileN + h * 128);
+                        tma_load_3d(st + kBlkBytes + (q * group + h - g) * part_bytes, &ad.tmH, fb, r0, q,
+                                    nt * kTileN + h * 128);
                   }
                   advance();
                 }

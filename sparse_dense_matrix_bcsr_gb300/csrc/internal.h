@@ -127,10 +127,9 @@ struct TileSegment {
 // The adapters of the same product (launch_bcsr_linear_adapters): tmU covers
 // the up matrices as [n_adapters * M rows, rank cols] with 64 x box boxes (or,
 // u_transposed, matrices of [n_adapters, rank rows, M cols] with box x 64 boxes,
-// 128-byte swizzle), tmH
-// covers H as [parts * N rows, rank cols] with 128 x box boxes, both swizzled in
-// the width of a box row; box = 16, 32 or 64 ranks; parts > 1: H is the sum of
-// its parts.
+// 128-byte swizzle), tmH covers H as [N rows, parts, rank cols] with 128 x 1 x box
+// boxes, both swizzled in the width of a box row; box = 16, 32 or 64 ranks; H is
+// the sum of its first `parts` parts.
 struct LinearAdapters {
   CUtensorMap tmU, tmH;
   const TileSegment *tile_segs;  // device, the tile's rows per tile
@@ -286,7 +285,7 @@ struct AdapterDownJob {
   CUtensorMap tmX;               // X as [N rows, K cols], 128 x 64 boxes, 128-byte swizzle
   CUtensorMap tmD;               // the down matrices as [n_adapters * rank rows, K cols], rank x 64 boxes, 128-byte
                                  // swizzle; transposed: as [n_adapters, K rows, rank cols], 64 x 64 boxes
-  uint16_t *H;                   // device, parts x N x rank: the rows of segments with an adapter
+  uint16_t *H;                   // device, N x parts x rank: the rows of segments with an adapter
   int32_t K, parts, transposed;
 };
 struct AdapterDownParams {
@@ -333,8 +332,10 @@ cudaError_t launch_adapter_decode(const CUtensorMap &tmA, const CUtensorMap &tmX
                                   bool bf16, bool out_bf16, cudaStream_t s);
 
 // Gradients of the adapters' weights (adapter_wgrad_kernel.cu).  tm_dy and tm_x
-// cover dY [N rows, M cols] and X [N rows, K cols], tm_h and tm_dh H and dH
-// [N rows, rank cols], all with 64 x 64 boxes, 128-byte swizzle.
+// cover dY [N rows, M cols] and X [N rows, K cols], tm_h and tm_dh the first
+// kWgradParts parts of H and dH [N rows, parts * rank cols], all with 64 x 64 boxes,
+// 128-byte swizzle.
+constexpr int kWgradParts = 2;
 struct AdapterWgradParams {
   CUtensorMap tm_dy, tm_x, tm_h, tm_dh;
   uint16_t *d_up, *d_down;
