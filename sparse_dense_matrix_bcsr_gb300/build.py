@@ -19,7 +19,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspmm_gb300.so")
 
 SOURCES = ["bcsr_kernel.cu", "bcsr_linear_kernel.cu", "wcsr_kernel.cu", "wcsr64_kernel.cu", "spmm_api.cu",
-           "adapters.cu", "adapter_decode_kernel.cu", "adapter_down_kernel.cu", "adapter_wgrad_kernel.cu", "route.cu",
+           "adapters.cu", "adapter_decode_kernel.cu", "adapter_down_kernel.cu", "adapter_wgrad_kernel.cu",
+           "adapter_group_kernel.cu", "route.cu",
            "adapters_api.cu", "format.cpp"]
 HEADERS = ["ptx.cuh", "internal.h", "format.h", "split_reduce.cuh", "handle.h", "segments.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -331,6 +331,26 @@ struct AdapterDecodeParams {
 cudaError_t launch_adapter_decode(const CUtensorMap &tmA, const CUtensorMap &tmX, AdapterDecodeParams p, int num_sms,
                                   bool bf16, bool out_bf16, cudaStream_t s);
 
+// Rows of a batch of at most kGroupRows sorted by adapter (adapter_group_kernel.cu):
+// row n's place, and the groups as segments of the sorted batch, n_groups of them
+// (at least as many as there can be adapters among the rows; the rest are empty).
+constexpr int kGroupRows = 1024;
+struct AdapterGroupParams {
+  const int64_t *seg_ptr;
+  const int32_t *seg_adapter;
+  int32_t n_seg, n_adapters, N, n_groups;
+  int32_t *place;          // device, N
+  int64_t *group_ptr;      // device, n_groups + 1
+  int32_t *group_adapter;  // device, n_groups
+  uint32_t *status;
+};
+// ... with X's rows (k of 16 bits) and dY's (m) copied to their places,
+cudaError_t launch_adapter_group(const AdapterGroupParams &p, const void *X, void *xs, int64_t k, const void *dY, void *dys,
+                                 int64_t m, cudaStream_t s);
+// and rows copied back from them.
+cudaError_t launch_adapter_ungroup(const int32_t *place, int64_t N, const void *src, void *dst, int64_t row_bytes,
+                                   cudaStream_t s);
+
 // Gradients of the adapters' weights (adapter_wgrad_kernel.cu).  tm_dy and tm_x
 // cover dY [N rows, M cols] and X [N rows, K cols], tm_h and tm_dh the first
 // kWgradParts parts of H and dH [N rows, parts * rank cols], all with 64 x 64 boxes,

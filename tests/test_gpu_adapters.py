@@ -440,3 +440,55 @@ def test_infinite_in_16_bits_is_not_nan(S):
     c.X, c.down, c.up = torch.full_like(c.X, 60.0), torch.full_like(c.down, 60.0), torch.full_like(c.up, 1.0)
     y = run(S, c)[0]
     assert (y == float("inf")).all()
+
+
+@pytest.mark.parametrize("m,k,n,segs,rank,n_adapters,in_t,out_t", [
+    pytest.param(1032, 2056, 300, singles(300, 7), 16, 7, "bf16", "bf16", id="300-single-rows"),
+    pytest.param(2056, 520, 1024, singles(1024, 40, seed=3), 72, 40, "f16", "f32", id="1024-single-rows"),
+    pytest.param(4104, 2056, 16, singles(16, 2), 8, 2, "bf16", "f32", id="16-single-rows"),
+    pytest.param(1032, 1032, 200, ragged(200, 1500, 5, gaps=True), 24, 5, "bf16", "f32", id="1500-segments-mostly-empty"),
+    pytest.param(1032, 1032, 700, ragged(700, 300, 200), 16, 200, "f16", "bf16", id="200-adapters"),
+])
+def test_gradients_of_many_short_segments(S, m, k, n, segs, rank, n_adapters, in_t, out_t):
+    """Batches whose rows are sorted by adapter on the way."""
+    c = Case(m, k, n, *segs, rank, n_adapters, in_t, out_t, keep=0.1)
+    got = run_grad(S, c)
+    for name, (value, bound) in c.reference_grad().items():
+        close(got[name], value, bound, name)
+    again = run_grad(S, c, with_dx=False)
+    for name in ("d_down", "d_up"):
+        assert np.array_equal(got[name].double().numpy(), again[name].double().numpy()), f"{name}: runs differ"
+
+
+def test_a_broken_adapter_keeps_to_itself_among_sorted_rows(S):
+    import torch
+    n = 300
+    ptr, ids = np.arange(n + 1), (np.arange(n) % 3).astype(np.int32)
+    c = Case(1032, 2056, n, ptr, ids, 16, 3)
+    ref = c.reference_grad()
+    c.down[1, 0, 0], c.up[1, 3, 1] = float("inf"), float("nan")
+    got = run_grad(S, c)
+    fine = torch.from_numpy(ids != 1)
+    close(got["dX"][fine], ref["dX"][0][fine], ref["dX"][1][fine], "dX of other rows")
+    for name in ("d_down", "d_up"):
+        for a in (0, 2):
+            close(got[name][a], ref[name][0][a], ref[name][1][a], f"{name}[{a}]")
+
+
+def test_sorted_rows_report_an_index_outside_the_pool(S):
+    import torch
+    n = 300
+    ids = (np.arange(n) % 3).astype(np.int32)
+    ids[7] = 5
+    c = Case(1032, 2056, n, np.arange(n + 1), ids, 16, 3)
+    layer_t, aset = c.layer(S, transposed=True), c.set(S)
+    X, dY, batch = c.X.cuda(), c.dY.cuda(), c.batch()
+    dX, dD, dU = torch.empty_like(X), torch.empty_like(batch[0]), torch.empty_like(batch[1])
+    aset.grad(layer_t, X, dY, dX, dD, dU, *batch)
+    torch.cuda.synchronize()
+    assert layer_t.check() == S.SPMM_ERR_DEVICE_CHECK
+    for name, got in (("dX", dX), ("d_down", dD), ("d_up", dU)):
+        value, bound = c.reference_grad()[name]
+        close(got.cpu(), value, bound, name)
+    layer_t.close()
+    aset.close()
