@@ -368,10 +368,14 @@ cudaError_t launch_adapter_wgrad(AdapterWgradParams p, int num_sms, bool bf16, c
   // (us with 1 / 2 / 4 / 8 CTAs an item and one part of S, 16384 rows; 16 items, rank 64: 96 / 60 / 43 /
   // 36; 64 items, rank 16: 69 / 46 / 41 / 49; 128 items, rank 64: 67 / 53 / 63 / 95); with
   // more items they only wait for one another (176: 119 / 153 / 150 / 179; 256: 61 / 58 /
-  // 79 / 135, and 30 / 34 / 48 / 76 for 4096 rows).
+  // 79 / 135, and 30 / 34 / 48 / 76 for 4096 rows).  Clusters are not persistent, so the
+  // items of adapters without rows limit them too (one adapter of 28 with 740 rows, 143
+  // tiles: 25 / 135).
   const int64_t active = p.n_seg < p.n_adapters ? (p.n_seg > 0 ? p.n_seg : 1) : p.n_adapters;
   p.split = 1;
-  while (p.split < 8 && p.tiles * active * p.split * 2 <= 2ll * num_sms && p.N >= 8ll * kK * active * p.split) p.split *= 2;
+  while (p.split < 8 && p.tiles * active * p.split * 2 <= 2ll * num_sms && p.N >= 8ll * kK * active * p.split &&
+         p.tiles * static_cast<int64_t>(p.n_adapters) * p.split * 2 <= 8ll * num_sms)
+    p.split *= 2;
   const bool split = p.split > 1;
   const int stage = kVBytes + s_boxes(p.rank) * kBox;
   p.q = (kSmemLimit - kMiscBytes - 1024) / stage;
