@@ -173,12 +173,15 @@ spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams
                          ad.box * 2);
   if (st == SPMM_OK)
     st = spmm::encode_3d(&ad.tmH, p.H, bf16, p.N, stored, p.rank, 128, 1, ad.box, ad.box * 2);
+  if (st == SPMM_OK)
+    st = spmm::encode_3d(&ad.tmHs, p.H, bf16, p.N, stored, p.rank, spmm::kAdapterFewRows, 1, ad.box, ad.box * 2);
   if (st != SPMM_OK) return st;
   ad.tile_segs = a->d_tile_segs;
   ad.tile_count = a->d_tile_count;
   ad.rank = p.rank;
   ad.parts = parts;
   ad.u_transposed = transposed ? 1 : 0;
+  ad.few = p.N <= 128 ? 1 : 0;
   ad.tile = tile;
   spmm::BcsrParams b;
   std::memset(&b, 0, sizeof b);

@@ -49,6 +49,13 @@
 // 18944 features.  The gradient's dX takes D_a where the forward pass takes U_a,
 // as it lies (MN-major).
 //
+// A stage of an adapter loads H by 128 rows, whatever the segment has of them.
+// Batches of at most 128 rows load segments of a few rows by 16 instead (`few`):
+// there every CTA reads the same lines of H for every adapter, and L2 cannot serve them
+// fast enough (dX of 79 rows with 38 adapters, 13752 features: 229 us, by 16 rows 125; 53
+// rows: 300 and 147).  Where H is larger the large box is faster (8192 rows in 500
+// segments: 139 us against 161).
+//
 // The tensor cores cut what their fp32 sums shift out instead of rounding it, ~1e-9
 // of the result for every term.  Where Y is bf16 its rounding hides that.  An fp32 Y
 // with adapters has its accumulator handed to the epilogue every kTurn blocks (512
@@ -77,6 +84,7 @@ constexpr int kNbuf = 2;                       // TMEM accumulators per CTA
 constexpr int kThreads = 192;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2, kEpiWarps = 4;
 constexpr int kMiscBytes = 1024;
+constexpr int kFewRows = kAdapterFewRows, kFewBoxes = 2;  // boxes of H for short segments
 constexpr int kTurn = 8;                       // blocks between two drains (fp32 outputs with adapters)
 
 // A tile of ROWS rows of X, CTAS CTAs per SM.
@@ -344,15 +352,34 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
                     const uint32_t fb = full0 + 8 * stage;
                     const uint32_t st = smem_addr(smem + stage * kStageBytes);
                     const uint32_t part_bytes = 128 * ad.box * 2;
-                    mbar_arrive_expect_tx(fb, kBlk * ad.box * 2 + (h1 - h0) * ad.parts * part_bytes);
-                    if (ad.u_transposed)
-                      tma_load_3d(st, &ad.tmU, fb, br * kBlk, r0, a);
-                    else
-                      tma_load_2d(st, &ad.tmU, fb, r0, a * p.M + br * kBlk);
-                    for (int q = 0; q < ad.parts; ++q)
-                      for (int h = h0; h < h1; ++h)
-                        tma_load_3d(st + kBlkBytes + (q * group + h - g) * part_bytes, &ad.tmH, fb, r0, q,
-                                    nt * kTileN + h * 128);
+                    auto copy_u = [&] {
+                      if (ad.u_transposed)
+                        tma_load_3d(st, &ad.tmU, fb, br * kBlk, r0, a);
+                      else
+                        tma_load_2d(st, &ad.tmU, fb, r0, a * p.M + br * kBlk);
+                    };
+                    const int row0 = nt * kTileN;
+                    if (!ad.few) {
+                      mbar_arrive_expect_tx(fb, kBlk * ad.box * 2 + (h1 - h0) * ad.parts * part_bytes);
+                      copy_u();
+                      for (int q = 0; q < ad.parts; ++q)
+                        for (int h = h0; h < h1; ++h)
+                          tma_load_3d(st + kBlkBytes + (q * group + h - g) * part_bytes, &ad.tmH, fb, r0, q, row0 + h * 128);
+                    } else {
+                      // the batch is one part: boxes of kFewRows rows that hold the segment's, or the large one
+                      const uint32_t few_bytes = kFewRows * ad.box * 2;
+                      const int b0 = begin / kFewRows, n = (end + kFewRows - 1) / kFewRows - b0;
+                      mbar_arrive_expect_tx(fb, kBlk * ad.box * 2 + ad.parts * (n <= kFewBoxes ? n * few_bytes : part_bytes));
+                      copy_u();
+                      for (int q = 0; q < ad.parts; ++q) {
+                        const uint32_t at = st + kBlkBytes + q * group * part_bytes;
+                        if (n > kFewBoxes)
+                          tma_load_3d(at, &ad.tmH, fb, r0, q, row0);
+                        else
+                          for (int b = b0; b < b0 + n; ++b)
+                            tma_load_3d(at + b * few_bytes, &ad.tmHs, fb, r0, q, row0 + b * kFewRows);
+                      }
+                    }
                   }
                   advance();
                 }

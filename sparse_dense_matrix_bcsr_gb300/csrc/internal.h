@@ -128,14 +128,16 @@ struct TileSegment {
 // the up matrices as [n_adapters * M rows, rank cols] with 64 x box boxes (or,
 // u_transposed, matrices of [n_adapters, rank rows, M cols] with box x 64 boxes,
 // 128-byte swizzle), tmH covers H as [N rows, parts, rank cols] with 128 x 1 x box
-// boxes, both swizzled in the width of a box row; box = 16, 32 or 64 ranks; H is
+// boxes (tmHs: kAdapterFewRows x 1 x box), all swizzled in the width of a box row; box = 16, 32 or 64 ranks; H is
 // the sum of its first `parts` parts.
+constexpr int kAdapterFewRows = 16;
 struct LinearAdapters {
-  CUtensorMap tmU, tmH;
+  CUtensorMap tmU, tmH, tmHs;
   const TileSegment *tile_segs;  // device, the tile's rows per tile
   const int32_t *tile_count;     // device, per tile: its segments with an adapter
   int32_t rank, parts, box;
   int32_t u_transposed;          // the gradient's: the adapters' down matrices
+  int32_t few;                   // segments of a few rows load H by kAdapterFewRows
   LinearTile tile;
 };
 // Launched as a programmatic dependent of the kernel that writes H and the
