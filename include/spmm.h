@@ -363,8 +363,9 @@ spmm_status spmm_wcsr_noalloc_check(void *stream);
  *   in_t          SPMM_F16 or SPMM_BF16, the type of X and of the adapters.
  *   max_rows, max_segments   the largest batch that calls will bring (below 2^30
  *                 rows, 2^27 segments).
- *   grad          nonzero to hold the workspace of spmm_adapters_grad too (with
- *                 copies of up to 1024 rows of X, dY and dX).
+ *   grad          nonzero to hold the workspace of spmm_adapters_grad too.
+ * The workspace is rank values per row (twice with grad) and copies of up to 1024
+ * rows of X and Y (and dX), as short batches are sorted by adapter.
  * Errors: INVALID_ARG, UNSUPPORTED (m, k or rank not a multiple of 8, rank
  * above 128), OOM, CUDA.  spmm_adapters_destroy waits for the device and frees
  * the set.

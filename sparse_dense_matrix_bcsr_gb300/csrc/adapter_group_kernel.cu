@@ -1,15 +1,15 @@
-// adapter_group_kernel.cu -- rows of a short batch sorted by their adapter, for the
-// gradients (spmm_adapters_grad).
+// adapter_group_kernel.cu -- rows of a short batch sorted by their adapter
+// (spmm_run_linear_adapters, spmm_adapters_grad).
 //
-// The gradients' kernels work in tiles of rows of one segment, and a segment of one
-// row costs them as much as one of 64: 432 segments of one row, 4 adapters of rank 8,
+// The tiled kernels work on rows of one segment, and a segment of one row costs them
+// as much as one of 64: the gradient of 432 segments of one row, 4 adapters of rank 8,
 // through 3880 x 16048 took 1004 us.  A batch with more segments than adapters is
-// therefore sorted first: one CTA gives every row its place (rows of adapter 0, of 1,
-// ..., then those without, each in the batch's order, so the sums' order is fixed),
-// X and dY are copied to their places, the kernels run on one segment per adapter,
-// and dX is copied back: 66 us.  The copies are a few bytes more than the batch's
-// own; the places come from a bitonic sort, 1024 rows one a thread (comparing every
-// row with every other took 30 us longer for 1000 rows).
+// therefore sorted first where that pays (see the rules at the calls): one CTA gives
+// every row its place (rows of adapter 0, of 1, ..., then those without, each in the
+// batch's order, so the sums' order is fixed), X and dY are copied to their places,
+// the kernels run on one segment per adapter, and Y or dX is copied back: 66 us.  The
+// places come from a bitonic sort, 1024 rows one a thread (comparing every row with
+// every other took 30 us longer for 1000 rows).
 #include "internal.h"
 #include "ptx.cuh"
 #include "segments.cuh"
@@ -128,7 +128,7 @@ cudaError_t launch_adapter_group(const AdapterGroupParams &p, const void *X, voi
   const MoveRows rows{{static_cast<const uint4 *>(X), static_cast<const uint4 *>(dY)},
                       {static_cast<uint4 *>(xs), static_cast<uint4 *>(dys)},
                       {k / 8, m / 8}};
-  adapter_move_rows_kernel<<<dim3(static_cast<unsigned>(p.N), 2), kCopyThreads, 0, s>>>(rows, p.place, false);
+  adapter_move_rows_kernel<<<dim3(static_cast<unsigned>(p.N), dY ? 2 : 1), kCopyThreads, 0, s>>>(rows, p.place, false);
   return cudaGetLastError();
 }
 

@@ -25,8 +25,8 @@ struct spmm_adapters_s {
 
   float *d_h = nullptr;        // max_rows x rank: scale * D x, in fp32 or in up to three 16-bit parts
   float *d_dh = nullptr;       // gradient: max_rows x rank: scale * U^T dy
-  // gradient of a short batch: its rows sorted by adapter
-  void *d_xs = nullptr, *d_dys = nullptr, *d_dxs = nullptr;
+  // a short batch's rows sorted by adapter: X, dY or Y, dX
+  void *d_xs = nullptr, *d_ys = nullptr, *d_dxs = nullptr;
   int64_t *d_group_ptr = nullptr;
   int32_t *d_group_adapter = nullptr, *d_place = nullptr;
   spmm::TileSegment *d_tile_segs = nullptr;  // the projection's row tiles: their segments with an adapter
@@ -44,7 +44,7 @@ void free_adapters(spmm_adapters a) {
   cudaFree(a->d_h);
   cudaFree(a->d_dh);
   cudaFree(a->d_xs);
-  cudaFree(a->d_dys);
+  cudaFree(a->d_ys);
   cudaFree(a->d_dxs);
   cudaFree(a->d_group_ptr);
   cudaFree(a->d_group_adapter);
@@ -218,10 +218,60 @@ bool rows_path(int64_t N, int32_t rank, int64_t n_seg) {
   return N <= kMostRows && N * (rank + 24) < 2300 + 290 * n_seg;
 }
 
-// Y = X W^T + adapters.
+// Sorts the batch's rows by adapter: X (and dY) to their places, p's segments one per
+// adapter.
+spmm_status sort_rows(spmm_adapters a, spmm::AdapterParams &p, const void *&X, const void **dY, int64_t groups, cudaStream_t s) {
+  const spmm::AdapterGroupParams g{p.seg_ptr, p.seg_adapter, p.n_seg, p.n_adapters, p.N, static_cast<int32_t>(groups),
+                                   a->d_place, a->d_group_ptr, a->d_group_adapter, p.status};
+  CUDA_TRY(spmm::launch_adapter_group(g, X, a->d_xs, a->k, dY ? *dY : nullptr, a->d_ys, a->m, s), "sorting of rows launch");
+  X = a->d_xs;
+  if (dY) *dY = a->d_ys;
+  p.seg_ptr = a->d_group_ptr;
+  p.seg_adapter = a->d_group_adapter;
+  p.n_seg = g.n_groups;
+  return SPMM_OK;
+}
+
+// As many segments as the sorted rows can have.
+int64_t most_groups(spmm_adapters a, int64_t N, int64_t n_seg) {
+  return std::min({N, n_seg, static_cast<int64_t>(a->n_adapters)});
+}
+
+// Whether the gradients sort the batch's rows by adapter first.  A segment less saves
+// 0.5 us or more, sorting costs ~6 us and 0.5 ps for each of the m + 2 k columns of a
+// row.  Gradients (us) as the rows come / sorted: 432 rows in 432 segments of 4 adapters,
+// 3880 x 16048: 1004 / 66; 500 in 500 of 64, 4096 x 4096: 301 / 79; 16 in 16 of 4,
+// 18944 x 3584: 57 / 40; 1000 in 100 of 20, 4096 x 4096: 71 / 60, in 40: 52 / 62; 300 in 32
+// of 8, 18944 x 3584: 69 / 63; 300 in 16 of 8, 3584 x 18944: 77 / 87.
+bool sorting_pays(spmm_adapters a, int64_t N, int64_t n_seg, int64_t groups) {
+  return N <= spmm::kGroupRows && (n_seg - groups) * 550 > 6000 + N * (a->m + 2 * a->k) / 2000;  // ns
+}
+
+// Whether the projection sorts them and takes the tiled path.  Against the row kernels
+// (us as they come / sorted): 160 single rows of 2 adapters of rank 128, 12424 x 2904: 112 /
+// 31; 421 of 3 of rank 64, 7728 x 3048: 103 / 39; 433 of 25 of rank 24, 12336 x 1056: 86 / 79;
+// 256 of 8 of rank 16, 18944 x 3584: 48 / 42, 3584 x 18944: 33 / 44; 128 of 8: 24 / 35; 512 of
+// 64: 97 / 111.  Against tiles as they come: 1000 rows of rank 64 in 200 segments of 4,
+// 18944 x 3584: 120 / 65; in 100 of 20, rank 32: 85 / 76, 4096 x 4096: 37 / 39; 412 of rank
+// 128 in 109 of 6, 2168 x 624: 69 / 33; 777 in 40 of 24: 70 / 80.  The terms are ns.
+bool sorting_pays_forward(spmm_adapters a, int64_t N, int64_t n_seg, int64_t groups) {
+  if (N > spmm::kGroupRows || n_seg <= groups) return false;
+  if (rows_path(N, a->rank, n_seg))
+    return 26000 + 20 * N + groups * a->m * 7 / 100 < N * (a->rank + 24) * (800 + a->m * 21 / 100) / 1000;
+  return (n_seg - groups) * (150 + a->m / 100) > 14000 + N * (a->k + a->m) / 2000;
+}
+
 spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const void *X, void *Y, const void *down,
                     const void *up, cudaStream_t s) {
   const bool bf16 = h->in_t == SPMM_BF16;
+  const int64_t groups = most_groups(a, p.N, p.n_seg);
+  const bool sorted = sorting_pays_forward(a, p.N, p.n_seg, groups);
+  void *const out = Y;
+  if (sorted) {
+    const spmm_status st = sort_rows(a, p, X, nullptr, groups, s);
+    if (st != SPMM_OK) return st;
+    Y = a->d_ys;
+  }
   p.X = X;
   p.Y = Y;
   p.H = a->d_h;
@@ -229,13 +279,16 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
   p.up = up;
   p.M = static_cast<int32_t>(h->m);
   p.K = static_cast<int32_t>(h->k);
-  if (!rows_path(p.N, p.rank, p.n_seg)) {
+  if (sorted || !rows_path(p.N, p.rank, p.n_seg)) {
     const int parts = h_parts(h);
     const spmm::LinearTile tile = spmm::linear_adapters_tile(h->n_groups, h->n_units, p.N, p.n_seg, h->out_t == SPMM_BF16,
                                                                p.num_sms);
-    const spmm_status st = down_project(a, p, {{X, down, a->d_h, p.K, parts, false}}, parts > 1,
-                                        spmm::linear_tile_rows(tile), s);
-    return st != SPMM_OK ? st : up_project(h, a, p, parts, parts, false, tile, s);
+    spmm_status st = down_project(a, p, {{X, down, a->d_h, p.K, parts, false}}, parts > 1, spmm::linear_tile_rows(tile), s);
+    if (st == SPMM_OK) st = up_project(h, a, p, parts, parts, false, tile, s);
+    if (st == SPMM_OK && sorted)
+      CUDA_TRY(spmm::launch_adapter_ungroup(a->d_place, p.N, Y, out, static_cast<int64_t>(p.M) * (h->out_t == SPMM_F32 ? 4 : 2), s),
+               "return of sorted rows launch");
+    return st;
   }
   spmm::AdapterDecodeParams d;
   std::memset(&d, 0, sizeof d);
@@ -261,16 +314,6 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
   CUDA_TRY(spmm::launch_adapter_decode(h->tm_vals, tmX, d, p.num_sms, bf16, h->out_t == SPMM_BF16, s),
            "projection with adapters launch");
   return SPMM_OK;
-}
-
-// Whether the gradients sort the batch's rows by adapter first.  A segment less saves
-// 0.5 us or more, sorting costs ~6 us and 0.5 ps for each of the m + 2 k columns of a
-// row.  Gradients (us) as the rows come / sorted: 432 rows in 432 segments of 4 adapters,
-// 3880 x 16048: 1004 / 66; 500 in 500 of 64, 4096 x 4096: 301 / 79; 16 in 16 of 4,
-// 18944 x 3584: 57 / 40; 1000 in 100 of 20, 4096 x 4096: 71 / 60, in 40: 52 / 62; 300 in 32
-// of 8, 18944 x 3584: 69 / 63; 300 in 16 of 8, 3584 x 18944: 77 / 87.
-bool sorting_pays(spmm_adapters a, int64_t N, int64_t n_seg, int64_t groups) {
-  return N <= spmm::kGroupRows && (n_seg - groups) * 550 > 6000 + N * (a->m + 2 * a->k) / 2000;  // ns
 }
 
 }  // namespace
@@ -317,15 +360,15 @@ spmm_status spmm_adapters_create(spmm_adapters *out, int64_t m, int64_t k, int32
     const size_t rows = (static_cast<size_t>(max_rows) / spmm::kMaxTileRows + 1) * spmm::kMaxTileRows;
     CUDA_TRY(cudaMalloc(&a->d_tile_segs, rows * sizeof(spmm::TileSegment)), "cudaMalloc(tile segments)");
     CUDA_TRY(cudaMalloc(&a->d_tile_count, rows / 256 * sizeof(int32_t)), "cudaMalloc(tile counts)");
+    const size_t g = static_cast<size_t>(std::max<int64_t>(std::min<int64_t>(max_rows, spmm::kGroupRows), 1));
+    CUDA_TRY(cudaMalloc(&a->d_xs, g * k * 2), "cudaMalloc(sorted rows)");
+    CUDA_TRY(cudaMalloc(&a->d_ys, g * m * 4), "cudaMalloc(sorted rows)");
+    CUDA_TRY(cudaMalloc(&a->d_group_ptr, (g + 1) * sizeof(int64_t)), "cudaMalloc(sorted segments)");
+    CUDA_TRY(cudaMalloc(&a->d_group_adapter, g * sizeof(int32_t)), "cudaMalloc(sorted segments)");
+    CUDA_TRY(cudaMalloc(&a->d_place, g * sizeof(int32_t)), "cudaMalloc(sorted segments)");
     if (a->grad) {
       CUDA_TRY(cudaMalloc(&a->d_dh, h), "cudaMalloc(adapter gradients)");
-      const size_t g = static_cast<size_t>(std::max<int64_t>(std::min<int64_t>(max_rows, spmm::kGroupRows), 1));
-      CUDA_TRY(cudaMalloc(&a->d_xs, g * k * 2), "cudaMalloc(sorted rows)");
-      CUDA_TRY(cudaMalloc(&a->d_dys, g * m * 2), "cudaMalloc(sorted rows)");
       CUDA_TRY(cudaMalloc(&a->d_dxs, g * k * 4), "cudaMalloc(sorted rows)");
-      CUDA_TRY(cudaMalloc(&a->d_group_ptr, (g + 1) * sizeof(int64_t)), "cudaMalloc(sorted segments)");
-      CUDA_TRY(cudaMalloc(&a->d_group_adapter, g * sizeof(int32_t)), "cudaMalloc(sorted segments)");
-      CUDA_TRY(cudaMalloc(&a->d_place, g * sizeof(int32_t)), "cudaMalloc(sorted segments)");
     }
     return SPMM_OK;
   };
@@ -382,18 +425,12 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
     return SPMM_OK;
   }
   void *const out = dX;
-  const int64_t groups = std::min({N, n_seg, static_cast<int64_t>(p.n_adapters)});
-  const bool grouped = sorting_pays(a, N, n_seg, groups);
-  if (grouped) {
-    spmm::AdapterGroupParams g{seg_ptr, seg_adapter, p.n_seg, p.n_adapters, p.N, static_cast<int32_t>(groups),
-                               a->d_place, a->d_group_ptr, a->d_group_adapter, p.status};
-    CUDA_TRY(spmm::launch_adapter_group(g, X, a->d_xs, k, dY, a->d_dys, m, s), "sorting of rows launch");
-    X = a->d_xs;
-    dY = a->d_dys;
+  const int64_t groups = most_groups(a, N, n_seg);
+  const bool sorted = sorting_pays(a, N, n_seg, groups);
+  if (sorted) {
+    st = sort_rows(a, p, X, &dY, groups, s);
+    if (st != SPMM_OK) return st;
     if (dX) dX = a->d_dxs;
-    p.seg_ptr = seg_ptr = a->d_group_ptr;
-    p.seg_adapter = seg_adapter = a->d_group_adapter;
-    p.n_seg = g.n_groups;
   }
   // H and dH, then dX with the roles of the adapters' two matrices exchanged
   const int parts = dX ? h_parts(h_t) : 1;
@@ -413,7 +450,7 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
     p.M = k;
     p.K = m;
     st = up_project(h_t, a, p, parts, stored, true, tile, s);
-    if (st == SPMM_OK && grouped)
+    if (st == SPMM_OK && sorted)
       CUDA_TRY(spmm::launch_adapter_ungroup(a->d_place, N, dX, out, static_cast<int64_t>(k) * (exact ? 4 : 2), s),
                "return of sorted rows launch");
   }
@@ -425,8 +462,8 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
   if (st != SPMM_OK) return st;
   w.d_up = static_cast<uint16_t *>(d_up);
   w.d_down = static_cast<uint16_t *>(d_down);
-  w.seg_ptr = seg_ptr;
-  w.seg_adapter = seg_adapter;
+  w.seg_ptr = p.seg_ptr;
+  w.seg_adapter = p.seg_adapter;
   w.n_seg = p.n_seg;
   w.n_adapters = p.n_adapters;
   w.rank = p.rank;

@@ -346,7 +346,7 @@ struct AdapterGroupParams {
   int32_t *group_adapter;  // device, n_groups
   uint32_t *status;
 };
-// ... with X's rows (k of 16 bits) and dY's (m) copied to their places,
+// ... with X's rows (k of 16 bits) and dY's (m; NULL: none) copied to their places,
 cudaError_t launch_adapter_group(const AdapterGroupParams &p, const void *X, void *xs, int64_t k, const void *dY, void *dys,
                                  int64_t m, cudaStream_t s);
 // and rows copied back from them.

@@ -492,3 +492,52 @@ def test_sorted_rows_report_an_index_outside_the_pool(S):
         close(got.cpu(), value, bound, name)
     layer_t.close()
     aset.close()
+
+
+@pytest.mark.parametrize("m,k,n,segs,rank,n_adapters,in_t,out_t", [
+    pytest.param(1032, 520, 400, singles(400, 3), 128, 3, "bf16", "bf16", id="400-single-rows"),
+    pytest.param(1032, 520, 400, singles(400, 3, seed=1), 128, 3, "bf16", "f32", id="400-single-rows-f32"),
+    pytest.param(1032, 200, 1024, ragged(1024, 100, 2), 128, 2, "f16", "f32", id="100-segments-of-1024"),
+    pytest.param(2056, 264, 900, ragged(900, 400, 4, gaps=True), 72, 4, "f16", "bf16", id="400-segments-gaps"),
+])
+def test_forward_of_many_short_segments(S, m, k, n, segs, rank, n_adapters, in_t, out_t):
+    """Batches whose rows are sorted by adapter on the way."""
+    c = Case(m, k, n, *segs, rank, n_adapters, in_t, out_t)
+    Y, bound = c.reference()
+    outs = run(S, c, runs=2)
+    close(outs[0], Y, bound, "Y")
+    assert np.array_equal(outs[0].double().numpy(), outs[1].double().numpy()), "runs differ"
+
+
+def test_a_broken_adapter_keeps_to_itself_among_sorted_rows_forward(S):
+    import torch
+    n = 400
+    ids = (np.arange(n) % 3).astype(np.int32)
+    c = Case(1032, 520, n, np.arange(n + 1), ids, 128, 3)
+    Y, bound = c.reference()
+    c.down[1, 0, 0], c.up[1, 3, 1] = float("inf"), float("nan")
+    fine = torch.from_numpy(ids != 1)
+    close(run(S, c)[0][fine], Y[fine], bound[fine], "other rows")
+
+
+def test_sorted_rows_in_graphs(S):
+    """A captured call replayed on new data gives what a plain call gives."""
+    import torch
+    c = Case(1032, 520, 400, *singles(400, 3), 128, 3)
+    want = run(S, c)[0]
+    layer, aset = c.layer(S), c.set(S, grad=False)
+    X, batch = c.X.cuda(), c.batch()
+    Y = torch.empty((c.n, c.m), dtype=torch.bfloat16, device="cuda")
+    graph, hold, ids = torch.cuda.CUDAGraph(), torch.zeros_like(X), torch.zeros_like(batch[4])
+    aset.linear(layer, hold, Y, *batch[:4], ids)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        aset.linear(layer, hold, Y, *batch[:4], ids)
+    hold.copy_(X)
+    ids.copy_(batch[4])
+    Y.fill_(float("nan"))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(Y.cpu(), want)
+    layer.close()
+    aset.close()
