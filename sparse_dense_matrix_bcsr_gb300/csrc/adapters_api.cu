@@ -35,6 +35,10 @@ struct spmm_adapters_s {
 
 namespace {
 
+// An H of at most this is loaded by a few rows for short segments (LinearAdapters::few):
+// at 3 to 23 KB up to twice as fast (figures at the kernel), at 64 KB 2048 rows in 128
+// segments, 18944 x 3584, take 145 for 120 us.
+constexpr int64_t kFewBytes = 24 * 1024;
 // 16-bit parts of H (fp16: 22 bits, bf16: 24) in the products whose result is h's output.
 constexpr int kMaxHParts = 3;
 int h_parts(spmm_handle h) { return h->out_t != SPMM_F32 ? 1 : h->in_t == SPMM_BF16 ? kMaxHParts : 2; }
@@ -181,7 +185,7 @@ spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams
   ad.rank = p.rank;
   ad.parts = parts;
   ad.u_transposed = transposed ? 1 : 0;
-  ad.few = p.N <= 128 ? 1 : 0;
+  ad.few = static_cast<int64_t>(p.N) * stored * p.rank * 2 <= kFewBytes ? 1 : 0;
   ad.tile = tile;
   spmm::BcsrParams b;
   std::memset(&b, 0, sizeof b);

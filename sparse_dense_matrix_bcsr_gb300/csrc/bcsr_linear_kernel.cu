@@ -49,12 +49,12 @@
 // 18944 features.  The gradient's dX takes D_a where the forward pass takes U_a,
 // as it lies (MN-major).
 //
-// A stage of an adapter loads H by 128 rows, whatever the segment has of them.
-// Batches of at most 128 rows load segments of a few rows by 16 instead (`few`):
-// there every CTA reads the same lines of H for every adapter, and L2 cannot serve them
-// fast enough (dX of 79 rows with 38 adapters, 13752 features: 229 us, by 16 rows 125; 53
-// rows: 300 and 147).  Where H is larger the large box is faster (8192 rows in 500
-// segments: 139 us against 161).
+// A stage of an adapter loads H by 128 rows, whatever the segment has of them.  Where
+// H is small (`few`) segments of a few rows load it by 16 instead: there every CTA reads
+// the same lines of H for every adapter, and L2 cannot serve them fast enough (dX of 79
+// rows with 38 adapters, 13752 features: 229 us, by 16 rows 122; gradient of 230 rows
+// with 59, 672 x 6984: 306 and 136).  Where H is larger the large box is faster (8192
+// rows in 500 segments: 139 us against 161).
 //
 // The tensor cores cut what their fp32 sums shift out instead of rounding it, ~1e-9
 // of the result for every term.  Where Y is bf16 its rounding hides that.  An fp32 Y
@@ -366,18 +366,21 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
                         for (int h = h0; h < h1; ++h)
                           tma_load_3d(st + kBlkBytes + (q * group + h - g) * part_bytes, &ad.tmH, fb, r0, q, row0 + h * 128);
                     } else {
-                      // the batch is one part: boxes of kFewRows rows that hold the segment's, or the large one
+                      // boxes of kFewRows rows that hold the segment's, or the large ones
                       const uint32_t few_bytes = kFewRows * ad.box * 2;
-                      const int b0 = begin / kFewRows, n = (end + kFewRows - 1) / kFewRows - b0;
-                      mbar_arrive_expect_tx(fb, kBlk * ad.box * 2 + ad.parts * (n <= kFewBoxes ? n * few_bytes : part_bytes));
+                      const int p0 = h0 * 128, b0 = (max(begin, p0) - p0) / kFewRows;
+                      const int n = h1 - h0 == 1 ? (min(end - p0, 128) + kFewRows - 1) / kFewRows - b0 : kFewBoxes + 1;
+                      const bool small = n <= kFewBoxes;
+                      mbar_arrive_expect_tx(fb, kBlk * ad.box * 2 + ad.parts * (small ? n * few_bytes : (h1 - h0) * part_bytes));
                       copy_u();
                       for (int q = 0; q < ad.parts; ++q) {
-                        const uint32_t at = st + kBlkBytes + q * group * part_bytes;
-                        if (n > kFewBoxes)
-                          tma_load_3d(at, &ad.tmH, fb, r0, q, row0);
-                        else
+                        const uint32_t at = st + kBlkBytes + (q * group + h0 - g) * part_bytes;
+                        if (small)
                           for (int b = b0; b < b0 + n; ++b)
-                            tma_load_3d(at + b * few_bytes, &ad.tmHs, fb, r0, q, row0 + b * kFewRows);
+                            tma_load_3d(at + b * few_bytes, &ad.tmHs, fb, r0, q, row0 + p0 + b * kFewRows);
+                        else
+                          for (int h = h0; h < h1; ++h)
+                            tma_load_3d(at + (h - h0) * part_bytes, &ad.tmH, fb, r0, q, row0 + h * 128);
                       }
                     }
                   }
