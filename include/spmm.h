@@ -388,9 +388,8 @@ spmm_status spmm_adapters_destroy(spmm_adapters a);
  * arrays that earlier work on the stream writes (spmm_route_sort's offsets).
  * An index outside the pool counts as -1 and is reported by spmm_check(h) as
  * SPMM_ERR_DEVICE_CHECK.  Sums are fp32.  Batches with few rows per adapter keep
- * h in fp32; longer ones take it as a matrix operand, rounded to in_t (to the
- * sum of two fp16 or three bf16 values where Y is fp32), so fp16 values of h above 65504 become infinite
- * there.  Asynchronous; results are bitwise reproducible run to run.
+ * h in fp32; longer ones take it as a matrix operand, the sum of three values of in_t
+ * (24 bits of bf16), so fp16 values of h above 65504 become infinite there.  Asynchronous; results are bitwise reproducible run to run.
  * Errors: as spmm_run_linear, plus INVALID_ARG for shapes, types or devices
  * that do not match and batches above the set's limits.
  */
@@ -404,9 +403,9 @@ spmm_status spmm_run_linear_adapters(spmm_handle h, spmm_adapters a, const void 
  *     dh[n] = scale[a] * U_a^T dY[n]
  *     dX[n] = A^T dY[n] + D_a^T dh[n]
  *     d_up_a = sum_n dY[n] h[n]^T       d_down_a = sum_n dh[n] X[n]^T
- * the sums over the rows of adapter a, in a fixed order.  On the way h and dh are
- * rounded to the sum of two values of in_t for d_up and d_down, dh to one for dX (two
- * fp16 or three bf16 for an fp32 dX); fp16 values have no bits below 2^-24.
+ * the sums over the rows of adapter a, in a fixed order.  On the way dh is the sum of
+ * three values of in_t for dX, and h and dh are rounded to the sum of two for d_up and
+ * d_down; fp16 values have no bits below 2^-24.
  *   h_t      a BCSR handle of A^T (k x m), of the set's in_t; dX has its out_t.
  *   X, dY    N x k and N x m row-major, in_t, 16-byte aligned.
  *   dX       N x k, or NULL where no gradient of the input is wanted.

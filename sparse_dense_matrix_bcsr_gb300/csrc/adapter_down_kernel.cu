@@ -21,11 +21,10 @@
 // The gradient wants two such products of a batch, of X and of dY: one launch
 // runs both, so that short batches fill the GPU with their sum.
 //
-// Where the projection's output is fp32, H is kept in 16-bit parts (the value
-// rounded, the rest rounded, ...): two of fp16 hold 22 bits, three of bf16 24 (two
-// of bf16, 16 bits, left 1.2e-6 of Y off where the adapters are most of it, three
-// 0.6e-6; 777 rows of 8192 columns in 40 segments, rank 64, take 112 for 90 us).  The
-// sums then leave the tensor cores, which cut what an fp32 sum shifts out instead of
+// H is kept in 16-bit parts (the value rounded, the rest rounded, ...), kHParts of them,
+// 24 bits of bf16 (two of bf16, 16 bits, left 1.2e-6 of an fp32 Y off where the adapters
+// are most of it, three 0.6e-6).  Where the output is fp32 the
+// sums leave the tensor cores, which cut what an fp32 sum shifts out instead of
 // rounding it (~1e-9 of the sum for every term), every kTurn stages and are added
 // in registers.
 #include <cuda_bf16.h>

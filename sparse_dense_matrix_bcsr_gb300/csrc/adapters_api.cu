@@ -23,7 +23,7 @@ struct spmm_adapters_s {
   int num_sms = 0;
   bool sm103 = false;
 
-  float *d_h = nullptr;        // max_rows x rank: scale * D x, in fp32 or in up to three 16-bit parts
+  float *d_h = nullptr;        // max_rows x rank: scale * D x, in fp32 or in 16-bit parts
   float *d_dh = nullptr;       // gradient: max_rows x rank: scale * U^T dy
   // a short batch's rows sorted by adapter: X, dY or Y, dX
   void *d_xs = nullptr, *d_ys = nullptr, *d_dxs = nullptr;
@@ -35,13 +35,10 @@ struct spmm_adapters_s {
 
 namespace {
 
-// An H of at most this is loaded by a few rows for short segments (LinearAdapters::few):
+// An H of at most this a part is loaded by a few rows for short segments (LinearAdapters::few):
 // at 3 to 23 KB up to twice as fast (figures at the kernel), at 64 KB 2048 rows in 128
 // segments, 18944 x 3584, take 145 for 120 us.
 constexpr int64_t kFewBytes = 24 * 1024;
-// 16-bit parts of H (fp16: 22 bits, bf16: 24) in the products whose result is h's output.
-constexpr int kMaxHParts = 3;
-int h_parts(spmm_handle h) { return h->out_t != SPMM_F32 ? 1 : h->in_t == SPMM_BF16 ? kMaxHParts : 2; }
 
 void free_adapters(spmm_adapters a) {
   if (!a) return;
@@ -162,13 +159,13 @@ spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, std::ini
 }
 
 // Y = X W^T + U H per row, H and the tile lists from down_project; U n_adapters x
-// M x rank, or transposed n_adapters x rank x M; the first `parts` of H's `stored` parts.
-spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams &p, int parts, int stored, bool transposed,
-                       spmm::LinearTile tile, cudaStream_t s) {
+// M x rank, or transposed n_adapters x rank x M.
+spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams &p, bool transposed, spmm::LinearTile tile,
+                       cudaStream_t s) {
   const bool bf16 = h->in_t == SPMM_BF16, out_bf16 = h->out_t == SPMM_BF16;
   CUtensorMap tmX, tmY;
   spmm::LinearAdapters ad;
-  ad.box = p.rank <= 16 ? 16 : p.rank <= 32 || parts > 2 ? 32 : 64;
+  ad.box = p.rank <= 16 ? 16 : 32;
   spmm_status st = spmm::encode_x(&tmX, p.X, bf16, p.N, p.K);
   if (st == SPMM_OK) st = spmm::encode_y(&tmY, p.Y, out_bf16, p.N, p.M, spmm::linear_tile_rows(tile));
   if (st == SPMM_OK && transposed) st = spmm::encode_3d(&ad.tmU, p.up, bf16, p.n_adapters, p.rank, p.M, 1, ad.box);
@@ -176,16 +173,15 @@ spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams
     st = spmm::encode_2d(&ad.tmU, p.up, bf16, static_cast<uint64_t>(p.n_adapters) * p.M, p.rank, p.rank, 64, ad.box,
                          ad.box * 2);
   if (st == SPMM_OK)
-    st = spmm::encode_3d(&ad.tmH, p.H, bf16, p.N, stored, p.rank, 128, 1, ad.box, ad.box * 2);
+    st = spmm::encode_3d(&ad.tmH, p.H, bf16, p.N, spmm::kHParts, p.rank, 128, 1, ad.box, ad.box * 2);
   if (st == SPMM_OK)
-    st = spmm::encode_3d(&ad.tmHs, p.H, bf16, p.N, stored, p.rank, spmm::kAdapterFewRows, 1, ad.box, ad.box * 2);
+    st = spmm::encode_3d(&ad.tmHs, p.H, bf16, p.N, spmm::kHParts, p.rank, spmm::kAdapterFewRows, 1, ad.box, ad.box * 2);
   if (st != SPMM_OK) return st;
   ad.tile_segs = a->d_tile_segs;
   ad.tile_count = a->d_tile_count;
   ad.rank = p.rank;
-  ad.parts = parts;
   ad.u_transposed = transposed ? 1 : 0;
-  ad.few = static_cast<int64_t>(p.N) * stored * p.rank * 2 <= kFewBytes ? 1 : 0;
+  ad.few = static_cast<int64_t>(p.N) * p.rank * 2 <= kFewBytes ? 1 : 0;
   ad.tile = tile;
   spmm::BcsrParams b;
   std::memset(&b, 0, sizeof b);
@@ -284,11 +280,10 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
   p.M = static_cast<int32_t>(h->m);
   p.K = static_cast<int32_t>(h->k);
   if (sorted || !rows_path(p.N, p.rank, p.n_seg)) {
-    const int parts = h_parts(h);
     const spmm::LinearTile tile = spmm::linear_adapters_tile(h->n_groups, h->n_units, p.N, p.n_seg, h->out_t == SPMM_BF16,
                                                                p.num_sms);
-    spmm_status st = down_project(a, p, {{X, down, a->d_h, p.K, parts, false}}, parts > 1, spmm::linear_tile_rows(tile), s);
-    if (st == SPMM_OK) st = up_project(h, a, p, parts, parts, false, tile, s);
+    spmm_status st = down_project(a, p, {{X, down, a->d_h, p.K, spmm::kHParts, false}}, h->out_t == SPMM_F32, spmm::linear_tile_rows(tile), s);
+    if (st == SPMM_OK) st = up_project(h, a, p, false, tile, s);
     if (st == SPMM_OK && sorted)
       CUDA_TRY(spmm::launch_adapter_ungroup(a->d_place, p.N, Y, out, static_cast<int64_t>(p.M) * (h->out_t == SPMM_F32 ? 4 : 2), s),
                "return of sorted rows launch");
@@ -358,7 +353,7 @@ spmm_status spmm_adapters_create(spmm_adapters *out, int64_t m, int64_t k, int32
     CUDA_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, a->device), "device attribute");
     a->sm103 = major == 10 && minor == 3;
     const size_t h = static_cast<size_t>(std::max<int64_t>(max_rows, 1)) * rank *
-                     std::max(sizeof(float), in_t == SPMM_BF16 ? kMaxHParts * sizeof(uint16_t) : 0);
+                     std::max(sizeof(float), spmm::kHParts * sizeof(uint16_t));
     CUDA_TRY(cudaMalloc(&a->d_h, h), "cudaMalloc(adapter activations)");
     // one entry per row of the tiles, one count per tile of the smallest
     const size_t rows = (static_cast<size_t>(max_rows) / spmm::kMaxTileRows + 1) * spmm::kMaxTileRows;
@@ -437,12 +432,10 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
     if (dX) dX = a->d_dxs;
   }
   // H and dH, then dX with the roles of the adapters' two matrices exchanged
-  const int parts = dX ? h_parts(h_t) : 1;
   const spmm::LinearTile tile = spmm::linear_adapters_tile(h_t->n_groups, h_t->n_units, p.N, p.n_seg, h_t->out_t == SPMM_BF16,
                                                                p.num_sms);
-  const int stored = std::max(parts, spmm::kWgradParts);
   const DownJob of_x{X, down, a->d_h, k, spmm::kWgradParts, false},
-      of_dy{dY, up, a->d_dh, m, stored, true};
+      of_dy{dY, up, a->d_dh, m, spmm::kHParts, true};
   const bool exact = h_t->out_t == SPMM_F32;  // with or without dX: the same d_up and d_down
   st = m > k ? down_project(a, p, {of_dy, of_x}, exact, spmm::linear_tile_rows(tile), s)  // the longer first
              : down_project(a, p, {of_x, of_dy}, exact, spmm::linear_tile_rows(tile), s);
@@ -453,7 +446,7 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
     p.up = down;
     p.M = k;
     p.K = m;
-    st = up_project(h_t, a, p, parts, stored, true, tile, s);
+    st = up_project(h_t, a, p, true, tile, s);
     if (st == SPMM_OK && sorted)
       CUDA_TRY(spmm::launch_adapter_ungroup(a->d_place, N, dX, out, static_cast<int64_t>(k) * (exact ? 4 : 2), s),
                "return of sorted rows launch");
@@ -462,7 +455,7 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
   if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dy, dY, bf16, N, m, m, 64, 64);
   if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_x, X, bf16, N, k, k, 64, 64);
   if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_h, a->d_h, bf16, N, spmm::kWgradParts * a->rank, spmm::kWgradParts * a->rank, 64, 64);
-  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dh, a->d_dh, bf16, N, spmm::kWgradParts * a->rank, stored * a->rank, 64, 64);
+  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dh, a->d_dh, bf16, N, spmm::kWgradParts * a->rank, spmm::kHParts * a->rank, 64, 64);
   if (st != SPMM_OK) return st;
   w.d_up = static_cast<uint16_t *>(d_up);
   w.d_down = static_cast<uint16_t *>(d_down);

@@ -39,9 +39,10 @@
 //
 // With adapters (spmm_run_linear_adapters) a tile has further stages after its
 // blocks: for every segment with an adapter among its rows, the block row's 64
-// rows of U_a as the N operand and the tile's rows of H as the M operand, 64
-// ranks a stage (H in one 16-bit part; in two parts, a stage takes both parts of
-// half the tile, so a segment within a half costs one stage either way).  Their
+// rows of U_a as the N operand and the tile's rows of H as the M operand, 16 or 32
+// ranks a stage.  H comes in kHParts 16-bit parts, which add up to the fp32 value, so
+// that Y is rounded once whatever its type; a stage holds all parts of the tile's rows
+// (16 ranks) or of half of them.  Their
 // MMAs update the segment's lanes only (the MMA's lane mask), so the other rows'
 // sums do not see the product at all: no zeroed copy of H, and an adapter with
 // infinities cannot reach other rows as 0 * inf.  The product with adapters reads
@@ -130,12 +131,13 @@ __device__ __forceinline__ void tile_coords(int64_t t, int n_block_rows, int n_t
   nt = static_cast<int>(g) * GROUP + static_cast<int>(r % gsz);
 }
 
-// Parts (128 rows) of the tile that a stage of an adapter holds: all of them, or as
-// many as leave room for H's 16-bit parts.
-template <int PARTS, bool OUT_BF16>
+// Parts (128 rows) of the tile that a stage of an adapter holds, with H's 16-bit
+// parts in the place of X: all of them, or half with boxes of 32 ranks.
+template <class T>
 __device__ __forceinline__ int stage_parts(const LinearAdapters &ad) {
-  if constexpr (OUT_BF16) return PARTS;
-  return PARTS > ad.parts ? PARTS / ad.parts : 1;
+  static_assert(T::kParts * kHParts * 128 * 16 * 2 <= T::kXBytes && T::kParts / 2 * kHParts * 128 * 32 * 2 <= T::kXBytes,
+                "an adapter's stage");
+  return ad.box == 16 ? T::kParts : T::kParts / 2;
 }
 
 // Y's store boxes: 32 rows (a warp's lanes of one part) x 128 or 64 bytes.
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
             for (int i = 0; i < cnt && ok; ++i) {
               const int32_t a = __shfl_sync(0xffffffffu, my.adapter, i);
               const int32_t begin = __shfl_sync(0xffffffffu, my.begin, i), end = __shfl_sync(0xffffffffu, my.end, i);
-              const int group = stage_parts<T::kParts, OUT_BF16>(ad);
+              const int group = stage_parts<T>(ad);
               for (int g = begin / 128 / group * group; g * 128 < end && ok; g += group) {
                 const int h0 = max(begin / 128, g), h1 = min((end + 127) / 128, g + group);
                 for (int32_t r0 = 0; r0 < ad.rank; r0 += ad.box) {
@@ -360,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
                     };
                     const int row0 = nt * kTileN;
                     if (!ad.few) {
-                      mbar_arrive_expect_tx(fb, kBlk * ad.box * 2 + (h1 - h0) * ad.parts * part_bytes);
+                      mbar_arrive_expect_tx(fb, kBlk * ad.box * 2 + (h1 - h0) * kHParts * part_bytes);
                       copy_u();
-                      for (int q = 0; q < ad.parts; ++q)
+                      for (int q = 0; q < kHParts; ++q)
                         for (int h = h0; h < h1; ++h)
                           tma_load_3d(st + kBlkBytes + (q * group + h - g) * part_bytes, &ad.tmH, fb, r0, q, row0 + h * 128);
                     } else {
@@ -371,9 +373,9 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
                       const int p0 = h0 * 128, b0 = (max(begin, p0) - p0) / kFewRows;
                       const int n = h1 - h0 == 1 ? (min(end - p0, 128) + kFewRows - 1) / kFewRows - b0 : kFewBoxes + 1;
                       const bool small = n <= kFewBoxes;
-                      mbar_arrive_expect_tx(fb, kBlk * ad.box * 2 + ad.parts * (small ? n * few_bytes : (h1 - h0) * part_bytes));
+                      mbar_arrive_expect_tx(fb, kBlk * ad.box * 2 + kHParts * (small ? n * few_bytes : (h1 - h0) * part_bytes));
                       copy_u();
-                      for (int q = 0; q < ad.parts; ++q) {
+                      for (int q = 0; q < kHParts; ++q) {
                         const uint32_t at = st + kBlkBytes + (q * group + h0 - g) * part_bytes;
                         if (small)
                           for (int b = b0; b < b0 + n; ++b)
@@ -504,14 +506,14 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
             const TileRec seg = tile_rec[stage];
             more = (seg.flags & kRecLast) == 0;
             const int begin = seg.rows & 0xffff, end = seg.rows >> 16;
-            const int parts = OUT_BF16 ? 1 : ad.parts, group = stage_parts<T::kParts, OUT_BF16>(ad);
+            const int group = stage_parts<T>(ad);
             const uint64_t bdesc0 = smem_desc_add(u_desc, stage * kStageBytes);
             const uint64_t adesc0 = smem_desc_add(h_desc, stage * kStageBytes);
             if (begin <= 128 * seg.part && end >= 128 * (seg.part + group)) {
               // the segment holds all rows of the stage: no lanes to mask; as for the
               // blocks, MMAs in a row go to different accumulators
               for (int kk = 0; kk < seg.stages; ++kk) {
-                for (int q = 0; q < parts; ++q) {
+                for (int q = 0; q < kHParts; ++q) {
 #pragma unroll
                   for (int i = 0; i < group; ++i)
                     umma_f16_elect(acc + (seg.part + i) * kBlk, smem_desc_add(adesc0, (q * group + i) * h_part + kk * 32),
@@ -524,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
                 if (end <= 128 * h || begin >= 128 * (h + 1)) continue;
                 uint32_t off[4];
                 lanes_off(begin - 128 * h, end - 128 * h, off);
-                for (int q = 0; q < parts; ++q) {
+                for (int q = 0; q < kHParts; ++q) {
                   const uint64_t adesc = smem_desc_add(adesc0, (q * group + i) * h_part);
                   for (int kk = 0; kk < seg.stages; ++kk)
                     umma_f16_lanes_elect(acc + h * kBlk, smem_desc_add(adesc, kk * 32), smem_desc_add(bdesc0, kk * u_step),

@@ -1,0 +1,130 @@
+"""Low-rank adapters on whole numbers, where every sum is exact and so is the answer: bounds are zero.
+
+h (or dh) has numbers of about 2^20 that cancel in pairs: what is left is below 256 and exact in the output's
+type, while an h held in fewer bits than it has would leave thousands.  The shared weight is zero, so nothing hides
+that.  Every way through the projection and every tile of it is reached, in both directions."""
+import numpy as np
+import pytest
+
+from test_gpu_adapters import S, Case, ragged, run, run_grad, singles  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def whole(rng, shape, lo=64, hi=128):
+    import torch
+    return torch.from_numpy(rng.integers(lo, hi, shape)).double()
+
+
+def zero_weight(m, k, n, segs, rank, n_adapters, in_t, out_t, scale, keep=0.4):
+    """A case with stored blocks of zeros, and whole numbers' generator."""
+    c = Case(m, k, n, *segs, rank, n_adapters, in_t, out_t, keep=keep)
+    c.vals[:] = 0
+    c.W.zero_()
+    c.scale[:] = scale
+    return c, np.random.default_rng([m, k, n, rank])
+
+
+def paired_ranks(rng, n_adapters, rank, width):
+    """(big [adapters, rank, width], out [adapters, rank, any]): ranks 2 j and 2 j + 1 of big differ by one in column at[a][j]."""
+    big = whole(rng, (n_adapters, rank, width))
+    big[:, 1::2] = big[:, 0::2]
+    at = rng.integers(0, width, (n_adapters, rank // 2))
+    for a in range(n_adapters):
+        for j in range(rank // 2):
+            big[a, 2 * j + 1, at[a, j]] -= 1
+    return big, at
+
+
+def signs(n_adapters, rank, width):
+    """[adapters, rank, width]: column w adds one pair of ranks, the first and less the second."""
+    import torch
+    s = torch.zeros((n_adapters, rank, width), dtype=torch.float64)
+    w = torch.arange(width)
+    for a in range(n_adapters):
+        j = (w + a) % (rank // 2)
+        s[a, 2 * j, w], s[a, 2 * j + 1, w] = 1.0, -1.0
+    return s
+
+
+def paired_rows(c, rng, width):
+    """Rows 2 t and 2 t + 1 equal but for one of the first 8 columns, where the second is one less."""
+    big = whole(rng, (c.n, width))
+    big[1::2] = big[0:c.n - 1:2]
+    for t in range(c.n // 2):
+        big[2 * t + 1, rng.integers(0, 8)] -= 1
+    return big
+
+
+def row_signs(c, width):
+    """[n, width]: column w takes the pairs of rows t = w, w + width, ..., the first row and less the second."""
+    import torch
+    s = torch.zeros((c.n, width), dtype=torch.float64)
+    for t in range(c.n // 2):
+        s[2 * t, t % width], s[2 * t + 1, t % width] = 1.0, -1.0
+    return s
+
+
+def even(segs):
+    """The same segments with even bounds."""
+    return np.asarray(segs[0]) // 2 * 2, segs[1]
+
+
+def same(got, want, what, unit=1.0):
+    import torch
+    assert (want / unit == (want / unit).round()).all() and want.abs().max() <= 256 * unit and want.any()
+    assert torch.equal(got.double(), want), f"{what}: {float((got.double() - want).abs().max()) / unit:.3g} units off"
+
+
+# m, k, n, segments, rank, adapters
+FORWARD = [
+    pytest.param(256, 200, 700, ragged(700, 5, 3), 16, 3, id="tile-256"),
+    pytest.param(328, 200, 700, ragged(700, 3, 2), 128, 2, id="tile-256-rank-128"),
+    pytest.param(4104, 136, 700, ragged(700, 7, 3), 8, 3, id="two-ctas"),
+    pytest.param(4104, 136, 700, ragged(700, 40, 9, gaps=True), 72, 9, id="two-ctas-rank-72"),
+    pytest.param(4160, 136, 2100, ragged(2100, 20, 4), 32, 4, id="two-ctas-rank-32"),
+    pytest.param(8192, 136, 5300, ragged(5300, 9, 4), 16, 4, id="tile-512"),
+    pytest.param(8200, 72, 5300, ragged(5300, 11, 3, gaps=True), 40, 3, id="tile-512-rank-40"),
+    pytest.param(1032, 520, 400, singles(400, 3), 128, 3, id="sorted"),
+    pytest.param(256, 264, 40, singles(40, 5), 24, 5, id="rows"),
+]
+
+
+def projection(S, m, k, n, segs, rank, n_adapters, in_t, out_t, scale=1.0):
+    c, rng = zero_weight(m, k, n, segs, rank, n_adapters, in_t, out_t, scale, keep=0.6)
+    D, _ = paired_ranks(rng, n_adapters, rank, k)
+    U = signs(n_adapters, rank, m).transpose(1, 2)
+    c.X, c.down, c.up = whole(rng, (n, k)).to(c.X.dtype), D.to(c.X.dtype), U.to(c.X.dtype).contiguous()
+    same(run(S, c)[0], c.reference()[0], "Y", scale)
+
+
+@pytest.mark.parametrize("out_t", ["bf16", "f32"])
+@pytest.mark.parametrize("m,k,n,segs,rank,n_adapters", FORWARD)
+def test_projection(S, m, k, n, segs, rank, n_adapters, out_t):
+    projection(S, m, k, n, segs, rank, n_adapters, "bf16", out_t)
+
+
+BACKWARD = [
+    pytest.param(200, 256, 700, ragged(700, 5, 3), 16, 3, id="tile-256"),
+    pytest.param(200, 328, 700, ragged(700, 3, 2), 128, 2, id="tile-256-rank-128"),
+    pytest.param(136, 4104, 700, ragged(700, 7, 3), 8, 3, id="two-ctas"),
+    pytest.param(136, 4104, 1100, ragged(1100, 40, 9, gaps=True), 72, 9, id="two-ctas-rank-72"),
+    pytest.param(136, 8192, 5300, ragged(5300, 9, 4), 16, 4, id="tile-512"),
+    pytest.param(72, 8200, 5300, ragged(5300, 11, 3, gaps=True), 40, 3, id="tile-512-rank-40"),
+    pytest.param(520, 1032, 400, singles(400, 3), 128, 3, id="sorted"),
+]
+
+
+def input_gradient(S, m, k, n, segs, rank, n_adapters, in_t, out_t, scale=1.0):
+    c, rng = zero_weight(m, k, n, segs, rank, n_adapters, in_t, out_t, scale, keep=0.6)
+    U, _ = paired_ranks(rng, n_adapters, rank, m)
+    c.dY, c.X = whole(rng, (n, m)).to(c.X.dtype), c.X * 0
+    c.up, c.down = U.transpose(1, 2).contiguous().to(c.X.dtype), signs(n_adapters, rank, k).to(c.X.dtype)
+    same(run_grad(S, c)["dX"], c.reference_grad()["dX"][0], "dX", scale)
+
+
+@pytest.mark.parametrize("out_t", ["bf16", "f32"])
+@pytest.mark.parametrize("m,k,n,segs,rank,n_adapters", BACKWARD)
+def test_input_gradient(S, m, k, n, segs, rank, n_adapters, out_t):
+    input_gradient(S, m, k, n, segs, rank, n_adapters, "bf16", out_t)
+
