@@ -403,9 +403,8 @@ spmm_status spmm_run_linear_adapters(spmm_handle h, spmm_adapters a, const void 
  *     dh[n] = scale[a] * U_a^T dY[n]
  *     dX[n] = A^T dY[n] + D_a^T dh[n]
  *     d_up_a = sum_n dY[n] h[n]^T       d_down_a = sum_n dh[n] X[n]^T
- * the sums over the rows of adapter a, in a fixed order.  On the way dh is the sum of
- * three values of in_t for dX, and h and dh are rounded to the sum of two for d_up and
- * d_down; fp16 values have no bits below 2^-24.
+ * the sums over the rows of adapter a, in a fixed order.  On the way h and dh are the
+ * sums of three values of in_t (24 bits of bf16); fp16 values have no bits below 2^-24.
  *   h_t      a BCSR handle of A^T (k x m), of the set's in_t; dX has its out_t.
  *   X, dY    N x k and N x m row-major, in_t, 16-byte aligned.
  *   dX       N x k, or NULL where no gradient of the input is wanted.

@@ -48,7 +48,6 @@ constexpr int kTurn = 8;                // stages between two drains of the accu
 constexpr int kMiscBytes = 1024;
 constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
 
-__host__ __device__ constexpr int rank16(int rank) { return (rank + 15) / 16 * 16; }
 // D's part of a stage: rank rows of 64 columns, or (transposed, never less) 64
 // rows of 64 ranks per box.
 __host__ __device__ constexpr int d_boxes(int rank) { return (rank + 63) / 64; }
@@ -82,10 +81,15 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
 }
 
 // Eight ranks of one row of H, rounded; a further part holds what the roundings
-// before it left (nothing of what is infinite in 16 bits).
+// before it left (nothing of what is infinite in 16 bits).  Ranks past the last are zeros.
 template <bool BF16>
-__device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int32_t rank, int32_t j, int parts, float (&v)[8]) {
-  for (int q = 0; q < parts; ++q) {
+__device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int32_t rank, int32_t j, float (&v)[8]) {
+  const int pitch = rank16(rank);
+  if (j >= rank)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+#pragma unroll
+  for (int q = 0; q < kHParts; ++q) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -94,7 +98,7 @@ __device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int32_t rank, 
       v[2 * i] = isinf(f.x) ? 0.0f : v[2 * i] - f.x;
       v[2 * i + 1] = isinf(f.y) ? 0.0f : v[2 * i + 1] - f.y;
     }
-    *reinterpret_cast<uint4 *>(H + (row * parts + q) * rank + j) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(H + (row * kHParts + q) * pitch + j) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -264,11 +268,10 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
         } else if (mine) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (c0 + 8 * h >= p.rank) continue;
             float o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = f * v[8 * h + i];
-            store_h<BF16>(job.H, row0 + r, p.rank, c0 + 8 * h, job.parts, o);
+            store_h<BF16>(job.H, row0 + r, p.rank, c0 + 8 * h, o);
           }
         }
       };
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
     if (piece.adapter >= 0) {
       // the segment's rows in equal shares
       const int32_t begin = static_cast<int32_t>(piece.begin - row0), n = static_cast<int32_t>(piece.end - piece.begin);
-      const int32_t r0 = begin + n * part / p.split, r1 = begin + n * (part + 1) / p.split, units = p.rank / 8;
+      const int32_t r0 = begin + n * part / p.split, r1 = begin + n * (part + 1) / p.split, units = n16 / 8;
       const uint32_t base = smem_addr(smem);
       const float f = p.scale[piece.adapter];
       for (int u = threadIdx.x; u < (r1 - r0) * units; u += kThreads) {
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
         cluster_sum8(base + (r * part_pitch(p.rank) + j) * 4, p.split, o);
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] *= f;
-        store_h<BF16>(job.H, row0 + r, p.rank, j, job.parts, o);
+        store_h<BF16>(job.H, row0 + r, p.rank, j, o);
       }
     }
     cluster_sync();  // the others may still read this CTA's sums

@@ -6,7 +6,7 @@
 // kernel does both: the rows are the MMA's K, 128 features of V the M operand
 // and the ranks the N operand, both MN-major as they lie in memory.
 //
-// Work item = (128 features, adapter).  A stage is 64 rows of one segment (a TMA
+// Work item = (128 features, adapter).  A stage is 64 or 32 rows of one segment (a TMA
 // box may start at any row), so K never runs across a segment; the rows after a
 // segment's end that the last box brings are zeroed in shared memory in both
 // operands before the MMA, as neither operand may hold another request's
@@ -14,11 +14,12 @@
 // S is read again by every feature tile, from L2.  16384 rows of 4 adapters of rank
 // 64, 18944 + 3584 features: 117 us, 6.3 TB/s of activations.
 //
-// S comes in two 16-bit parts (the value rounded, and the rest rounded), whose sums
-// are added at the end: rounded once, h and dh alone would put the gradients'
-// error at 1.4 times what rounding the result to 16 bits does (up to 1.6 with few rows).
-// Up to rank 64 the parts lie side by side and one MMA of N = 2 rank takes both; one
-// MMA for each takes 121 us in place of 117, and a single part 102.
+// S comes in kHParts 16-bit parts, 24 bits of bf16 together, whose sums are added at
+// the end: with h and dh rounded to two, sums that cancel kept 16 bits of theirs.
+// One MMA takes as many parts as N = 256 holds, side by side (three up to rank 80, two
+// above), so that the features' operand passes shared memory less often: its bandwidth is
+// the bound at the larger ranks (the gradient of 16384 rows, 4 adapters of rank 64,
+// 18944 x 3584: 621 us, with an MMA for each part 729).
 //
 // With items enough for every SM, CTAs (two per SM) are persistent and take items
 // in turn, two TMEM accumulators alternating, so one item's sums are stored while
@@ -39,29 +40,26 @@ namespace spmm {
 namespace {
 
 constexpr int kFeat = 128;            // features per CTA
-constexpr int kK = 64;                // rows per stage
-constexpr int kBox = kK * 128;        // one box: 64 rows x 64 columns
-constexpr int kVBytes = kFeat / 64 * kBox;
-constexpr int kSParts = kWgradParts;
-constexpr int kJointRank = 64;        // up to this rank one MMA takes both parts
-static_assert(kSParts == 2, "the MMA loop");
-constexpr int kMaxQ = 4;
+constexpr int kMaxQ = 6;
 constexpr int kThreads = 192;
 constexpr int kTmaWarp = 0, kMmaWarp = 1;
 constexpr int kMiscBytes = 1024;
 constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
 
-__host__ __device__ constexpr int rank16(int rank) { return (rank + 15) / 16 * 16; }
-__host__ __device__ constexpr int rank_boxes(int rank) { return (rank + 63) / 64; }
-// Boxes of S in a stage: its parts side by side, or (too wide for an accumulator) each
-// by itself.
+// Parts of S that the first MMA takes; a second one takes the rest, if there is one.
+__host__ __device__ constexpr int joint_parts(int rank) { return kHParts * rank16(rank) <= 256 ? kHParts : kHParts - 1; }
+static_assert((kHParts - 1) * kMaxRank <= 256, "two MMAs at most");
+__host__ __device__ constexpr int col_boxes(int cols) { return (cols + 63) / 64; }
+// Boxes of S in a stage, the second MMA's after the first one's.
+__host__ __device__ constexpr int joint_boxes(int rank) { return col_boxes(joint_parts(rank) * rank16(rank)); }
 __host__ __device__ constexpr int s_boxes(int rank) {
-  return rank <= kJointRank ? rank_boxes(kSParts * rank) : kSParts * rank_boxes(rank);
+  return joint_boxes(rank) + (joint_parts(rank) < kHParts ? col_boxes(rank16(rank)) : 0);
 }
+// Rows of a stage: as many as leave three stages or more in half an SM's shared memory.
+__host__ __device__ constexpr int stage_rows(int rank) { return s_boxes(rank) <= 2 ? 64 : s_boxes(rank) <= 4 ? 48 : 32; }
 __host__ __device__ constexpr int part_pitch(int rank) { return rank16(rank) + 4; }
 
-constexpr int kNbuf = 2;              // accumulators
-static_assert(2 * kNbuf * kMaxRank <= 512 && 2 * kNbuf * kSParts * kJointRank <= 512, "TMEM columns of two CTAs");
+constexpr int kNbuf = 2;              // accumulators, where two CTAs have the columns for that
 
 struct Misc {
   uint64_t full[kMaxQ], empty[kMaxQ], acc_full[kNbuf], acc_empty[kNbuf], drained;
@@ -112,18 +110,20 @@ template <bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid_constant__ AdapterWgradParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const bool joint = p.rank <= kJointRank;
-  const int rb = rank_boxes(p.rank), boxes = s_boxes(p.rank);
-  const int stage_bytes = kVBytes + boxes * kBox;
+  const int joint = joint_parts(p.rank), jb = joint_boxes(p.rank), boxes = s_boxes(p.rank);
+  const int stage_k = stage_rows(p.rank);
+  const int box_bytes = stage_k * 128, v_bytes = kFeat / 64 * box_bytes;  // a box: a stage's rows x 64 columns
+  const int stage_bytes = v_bytes + boxes * box_bytes;
   Misc *mi = reinterpret_cast<Misc *>(smem + p.q * stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t part = SPLIT ? blockIdx.x % p.split : 0, split = SPLIT ? p.split : 1;
   const int64_t first = blockIdx.x / split, step = gridDim.x / split;  // this CTA's items
   const int64_t items = SPLIT ? first + 1 : static_cast<int64_t>(p.tiles) * p.n_adapters;
   const int n16 = rank16(p.rank);                  // ranks of an accumulator
-  const int mma_n = joint ? kSParts * p.rank : n16;
+  const int mma_n = joint * n16;
   uint32_t acc_cols = 32;
   while (static_cast<int>(acc_cols) < mma_n) acc_cols <<= 1;
+  const uint32_t nbuf = acc_cols > 128 ? 1 : kNbuf;
 
   if (threadIdx.x == 0) {
     for (int q = 0; q < p.q; ++q) {
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(smem_addr(&mi->tmem), kNbuf * acc_cols);
+    tmem_alloc(smem_addr(&mi->tmem), nbuf * acc_cols);
     tmem_relinquish();
   }
   tc_fence_before_sync();
@@ -186,22 +186,22 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
           todo &= todo - 1;
           const int32_t sb = __shfl_sync(0xffffffffu, static_cast<int32_t>(begin), i);
           const int32_t se = __shfl_sync(0xffffffffu, static_cast<int32_t>(end), i);
-          for (int32_t n = sb; n < se; n = se - n > kK ? n + kK : se) {
+          for (int32_t n = sb; n < se; n = se - n > stage_k ? n + stage_k : se) {
             const bool take = turn == part;
             if (++turn == split) turn = 0;
             if (!take) continue;
             ok = claim();
             if (!ok) break;
             if (lane == 0) {
-              mi->rows[stage] = min(se - n, kK);
+              mi->rows[stage] = min(se - n, stage_k);
               const uint32_t fb = smem_addr(&mi->full[stage]);
               const uint32_t st = smem_addr(smem + stage * stage_bytes);
               mbar_arrive_expect_tx(fb, stage_bytes);
               tma_load_2d(st, tmV, fb, item.f0, n);
-              tma_load_2d(st + kBox, tmV, fb, item.f0 + 64, n);
+              tma_load_2d(st + box_bytes, tmV, fb, item.f0 + 64, n);
               for (int c = 0; c < boxes; ++c) {
-                const int32_t col = joint ? c * 64 : c / rb * p.rank + c % rb * 64;
-                tma_load_2d(st + kVBytes + c * kBox, tmS, fb, col, n);
+                const int32_t col = c < jb ? c * 64 : joint * n16 + (c - jb) * 64;
+                tma_load_2d(st + v_bytes + c * box_bytes, tmS, fb, col, n);
               }
             }
             __syncwarp();
@@ -234,11 +234,12 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
     }
   } else if (warp == kMmaWarp) {
     const uint32_t idesc = idesc_f16(BF16, /*a_mn_major=*/true, /*b_mn_major=*/true, kFeat, static_cast<uint32_t>(mma_n));
+    const uint32_t idesc_rest = idesc_f16(BF16, true, true, kFeat, static_cast<uint32_t>(n16));
     uint32_t stage = 0, phase = 0, count = 0;
     bool ok = true;
     for (int64_t it = first; it < items && ok; it += step, ++count) {
-      const uint32_t buf = count % kNbuf;
-      ok = wait_phase(mi->acc_empty[buf], ((count / kNbuf) & 1u) ^ 1u);
+      const uint32_t buf = count % nbuf;
+      ok = wait_phase(mi->acc_empty[buf], ((count / nbuf) & 1u) ^ 1u);
       if (!ok) break;
       tc_fence_after_sync();
       const uint32_t acc = tmem + buf * acc_cols;
@@ -255,17 +256,18 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
             const int n = (16 * steps - rows) * 8;
             uint8_t *st = smem + stage * stage_bytes + rows * 128;
             for (int box = 0; box < kFeat / 64 + boxes; ++box)
-              for (int u = lane; u < n; u += 32) *reinterpret_cast<uint4 *>(st + box * kBox + u * 16) = make_uint4(0, 0, 0, 0);
+              for (int u = lane; u < n; u += 32) *reinterpret_cast<uint4 *>(st + box * box_bytes + u * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
           }
           tc_fence_after_sync();
           const uint32_t st = smem_addr(smem + stage * stage_bytes);
-          const uint64_t v = smem_desc_sw128(st, kBox, 1024);
-          const uint64_t s = smem_desc_sw128(st + kVBytes, kBox, 1024);
+          const uint64_t v = smem_desc_sw128(st, box_bytes, 1024);
+          const uint64_t s = smem_desc_sw128(st + v_bytes, box_bytes, 1024);
           for (int kk = 0; kk < steps; ++kk) {
             umma_f16_elect(acc, smem_desc_add(v, kk * 2048), smem_desc_add(s, kk * 2048), idesc, (any || kk > 0) ? 1u : 0u);
-            if (!joint) umma_f16_elect(acc, smem_desc_add(v, kk * 2048), smem_desc_add(s, rb * kBox + kk * 2048), idesc, 1u);
+            if (joint < kHParts)
+              umma_f16_elect(acc, smem_desc_add(v, kk * 2048), smem_desc_add(s, jb * box_bytes + kk * 2048), idesc_rest, 1u);
           }
           any = true;
         }
@@ -295,8 +297,8 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
     const int r = sp * 32 + lane;  // feature f0 + r
     uint32_t count = 0;
     for (int64_t it = first; it < items; it += step, ++count) {
-      const uint32_t buf = count % kNbuf;
-      if (!wait_phase(mi->acc_full[buf], (count / kNbuf) & 1u)) {
+      const uint32_t buf = count % nbuf;
+      if (!wait_phase(mi->acc_full[buf], (count / nbuf) & 1u)) {
         give_up();
         break;
       }
@@ -306,13 +308,17 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
       for (int c0 = 0; c0 < n16; c0 += 16) {
         float v[16] = {};
         if (any) {
-          uint32_t hi[16], lo[16];
+          uint32_t part_sum[kHParts][16];
           const uint32_t at = tmem + buf * acc_cols + (static_cast<uint32_t>(sp * 32) << 16) + c0;
-          tmem_ld_32x32b_x16(at, hi);
-          if (joint) tmem_ld_32x32b_x16(at + p.rank, lo);
+#pragma unroll
+          for (int q = 0; q < kHParts; ++q)
+            if (q < joint) tmem_ld_32x32b_x16(at + q * n16, part_sum[q]);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(hi[i]) + (joint ? __uint_as_float(lo[i]) : 0.0f);
+          for (int q = kHParts - 1; q >= 0; --q)  // the smallest first
+            if (q < joint)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(part_sum[q][i]);
         }
         if constexpr (SPLIT) {
           float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(smem) + r * part_pitch(p.rank) + c0);  // the stages are done with
@@ -354,11 +360,13 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, kNbuf * acc_cols);
+    tmem_dealloc(tmem, nbuf * acc_cols);
   }
 }
 
 }  // namespace
+
+int wgrad_stage_rows(int rank) { return stage_rows(rank); }
 
 cudaError_t launch_adapter_wgrad(AdapterWgradParams p, int num_sms, bool bf16, cudaStream_t s) {
   p.up_tiles = (p.M + kFeat - 1) / kFeat;
@@ -373,11 +381,11 @@ cudaError_t launch_adapter_wgrad(AdapterWgradParams p, int num_sms, bool bf16, c
   // tiles: 25 / 135).
   const int64_t active = p.n_seg < p.n_adapters ? (p.n_seg > 0 ? p.n_seg : 1) : p.n_adapters;
   p.split = 1;
-  while (p.split < 8 && p.tiles * active * p.split * 2 <= 2ll * num_sms && p.N >= 8ll * kK * active * p.split &&
+  while (p.split < 8 && p.tiles * active * p.split * 2 <= 2ll * num_sms && p.N >= 512ll * active * p.split &&
          p.tiles * static_cast<int64_t>(p.n_adapters) * p.split * 2 <= 8ll * num_sms)
     p.split *= 2;
   const bool split = p.split > 1;
-  const int stage = kVBytes + s_boxes(p.rank) * kBox;
+  const int stage = (kFeat / 64 + s_boxes(p.rank)) * stage_rows(p.rank) * 128;
   p.q = (kSmemLimit - kMiscBytes - 1024) / stage;
   if (p.q > kMaxQ) p.q = kMaxQ;
   const int smem = p.q * stage + kMiscBytes + 1024;

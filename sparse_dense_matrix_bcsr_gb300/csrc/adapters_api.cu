@@ -113,13 +113,12 @@ spmm::AdapterParams make_params(spmm_handle h, spmm_adapters a, int64_t N, const
   return p;
 }
 
-// One product of down_project: H = scale * X D^T in 16 bits (`parts` of them), D
+// One product of down_project: H = scale * X D^T in 16-bit parts, D
 // n_adapters x rank x K, or transposed n_adapters x K x rank.
 struct DownJob {
   const void *X, *D;
   float *H;
   int64_t K;
-  int parts;
   bool transposed;
 };
 
@@ -138,7 +137,6 @@ spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, std::ini
     if (st != SPMM_OK) return st;
     o.H = reinterpret_cast<uint16_t *>(j.H);
     o.K = static_cast<int32_t>(j.K);
-    o.parts = j.parts;
     o.transposed = j.transposed ? 1 : 0;
   }
   d.exact = exact ? 1 : 0;
@@ -173,9 +171,9 @@ spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams
     st = spmm::encode_2d(&ad.tmU, p.up, bf16, static_cast<uint64_t>(p.n_adapters) * p.M, p.rank, p.rank, 64, ad.box,
                          ad.box * 2);
   if (st == SPMM_OK)
-    st = spmm::encode_3d(&ad.tmH, p.H, bf16, p.N, spmm::kHParts, p.rank, 128, 1, ad.box, ad.box * 2);
+    st = spmm::encode_3d(&ad.tmH, p.H, bf16, p.N, spmm::kHParts, spmm::rank16(p.rank), 128, 1, ad.box, ad.box * 2);
   if (st == SPMM_OK)
-    st = spmm::encode_3d(&ad.tmHs, p.H, bf16, p.N, spmm::kHParts, p.rank, spmm::kAdapterFewRows, 1, ad.box, ad.box * 2);
+    st = spmm::encode_3d(&ad.tmHs, p.H, bf16, p.N, spmm::kHParts, spmm::rank16(p.rank), spmm::kAdapterFewRows, 1, ad.box, ad.box * 2);
   if (st != SPMM_OK) return st;
   ad.tile_segs = a->d_tile_segs;
   ad.tile_count = a->d_tile_count;
@@ -282,7 +280,7 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
   if (sorted || !rows_path(p.N, p.rank, p.n_seg)) {
     const spmm::LinearTile tile = spmm::linear_adapters_tile(h->n_groups, h->n_units, p.N, p.n_seg, h->out_t == SPMM_BF16,
                                                                p.num_sms);
-    spmm_status st = down_project(a, p, {{X, down, a->d_h, p.K, spmm::kHParts, false}}, h->out_t == SPMM_F32, spmm::linear_tile_rows(tile), s);
+    spmm_status st = down_project(a, p, {{X, down, a->d_h, p.K, false}}, h->out_t == SPMM_F32, spmm::linear_tile_rows(tile), s);
     if (st == SPMM_OK) st = up_project(h, a, p, false, tile, s);
     if (st == SPMM_OK && sorted)
       CUDA_TRY(spmm::launch_adapter_ungroup(a->d_place, p.N, Y, out, static_cast<int64_t>(p.M) * (h->out_t == SPMM_F32 ? 4 : 2), s),
@@ -352,8 +350,8 @@ spmm_status spmm_adapters_create(spmm_adapters *out, int64_t m, int64_t k, int32
     CUDA_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, a->device), "device attribute");
     CUDA_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, a->device), "device attribute");
     a->sm103 = major == 10 && minor == 3;
-    const size_t h = static_cast<size_t>(std::max<int64_t>(max_rows, 1)) * rank *
-                     std::max(sizeof(float), spmm::kHParts * sizeof(uint16_t));
+    const size_t h = static_cast<size_t>(std::max<int64_t>(max_rows, 1)) * spmm::rank16(rank) * spmm::kHParts * sizeof(uint16_t);
+    static_assert(spmm::kHParts * sizeof(uint16_t) >= sizeof(float), "fp32 values too");
     CUDA_TRY(cudaMalloc(&a->d_h, h), "cudaMalloc(adapter activations)");
     // one entry per row of the tiles, one count per tile of the smallest
     const size_t rows = (static_cast<size_t>(max_rows) / spmm::kMaxTileRows + 1) * spmm::kMaxTileRows;
@@ -434,8 +432,8 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
   // H and dH, then dX with the roles of the adapters' two matrices exchanged
   const spmm::LinearTile tile = spmm::linear_adapters_tile(h_t->n_groups, h_t->n_units, p.N, p.n_seg, h_t->out_t == SPMM_BF16,
                                                                p.num_sms);
-  const DownJob of_x{X, down, a->d_h, k, spmm::kWgradParts, false},
-      of_dy{dY, up, a->d_dh, m, spmm::kHParts, true};
+  const DownJob of_x{X, down, a->d_h, k, false},
+      of_dy{dY, up, a->d_dh, m, true};
   const bool exact = h_t->out_t == SPMM_F32;  // with or without dX: the same d_up and d_down
   st = m > k ? down_project(a, p, {of_dy, of_x}, exact, spmm::linear_tile_rows(tile), s)  // the longer first
              : down_project(a, p, {of_x, of_dy}, exact, spmm::linear_tile_rows(tile), s);
@@ -452,10 +450,12 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
                "return of sorted rows launch");
   }
   spmm::AdapterWgradParams w;
-  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dy, dY, bf16, N, m, m, 64, 64);
-  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_x, X, bf16, N, k, k, 64, 64);
-  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_h, a->d_h, bf16, N, spmm::kWgradParts * a->rank, spmm::kWgradParts * a->rank, 64, 64);
-  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dh, a->d_dh, bf16, N, spmm::kWgradParts * a->rank, spmm::kHParts * a->rank, 64, 64);
+  const int rows = spmm::wgrad_stage_rows(a->rank);
+  const int64_t cols = spmm::kHParts * spmm::rank16(a->rank);
+  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dy, dY, bf16, N, m, m, rows, 64);
+  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_x, X, bf16, N, k, k, rows, 64);
+  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_h, a->d_h, bf16, N, cols, cols, rows, 64);
+  if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dh, a->d_dh, bf16, N, cols, cols, rows, 64);
   if (st != SPMM_OK) return st;
   w.d_up = static_cast<uint16_t *>(d_up);
   w.d_down = static_cast<uint16_t *>(d_down);

@@ -127,13 +127,15 @@ struct TileSegment {
 // The adapters of the same product (launch_bcsr_linear_adapters): tmU covers
 // the up matrices as [n_adapters * M rows, rank cols] with 64 x box boxes (or,
 // u_transposed, matrices of [n_adapters, rank rows, M cols] with box x 64 boxes,
-// 128-byte swizzle), tmH covers H as [N rows, kHParts, rank cols] with 128 x 1 x box
+// 128-byte swizzle), tmH covers H as [N rows, kHParts, rank16 cols] with 128 x 1 x box
 // boxes (tmHs: kAdapterFewRows x 1 x box), all swizzled in the width of a box row; box =
 // 16 or 32 ranks; H is the sum of its parts.
 // A 32-bit h as a matrix operand: its value in 16 bits, what that rounding left, and what
 // that one did, 24 bits of bf16 (one part alone moved a bf16 Y by 1.2e-3 of it where the
 // adapters are most of it, two hold 16 bits).
 constexpr int kHParts = 3;
+// Ranks in H's rows, a whole number of MMA steps; those past the rank hold zeros.
+__host__ __device__ constexpr int rank16(int rank) { return (rank + 15) / 16 * 16; }
 constexpr int kAdapterFewRows = 16;
 struct LinearAdapters {
   CUtensorMap tmU, tmH, tmHs;
@@ -291,8 +293,8 @@ struct AdapterDownJob {
   CUtensorMap tmX;               // X as [N rows, K cols], 128 x 64 boxes, 128-byte swizzle
   CUtensorMap tmD;               // the down matrices as [n_adapters * rank rows, K cols], rank x 64 boxes, 128-byte
                                  // swizzle; transposed: as [n_adapters, K rows, rank cols], 64 x 64 boxes
-  uint16_t *H;                   // device, N x parts x rank: the rows of segments with an adapter
-  int32_t K, parts, transposed;
+  uint16_t *H;                   // device, N x kHParts x rank16(rank): the rows of segments with an adapter
+  int32_t K, transposed;
 };
 struct AdapterDownParams {
   int32_t exact;                 // sums leave the tensor cores often (fp32 outputs)
@@ -358,10 +360,9 @@ cudaError_t launch_adapter_ungroup(const int32_t *place, int64_t N, const void *
                                    cudaStream_t s);
 
 // Gradients of the adapters' weights (adapter_wgrad_kernel.cu).  tm_dy and tm_x
-// cover dY [N rows, M cols] and X [N rows, K cols], tm_h and tm_dh the first
-// kWgradParts parts of H and dH [N rows, parts * rank cols], all with 64 x 64 boxes,
-// 128-byte swizzle.
-constexpr int kWgradParts = 2;
+// cover dY [N rows, M cols] and X [N rows, K cols], tm_h and tm_dh H and dH [N rows,
+// kHParts * rank16 cols], all with boxes of wgrad_stage_rows(rank) x 64, 128-byte swizzle.
+int wgrad_stage_rows(int rank);
 struct AdapterWgradParams {
   CUtensorMap tm_dy, tm_x, tm_h, tm_dh;
   uint16_t *d_up, *d_down;

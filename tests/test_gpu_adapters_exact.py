@@ -128,3 +128,45 @@ def input_gradient(S, m, k, n, segs, rank, n_adapters, in_t, out_t, scale=1.0):
 def test_input_gradient(S, m, k, n, segs, rank, n_adapters, out_t):
     input_gradient(S, m, k, n, segs, rank, n_adapters, "bf16", out_t)
 
+
+WEIGHTS = [
+    # n, segments, rank, adapters
+    pytest.param(700, ragged(700, 5, 3, none=0.0), 8, 3, id="rank-8"),
+    pytest.param(700, ragged(700, 5, 3, none=0.0), 16, 3, id="rank-16"),
+    pytest.param(1024, ragged(1024, 9, 4, none=0.0), 24, 4, id="rank-24"),
+    pytest.param(700, ragged(700, 5, 3, none=0.0), 40, 3, id="rank-40"),
+    pytest.param(700, ragged(700, 20, 6, gaps=True), 48, 6, id="rank-48"),
+    pytest.param(700, ragged(700, 5, 3, none=0.0), 64, 3, id="rank-64"),
+    pytest.param(520, ragged(520, 5, 2, none=0.0), 72, 2, id="rank-72"),
+    pytest.param(700, ragged(700, 5, 3, none=0.0), 128, 3, id="rank-128"),
+    pytest.param(5200, ragged(5200, 3, 1, none=0.0), 16, 1, id="long"),
+    pytest.param(5200, ragged(5200, 3, 1, none=0.0), 128, 1, id="long-rank-128"),
+    pytest.param(6000, ragged(6000, 200, 40, none=0.0), 16, 40, id="40-adapters"),
+]
+
+
+def weight_gradients(S, n, segs, rank, n_adapters, in_t, out_t="bf16", scale=1.0, size=1.0, with_dx=False):
+    # d_up[f][i] is the difference of two rows' h[i], d_down[i][c] of two rows' dh[i]
+    m, k = 456, 328
+    c, rng = zero_weight(m, k, n, even(segs), rank, n_adapters, in_t, out_t, scale)
+    dt = c.X.dtype
+    for up in (True, False):
+        width = k if up else m
+        weights = whole(rng, (n_adapters, rank, width))
+        weights[:, :, :8] = whole(rng, (n_adapters, rank, 8), 1, 16)
+        big, one = paired_rows(c, rng, width).to(dt), (row_signs(c, m if up else k) * size).to(dt)
+        c.X, c.dY = (big, one) if up else (one, big)
+        c.down = (weights if up else torch_zeros(n_adapters, rank, k)).to(dt)
+        c.up = (torch_zeros(n_adapters, m, rank) if up else weights.transpose(1, 2).contiguous()).to(dt)
+        name = "d_up" if up else "d_down"
+        same(run_grad(S, c, with_dx=with_dx)[name], c.reference_grad()[name][0], name, scale * size)
+
+
+def torch_zeros(*shape):
+    import torch
+    return torch.zeros(shape, dtype=torch.float64)
+
+
+@pytest.mark.parametrize("n,segs,rank,n_adapters", WEIGHTS)
+def test_weight_gradients(S, n, segs, rank, n_adapters):
+    weight_gradients(S, n, segs, rank, n_adapters, "bf16")
