@@ -35,10 +35,6 @@ struct spmm_adapters_s {
 
 namespace {
 
-// An H of at most this a part is loaded by a few rows for short segments (LinearAdapters::few):
-// at 3 to 23 KB up to twice as fast (figures at the kernel), at 64 KB 2048 rows in 128
-// segments, 18944 x 3584, take 145 for 120 us.
-constexpr int64_t kFewBytes = 24 * 1024;
 
 void free_adapters(spmm_adapters a) {
   if (!a) return;
@@ -163,23 +159,26 @@ spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams
   const bool bf16 = h->in_t == SPMM_BF16, out_bf16 = h->out_t == SPMM_BF16;
   CUtensorMap tmX, tmY;
   spmm::LinearAdapters ad;
-  ad.box = p.rank <= 16 ? 16 : 32;
+  const int r16 = spmm::rank16(p.rank);
+  ad.groups = p.rank <= 64 ? 1 : 2;
+  ad.cols = ad.groups > 1 ? r16 : spmm::kHParts * r16;
+  ad.boxes = ad.groups > 1 ? spmm::kHParts : (ad.cols + 63) / 64;
+  ad.u_cols = r16 <= 16 ? 16 : r16 <= 32 ? 32 : 64;
+  ad.u_steps = ad.groups > 1 ? 4 : r16 / 16;
   spmm_status st = spmm::encode_x(&tmX, p.X, bf16, p.N, p.K);
   if (st == SPMM_OK) st = spmm::encode_y(&tmY, p.Y, out_bf16, p.N, p.M, spmm::linear_tile_rows(tile));
-  if (st == SPMM_OK && transposed) st = spmm::encode_3d(&ad.tmU, p.up, bf16, p.n_adapters, p.rank, p.M, 1, ad.box);
+  if (st == SPMM_OK && transposed) st = spmm::encode_3d(&ad.tmU, p.up, bf16, p.n_adapters, p.rank, p.M, 1, ad.u_cols);
   if (st == SPMM_OK && !transposed)
-    st = spmm::encode_2d(&ad.tmU, p.up, bf16, static_cast<uint64_t>(p.n_adapters) * p.M, p.rank, p.rank, 64, ad.box,
-                         ad.box * 2);
+    st = spmm::encode_2d(&ad.tmU, p.up, bf16, static_cast<uint64_t>(p.n_adapters) * p.M, p.rank, p.rank, 64, ad.u_cols,
+                         ad.u_cols * 2);
   if (st == SPMM_OK)
-    st = spmm::encode_3d(&ad.tmH, p.H, bf16, p.N, spmm::kHParts, spmm::rank16(p.rank), 128, 1, ad.box, ad.box * 2);
+    st = spmm::encode_3d(&ad.tmH, p.H, bf16, p.N, spmm::kHParts * r16 / ad.cols, ad.cols, 128, 1);
   if (st == SPMM_OK)
-    st = spmm::encode_3d(&ad.tmHs, p.H, bf16, p.N, spmm::kHParts, spmm::rank16(p.rank), spmm::kAdapterFewRows, 1, ad.box, ad.box * 2);
+    st = spmm::encode_3d(&ad.tmHs, p.H, bf16, p.N, spmm::kHParts * r16 / ad.cols, ad.cols, spmm::kAdapterFewRows, 1);
   if (st != SPMM_OK) return st;
   ad.tile_segs = a->d_tile_segs;
   ad.tile_count = a->d_tile_count;
-  ad.rank = p.rank;
   ad.u_transposed = transposed ? 1 : 0;
-  ad.few = static_cast<int64_t>(p.N) * p.rank * 2 <= kFewBytes ? 1 : 0;
   ad.tile = tile;
   spmm::BcsrParams b;
   std::memset(&b, 0, sizeof b);

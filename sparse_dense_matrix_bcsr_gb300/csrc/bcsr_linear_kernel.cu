@@ -39,10 +39,13 @@
 //
 // With adapters (spmm_run_linear_adapters) a tile has further stages after its
 // blocks: for every segment with an adapter among its rows, the block row's 64
-// rows of U_a as the N operand and the tile's rows of H as the M operand, 16 or 32
-// ranks a stage.  H comes in kHParts 16-bit parts, which add up to the fp32 value, so
-// that Y is rounded once whatever its type; a stage holds all parts of the tile's rows
-// (16 ranks) or of half of them.  Their
+// rows of U_a as the N operand and the tile's rows of H as the M operand.  H comes in
+// kHParts 16-bit parts, which add up to the fp32 value, so that Y is rounded once
+// whatever its type.  The parts of a row lie side by side and are loaded as one matrix of
+// kHParts * rank columns in boxes of 64, several a stage; U is loaded whole (up to rank 64, else
+// in halves) and each 16 columns of H meet its 16 ranks.  (A box for each part, 16 or 32
+// ranks wide, through 18944 x 3584: 1386 us for 1330 with 65536 rows in 9 segments, rank 16;
+// 617 for 513 with 8192 rows in 500; 530 for 521 with 16384 in 9, rank 64.)  Their
 // MMAs update the segment's lanes only (the MMA's lane mask), so the other rows'
 // sums do not see the product at all: no zeroed copy of H, and an adapter with
 // infinities cannot reach other rows as 0 * inf.  The product with adapters reads
@@ -50,12 +53,12 @@
 // 18944 features.  The gradient's dX takes D_a where the forward pass takes U_a,
 // as it lies (MN-major).
 //
-// A stage of an adapter loads H by 128 rows, whatever the segment has of them.  Where
-// H is small (`few`) segments of a few rows load it by 16 instead: there every CTA reads
-// the same lines of H for every adapter, and L2 cannot serve them fast enough (dX of 79
-// rows with 38 adapters, 13752 features: 229 us, by 16 rows 122; gradient of 230 rows
-// with 59, 672 x 6984: 306 and 136).  Where H is larger the large box is faster (8192
-// rows in 500 segments: 139 us against 161).
+// A stage of an adapter loads H by 128 rows, segments of at most two boxes of 16 rows by
+// 16: in short batches every CTA reads the same lines of H for every adapter, and L2 cannot
+// serve them fast enough (dX of 79 rows with 38 adapters, 13752 features, one part of H: 229
+// us, by 16 rows 122; gradient of 230 rows with 59, 672 x 6984: 306 and 136); in longer ones
+// the small boxes write less to shared memory (8192 rows in 500 segments, 18944 x 3584: 522 us
+// for 536; 2048 in 128: 159 for 169).
 //
 // The tensor cores cut what their fp32 sums shift out instead of rounding it, ~1e-9
 // of the result for every term.  Where Y is bf16 its rounding hides that.  An fp32 Y
@@ -85,6 +88,7 @@ constexpr int kNbuf = 2;                       // TMEM accumulators per CTA
 constexpr int kThreads = 192;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2, kEpiWarps = 4;
 constexpr int kMiscBytes = 1024;
+constexpr int kHBytes = 128 * 128;               // a box of H: 128 rows x 64 columns
 constexpr int kFewRows = kAdapterFewRows, kFewBoxes = 2;  // boxes of H for short segments
 constexpr int kTurn = 8;                       // blocks between two drains (fp32 outputs with adapters)
 
@@ -109,16 +113,15 @@ struct Tile {
 constexpr int32_t kRecEmpty = 1, kRecEnd = 2, kRecAdapters = 4, kRecLast = 8, kRecMore = 16;
 // What the producer tells the MMA warp with a tile's first stage: the tile, how
 // many stages of blocks it has and whether adapters follow.  With a stage of an
-// adapter: its steps of 16 ranks, its rows of the tile (begin | end << 16), the
-// first part that the stage holds and whether it is the tile's last.
+// adapter: its boxes of H (the first | their number << 8 | U's group << 16), its rows of
+// the tile (begin | end << 16) and whether it is the tile's last.
 struct TileRec {
   int32_t br;
   int32_t nt;
   int32_t flags;
-  int32_t stages;  // or steps
+  int32_t stages;  // or boxes
   int32_t rows;
-  int32_t part;
-  int32_t pad_[2];
+  int32_t pad_[3];
 };
 
 template <int GROUP>
@@ -129,15 +132,6 @@ __device__ __forceinline__ void tile_coords(int64_t t, int n_block_rows, int n_t
   const int gsz = min(GROUP, n_tiles_n - static_cast<int>(g) * GROUP);
   br = static_cast<int>(r / gsz);
   nt = static_cast<int>(g) * GROUP + static_cast<int>(r % gsz);
-}
-
-// Parts (128 rows) of the tile that a stage of an adapter holds, with H's 16-bit
-// parts in the place of X: all of them, or half with boxes of 32 ranks.
-template <class T>
-__device__ __forceinline__ int stage_parts(const LinearAdapters &ad) {
-  static_assert(T::kParts * kHParts * 128 * 16 * 2 <= T::kXBytes && T::kParts / 2 * kHParts * 128 * 32 * 2 <= T::kXBytes,
-                "an adapter's stage");
-  return ad.box == 16 ? T::kParts : T::kParts / 2;
 }
 
 // Y's store boxes: 32 rows (a warp's lanes of one part) x 128 or 64 bytes.
@@ -280,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
           ok = claim();
           if (!ok) break;
           if (lane == 0) {
-            tile_rec[stage] = TileRec{br, nt, first_flags, 1, 0, 0, {}};
+            tile_rec[stage] = TileRec{br, nt, first_flags, 1, 0, {}};
             const uint32_t fb = full0 + 8 * stage;
             const uint32_t st = smem_addr(smem + stage * kStageBytes);
             mbar_arrive_expect_tx(fb, kStageBytes);
@@ -292,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
           ok = claim();
           if (!ok) break;
           if (lane == 0) {
-            tile_rec[stage] = TileRec{br, nt, kRecEmpty, 0, 0, 0, {}};
+            tile_rec[stage] = TileRec{br, nt, kRecEmpty, 0, 0, {}};
             mbar_arrive(full0 + 8 * stage);
           }
           advance();
@@ -306,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
             if (!ok) break;
             if (lane == 0) {
               const int64_t j = jbase + i;
-              if (j == jb) tile_rec[stage] = TileRec{br, nt, first_flags, static_cast<int32_t>(je - jb), 0, 0, {}};
+              if (j == jb) tile_rec[stage] = TileRec{br, nt, first_flags, static_cast<int32_t>(je - jb), 0, {}};
               const uint32_t fb = full0 + 8 * stage;
               const uint32_t st = smem_addr(smem + stage * kStageBytes);
               mbar_arrive_expect_tx(fb, kStageBytes);
@@ -328,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
               ok = claim();
               if (!ok) break;
               if (lane == 0) {
-                tile_rec[stage] = TileRec{br, nt, kRecLast, 0, 0, 0, {}};
+                tile_rec[stage] = TileRec{br, nt, kRecLast, 0, 0, {}};
                 mbar_arrive(full0 + 8 * stage);
               }
               advance();
@@ -341,49 +335,35 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
             for (int i = 0; i < cnt && ok; ++i) {
               const int32_t a = __shfl_sync(0xffffffffu, my.adapter, i);
               const int32_t begin = __shfl_sync(0xffffffffu, my.begin, i), end = __shfl_sync(0xffffffffu, my.end, i);
-              const int group = stage_parts<T>(ad);
-              for (int g = begin / 128 / group * group; g * 128 < end && ok; g += group) {
-                const int h0 = max(begin / 128, g), h1 = min((end + 127) / 128, g + group);
-                for (int32_t r0 = 0; r0 < ad.rank; r0 += ad.box) {
+              const int h0 = begin / 128, h1 = (end + 127) / 128, nh = h1 - h0, per = T::kParts / nh;
+              for (int32_t g = 0; g < ad.groups && ok; ++g) {
+                for (int32_t b0 = 0; b0 < ad.boxes; b0 += per) {
+                  const int32_t nb = min(ad.boxes - b0, per);
                   ok = claim();
                   if (!ok) break;
                   if (lane == 0) {
-                    const bool last = base + i == segs - 1 && (g + group) * 128 >= end && r0 + ad.box >= ad.rank;
-                    tile_rec[stage] = TileRec{br, nt, last ? kRecLast : 0, (min(ad.rank - r0, ad.box) + 15) / 16,
-                                              begin | end << 16, g, {}};
+                    const bool last = base + i == segs - 1 && g + 1 == ad.groups && b0 + nb == ad.boxes;
+                    tile_rec[stage] = TileRec{br, nt, last ? kRecLast : 0, b0 | nb << 8 | g << 16, begin | end << 16, {}};
                     const uint32_t fb = full0 + 8 * stage;
                     const uint32_t st = smem_addr(smem + stage * kStageBytes);
-                    const uint32_t part_bytes = 128 * ad.box * 2;
-                    auto copy_u = [&] {
-                      if (ad.u_transposed)
-                        tma_load_3d(st, &ad.tmU, fb, br * kBlk, r0, a);
-                      else
-                        tma_load_2d(st, &ad.tmU, fb, r0, a * p.M + br * kBlk);
-                    };
+                    // Segments of a few rows can come in boxes of kFewRows: the ones of part h0 that hold them
+                    const int first = (begin - h0 * 128) / kFewRows;
+                    const int small = nh == 1 ? (min(end - h0 * 128, 128) + kFewRows - 1) / kFewRows - first : kFewBoxes + 1;
+                    const bool few = small <= kFewBoxes;
+                    mbar_arrive_expect_tx(fb, kBlk * ad.u_cols * 2 + nb * (few ? small * kFewRows * 128 : nh * kHBytes));
+                    if (ad.u_transposed)
+                      tma_load_3d(st, &ad.tmU, fb, br * kBlk, g * 64, a);
+                    else
+                      tma_load_2d(st, &ad.tmU, fb, g * 64, a * p.M + br * kBlk);
                     const int row0 = nt * kTileN;
-                    if (!ad.few) {
-                      mbar_arrive_expect_tx(fb, kBlk * ad.box * 2 + (h1 - h0) * kHParts * part_bytes);
-                      copy_u();
-                      for (int q = 0; q < kHParts; ++q)
-                        for (int h = h0; h < h1; ++h)
-                          tma_load_3d(st + kBlkBytes + (q * group + h - g) * part_bytes, &ad.tmH, fb, r0, q, row0 + h * 128);
-                    } else {
-                      // boxes of kFewRows rows that hold the segment's, or the large ones
-                      const uint32_t few_bytes = kFewRows * ad.box * 2;
-                      const int p0 = h0 * 128, b0 = (max(begin, p0) - p0) / kFewRows;
-                      const int n = h1 - h0 == 1 ? (min(end - p0, 128) + kFewRows - 1) / kFewRows - b0 : kFewBoxes + 1;
-                      const bool small = n <= kFewBoxes;
-                      mbar_arrive_expect_tx(fb, kBlk * ad.box * 2 + kHParts * (small ? n * few_bytes : (h1 - h0) * part_bytes));
-                      copy_u();
-                      for (int q = 0; q < kHParts; ++q) {
-                        const uint32_t at = st + kBlkBytes + (q * group + h0 - g) * part_bytes;
-                        if (small)
-                          for (int b = b0; b < b0 + n; ++b)
-                            tma_load_3d(at + b * few_bytes, &ad.tmHs, fb, r0, q, row0 + p0 + b * kFewRows);
-                        else
-                          for (int h = h0; h < h1; ++h)
-                            tma_load_3d(at + (h - h0) * part_bytes, &ad.tmH, fb, r0, q, row0 + h * 128);
-                      }
+                    for (int32_t b = b0; b < b0 + nb; ++b) {
+                      const int32_t x = ad.groups > 1 ? g * 64 : b * 64, y = ad.groups > 1 ? b : 0;
+                      const uint32_t at = st + kBlkBytes + (b - b0) * nh * kHBytes;
+                      if (few)
+                        for (int r = first; r < first + small; ++r)
+                          tma_load_3d(at + r * (kFewRows * 128), &ad.tmHs, fb, x, y, row0 + h0 * 128 + r * kFewRows);
+                      else
+                        for (int h = h0; h < h1; ++h) tma_load_3d(at + (h - h0) * kHBytes, &ad.tmH, fb, x, y, row0 + h * 128);
                     }
                   }
                   advance();
@@ -397,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
     if (ok) {
       ok = claim();
       if (ok && lane == 0) {
-        tile_rec[stage] = TileRec{-1, -1, kRecEnd, 0, 0, 0, {}};
+        tile_rec[stage] = TileRec{-1, -1, kRecEnd, 0, 0, {}};
         mbar_arrive(full0 + 8 * stage);
       }
     }
@@ -426,18 +406,16 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
     // the M operand (part h its rows 128 h .. 128 h + 127).
     const uint64_t blk_desc = smem_desc_sw128(smem_addr(smem), 16, 1024);
     const uint64_t x_desc = smem_desc_sw128(smem_addr(smem) + kBlkBytes, 16, 1024);
-    // An adapter's operands lie in the same places, in rows of ad.box ranks.
-    uint64_t u_desc = 0, h_desc = 0;
-    uint32_t h_part = 0, u_step = 32, u_idesc = idesc;
+    // An adapter's operands lie in the same places; U in rows of u_cols ranks.
+    uint64_t u_desc = 0;
+    uint32_t u_step = 32, u_idesc = idesc;
     if constexpr (kAdapt) {
-      h_part = 128 * ad.box * 2;
-      u_desc = smem_desc_k_major(smem_addr(smem), ad.box * 2);
+      u_desc = smem_desc_k_major(smem_addr(smem), ad.u_cols * 2);
       if (ad.u_transposed) {  // rows of 64 features, one per rank
         u_desc = smem_desc_sw128(smem_addr(smem), 16, 1024);
         u_step = 16 * 128;
         u_idesc = idesc_f16(IN_BF16, false, /*b_mn_major=*/true, 128, kBlk);
       }
-      h_desc = smem_desc_k_major(smem_addr(smem) + kBlkBytes, ad.box * 2);
     }
     while (true) {
       ok = wait_full();
@@ -505,33 +483,41 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
             tc_fence_after_sync();
             const TileRec seg = tile_rec[stage];
             more = (seg.flags & kRecLast) == 0;
-            const int begin = seg.rows & 0xffff, end = seg.rows >> 16;
-            const int group = stage_parts<T>(ad);
+            const int begin = seg.rows & 0xffff, end = seg.rows >> 16, h0 = begin / 128, h1 = (end + 127) / 128;
+            const int b0 = seg.stages & 0xff, nb = seg.stages >> 8 & 0xff;
             const uint64_t bdesc0 = smem_desc_add(u_desc, stage * kStageBytes);
-            const uint64_t adesc0 = smem_desc_add(h_desc, stage * kStageBytes);
-            if (begin <= 128 * seg.part && end >= 128 * (seg.part + group)) {
-              // the segment holds all rows of the stage: no lanes to mask; as for the
-              // blocks, MMAs in a row go to different accumulators
-              for (int kk = 0; kk < seg.stages; ++kk) {
-                for (int q = 0; q < kHParts; ++q) {
-#pragma unroll
-                  for (int i = 0; i < group; ++i)
-                    umma_f16_elect(acc + (seg.part + i) * kBlk, smem_desc_add(adesc0, (q * group + i) * h_part + kk * 32),
-                                   smem_desc_add(bdesc0, kk * u_step), u_idesc, 1u);
+            const uint64_t adesc0 = smem_desc_add(x_desc, stage * kStageBytes);
+            // the stage's steps: 16 columns of H (16 ranks of one of its parts) by the same
+            // ranks of U; box b starts b * nh * kHBytes after H's first
+            const int nh = h1 - h0;
+            auto steps = [&](auto &&mma) {
+              for (int b = 0; b < nb; ++b) {
+                const int x = ad.groups > 1 ? (seg.stages >> 16) * 64 : (b0 + b) * 64;
+                const int n = min(ad.cols - x, 64) / 16;
+                int u = ad.groups > 1 ? 0 : static_cast<int>(static_cast<uint32_t>(x / 16) % static_cast<uint32_t>(ad.u_steps));
+                uint64_t adesc = smem_desc_add(adesc0, b * nh * kHBytes);
+                for (int k = 0; k < n; ++k) {
+                  mma(adesc, smem_desc_add(bdesc0, u * u_step));
+                  adesc = smem_desc_add(adesc, 32);
+                  if (++u == ad.u_steps) u = 0;
                 }
               }
+            };
+            if (begin == 0 && end == kTileN) {
+              // the segment holds all rows of the tile: no lanes to mask; as for the
+              // blocks, MMAs in a row go to different accumulators
+              steps([&](uint64_t adesc, uint64_t bdesc) {
+#pragma unroll
+                for (int h = 0; h < T::kParts; ++h)
+                  umma_f16_elect(acc + h * kBlk, smem_desc_add(adesc, h * kHBytes), bdesc, u_idesc, 1u);
+              });
             } else {
-              for (int i = 0; i < group; ++i) {
-                const int h = seg.part + i;
-                if (end <= 128 * h || begin >= 128 * (h + 1)) continue;
+              for (int h = h0; h < h1; ++h) {
                 uint32_t off[4];
                 lanes_off(begin - 128 * h, end - 128 * h, off);
-                for (int q = 0; q < kHParts; ++q) {
-                  const uint64_t adesc = smem_desc_add(adesc0, (q * group + i) * h_part);
-                  for (int kk = 0; kk < seg.stages; ++kk)
-                    umma_f16_lanes_elect(acc + h * kBlk, smem_desc_add(adesc, kk * 32), smem_desc_add(bdesc0, kk * u_step),
-                                         u_idesc, 1u, off);
-                }
+                steps([&](uint64_t adesc, uint64_t bdesc) {
+                  umma_f16_lanes_elect(acc + h * kBlk, smem_desc_add(adesc, (h - h0) * kHBytes), bdesc, u_idesc, 1u, off);
+                });
               }
             }
             release();

@@ -125,11 +125,12 @@ struct TileSegment {
   int32_t adapter, begin, end, pad_;
 };
 // The adapters of the same product (launch_bcsr_linear_adapters): tmU covers
-// the up matrices as [n_adapters * M rows, rank cols] with 64 x box boxes (or,
-// u_transposed, matrices of [n_adapters, rank rows, M cols] with box x 64 boxes,
-// 128-byte swizzle), tmH covers H as [N rows, kHParts, rank16 cols] with 128 x 1 x box
-// boxes (tmHs: kAdapterFewRows x 1 x box), all swizzled in the width of a box row; box =
-// 16 or 32 ranks; H is the sum of its parts.
+// the up matrices as [n_adapters * M rows, rank cols] with 64 x u_cols boxes, swizzled
+// in the width of a box row (or, u_transposed, matrices of [n_adapters, rank rows, M cols]
+// with u_cols x 64 boxes, 128-byte swizzle), u_cols = 16, 32 or 64; tmH covers H, up to rank 64
+// as one matrix [N rows, cols = kHParts * rank16 cols], above (groups = 2 of 64 ranks) as
+// [N rows, kHParts, cols = rank16 cols], with 128 x 1 x 64 boxes (tmHs: kAdapterFewRows x 1 x
+// 64), 128-byte swizzle.  H is the sum of its parts.
 // A 32-bit h as a matrix operand: its value in 16 bits, what that rounding left, and what
 // that one did, 24 bits of bf16 (one part alone moved a bf16 Y by 1.2e-3 of it where the
 // adapters are most of it, two hold 16 bits).
@@ -141,9 +142,9 @@ struct LinearAdapters {
   CUtensorMap tmU, tmH, tmHs;
   const TileSegment *tile_segs;  // device, the tile's rows per tile
   const int32_t *tile_count;     // device, per tile: its segments with an adapter
-  int32_t rank, box;
+  int32_t cols, boxes, groups;   // of H: columns, boxes for each group of ranks
+  int32_t u_cols, u_steps;       // of U: ranks of a box, steps of 16 ranks before they repeat
   int32_t u_transposed;          // the gradient's: the adapters' down matrices
-  int32_t few;                   // segments of a few rows load H by kAdapterFewRows
   LinearTile tile;
 };
 // Launched as a programmatic dependent of the kernel that writes H and the
