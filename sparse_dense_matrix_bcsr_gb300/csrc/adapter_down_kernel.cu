@@ -23,8 +23,7 @@
 //
 // H is kept in 16-bit parts (the value rounded, the rest rounded, ...), kHParts of them,
 // 24 bits of bf16 (two of bf16, 16 bits, left 1.2e-6 of an fp32 Y off where the adapters
-// are most of it, three 0.6e-6).  Where the output is fp32 the
-// sums leave the tensor cores, which cut what an fp32 sum shifts out instead of
+// are most of it, three 0.6e-6).  The sums leave the tensor cores, which cut what an fp32 sum shifts out instead of
 // rounding it (~1e-9 of the sum for every term), every kTurn stages and are added
 // in registers.
 #include <cuda_bf16.h>
@@ -44,7 +43,7 @@ constexpr int kMaxSplit = 16;           // CTAs of a cluster (above 8 a kernel h
 constexpr int kThreads = 192;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2;
 constexpr int kNbuf = 2;                // accumulators
-constexpr int kTurn = 8;                // stages between two drains of the accumulator (TURNS)
+constexpr int kTurn = 8;                // stages between two drains of the accumulator
 constexpr int kMiscBytes = 1024;
 constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
 
@@ -102,8 +101,7 @@ __device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int32_t rank, 
   }
 }
 
-// TURNS: the sums leave the tensor cores every kTurn stages.
-template <bool BF16, bool TURNS>
+template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_constant__ AdapterDownParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -119,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
   const int n16 = rank16(p.rank);
   uint32_t acc_cols = 32;
   while (static_cast<int>(acc_cols) < n16) acc_cols <<= 1;
-  const uint32_t tmem_cols = TURNS ? kNbuf * acc_cols : acc_cols;
+  const uint32_t tmem_cols = kNbuf * acc_cols;
 
   if (warp == kTmaWarp) {
     if (lane == 0) {
@@ -202,9 +200,9 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
       bool ok = true;
       for (int32_t c = k_begin; c < k_end; ++c) {
         const int32_t i = c - k_begin;
-        const uint32_t turn = TURNS ? i / kTurn : 0, buf = turn % kNbuf, acc = tmem + buf * acc_cols;
-        const bool first = TURNS ? i % kTurn == 0 : i == 0;
-        if (TURNS && first) {
+        const uint32_t turn = i / kTurn, buf = turn % kNbuf, acc = tmem + buf * acc_cols;
+        const bool first = i % kTurn == 0;
+        if (first) {
           const bool r = mbar_wait_warp(smem_addr(&mi->acc_empty[buf]), ((turn / kNbuf) & 1u) ^ 1u, p.wait_limit_ns);
           ok = __shfl_sync(0xffffffffu, r && !mi->abort_flag, 0);
           if (!ok) break;
@@ -220,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
         for (int kk = 0; kk < 4; ++kk)
           umma_f16_elect(acc, smem_desc_add(x, kk * 32), smem_desc_add(d, kk * step), idesc, (first && kk == 0) ? 0u : 1u);
         umma_commit_elect(smem_addr(&mi->empty[stage]));
-        if (c == k_end - 1 || (TURNS && i % kTurn == kTurn - 1)) umma_commit_elect(smem_addr(&mi->acc_full[buf]));
+        if (c == k_end - 1 || i % kTurn == kTurn - 1) umma_commit_elect(smem_addr(&mi->acc_full[buf]));
         if (++stage == static_cast<uint32_t>(p.q)) {
           stage = 0;
           phase ^= 1u;
@@ -275,39 +273,27 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
           }
         }
       };
-      if constexpr (TURNS) {
-        float sum[kMaxRank] = {};
-        const int32_t turns = (k_end - k_begin + kTurn - 1) / kTurn;
-        for (int32_t t = 0; t < turns && ok; ++t) {
-          wait_acc(t);
-          if (!ok) break;
+      float sum[kMaxRank] = {};
+      const int32_t turns = (k_end - k_begin + kTurn - 1) / kTurn;
+      for (int32_t t = 0; t < turns && ok; ++t) {
+        wait_acc(t);
+        if (!ok) break;
 #pragma unroll
-          for (int c0 = 0; c0 < kMaxRank; c0 += 16) {
-            if (c0 < n16) {
-              uint32_t v[16];
-              load16(t % kNbuf, c0, v);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) sum[c0 + i] += __uint_as_float(v[i]);
-            }
-          }
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&mi->acc_empty[t % kNbuf]));
-        }
-#pragma unroll
-        for (int c0 = 0; c0 < kMaxRank; c0 += 16)
-          if (c0 < n16 && ok) put16(c0, sum + c0);
-      } else {
-        wait_acc(0);
-        for (int c0 = 0; c0 < n16 && ok; c0 += 16) {
+        for (int c0 = 0; c0 < kMaxRank; c0 += 16) {
+          if (c0 >= n16) break;
           uint32_t v[16];
-          load16(0, c0, v);
-          float o[16];
+          load16(t % kNbuf, c0, v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(v[i]);
-          put16(c0, o);
+          for (int i = 0; i < 16; ++i) sum[c0 + i] += __uint_as_float(v[i]);
         }
         tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&mi->acc_empty[t % kNbuf]));
+      }
+#pragma unroll
+      for (int c0 = 0; c0 < kMaxRank; c0 += 16) {
+        if (c0 >= n16 || !ok) break;
+        put16(c0, sum + c0);
       }
     }
   }
@@ -364,14 +350,12 @@ cudaError_t launch_adapter_down(AdapterDownParams p, int num_sms, bool bf16, cud
   p.q = (kSmemLimit - kMiscBytes - 1024) / p.stage_bytes;
   if (p.q > kMaxQ) p.q = kMaxQ;
   const int smem = p.q * p.stage_bytes + kMiscBytes + 1024;
-  const bool turns = p.exact != 0;
-  auto kern = bf16 ? (turns ? adapter_down_kernel<true, true> : adapter_down_kernel<true, false>)
-                   : (turns ? adapter_down_kernel<false, true> : adapter_down_kernel<false, false>);
-  const int variant = (bf16 ? 2 : 0) + (turns ? 1 : 0);
-  static std::atomic<uint64_t> smem_set[4];
+  auto kern = bf16 ? adapter_down_kernel<true> : adapter_down_kernel<false>;
+  const int variant = bf16 ? 1 : 0;
+  static std::atomic<uint64_t> smem_set[2];
   cudaError_t e = set_smem_limit_once(kern, kSmemLimit, smem_set[variant]);
   if (e != cudaSuccess) return e;
-  static std::atomic<uint64_t> cluster_set[4];
+  static std::atomic<uint64_t> cluster_set[2];
   e = allow_large_clusters_once(kern, cluster_set[variant]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -21,8 +21,14 @@
 // the bound at the larger ranks (the gradient of 16384 rows, 4 adapters of rank 64,
 // 18944 x 3584: 621 us, with an MMA for each part 729).
 //
+// The tensor cores cut what their fp32 sums shift out instead of rounding it: sums of
+// 131072 positive rows came out 7.8e-4 low, more than rounding to fp16 does.  So the sums
+// leave them every kTurnRows rows and are added in registers (16384 rows, rank 64: 278 us
+// with the down projections; every 512 rows 283, every 2048 275, never 272).
+//
 // With items enough for every SM, CTAs (two per SM) are persistent and take items
-// in turn, two TMEM accumulators alternating, so one item's sums are stored while
+// in turn, two TMEM accumulators alternating (one above 42 ranks, whose three parts fill an
+// SM's half), so one item's sums are stored while
 // the next one's rows arrive.  A CTA per item instead, each with a start and an end
 // of its own, with one part of S: 37 us for 24 with 100 segments of 20 rows (20 adapters of
 // rank 32, 4096 + 4096 features), 52 for 39 with 4096 rows of 4 adapters of rank 64
@@ -61,11 +67,14 @@ __host__ __device__ constexpr int part_pitch(int rank) { return rank16(rank) + 4
 
 constexpr int kNbuf = 2;              // accumulators, where two CTAs have the columns for that
 
+constexpr int kTurnRows = 1024;       // rows between two drains of an accumulator
+constexpr int32_t kTurnSums = 1, kTurnLast = 2;  // it has sums; it is the item's last
+
 struct Misc {
   uint64_t full[kMaxQ], empty[kMaxQ], acc_full[kNbuf], acc_empty[kNbuf], drained;
   int32_t rows[kMaxQ];  // rows of the stage, 0: the item has no more stages
   uint32_t tmem;
-  int32_t any[kNbuf];   // the item had a stage
+  int32_t turn[kNbuf];  // what the accumulator holds: kTurnSums | kTurnLast
   volatile int32_t abort_flag;
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc area");
@@ -105,8 +114,8 @@ __device__ __forceinline__ void store_grad(const AdapterWgradParams &p, const It
   }
 }
 
-// SPLIT: a cluster of p.split CTAs per item; else persistent CTAs.
-template <bool BF16, bool SPLIT>
+// SPLIT: a cluster of p.split CTAs per item; else persistent CTAs.  Ranks up to RANKS.
+template <bool BF16, bool SPLIT, int RANKS>
 __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid_constant__ AdapterWgradParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -235,56 +244,59 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
   } else if (warp == kMmaWarp) {
     const uint32_t idesc = idesc_f16(BF16, /*a_mn_major=*/true, /*b_mn_major=*/true, kFeat, static_cast<uint32_t>(mma_n));
     const uint32_t idesc_rest = idesc_f16(BF16, true, true, kFeat, static_cast<uint32_t>(n16));
+    const int turn_stages = kTurnRows / stage_k;
     uint32_t stage = 0, phase = 0, count = 0;
     bool ok = true;
-    for (int64_t it = first; it < items && ok; it += step, ++count) {
-      const uint32_t buf = count % nbuf;
-      ok = wait_phase(mi->acc_empty[buf], ((count / nbuf) & 1u) ^ 1u);
-      if (!ok) break;
-      tc_fence_after_sync();
-      const uint32_t acc = tmem + buf * acc_cols;
-      bool any = false;
-      while (true) {
-        ok = wait_phase(mi->full[stage], phase);
+    for (int64_t it = first; it < items && ok; it += step) {
+      for (bool last = false; !last && ok; ++count) {  // a turn
+        const uint32_t buf = count % nbuf, acc = tmem + buf * acc_cols;
+        ok = wait_phase(mi->acc_empty[buf], ((count / nbuf) & 1u) ^ 1u);
         if (!ok) break;
-        const int32_t rows = mi->rows[stage];
-        if (rows > 0) {
-          const int steps = (rows + 15) / 16;
-          if (rows % 16 != 0) {
-            // rows [rows, 16 * steps) belong to another segment: a swizzled row is
-            // 128 contiguous bytes of its box, so whole rows can be cleared
-            const int n = (16 * steps - rows) * 8;
-            uint8_t *st = smem + stage * stage_bytes + rows * 128;
-            for (int box = 0; box < kFeat / 64 + boxes; ++box)
-              for (int u = lane; u < n; u += 32) *reinterpret_cast<uint4 *>(st + box * box_bytes + u * 16) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
+        tc_fence_after_sync();
+        int stages = 0;
+        while (stages < turn_stages) {
+          ok = wait_phase(mi->full[stage], phase);
+          if (!ok) break;
+          const int32_t rows = mi->rows[stage];
+          last = rows == 0;
+          if (!last) {
+            const int steps = (rows + 15) / 16;
+            if (rows % 16 != 0) {
+              // rows [rows, 16 * steps) belong to another segment: a swizzled row is
+              // 128 contiguous bytes of its box, so whole rows can be cleared
+              const int n = (16 * steps - rows) * 8;
+              uint8_t *st = smem + stage * stage_bytes + rows * 128;
+              for (int box = 0; box < kFeat / 64 + boxes; ++box)
+                for (int u = lane; u < n; u += 32) *reinterpret_cast<uint4 *>(st + box * box_bytes + u * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            tc_fence_after_sync();
+            const uint32_t st = smem_addr(smem + stage * stage_bytes);
+            const uint64_t v = smem_desc_sw128(st, box_bytes, 1024);
+            const uint64_t s = smem_desc_sw128(st + v_bytes, box_bytes, 1024);
+            for (int kk = 0; kk < steps; ++kk) {
+              umma_f16_elect(acc, smem_desc_add(v, kk * 2048), smem_desc_add(s, kk * 2048), idesc, (stages > 0 || kk > 0) ? 1u : 0u);
+              if (joint < kHParts)
+                umma_f16_elect(acc, smem_desc_add(v, kk * 2048), smem_desc_add(s, jb * box_bytes + kk * 2048), idesc_rest, 1u);
+            }
+            ++stages;
           }
-          tc_fence_after_sync();
-          const uint32_t st = smem_addr(smem + stage * stage_bytes);
-          const uint64_t v = smem_desc_sw128(st, box_bytes, 1024);
-          const uint64_t s = smem_desc_sw128(st + v_bytes, box_bytes, 1024);
-          for (int kk = 0; kk < steps; ++kk) {
-            umma_f16_elect(acc, smem_desc_add(v, kk * 2048), smem_desc_add(s, kk * 2048), idesc, (any || kk > 0) ? 1u : 0u);
-            if (joint < kHParts)
-              umma_f16_elect(acc, smem_desc_add(v, kk * 2048), smem_desc_add(s, jb * box_bytes + kk * 2048), idesc_rest, 1u);
+          umma_commit_elect(smem_addr(&mi->empty[stage]));
+          if (++stage == static_cast<uint32_t>(p.q)) {
+            stage = 0;
+            phase ^= 1u;
           }
-          any = true;
+          if (last) break;
         }
-        umma_commit_elect(smem_addr(&mi->empty[stage]));
-        if (++stage == static_cast<uint32_t>(p.q)) {
-          stage = 0;
-          phase ^= 1u;
+        if (!ok) break;
+        if (lane == 0) {
+          mi->turn[buf] = (stages > 0 ? kTurnSums : 0) | (last ? kTurnLast : 0);
+          mbar_arrive(smem_addr(&mi->acc_full[buf]));
         }
-        if (rows == 0) break;
+        __syncwarp();
+        umma_commit_elect(smem_addr(&mi->acc_full[buf]));
       }
-      if (!ok) break;
-      if (lane == 0) {
-        mi->any[buf] = any;
-        mbar_arrive(smem_addr(&mi->acc_full[buf]));
-      }
-      __syncwarp();
-      umma_commit_elect(smem_addr(&mi->acc_full[buf]));
     }
     if (!ok) {
       give_up();
@@ -296,49 +308,59 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
     const int sp = warp & 3;
     const int r = sp * 32 + lane;  // feature f0 + r
     uint32_t count = 0;
-    for (int64_t it = first; it < items; it += step, ++count) {
-      const uint32_t buf = count % nbuf;
-      if (!wait_phase(mi->acc_full[buf], (count / nbuf) & 1u)) {
-        give_up();
-        break;
-      }
-      tc_fence_after_sync();
+    bool ok = true;
+    for (int64_t it = first; it < items && ok; it += step) {
       const Item item(p, it);
-      const bool any = mi->any[buf];
-      for (int c0 = 0; c0 < n16; c0 += 16) {
-        float v[16] = {};
-        if (any) {
-          uint32_t part_sum[kHParts][16];
-          const uint32_t at = tmem + buf * acc_cols + (static_cast<uint32_t>(sp * 32) << 16) + c0;
-#pragma unroll
-          for (int q = 0; q < kHParts; ++q)
-            if (q < joint) tmem_ld_32x32b_x16(at + q * n16, part_sum[q]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int q = kHParts - 1; q >= 0; --q)  // the smallest first
-            if (q < joint)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(part_sum[q][i]);
+      float sum[RANKS] = {};
+      for (int32_t turn = 0; (turn & kTurnLast) == 0; ++count) {
+        const uint32_t buf = count % nbuf;
+        ok = wait_phase(mi->acc_full[buf], (count / nbuf) & 1u);
+        if (!ok) {
+          give_up();
+          break;
         }
+        tc_fence_after_sync();
+        turn = mi->turn[buf];
+        if (turn & kTurnSums) {
+          const uint32_t at = tmem + buf * acc_cols + (static_cast<uint32_t>(sp * 32) << 16);
+#pragma unroll
+          for (int c0 = 0; c0 < RANKS; c0 += 16) {
+            if (c0 >= n16) break;
+            constexpr int kAtOnce = RANKS > 64 ? 1 : kHParts;  // what the registers hold beside the sums
+            uint32_t v[kAtOnce][16];
+#pragma unroll
+            for (int q = kHParts - 1; q >= 0; --q) {  // the smallest first
+              if (q >= joint) continue;
+              if (kAtOnce == 1 || q == joint - 1) {
+#pragma unroll
+                for (int o = 0; o < kAtOnce; ++o)
+                  if (o < joint) tmem_ld_32x32b_x16(at + (kAtOnce == 1 ? q : o) * n16 + c0, v[o]);
+                tmem_ld_wait();
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum[c0 + i] += __uint_as_float(v[kAtOnce == 1 ? 0 : q][i]);
+            }
+          }
+          tc_fence_before_sync();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&mi->acc_empty[buf]));
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int c0 = 0; c0 < RANKS; c0 += 8) {
+        if (c0 >= p.rank) break;
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = sum[c0 + i];
         if constexpr (SPLIT) {
           float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(smem) + r * part_pitch(p.rank) + c0);  // the stages are done with
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+          dst[1] = make_float4(o[4], o[5], o[6], o[7]);
         } else if (item.f0 + r < item.F) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (c0 + 8 * h >= p.rank) continue;
-            float o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = v[8 * h + i];
-            store_grad<BF16>(p, item, r, c0 + 8 * h, o);
-          }
+          store_grad<BF16>(p, item, r, c0, o);
         }
       }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&mi->acc_empty[buf]));
     }
   }
   if constexpr (SPLIT) {
@@ -389,10 +411,13 @@ cudaError_t launch_adapter_wgrad(AdapterWgradParams p, int num_sms, bool bf16, c
   p.q = (kSmemLimit - kMiscBytes - 1024) / stage;
   if (p.q > kMaxQ) p.q = kMaxQ;
   const int smem = p.q * stage + kMiscBytes + 1024;
-  auto kern = bf16 ? (split ? adapter_wgrad_kernel<true, true> : adapter_wgrad_kernel<true, false>)
-                   : (split ? adapter_wgrad_kernel<false, true> : adapter_wgrad_kernel<false, false>);
-  static std::atomic<uint64_t> smem_set[4];
-  cudaError_t e = set_smem_limit_once(kern, kSmemLimit, smem_set[(bf16 ? 2 : 0) + (split ? 1 : 0)]);
+  const bool wide = p.rank > 64;
+  auto kern = wide ? (bf16 ? (split ? adapter_wgrad_kernel<true, true, 128> : adapter_wgrad_kernel<true, false, 128>)
+                           : (split ? adapter_wgrad_kernel<false, true, 128> : adapter_wgrad_kernel<false, false, 128>))
+                   : (bf16 ? (split ? adapter_wgrad_kernel<true, true, 64> : adapter_wgrad_kernel<true, false, 64>)
+                           : (split ? adapter_wgrad_kernel<false, true, 64> : adapter_wgrad_kernel<false, false, 64>));
+  static std::atomic<uint64_t> smem_set[8];
+  cudaError_t e = set_smem_limit_once(kern, kSmemLimit, smem_set[(wide ? 4 : 0) + (bf16 ? 2 : 0) + (split ? 1 : 0)]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int64_t items = static_cast<int64_t>(p.tiles) * p.n_adapters;

@@ -119,8 +119,8 @@ struct DownJob {
 };
 
 // One or two such products, with the lists of the projection's tiles.
-spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, std::initializer_list<DownJob> jobs, bool exact,
-                         int tile_rows, cudaStream_t s) {
+spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, std::initializer_list<DownJob> jobs, int tile_rows,
+                         cudaStream_t s) {
   const bool bf16 = a->in_t == SPMM_BF16;
   spmm::AdapterDownParams d;
   std::memset(&d, 0, sizeof d);
@@ -135,7 +135,6 @@ spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, std::ini
     o.K = static_cast<int32_t>(j.K);
     o.transposed = j.transposed ? 1 : 0;
   }
-  d.exact = exact ? 1 : 0;
   d.tile_segs = a->d_tile_segs;
   d.tile_count = a->d_tile_count;
   d.scale = p.scale;
@@ -279,7 +278,7 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
   if (sorted || !rows_path(p.N, p.rank, p.n_seg)) {
     const spmm::LinearTile tile = spmm::linear_adapters_tile(h->n_groups, h->n_units, p.N, p.n_seg, h->out_t == SPMM_BF16,
                                                                p.num_sms);
-    spmm_status st = down_project(a, p, {{X, down, a->d_h, p.K, false}}, h->out_t == SPMM_F32, spmm::linear_tile_rows(tile), s);
+    spmm_status st = down_project(a, p, {{X, down, a->d_h, p.K, false}}, spmm::linear_tile_rows(tile), s);
     if (st == SPMM_OK) st = up_project(h, a, p, false, tile, s);
     if (st == SPMM_OK && sorted)
       CUDA_TRY(spmm::launch_adapter_ungroup(a->d_place, p.N, Y, out, static_cast<int64_t>(p.M) * (h->out_t == SPMM_F32 ? 4 : 2), s),
@@ -433,9 +432,8 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
                                                                p.num_sms);
   const DownJob of_x{X, down, a->d_h, k, false},
       of_dy{dY, up, a->d_dh, m, true};
-  const bool exact = h_t->out_t == SPMM_F32;  // with or without dX: the same d_up and d_down
-  st = m > k ? down_project(a, p, {of_dy, of_x}, exact, spmm::linear_tile_rows(tile), s)  // the longer first
-             : down_project(a, p, {of_x, of_dy}, exact, spmm::linear_tile_rows(tile), s);
+  st = m > k ? down_project(a, p, {of_dy, of_x}, spmm::linear_tile_rows(tile), s)  // the longer first
+             : down_project(a, p, {of_x, of_dy}, spmm::linear_tile_rows(tile), s);
   if (st == SPMM_OK && dX) {
     p.X = dY;
     p.Y = dX;
@@ -445,7 +443,7 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
     p.K = m;
     st = up_project(h_t, a, p, true, tile, s);
     if (st == SPMM_OK && sorted)
-      CUDA_TRY(spmm::launch_adapter_ungroup(a->d_place, N, dX, out, static_cast<int64_t>(k) * (exact ? 4 : 2), s),
+      CUDA_TRY(spmm::launch_adapter_ungroup(a->d_place, N, dX, out, static_cast<int64_t>(k) * (h_t->out_t == SPMM_F32 ? 4 : 2), s),
                "return of sorted rows launch");
   }
   spmm::AdapterWgradParams w;

@@ -298,7 +298,6 @@ struct AdapterDownJob {
   int32_t K, transposed;
 };
 struct AdapterDownParams {
-  int32_t exact;                 // sums leave the tensor cores often (fp32 outputs)
   AdapterDownJob job[2];
   TileSegment *tile_segs;
   int32_t *tile_count;

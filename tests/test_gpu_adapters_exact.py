@@ -170,3 +170,37 @@ def torch_zeros(*shape):
 @pytest.mark.parametrize("n,segs,rank,n_adapters", WEIGHTS)
 def test_weight_gradients(S, n, segs, rank, n_adapters):
     weight_gradients(S, n, segs, rank, n_adapters, "bf16")
+
+
+def test_weight_gradients_of_many_rows_are_not_cut(S):
+    """Sums over 131072 rows of positive terms.  Left in one accumulator they would be cut by up to a unit of 2^-23 at
+    each of 8192 steps of 16 rows.  A chain of 512 rows has 32, the chains are added with rounding, and of the result's
+    own rounding to 11 bits (at most 2^-11, without a direction) little is left in the mean."""
+    import torch
+    n, m, k, rank, pool = 131072, 256, 256, 16, 200  # enough adapters for a CTA an item
+    c = Case(m, k, 64, [0, 64], [0], rank, 1, "f16", "bf16")  # the layer
+    layer_t = c.layer(S, transposed=True)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+
+    def draw(*shape, top):
+        return ((torch.rand(shape, generator=gen, device="cuda") + 0.5) * top).half()
+
+    X, dY = draw(n, k, top=1.0), draw(n, m, top=2.0 ** -10)
+    down, up = draw(pool, rank, k, top=1.0 / k), draw(pool, m, rank, top=1.0 / m)
+    scale = torch.ones(pool, device="cuda")
+    ptr = torch.full((pool + 1,), n, dtype=torch.int64, device="cuda")
+    ptr[0] = 0
+    ids = torch.arange(pool, dtype=torch.int32, device="cuda")
+    aset = S.Adapters(m, k, pool, rank, "f16", max_rows=n, max_segments=pool)
+    dD, dU = torch.empty_like(down), torch.empty_like(up)
+    aset.grad(layer_t, X, dY, None, dD, dU, down, up, scale, ptr, ids)
+    x, dy = X.double(), dY.double()
+    want = {"d_up": (dU[0], dy.t() @ (x @ down[0].double().t())), "d_down": (dD[0], (dy @ up[0].double()).t() @ x)}
+    for name, (got, value) in want.items():
+        off = ((got.double() - value) / value)
+        own = 6 * 2.0 ** -11 / off.numel() ** 0.5
+        assert abs(float(off.mean())) <= 2 * 64 * 2.0 ** -23 + own, f"{name}: {float(off.mean()):.3g}"
+        assert float(off.abs().max()) <= 2.0 ** -11 + 4 * 64 * 2.0 ** -23, name
+    assert layer_t.check() == S.SPMM_OK
+    layer_t.close()
+    aset.close()
