@@ -387,9 +387,10 @@ spmm_status spmm_adapters_destroy(spmm_adapters a);
  * The segments are read on the device only, so a batch can be described by
  * arrays that earlier work on the stream writes (spmm_route_sort's offsets).
  * An index outside the pool counts as -1 and is reported by spmm_check(h) as
- * SPMM_ERR_DEVICE_CHECK.  Sums are fp32.  Batches with few rows per adapter keep
- * h in fp32; longer ones take it as a matrix operand, the sum of three values of in_t
- * (24 bits of bf16), so fp16 values of h above 65504 become infinite there.  Asynchronous; results are bitwise reproducible run to run.
+ * SPMM_ERR_DEVICE_CHECK.  Sums are fp32, and so is h: batches with few rows per adapter
+ * multiply it in fp32, longer ones as a matrix operand, the sum of three values of in_t
+ * (for fp16 behind a power of two for each row, so that neither its range nor its smallest
+ * value limits h).  Asynchronous; results are bitwise reproducible run to run.
  * Errors: as spmm_run_linear, plus INVALID_ARG for shapes, types or devices
  * that do not match and batches above the set's limits.
  */
@@ -404,7 +405,9 @@ spmm_status spmm_run_linear_adapters(spmm_handle h, spmm_adapters a, const void 
  *     dX[n] = A^T dY[n] + D_a^T dh[n]
  *     d_up_a = sum_n dY[n] h[n]^T       d_down_a = sum_n dh[n] X[n]^T
  * the sums over the rows of adapter a, in a fixed order.  On the way h and dh are the
- * sums of three values of in_t (24 bits of bf16); fp16 values have no bits below 2^-24.
+ * sums of three values of in_t; for fp16 those of up to 128 rows of a segment share a
+ * power of two in d_up and d_down, where an h below 2^-16 of their largest has fewer
+ * than fp32's 24 bits.
  *   h_t      a BCSR handle of A^T (k x m), of the set's in_t; dX has its out_t.
  *   X, dY    N x k and N x m row-major, in_t, 16-byte aligned.
  *   dX       N x k, or NULL where no gradient of the input is wanted.

@@ -36,7 +36,8 @@
 namespace spmm {
 namespace {
 
-constexpr int kRows = 128;
+constexpr int kRows = kPieceRows;
+static_assert(kRows == 128, "the MMA's M");
 constexpr int kXBytes = kRows * 128;  // 128 rows x 64 columns
 constexpr int kMaxQ = 8;
 constexpr int kMaxSplit = 16;           // CTAs of a cluster (above 8 a kernel has to ask for it)
@@ -58,6 +59,7 @@ __host__ __device__ constexpr int part_pitch(int rank) { return rank16(rank) + 4
 struct Misc {
   uint64_t full[kMaxQ], empty[kMaxQ], acc_full[kNbuf], acc_empty[kNbuf], drained;
   RowPiece piece;
+  uint32_t row_max[kRows], piece_max;  // bits of the largest finite |h| of each row, of the CTA's rows
   uint32_t tmem;
   volatile int32_t abort_flag;
 };
@@ -79,14 +81,31 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
+// Powers of two that the fp16 values of a group are multiplied and divided by, from the
+// bits of its largest finite |h|: a value of 2^e .. 2^(e + 1) comes to 2^14 .. 2^15.
+struct Power {
+  float down, up;
+  __device__ __forceinline__ explicit Power(uint32_t max_bits) {
+    const uint32_t e = max(max_bits >> 23, 40u);  // zeros and values below 2^-87: as 2^-87
+    down = __uint_as_float((268u - e) << 23);
+    up = __uint_as_float((e - 14u) << 23);
+  }
+};
+__device__ __forceinline__ uint32_t finite_bits(float v) {
+  const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+  return b < 0x7f800000u ? b : 0u;
+}
+
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
 // Eight ranks of one row of H, rounded; a further part holds what the roundings
 // before it left (nothing of what is infinite in 16 bits).  Ranks past the last are zeros.
 template <bool BF16>
-__device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int32_t rank, int32_t j, float (&v)[8]) {
+__device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int32_t rank, int32_t j, const float (&h)[8], float by) {
   const int pitch = rank16(rank);
-  if (j >= rank)
+  float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  for (int i = 0; i < 8; ++i) v[i] = j >= rank ? 0.0f : h[i] * by;
 #pragma unroll
   for (int q = 0; q < kHParts; ++q) {
     uint32_t w[4];
@@ -148,6 +167,11 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
                                     min(tile0 + p.tile_rows, static_cast<int64_t>(p.N)), p.tile_segs + tile0,
                                     p.tile_rows, p.status);
     if (lane == 0) p.tile_count[unit] = c;
+    if (p.row_scale) {  // rows outside every segment
+      const int64_t b = p.n_seg > 0 ? p.seg_ptr[0] : p.N, e = p.n_seg > 0 ? p.seg_ptr[p.n_seg] : 0;
+      for (int64_t n = tile0 + lane; n < min(tile0 + p.tile_rows, static_cast<int64_t>(p.N)); n += 32)
+        if (n < b || n >= e) p.row_scale[n] = 0.0f;
+    }
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -159,6 +183,8 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
   const int32_t k_begin = static_cast<int32_t>(static_cast<int64_t>(nk) * part / p.split);
   const int32_t k_end = static_cast<int32_t>(static_cast<int64_t>(nk) * (part + 1) / p.split);
 
+  if (!BF16 && piece.adapter < 0 && part == 0 && job.rows)
+    for (int64_t n = piece.begin + threadIdx.x; n < piece.end; n += kThreads) p.row_scale[n] = 0.0f;
   if (piece.adapter >= 0) {
     if (warp == kTmaWarp) {
       uint32_t stage = 0, phase = 0;
@@ -257,22 +283,6 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
         tmem_ld_32x32b_x16(tmem + buf * acc_cols + (static_cast<uint32_t>(sp * 32) << 16) + c0, v);
         tmem_ld_wait();
       };
-      // ranks c0 .. c0 + 15 of row r
-      auto put16 = [&](int c0, const float *v) {
-        if (p.split > 1) {
-          float4 *dst = reinterpret_cast<float4 *>(sums + r * part_pitch(p.rank) + c0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else if (mine) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = f * v[8 * h + i];
-            store_h<BF16>(job.H, row0 + r, p.rank, c0 + 8 * h, o);
-          }
-        }
-      };
       float sum[kMaxRank] = {};
       const int32_t turns = (k_end - k_begin + kTurn - 1) / kTurn;
       for (int32_t t = 0; t < turns && ok; ++t) {
@@ -290,14 +300,50 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&mi->acc_empty[t % kNbuf]));
       }
+      if (p.split > 1) {
+        if (ok)
 #pragma unroll
-      for (int c0 = 0; c0 < kMaxRank; c0 += 16) {
-        if (c0 >= n16 || !ok) break;
-        put16(c0, sum + c0);
+          for (int c0 = 0; c0 < kMaxRank; c0 += 4) {
+            if (c0 >= n16) break;
+            *reinterpret_cast<float4 *>(sums + r * part_pitch(p.rank) + c0) =
+                make_float4(sum[c0], sum[c0 + 1], sum[c0 + 2], sum[c0 + 3]);
+          }
+      } else {
+        uint32_t top = 0, piece_top = 0;
+        if constexpr (!BF16) {
+#pragma unroll
+          for (int c = 0; c < kMaxRank; c += 8) {
+            if (c >= p.rank || !mine) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max(top, finite_bits(f * sum[c + i]));
+          }
+          if (job.sums) {  // one power of two for the piece
+            const uint32_t warp_top = __reduce_max_sync(0xffffffffu, top);
+            if (lane == 0) mi->row_max[sp] = warp_top;
+            epilogue_sync();
+#pragma unroll
+            for (int w = 0; w < 4; ++w) piece_top = max(piece_top, mi->row_max[w]);
+          }
+        }
+        const Power row(top), all(piece_top);
+        if (mine && ok) {
+          if (!BF16 && job.rows) p.row_scale[row0 + r] = row.up;
+          if (!BF16 && job.sums) job.sum_scale[row0 + r] = all.up;
+#pragma unroll
+          for (int c = 0; c < kMaxRank; c += 8) {
+            if (c >= n16) break;
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = f * sum[c + i];
+            if (BF16 || job.rows) store_h<BF16>(job.rows, row0 + r, p.rank, c, o, BF16 ? 1.0f : row.down);
+            if (!BF16 && job.sums) store_h<BF16>(job.sums, row0 + r, p.rank, c, o, all.down);
+          }
+        }
       }
     }
   }
   if (p.split > 1) {
+    if (!BF16 && threadIdx.x < kRows) mi->row_max[threadIdx.x] = 0;
     // every CTA of the cluster comes here, whatever happened before
     cluster_sync();
     if (piece.adapter >= 0) {
@@ -306,13 +352,63 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
       const int32_t r0 = begin + n * part / p.split, r1 = begin + n * (part + 1) / p.split, units = n16 / 8;
       const uint32_t base = smem_addr(smem);
       const float f = p.scale[piece.adapter];
-      for (int u = threadIdx.x; u < (r1 - r0) * units; u += kThreads) {
-        const int r = r0 + u / units, j = (u % units) * 8;
-        float o[8];
-        cluster_sum8(base + (r * part_pitch(p.rank) + j) * 4, p.split, o);
+      float o[8];
+      auto each = [&](auto &&eight) {  // eight(row, its first rank, where the eight sums lie)
+        for (int u = threadIdx.x; u < (r1 - r0) * units; u += kThreads) {
+          const int r = r0 + u / units, j = (u % units) * 8;
+          eight(r, j, (r * part_pitch(p.rank) + j) * 4);
+        }
+      };
+      if constexpr (BF16) {
+        each([&](int r, int j, int at) {
+          cluster_sum8(base + at, p.split, o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] *= f;
-        store_h<BF16>(job.H, row0 + r, p.rank, j, o);
+          for (int i = 0; i < 8; ++i) o[i] *= f;
+          store_h<BF16>(job.rows, row0 + r, p.rank, j, o, 1.0f);
+        });
+      } else {
+        // the share's sums in the place of this CTA's own, which no other CTA reads
+        each([&](int r, int j, int at) {
+          cluster_sum8(base + at, p.split, o);
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            o[i] *= f;
+            if (j < p.rank) top = max(top, finite_bits(o[i]));
+          }
+          float4 *own = reinterpret_cast<float4 *>(smem + at);
+          own[0] = make_float4(o[0], o[1], o[2], o[3]);
+          own[1] = make_float4(o[4], o[5], o[6], o[7]);
+          atomicMax(&mi->row_max[r], top);
+        });
+        __syncthreads();
+        uint32_t piece_top = 0;
+        if (job.sums) {
+          if (warp == 0) {
+            uint32_t top = 0;
+            for (int r = lane; r < kRows; r += 32) top = max(top, mi->row_max[r]);
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (lane == 0) mi->piece_max = top;
+          }
+          cluster_sync();
+          for (int c = 0; c < p.split; ++c) piece_top = max(piece_top, cluster_load_u32(cluster_map(smem_addr(&mi->piece_max), c)));
+        }
+        const Power all(piece_top);
+        each([&](int r, int j, int at) {
+          const Power row(mi->row_max[r]);
+          const float4 *own = reinterpret_cast<const float4 *>(smem + at);
+          const float4 a = own[0], b = own[1];
+          o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
+          o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+          if (job.rows) {
+            if (j == 0) p.row_scale[row0 + r] = row.up;
+            store_h<BF16>(job.rows, row0 + r, p.rank, j, o, row.down);
+          }
+          if (job.sums) {
+            if (j == 0) job.sum_scale[row0 + r] = all.up;
+            store_h<BF16>(job.sums, row0 + r, p.rank, j, o, all.down);
+          }
+        });
       }
     }
     cluster_sync();  // the others may still read this CTA's sums

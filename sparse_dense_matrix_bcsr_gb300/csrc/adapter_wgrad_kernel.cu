@@ -10,7 +10,9 @@
 // box may start at any row), so K never runs across a segment; the rows after a
 // segment's end that the last box brings are zeroed in shared memory in both
 // operands before the MMA, as neither operand may hold another request's
-// infinities.  Every element of dY and X is read once, so HBM bounds the kernel;
+// infinities.  With fp16 a stage does not run across the pieces either that S is divided by
+// powers of two in (see kHParts), and each piece's sums are taken out and multiplied by
+// its power.  Every element of dY and X is read once, so HBM bounds the kernel;
 // S is read again by every feature tile, from L2.  16384 rows of 4 adapters of rank
 // 64, 18944 + 3584 features: 117 us, 6.3 TB/s of activations.
 //
@@ -69,10 +71,13 @@ constexpr int kNbuf = 2;              // accumulators, where two CTAs have the c
 
 constexpr int kTurnRows = 1024;       // rows between two drains of an accumulator
 constexpr int32_t kTurnSums = 1, kTurnLast = 2;  // it has sums; it is the item's last
+constexpr int32_t kPieceEnd = 1 << 16;
 
 struct Misc {
   uint64_t full[kMaxQ], empty[kMaxQ], acc_full[kNbuf], acc_empty[kNbuf], drained;
-  int32_t rows[kMaxQ];  // rows of the stage, 0: the item has no more stages
+  int32_t rows[kMaxQ];  // rows of the stage, 0: the item has no more stages; fp16: kPieceEnd with a piece's last
+  int32_t row[kMaxQ];   // its first row
+  int32_t turn_row[kNbuf];  // a row of what the accumulator holds
   uint32_t tmem;
   int32_t turn[kNbuf];  // what the accumulator holds: kTurnSums | kTurnLast
   volatile int32_t abort_flag;
@@ -195,14 +200,19 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
           todo &= todo - 1;
           const int32_t sb = __shfl_sync(0xffffffffu, static_cast<int32_t>(begin), i);
           const int32_t se = __shfl_sync(0xffffffffu, static_cast<int32_t>(end), i);
-          for (int32_t n = sb; n < se; n = se - n > stage_k ? n + stage_k : se) {
+          int32_t next = sb;
+          for (int32_t n = sb; n < se; n = next) {
+            next = se - n > stage_k ? n + stage_k : se;
+            const int32_t piece_end = (n / kPieceRows + 1) * kPieceRows;
+            if (!BF16) next = min(next, piece_end);
             const bool take = turn == part;
             if (++turn == split) turn = 0;
             if (!take) continue;
             ok = claim();
             if (!ok) break;
             if (lane == 0) {
-              mi->rows[stage] = min(se - n, stage_k);
+              mi->rows[stage] = (next - n) | (!BF16 && (SPLIT || next == se || next == piece_end) ? kPieceEnd : 0);
+              mi->row[stage] = n;
               const uint32_t fb = smem_addr(&mi->full[stage]);
               const uint32_t st = smem_addr(smem + stage * stage_bytes);
               mbar_arrive_expect_tx(fb, stage_bytes);
@@ -257,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
         while (stages < turn_stages) {
           ok = wait_phase(mi->full[stage], phase);
           if (!ok) break;
-          const int32_t rows = mi->rows[stage];
+          const int32_t rec = mi->rows[stage], rows = rec & (kPieceEnd - 1);
+          if (!BF16 && lane == 0 && rows > 0) mi->turn_row[buf] = mi->row[stage];
           last = rows == 0;
           if (!last) {
             const int steps = (rows + 15) / 16;
@@ -287,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
             stage = 0;
             phase ^= 1u;
           }
-          if (last) break;
+          if (last || (!BF16 && rec & kPieceEnd)) break;
         }
         if (!ok) break;
         if (lane == 0) {
@@ -323,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
         turn = mi->turn[buf];
         if (turn & kTurnSums) {
           const uint32_t at = tmem + buf * acc_cols + (static_cast<uint32_t>(sp * 32) << 16);
+          const float by = BF16 ? 1.0f : (item.up ? p.h_scale : p.dh_scale)[mi->turn_row[buf]];
 #pragma unroll
           for (int c0 = 0; c0 < RANKS; c0 += 16) {
             if (c0 >= n16) break;
@@ -338,7 +350,10 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
                 tmem_ld_wait();
               }
 #pragma unroll
-              for (int i = 0; i < 16; ++i) sum[c0 + i] += __uint_as_float(v[kAtOnce == 1 ? 0 : q][i]);
+              for (int i = 0; i < 16; ++i) {
+                const float s = __uint_as_float(v[kAtOnce == 1 ? 0 : q][i]);
+                sum[c0 + i] = BF16 ? sum[c0 + i] + s : fmaf(by, s, sum[c0 + i]);
+              }
             }
           }
           tc_fence_before_sync();

@@ -25,6 +25,8 @@ struct spmm_adapters_s {
 
   float *d_h = nullptr;        // max_rows x rank: scale * D x, in fp32 or in 16-bit parts
   float *d_dh = nullptr;       // gradient: max_rows x rank: scale * U^T dy
+  // fp16: dh divided by rows (d_dh by pieces), and what rows of H and dH were divided by
+  float *d_dh_rows = nullptr, *d_row_scale = nullptr, *d_h_scale = nullptr, *d_dh_scale = nullptr;
   // a short batch's rows sorted by adapter: X, dY or Y, dX
   void *d_xs = nullptr, *d_ys = nullptr, *d_dxs = nullptr;
   int64_t *d_group_ptr = nullptr;
@@ -40,6 +42,10 @@ void free_adapters(spmm_adapters a) {
   if (!a) return;
   cudaFree(a->d_h);
   cudaFree(a->d_dh);
+  cudaFree(a->d_dh_rows);
+  cudaFree(a->d_row_scale);
+  cudaFree(a->d_h_scale);
+  cudaFree(a->d_dh_scale);
   cudaFree(a->d_xs);
   cudaFree(a->d_ys);
   cudaFree(a->d_dxs);
@@ -113,7 +119,7 @@ spmm::AdapterParams make_params(spmm_handle h, spmm_adapters a, int64_t N, const
 // n_adapters x rank x K, or transposed n_adapters x K x rank.
 struct DownJob {
   const void *X, *D;
-  float *H;
+  float *rows, *sums, *sum_scale;  // H for products of its rows, and for those that sum over them (fp16)
   int64_t K;
   bool transposed;
 };
@@ -131,7 +137,10 @@ spmm_status down_project(spmm_adapters a, const spmm::AdapterParams &p, std::ini
     st = j.transposed ? spmm::encode_3d(&o.tmD, j.D, bf16, p.n_adapters, j.K, p.rank, 1, 64)
                       : spmm::encode_2d(&o.tmD, j.D, bf16, static_cast<uint64_t>(p.n_adapters) * p.rank, j.K, j.K, p.rank, 64);
     if (st != SPMM_OK) return st;
-    o.H = reinterpret_cast<uint16_t *>(j.H);
+    o.rows = reinterpret_cast<uint16_t *>(j.rows);
+    o.sums = reinterpret_cast<uint16_t *>(j.sums);
+    o.sum_scale = j.sum_scale;
+    if (!bf16 && j.rows) d.row_scale = a->d_row_scale;
     o.K = static_cast<int32_t>(j.K);
     o.transposed = j.transposed ? 1 : 0;
   }
@@ -178,6 +187,7 @@ spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams
   ad.tile_segs = a->d_tile_segs;
   ad.tile_count = a->d_tile_count;
   ad.u_transposed = transposed ? 1 : 0;
+  ad.row_scale = a->d_row_scale;
   ad.tile = tile;
   spmm::BcsrParams b;
   std::memset(&b, 0, sizeof b);
@@ -276,9 +286,9 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
   p.M = static_cast<int32_t>(h->m);
   p.K = static_cast<int32_t>(h->k);
   if (sorted || !rows_path(p.N, p.rank, p.n_seg)) {
-    const spmm::LinearTile tile = spmm::linear_adapters_tile(h->n_groups, h->n_units, p.N, p.n_seg, h->out_t == SPMM_BF16,
-                                                               p.num_sms);
-    spmm_status st = down_project(a, p, {{X, down, a->d_h, p.K, false}}, spmm::linear_tile_rows(tile), s);
+    const spmm::LinearTile tile = spmm::linear_adapters_tile(h->n_groups, h->n_units, p.N, p.n_seg, bf16,
+                                                             h->out_t == SPMM_BF16, p.num_sms);
+    spmm_status st = down_project(a, p, {{X, down, a->d_h, nullptr, nullptr, p.K, false}}, spmm::linear_tile_rows(tile), s);
     if (st == SPMM_OK) st = up_project(h, a, p, false, tile, s);
     if (st == SPMM_OK && sorted)
       CUDA_TRY(spmm::launch_adapter_ungroup(a->d_place, p.N, Y, out, static_cast<int64_t>(p.M) * (h->out_t == SPMM_F32 ? 4 : 2), s),
@@ -361,6 +371,13 @@ spmm_status spmm_adapters_create(spmm_adapters *out, int64_t m, int64_t k, int32
     CUDA_TRY(cudaMalloc(&a->d_group_ptr, (g + 1) * sizeof(int64_t)), "cudaMalloc(sorted segments)");
     CUDA_TRY(cudaMalloc(&a->d_group_adapter, g * sizeof(int32_t)), "cudaMalloc(sorted segments)");
     CUDA_TRY(cudaMalloc(&a->d_place, g * sizeof(int32_t)), "cudaMalloc(sorted segments)");
+    const size_t scales = static_cast<size_t>(std::max<int64_t>(max_rows, 1)) * sizeof(float);
+    if (in_t == SPMM_F16) CUDA_TRY(cudaMalloc(&a->d_row_scale, scales), "cudaMalloc(row scales)");
+    if (a->grad && in_t == SPMM_F16) {
+      CUDA_TRY(cudaMalloc(&a->d_dh_rows, h), "cudaMalloc(adapter gradients)");
+      CUDA_TRY(cudaMalloc(&a->d_h_scale, scales), "cudaMalloc(row scales)");
+      CUDA_TRY(cudaMalloc(&a->d_dh_scale, scales), "cudaMalloc(row scales)");
+    }
     if (a->grad) {
       CUDA_TRY(cudaMalloc(&a->d_dh, h), "cudaMalloc(adapter gradients)");
       CUDA_TRY(cudaMalloc(&a->d_dxs, g * k * 4), "cudaMalloc(sorted rows)");
@@ -428,16 +445,19 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
     if (dX) dX = a->d_dxs;
   }
   // H and dH, then dX with the roles of the adapters' two matrices exchanged
-  const spmm::LinearTile tile = spmm::linear_adapters_tile(h_t->n_groups, h_t->n_units, p.N, p.n_seg, h_t->out_t == SPMM_BF16,
-                                                               p.num_sms);
-  const DownJob of_x{X, down, a->d_h, k, false},
-      of_dy{dY, up, a->d_dh, m, true};
+  const spmm::LinearTile tile = spmm::linear_adapters_tile(h_t->n_groups, h_t->n_units, p.N, p.n_seg, bf16,
+                                                           h_t->out_t == SPMM_BF16, p.num_sms);
+  float *const dh_rows = bf16 ? a->d_dh : a->d_dh_rows;
+  const DownJob of_x = bf16 ? DownJob{X, down, a->d_h, nullptr, nullptr, k, false}
+                            : DownJob{X, down, nullptr, a->d_h, a->d_h_scale, k, false};
+  const DownJob of_dy = bf16 ? DownJob{dY, up, dh_rows, nullptr, nullptr, m, true}
+                             : DownJob{dY, up, dX ? dh_rows : nullptr, a->d_dh, a->d_dh_scale, m, true};
   st = m > k ? down_project(a, p, {of_dy, of_x}, spmm::linear_tile_rows(tile), s)  // the longer first
              : down_project(a, p, {of_x, of_dy}, spmm::linear_tile_rows(tile), s);
   if (st == SPMM_OK && dX) {
     p.X = dY;
     p.Y = dX;
-    p.H = a->d_dh;
+    p.H = dh_rows;
     p.up = down;
     p.M = k;
     p.K = m;
@@ -454,6 +474,8 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
   if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_h, a->d_h, bf16, N, cols, cols, rows, 64);
   if (st == SPMM_OK) st = spmm::encode_2d(&w.tm_dh, a->d_dh, bf16, N, cols, cols, rows, 64);
   if (st != SPMM_OK) return st;
+  w.h_scale = a->d_h_scale;
+  w.dh_scale = a->d_dh_scale;
   w.d_up = static_cast<uint16_t *>(d_up);
   w.d_down = static_cast<uint16_t *>(d_down);
   w.seg_ptr = p.seg_ptr;

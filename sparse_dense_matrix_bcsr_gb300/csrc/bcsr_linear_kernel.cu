@@ -69,6 +69,11 @@
 // rows, 409 for 398 us.  Every 4 blocks: 3.8e-7, and up to 4 % slower; every 16:
 // 1.2e-6 and as fast as 8.  Tiles of 512 rows, whose sums the registers cannot hold,
 // are for fp32 only where block rows average less than a turn.
+//
+// With fp16 inputs the rows of H are divided by powers of two (see kHParts).  There the
+// adapters' sums of a tile are a turn of their own, and the epilogue multiplies them by
+// their rows' powers as it adds; a segment's first MMA overwrites what its lanes held, and
+// the lanes of rows without an adapter are not read.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -110,7 +115,7 @@ struct Tile {
   static_assert(CTAS * kTmemCols <= 512, "TMEM");
 };
 
-constexpr int32_t kRecEmpty = 1, kRecEnd = 2, kRecAdapters = 4, kRecLast = 8, kRecMore = 16;
+constexpr int32_t kRecEmpty = 1, kRecEnd = 2, kRecAdapters = 4, kRecLast = 8, kRecMore = 16, kRecScaled = 32;
 // What the producer tells the MMA warp with a tile's first stage: the tile, how
 // many stages of blocks it has and whether adapters follow.  With a stage of an
 // adapter: its boxes of H (the first | their number << 8 | U's group << 16), its rows of
@@ -143,7 +148,9 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
   constexpr bool kAdapt = std::is_same_v<Adapters, LinearAdapters>;
   constexpr int kQ = T::kQ, kStageBytes = T::kStageBytes, kStagingBytes = T::kStagingBytes;
   constexpr int kAccCols = T::kAccCols, kTmemCols = T::kTmemCols, kTileN = T::kRows;
-  constexpr bool kTurns = kAdapt && !OUT_BF16 && T::kRows == 256;
+  constexpr bool kScaled = kAdapt && !IN_BF16;  // the adapters' sums are kept apart and multiplied by their rows' powers of two
+  constexpr bool kTurns = kAdapt && T::kRows == 256 && (!OUT_BF16 || kScaled);
+  static_assert(kTurns || !kScaled, "registers for the sums");
   constexpr int kOutBytes = OUT_BF16 ? 2 : 4;
   constexpr int kBoxCols = T::kBoxBytes / kOutBytes;  // features per box row
   constexpr int kBoxes = kBlk / kBoxCols;             // store boxes per warp and part
@@ -477,6 +484,12 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
         }
         if constexpr (kAdapt) {
           bool more = (rec.flags & kRecAdapters) != 0 && ok;
+          if (kScaled && more) {
+            hand_over(kRecMore);
+            buf = tcount % kNbuf;
+            ok = more = wait_phase(acce0 + 8 * buf, ((tcount / kNbuf) & 1u) ^ 1u);
+            acc = tmem + buf * kAccCols;
+          }
           while (more) {
             ok = wait_full();
             if (!ok) break;
@@ -491,13 +504,15 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
             // ranks of U; box b starts b * nh * kHBytes after H's first
             const int nh = h1 - h0;
             auto steps = [&](auto &&mma) {
+              uint32_t accumulate = kScaled && seg.stages >> 16 == 0 && b0 == 0 ? 0 : 1;  // the segment's first step
               for (int b = 0; b < nb; ++b) {
                 const int x = ad.groups > 1 ? (seg.stages >> 16) * 64 : (b0 + b) * 64;
                 const int n = min(ad.cols - x, 64) / 16;
                 int u = ad.groups > 1 ? 0 : static_cast<int>(static_cast<uint32_t>(x / 16) % static_cast<uint32_t>(ad.u_steps));
                 uint64_t adesc = smem_desc_add(adesc0, b * nh * kHBytes);
                 for (int k = 0; k < n; ++k) {
-                  mma(adesc, smem_desc_add(bdesc0, u * u_step));
+                  mma(adesc, smem_desc_add(bdesc0, u * u_step), accumulate);
+                  accumulate = 1;
                   adesc = smem_desc_add(adesc, 32);
                   if (++u == ad.u_steps) u = 0;
                 }
@@ -506,17 +521,17 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
             if (begin == 0 && end == kTileN) {
               // the segment holds all rows of the tile: no lanes to mask; as for the
               // blocks, MMAs in a row go to different accumulators
-              steps([&](uint64_t adesc, uint64_t bdesc) {
+              steps([&](uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
 #pragma unroll
                 for (int h = 0; h < T::kParts; ++h)
-                  umma_f16_elect(acc + h * kBlk, smem_desc_add(adesc, h * kHBytes), bdesc, u_idesc, 1u);
+                  umma_f16_elect(acc + h * kBlk, smem_desc_add(adesc, h * kHBytes), bdesc, u_idesc, accumulate);
               });
             } else {
               for (int h = h0; h < h1; ++h) {
                 uint32_t off[4];
                 lanes_off(begin - 128 * h, end - 128 * h, off);
-                steps([&](uint64_t adesc, uint64_t bdesc) {
-                  umma_f16_lanes_elect(acc + h * kBlk, smem_desc_add(adesc, (h - h0) * kHBytes), bdesc, u_idesc, 1u, off);
+                steps([&](uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
+                  umma_f16_lanes_elect(acc + h * kBlk, smem_desc_add(adesc, (h - h0) * kHBytes), bdesc, u_idesc, accumulate, off);
                 });
               }
             }
@@ -525,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
         }
         if (!ok) break;
       }
-      hand_over(rec.flags & kRecEmpty);
+      hand_over((rec.flags & kRecEmpty) | (kScaled && rec.flags & kRecAdapters ? kRecScaled : 0));
     }
     if (!ok) {
       if (leader) {
@@ -551,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
     uint8_t *stg = staging + (warp - kEpiWarp0) * (32 * T::kBoxBytes);
     const uint32_t row_sw = static_cast<uint32_t>(T::kBoxBytes == 128 ? lane & 7 : (lane >> 1) & 3);
     uint32_t tcount = 0;
-    float sum[kTurns ? kAccCols : 1] = {};  // fp32 with adapters: the tile's sums so far
+    float sum[kTurns ? kAccCols : 1] = {};  // the tile's sums so far
     while (true) {
       const uint32_t buf = tcount % kNbuf;
       const bool r = mbar_wait_warp(accf0 + 8 * buf, (tcount / kNbuf) & 1u, p.wait_limit_ns);
@@ -571,13 +586,30 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
       const uint32_t tbase = tmem + (static_cast<uint32_t>(sp * 32) << 16) + buf * kAccCols;
       if constexpr (kTurns) {
         if (!zero) {
+          float by[T::kParts];  // 0: the row has no adapter, its lanes hold nothing
+#pragma unroll
+          for (int h = 0; h < T::kParts; ++h) by[h] = 1.0f;
+          if constexpr (kScaled) {
+            if (flags & kRecScaled) {
+              grid_dependency_wait();  // the powers come from the kernel that made H
+#pragma unroll
+              for (int h = 0; h < T::kParts; ++h) by[h] = n0 + lane + h * 128 < p.N ? __ldcg(ad.row_scale + n0 + lane + h * 128) : 0.0f;
+            }
+          }
 #pragma unroll
           for (int c = 0; c < kAccCols; c += 16) {
             uint32_t v[16];
             tmem_ld_32x32b_x16(tbase + c, v);
             tmem_ld_wait();
+            if (kScaled) {
+              const float f = by[c / kBlk];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
+              for (int i = 0; i < 16; ++i)
+                if (f != 0.0f) sum[c + i] = fmaf(f, __uint_as_float(v[i]), sum[c + i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
+            }
           }
           tc_fence_before_sync();
         }
@@ -590,10 +622,22 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
           if (lane == 0) bulk_wait_group_read<0>();
           __syncwarp();
           uint8_t *row = stg + lane * T::kBoxBytes;
+          constexpr int kPer = 16 / kOutBytes;  // features of a 16-byte word
 #pragma unroll
-          for (int q = 0; q < kBoxCols / 4; ++q)
-            *reinterpret_cast<float4 *>(row + ((static_cast<uint32_t>(q) ^ row_sw) << 4)) =
-                make_float4(sum[c + 4 * q], sum[c + 4 * q + 1], sum[c + 4 * q + 2], sum[c + 4 * q + 3]);
+          for (int q = 0; q < kBoxCols / kPer; ++q) {
+            uint4 w;
+            if constexpr (OUT_BF16) {
+              const __nv_bfloat162 b[4] = {__floats2bfloat162_rn(sum[c + 8 * q], sum[c + 8 * q + 1]),
+                                           __floats2bfloat162_rn(sum[c + 8 * q + 2], sum[c + 8 * q + 3]),
+                                           __floats2bfloat162_rn(sum[c + 8 * q + 4], sum[c + 8 * q + 5]),
+                                           __floats2bfloat162_rn(sum[c + 8 * q + 6], sum[c + 8 * q + 7])};
+              w = *reinterpret_cast<const uint4 *>(b);
+            } else {
+              w = make_uint4(__float_as_uint(sum[c + 4 * q]), __float_as_uint(sum[c + 4 * q + 1]),
+                             __float_as_uint(sum[c + 4 * q + 2]), __float_as_uint(sum[c + 4 * q + 3]));
+            }
+            *reinterpret_cast<uint4 *>(row + ((static_cast<uint32_t>(q) ^ row_sw) << 4)) = w;
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -704,11 +748,13 @@ template <class T, class Adapters>
 cudaError_t launch_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY, const BcsrParams &p,
                                const Adapters &ad, bool in_bf16, bool out_bf16, cudaStream_t stream) {
   if (p.n_block_rows == 0 || p.N == 0) return cudaSuccess;
-  if (out_bf16)
-    return in_bf16 ? launch_linear_variant<true, true, T>(tmA, tmX, tmY, p, ad, stream)
-                   : launch_linear_variant<false, true, T>(tmA, tmX, tmY, p, ad, stream);
-  return in_bf16 ? launch_linear_variant<true, false, T>(tmA, tmX, tmY, p, ad, stream)
-                 : launch_linear_variant<false, false, T>(tmA, tmX, tmY, p, ad, stream);
+  if (in_bf16)
+    return out_bf16 ? launch_linear_variant<true, true, T>(tmA, tmX, tmY, p, ad, stream)
+                    : launch_linear_variant<true, false, T>(tmA, tmX, tmY, p, ad, stream);
+  if constexpr (T::kRows == 256)
+    return out_bf16 ? launch_linear_variant<false, true, T>(tmA, tmX, tmY, p, ad, stream)
+                    : launch_linear_variant<false, false, T>(tmA, tmX, tmY, p, ad, stream);
+  return cudaErrorInvalidValue;  // not chosen by linear_adapters_tile
 }
 
 }  // namespace
@@ -722,15 +768,16 @@ cudaError_t launch_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const 
 //   fewer, short block rows, many tiles (65536 rows, 18944 x 3584, 9): 1477 / 1386 / 1218
 //   few tiles (2048 rows in 4):                                         83 /   70 /   71
 //   fewer, block rows of 16 blocks or more (16384 rows, 3584 x 18944):  380 /  411 /  390
-// (bf16 outputs; an fp32 Y of 512-row tiles needs short block rows, see the top.)
-LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t N, int64_t n_seg, bool out_bf16,
-                                int num_sms) {
+// (bf16 outputs; an fp32 Y of 512-row tiles needs short block rows, and fp16 inputs have
+// none, see the top.)
+LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t N, int64_t n_seg, bool in_bf16,
+                                bool out_bf16, int num_sms) {
   const int64_t row_tiles = (N + 255) / 256;
   if (n_block_rows * row_tiles <= num_sms) return LinearTile::k256;
   if (n_seg >= row_tiles) return LinearTile::k256x2;
   if (n_blocks >= 16 * n_block_rows) return LinearTile::k256;
   if (n_block_rows * ((N + 511) / 512) < 8ll * num_sms) return LinearTile::k256x2;
-  return out_bf16 || n_blocks < kTurn * n_block_rows ? LinearTile::k512 : LinearTile::k256x2;
+  return in_bf16 && (out_bf16 || n_blocks < kTurn * n_block_rows) ? LinearTile::k512 : LinearTile::k256x2;
 }
 
 cudaError_t launch_bcsr_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,

@@ -117,8 +117,8 @@ cudaError_t launch_bcsr_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, c
 // by one CTA per SM (as without adapters) or by two, or 512 rows by one.
 constexpr int kMaxTileRows = 512;
 enum class LinearTile : int32_t { k256, k256x2, k512 };
-LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t N, int64_t n_seg, bool out_bf16,
-                                int num_sms);
+LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t N, int64_t n_seg, bool in_bf16,
+                                bool out_bf16, int num_sms);
 inline int linear_tile_rows(LinearTile t) { return t == LinearTile::k512 ? 512 : 256; }
 // A segment with an adapter among a tile's rows: rows [begin, end) of the tile.
 struct TileSegment {
@@ -134,7 +134,14 @@ struct TileSegment {
 // A 32-bit h as a matrix operand: its value in 16 bits, what that rounding left, and what
 // that one did, 24 bits of bf16 (one part alone moved a bf16 Y by 1.2e-3 of it where the
 // adapters are most of it, two hold 16 bits).
+// fp16 has neither fp32's range nor bits below 2^-24, so there h is first divided by a
+// power of two that brings the largest finite value of its group to 2^14 .. 2^15, and the
+// product's sums are multiplied by it: three parts then hold 24 bits of everything down to
+// 2^-16 of that value.  The group is a row where the product's rows are H's (Y, dX), so
+// that rows stay independent, and a piece of kPieceRows or less of a segment's rows where
+// it sums over them (the weights' gradients).
 constexpr int kHParts = 3;
+constexpr int kPieceRows = 128;  // pieces end at multiples of it
 // Ranks in H's rows, a whole number of MMA steps; those past the rank hold zeros.
 __host__ __device__ constexpr int rank16(int rank) { return (rank + 15) / 16 * 16; }
 constexpr int kAdapterFewRows = 16;
@@ -145,6 +152,7 @@ struct LinearAdapters {
   int32_t cols, boxes, groups;   // of H: columns, boxes for each group of ranks
   int32_t u_cols, u_steps;       // of U: ranks of a box, steps of 16 ranks before they repeat
   int32_t u_transposed;          // the gradient's: the adapters' down matrices
+  const float *row_scale;        // fp16: what the rows of H were divided by, 0: no adapter
   LinearTile tile;
 };
 // Launched as a programmatic dependent of the kernel that writes H and the
@@ -294,11 +302,16 @@ struct AdapterDownJob {
   CUtensorMap tmX;               // X as [N rows, K cols], 128 x 64 boxes, 128-byte swizzle
   CUtensorMap tmD;               // the down matrices as [n_adapters * rank rows, K cols], rank x 64 boxes, 128-byte
                                  // swizzle; transposed: as [n_adapters, K rows, rank cols], 64 x 64 boxes
-  uint16_t *H;                   // device, N x kHParts x rank16(rank): the rows of segments with an adapter
+  // device, N x kHParts x rank16(rank), the rows of segments with an adapter: for products
+  // whose rows are H's, and (fp16 only) for those that sum over them, with what the latter's
+  // pieces were divided by for each row; each can be NULL
+  uint16_t *rows, *sums;
+  float *sum_scale;
   int32_t K, transposed;
 };
 struct AdapterDownParams {
   AdapterDownJob job[2];
+  float *row_scale;              // device, N: what the rows of job[..].rows were divided by, 0: no adapter (NULL: not wanted)
   TileSegment *tile_segs;
   int32_t *tile_count;
   const float *scale;
@@ -365,6 +378,7 @@ cudaError_t launch_adapter_ungroup(const int32_t *place, int64_t N, const void *
 int wgrad_stage_rows(int rank);
 struct AdapterWgradParams {
   CUtensorMap tm_dy, tm_x, tm_h, tm_dh;
+  const float *h_scale, *dh_scale;  // fp16: what the rows' pieces of H and dH were divided by
   uint16_t *d_up, *d_down;
   const int64_t *seg_ptr;
   const int32_t *seg_adapter;

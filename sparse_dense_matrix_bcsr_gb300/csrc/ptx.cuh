@@ -272,6 +272,12 @@ __device__ __forceinline__ float4 cluster_load_f4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t cluster_load_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // o[0..7] = the sum over the cluster's first `ctas` CTAs (1, 2, 4, 8 or 16), in
 // their order, of the eight floats at shared-memory address `saddr` of each; the
 // loads of up to eight CTAs are in flight together.

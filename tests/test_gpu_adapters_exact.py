@@ -204,3 +204,50 @@ def test_weight_gradients_of_many_rows_are_not_cut(S):
     assert layer_t.check() == S.SPMM_OK
     layer_t.close()
     aset.close()
+
+
+# fp16 has no numbers above 65504 and no bits below 2^-24: h of 2^20, 2^-10 and 2^40
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -30, 2.0 ** 20])
+@pytest.mark.parametrize("out_t", ["bf16", "f32"])
+@pytest.mark.parametrize("m,k,n,segs,rank,n_adapters", FORWARD)
+def test_projection_f16(S, m, k, n, segs, rank, n_adapters, out_t, scale):
+    projection(S, m, k, n, segs, rank, n_adapters, "f16", out_t, scale)
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -30, 2.0 ** 20])
+@pytest.mark.parametrize("out_t", ["bf16", "f32"])
+@pytest.mark.parametrize("m,k,n,segs,rank,n_adapters", BACKWARD)
+def test_input_gradient_f16(S, m, k, n, segs, rank, n_adapters, out_t, scale):
+    input_gradient(S, m, k, n, segs, rank, n_adapters, "f16", out_t, scale)
+
+
+@pytest.mark.parametrize("scale,size", [(1.0, 1.0), (2.0 ** -30, 2.0 ** 10), (2.0 ** 20, 2.0 ** -18)])
+@pytest.mark.parametrize("n,segs,rank,n_adapters", WEIGHTS)
+def test_weight_gradients_f16(S, n, segs, rank, n_adapters, scale, size):
+    weight_gradients(S, n, segs, rank, n_adapters, "f16", "bf16", scale, size, with_dx=rank == 16)
+
+
+def test_small_gradients_f16(S):
+    """The first tuning steps, with up close to zero: dh of 1e-6, whose 16-bit values have a few bits.  The bound is the
+    result's own rounding (2^-11, and 2^-25 below fp16's normal numbers) and that of fp32 sums."""
+    c = Case(1000, 520, 1000, *ragged(1000, 7, 3, none=0.0), 16, 3, "f16", "f32")
+    c.up, c.dY = (c.up.double() * 2.0 ** -14).to(c.X.dtype), (c.dY.double() * 2.0 ** -10).to(c.X.dtype)
+    got, ref = run_grad(S, c)["d_down"].double(), c.reference_grad()["d_down"][0]
+    bound = ref.abs() * 2.0 ** -11 + 2.0 ** -25
+    for b, e, a in c.spans():
+        s, x, dy, U, D = float(c.scale[a]), c.X[b:e].double(), c.dY[b:e].double(), c.up[a].double(), c.down[a].double()
+        bound[a] += s * 2.0 ** -16 * ((dy.abs() @ U.abs()).t() @ x.abs())
+    assert float(((got - ref).abs() / bound).max()) <= 1.0
+
+
+def test_rows_of_very_different_sizes_f16(S):
+    """Rows are independent: one of 2^30 times the others in its segment takes no bits from theirs."""
+    import torch
+    n = 300
+    c, rng = zero_weight(320, 200, n, ([0, 100, n], [1, 0]), 16, 2, "f16", "f32", 1.0)
+    D, _ = paired_ranks(rng, 2, 16, 200)
+    X = whole(rng, (n, 200))
+    X[::2] *= 2.0 ** -24
+    c.X, c.down, c.up = X.to(c.X.dtype), D.to(c.X.dtype), signs(2, 16, 320).transpose(1, 2).contiguous().to(c.X.dtype)
+    got, want = run(S, c)[0].double(), c.reference()[0]
+    assert torch.equal(got, want) and want[::2].abs().max() < 2.0 ** -15 < want[1::2].abs().max()
