@@ -31,9 +31,8 @@
 // CTA order.
 //
 // The tensor cores cut what their fp32 sums shift out instead of rounding it, ~1e-9
-// of the result for every term of a chain.  Where y is bf16 its rounding hides that;
-// where it is fp32, blocks go to 8 accumulators in turn (4 with 64 rows), which are
-// added with rounding.
+// of the result for every term of a chain.  So blocks go to 8 accumulators in turn (4
+// with 64 rows), which are added with rounding; one alone is no faster.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -52,7 +51,7 @@ constexpr int kTmaWarp = 0, kMmaWarp = 1, kSumWarp0 = 2, kSumWarps = 8;
 constexpr int kThreads = (kSumWarp0 + kSumWarps) * 32;
 constexpr int kUnitDepth = 2;           // units of U (2 KB) in flight per summing warp
 constexpr int kPitch = kBlk + 4;        // floats per row of y in shared memory
-constexpr int kAccCols = 256;           // TMEM columns of the accumulators where the output is fp32, half an SM's
+constexpr int kAccCols = 256;           // TMEM columns of the accumulators, half an SM's
 constexpr int kMiscBytes = 2560;
 constexpr int kSmemLimit = 112 * 1024;  // two CTAs per SM
 
@@ -216,8 +215,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int32_t rows = min(p.N - row0, p.tile);
   const int32_t feats = min(p.M - br * kBlk, kBlk);
   const uint32_t acc_cols = p.tile < 32 ? 32 : p.tile;
-  const uint32_t n_acc = OUT_BF16 ? 1 : kAccCols / acc_cols;
-  const uint32_t tmem_cols = OUT_BF16 ? acc_cols : kAccCols;
+  const uint32_t n_acc = kAccCols / acc_cols;
   const int64_t row_begin = p.block_row_ptr[br];
   const int64_t blocks = p.block_row_ptr[br + 1] - row_begin;
 
@@ -233,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     fence_barrier_init();
     __syncwarp();
-    tmem_alloc(smem_addr(&mi->tmem), tmem_cols);
+    tmem_alloc(smem_addr(&mi->tmem), kAccCols);
     tmem_relinquish();
   }
   tc_fence_before_sync();
@@ -443,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (p.split > 1) cluster_sync();  // the others may still read this CTA's sums
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, tmem_cols);
+    tmem_dealloc(tmem, kAccCols);
   }
 }
 

@@ -61,14 +61,16 @@
 // for 536; 2048 in 128: 159 for 169).
 //
 // The tensor cores cut what their fp32 sums shift out instead of rounding it, ~1e-9
-// of the result for every term.  Where Y is bf16 its rounding hides that.  An fp32 Y
-// with adapters has its accumulator handed to the epilogue every kTurn blocks (512
-// terms), whose warps keep a 256-row tile's sums in registers and add with rounding:
+// of the result for every term.  With adapters the accumulator is therefore handed to the
+// epilogue every 8 blocks (512 terms) where Y is fp32 and every 64 where it is bf16, whose
+// warps keep a 256-row tile's sums in registers and add with rounding.  fp32:
 // 6.6e-7 off in place of 2.7e-6 with 777 rows of 8192 x 8192, 75 % zero blocks (90 us
 // either way), and in place of 2.2e-5 with 18944 dense columns; 3584 x 18944, 16384
 // rows, 409 for 398 us.  Every 4 blocks: 3.8e-7, and up to 4 % slower; every 16:
-// 1.2e-6 and as fast as 8.  Tiles of 512 rows, whose sums the registers cannot hold,
-// are for fp32 only where block rows average less than a turn.
+// 1.2e-6 and as fast as 8.  bf16, every 64: block rows of 148 blocks take 326 for 307 us
+// (4096 rows), of 30 424 for 430.  Tiles of 512 rows, whose sums the registers cannot hold,
+// are only for layers whose longest block row is one turn (an fp32 Y of 65536 rows, 18944 x
+// 3584, block rows of up to 14: 1876 for 1746).
 //
 // With fp16 inputs the rows of H are divided by powers of two (see kHParts).  There the
 // adapters' sums of a tile are a turn of their own, and the epilogue multiplies them by
@@ -95,7 +97,8 @@ constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2, kEpiWarps = 4;
 constexpr int kMiscBytes = 1024;
 constexpr int kHBytes = 128 * 128;               // a box of H: 128 rows x 64 columns
 constexpr int kFewRows = kAdapterFewRows, kFewBoxes = 2;  // boxes of H for short segments
-constexpr int kTurn = 8;                       // blocks between two drains (fp32 outputs with adapters)
+// Blocks between two drains with adapters; a tile of 512 rows takes no longer block rows.
+__host__ __device__ constexpr int turn_blocks(bool out_bf16) { return out_bf16 ? 64 : 8; }
 
 // A tile of ROWS rows of X, CTAS CTAs per SM.
 template <int ROWS, int CTAS>
@@ -149,7 +152,8 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
   constexpr int kQ = T::kQ, kStageBytes = T::kStageBytes, kStagingBytes = T::kStagingBytes;
   constexpr int kAccCols = T::kAccCols, kTmemCols = T::kTmemCols, kTileN = T::kRows;
   constexpr bool kScaled = kAdapt && !IN_BF16;  // the adapters' sums are kept apart and multiplied by their rows' powers of two
-  constexpr bool kTurns = kAdapt && T::kRows == 256 && (!OUT_BF16 || kScaled);
+  constexpr bool kTurns = kAdapt && T::kRows == 256;
+  constexpr int kTurn = turn_blocks(OUT_BF16);
   static_assert(kTurns || !kScaled, "registers for the sums");
   constexpr int kOutBytes = OUT_BF16 ? 2 : 4;
   constexpr int kBoxCols = T::kBoxBytes / kOutBytes;  // features per box row
@@ -768,16 +772,16 @@ cudaError_t launch_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const 
 //   fewer, short block rows, many tiles (65536 rows, 18944 x 3584, 9): 1477 / 1386 / 1218
 //   few tiles (2048 rows in 4):                                         83 /   70 /   71
 //   fewer, block rows of 16 blocks or more (16384 rows, 3584 x 18944):  380 /  411 /  390
-// (bf16 outputs; an fp32 Y of 512-row tiles needs short block rows, and fp16 inputs have
+// (bf16 outputs; 512-row tiles need a longest block row of one turn, and fp16 inputs have
 // none, see the top.)
-LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t N, int64_t n_seg, bool in_bf16,
-                                bool out_bf16, int num_sms) {
+LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t longest, int64_t N, int64_t n_seg,
+                                bool in_bf16, bool out_bf16, int num_sms) {
   const int64_t row_tiles = (N + 255) / 256;
   if (n_block_rows * row_tiles <= num_sms) return LinearTile::k256;
   if (n_seg >= row_tiles) return LinearTile::k256x2;
   if (n_blocks >= 16 * n_block_rows) return LinearTile::k256;
   if (n_block_rows * ((N + 511) / 512) < 8ll * num_sms) return LinearTile::k256x2;
-  return in_bf16 && (out_bf16 || n_blocks < kTurn * n_block_rows) ? LinearTile::k512 : LinearTile::k256x2;
+  return in_bf16 && longest <= turn_blocks(out_bf16) ? LinearTile::k512 : LinearTile::k256x2;
 }
 
 cudaError_t launch_bcsr_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,

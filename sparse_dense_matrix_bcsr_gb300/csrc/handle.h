@@ -48,6 +48,7 @@ struct spmm_handle_s {
   int num_sms = 0;
   bool sm103 = false;
   int64_t n_groups = 0, n_units = 0, stored = 0;
+  int64_t longest = 0;  // BCSR: blocks of the longest block row
 
   int64_t *d_ptr = nullptr;
   int32_t *d_idx = nullptr;

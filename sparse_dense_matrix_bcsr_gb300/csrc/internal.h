@@ -117,8 +117,9 @@ cudaError_t launch_bcsr_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, c
 // by one CTA per SM (as without adapters) or by two, or 512 rows by one.
 constexpr int kMaxTileRows = 512;
 enum class LinearTile : int32_t { k256, k256x2, k512 };
-LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t N, int64_t n_seg, bool in_bf16,
-                                bool out_bf16, int num_sms);
+// longest: blocks of the longest block row.
+LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t longest, int64_t N, int64_t n_seg,
+                                bool in_bf16, bool out_bf16, int num_sms);
 inline int linear_tile_rows(LinearTile t) { return t == LinearTile::k512 ? 512 : 256; }
 // A segment with an adapter among a tile's rows: rows [begin, end) of the tile.
 struct TileSegment {

@@ -293,7 +293,10 @@ spmm_status build_stages(spmm_handle h, const std::vector<int64_t> &wptr, const 
 spmm_status build_bcsr_split(spmm_handle h, const std::vector<int64_t> &bptr) {
   const int64_t nbr = h->n_groups;
   std::vector<int64_t> srp(nbr + 1, 0);
-  for (int64_t r = 0; r < nbr; ++r) srp[r + 1] = srp[r] + std::max<int64_t>(1, bptr[r + 1] - bptr[r]);
+  for (int64_t r = 0; r < nbr; ++r) {
+    srp[r + 1] = srp[r] + std::max<int64_t>(1, bptr[r + 1] - bptr[r]);
+    h->longest = std::max(h->longest, bptr[r + 1] - bptr[r]);
+  }
   h->n_stages = srp[nbr];
   CUDA_TRY(cudaMalloc(&h->d_stage_row_ptr, srp.size() * sizeof(int64_t)), "cudaMalloc(stage row pointers)");
   CUDA_TRY(cudaMemcpy(h->d_stage_row_ptr, srp.data(), srp.size() * sizeof(int64_t), cudaMemcpyHostToDevice),

@@ -6,6 +6,7 @@ that.  Every way through the projection and every tile of it is reached, in both
 import numpy as np
 import pytest
 
+import spmm_workloads as W
 from test_gpu_adapters import S, Case, ragged, run, run_grad, singles  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -251,3 +252,36 @@ def test_rows_of_very_different_sizes_f16(S):
     c.X, c.down, c.up = X.to(c.X.dtype), D.to(c.X.dtype), signs(2, 16, 320).transpose(1, 2).contiguous().to(c.X.dtype)
     got, want = run(S, c)[0].double(), c.reference()[0]
     assert torch.equal(got, want) and want[::2].abs().max() < 2.0 ** -15 < want[1::2].abs().max()
+
+
+@pytest.mark.parametrize("out_t", ["bf16", "f32"])
+def test_sums_of_one_long_block_row_are_rounded(S, out_t):
+    """A layer of short block rows but one, of 16384 positive terms: that one is summed in chains too, whatever the
+    others' length makes of the tile.  A chain of 512 (fp32) or 4096 terms (bf16) has a step for every 16, each of which cuts
+    up to two units of 2^-23 of the accumulator; then chains are added with rounding.  Left in one accumulator: 1024 steps."""
+    import torch
+    m, k, n = 8192, 16384, 5120
+    rows = np.full(m, 64, np.int64)
+    rows[64:128] = k
+    rp = np.concatenate([[0], np.cumsum(rows)])
+    ci = np.concatenate([np.arange(r, dtype=np.int32) for r in rows])
+    rng = np.random.default_rng(3)
+    vals = W.draw_values(rng, len(ci), "u1", "bf16") & np.uint16(0x7FFF)
+    layer = S.SpMM("bcsr", m, k, rp, ci, vals, "bf16", out_t)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    X = torch.rand((n, k), generator=gen, device="cuda").bfloat16()
+    down, up = torch.zeros((1, 8, k), device="cuda").bfloat16(), torch.zeros((1, m, 8), device="cuda").bfloat16()
+    aset = S.Adapters(m, k, 1, 8, "bf16", max_rows=n, max_segments=1, grad=False)
+    Y = torch.empty((n, m), device="cuda", dtype=torch.bfloat16 if out_t == "bf16" else torch.float32)
+    aset.linear(layer, X, Y, down, up, torch.ones(1, device="cuda"), torch.tensor([0, n], device="cuda"),
+                torch.zeros(1, dtype=torch.int32, device="cuda"))
+    w = torch.from_numpy(W.bits_to_f32(vals[rp[64]:rp[128]], "bf16").reshape(64, k)).cuda().double()
+    want = X.double() @ w.t()
+    steps = (4096 if out_t == "bf16" else 512) // 16
+    chains = 2 * steps * 2.0 ** -23 + (16384 // 16 // steps + 8) * 2.0 ** -24
+    low, high = ((want * (1 + e)).to(Y.dtype).double() for e in (-chains, chains))  # rounded once, as Y is
+    got = Y[:, 64:128].double()
+    assert bool(((low <= got) & (got <= high)).all()), f"{int(((low > got) | (got > high)).sum())} of {got.numel()}"
+    assert layer.check() == S.SPMM_OK
+    layer.close()
+    aset.close()
