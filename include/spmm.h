@@ -392,7 +392,8 @@ spmm_status spmm_adapters_destroy(spmm_adapters a);
  * (for fp16 behind a power of two for each row, so that neither its range nor its smallest
  * value limits h).  Asynchronous; results are bitwise reproducible run to run.
  * Errors: as spmm_run_linear, plus INVALID_ARG for shapes, types or devices
- * that do not match and batches above the set's limits.
+ * that do not match, batches above the set's limits and a current device that is
+ * not the set's.
  */
 spmm_status spmm_run_linear_adapters(spmm_handle h, spmm_adapters a, const void *X, void *Y, int64_t N,
                                      const void *down, const void *up, const float *scale, const int64_t *seg_ptr,
@@ -457,6 +458,7 @@ spmm_status spmm_route_sort(const int32_t *ids, int64_t T, int32_t topk, int32_t
  * spmm_route_combine_grad  dy[position[t, j]] = weights[t, j] * dout[t], slots from
  *                          *n_kept on 0; dweights[t, j] = <dout[t], y[position[t, j]]>,
  *                          0 for dropped entries.
+ * The kernels run on the current device, where all pointers and the stream have to be.
  * Bases that are 16-byte aligned with d * element size a multiple of 16 take
  * 16-byte accesses; others run element by element.
  * Errors: INVALID_ARG (NULL, sizes, dtype), UNSUPPORTED (topk > 32, T * topk

@@ -415,16 +415,18 @@ class SpMM:
 # decoding step makes several of them, each a few microseconds of host time.
 _torch = None
 _raw_stream = None
+_current_device = None
 _ROW_DTYPES = {}
 
 
 def _load_torch():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current_device
     import torch
     _ROW_DTYPES.update({torch.float16: SPMM_F16, torch.bfloat16: SPMM_BF16, torch.float32: SPMM_F32})
     # the current stream's handle without building a Stream object around it (3 us)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     load_library()
     _torch = torch
     return torch
@@ -440,6 +442,17 @@ def _tensor(t, what, dtype, shape, device):
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device or device < 0 or not t.is_contiguous():
         _refuse(what, t, dtype, shape)
     return t.data_ptr()
+
+
+def _stream(device, stream=None):
+    """The stream's handle; raises ValueError unless `device`, where the tensors are, is the current device: the library
+    launches there, whatever its arguments point to."""
+    if device < 0:
+        raise ValueError("the tensors are not on a CUDA device")
+    if device != _current_device():
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{_current_device()}: call it under "
+                         "torch.cuda.device")
+    return (stream.cuda_stream if stream is not None else _raw_stream(device)) or None
 
 
 class Adapters:
@@ -458,12 +471,15 @@ class Adapters:
         self._dtype = {SPMM_F16: torch.float16, SPMM_BF16: torch.bfloat16}.get(_dt(in_t))
         self._down, self._up, self._scale = (n_adapters, rank, k), (n_adapters, m, rank), (n_adapters,)
         self.a = spmm_adapters_create(m, k, n_adapters, rank, in_t, max_rows, max_segments, grad)
+        self.device = _current_device()
 
     def _out(self, layer):
         return _torch.bfloat16 if _dt(layer.out_t) == SPMM_BF16 else _torch.float32
 
     def _batch(self, device, down, up, scale, seg_ptr, seg_adapter):
         n_seg, dtype = seg_adapter.shape[0], self._dtype
+        if device != self.device:
+            raise ValueError(f"the tensors are on device {device}, the adapters' workspace on cuda:{self.device}")
         return (_tensor(down, "down", dtype, self._down, device), _tensor(up, "up", dtype, self._up, device),
                 _tensor(scale, "scale", _torch.float32, self._scale, device),
                 _tensor(seg_ptr, "seg_ptr", _torch.int64, (n_seg + 1,), device),
@@ -476,7 +492,7 @@ class Adapters:
             layer.h, self.a, _tensor(X, "X", self._dtype, (N, self.k), device),
             _tensor(Y, "Y", self._out(layer), (N, self.m), device), N,
             *self._batch(device, down, up, scale, seg_ptr, seg_adapter),
-            (stream.cuda_stream if stream is not None else _raw_stream(device)) or None)
+            _stream(device, stream))
         if status:
             _check(status, "spmm_run_linear_adapters")
         return Y
@@ -489,7 +505,7 @@ class Adapters:
             None if dX is None else _tensor(dX, "dX", self._out(layer_t), (N, self.k), device),
             _tensor(d_down, "d_down", dtype, self._down, device), _tensor(d_up, "d_up", dtype, self._up, device), N,
             *self._batch(device, down, up, scale, seg_ptr, seg_adapter),
-            (stream.cuda_stream if stream is not None else _raw_stream(device)) or None)
+            _stream(device, stream))
         if status:
             _check(status, "spmm_adapters_grad")
 
@@ -518,14 +534,14 @@ def route_sort(ids, n_experts: int):
     torch = _torch or _load_torch()
     T, topk = shape = ids.shape
     n, at, where = T * topk, ids.get_device(), ids.device
-    p = _tensor(ids, "ids", torch.int32, shape, at)
+    p, stream = _tensor(ids, "ids", torch.int32, shape, at), _stream(at)
     offsets = torch.empty(n_experts + 1, dtype=torch.int64, device=where)
     order = torch.empty(n, dtype=torch.int32, device=where)
     position = torch.empty_like(ids)
     size = _lib.spmm_route_workspace_bytes(T, topk, n_experts) if n > 4096 else 0  # short lists need none
     work = torch.empty(size, dtype=torch.uint8, device=where) if size else None
     status = _lib.spmm_route_sort(p, T, topk, n_experts, offsets.data_ptr(), order.data_ptr(), position.data_ptr(),
-                                  work.data_ptr() if size else None, _raw_stream(at) or None)
+                                  work.data_ptr() if size else None, stream)
     if status:
         _check(status, "spmm_route_sort")
     return offsets, order, position
@@ -536,11 +552,12 @@ def route_gather(x, position, offsets):
     torch = _torch or _load_torch()
     T, topk = shape = position.shape
     d, dtype, at, last = x.shape[1], x.dtype, x.get_device(), offsets.shape[0] - 1
+    stream = _stream(at)
     out = torch.empty((T * topk, d), dtype=dtype, device=x.device)
     status = _lib.spmm_route_gather(
         _tensor(x, "x", dtype, (T, d), at), _tensor(position, "position", torch.int32, shape, at),
         _tensor(offsets, "offsets", torch.int64, (last + 1,), at) + 8 * last, out.data_ptr(), T, topk, d, _row_dtype(x),
-        _raw_stream(at) or None)
+        stream)
     if status:
         _check(status, "spmm_route_gather")
     return out
@@ -551,11 +568,12 @@ def route_combine(y, position, weights=None):
     torch = _torch or _load_torch()
     T, topk = shape = position.shape
     d, dtype, at = y.shape[1], y.dtype, y.get_device()
+    stream = _stream(at)
     out = torch.empty((T, d), dtype=dtype, device=y.device)
     status = _lib.spmm_route_combine(
         _tensor(y, "y", dtype, (T * topk, d), at), _tensor(position, "position", torch.int32, shape, at),
         None if weights is None else _tensor(weights, "weights", torch.float32, shape, at), out.data_ptr(), T, topk, d,
-        _row_dtype(y), _raw_stream(at) or None)
+        _row_dtype(y), stream)
     if status:
         _check(status, "spmm_route_combine")
     return out
@@ -566,6 +584,7 @@ def route_combine_grad(dout, y, position, weights, offsets):
     torch = _torch or _load_torch()
     T, topk = shape = position.shape
     d, dtype, at, last = y.shape[1], y.dtype, y.get_device(), offsets.shape[0] - 1
+    stream = _stream(at)
     dy = torch.empty_like(y)
     dw = torch.empty(shape, dtype=torch.float32, device=y.device)
     status = _lib.spmm_route_combine_grad(
@@ -573,7 +592,7 @@ def route_combine_grad(dout, y, position, weights, offsets):
         _tensor(position, "position", torch.int32, shape, at),
         None if weights is None else _tensor(weights, "weights", torch.float32, shape, at),
         _tensor(offsets, "offsets", torch.int64, (last + 1,), at) + 8 * last, dy.data_ptr(), dw.data_ptr(), T, topk, d,
-        _row_dtype(y), _raw_stream(at) or None)
+        _row_dtype(y), stream)
     if status:
         _check(status, "spmm_route_combine_grad")
     return dy, dw

@@ -90,6 +90,10 @@ spmm_status check_batch(spmm_handle h, spmm_adapters a, int64_t rows, int64_t co
   if (misaligned({scale, seg_adapter}, 4) || misaligned({seg_ptr}, 8))
     return fail(SPMM_ERR_UNSUPPORTED, "scale, seg_ptr or seg_adapter is not aligned to its type");
   if (!a->sm103) return fail(SPMM_ERR_UNSUPPORTED, "the kernels need an sm_103 (GB300) device");
+  int current = -1;
+  CUDA_TRY(cudaGetDevice(&current), "cudaGetDevice");
+  if (current != a->device)
+    return fail(SPMM_ERR_INVALID_ARG, "the current device is %d, the adapters' device %d", current, a->device);
   return SPMM_OK;
 }
 
