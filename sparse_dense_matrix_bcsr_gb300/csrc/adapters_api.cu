@@ -400,9 +400,12 @@ spmm_status spmm_adapters_create(spmm_adapters *out, int64_t m, int64_t k, int32
 
 spmm_status spmm_adapters_destroy(spmm_adapters a) {
   if (!a) return fail(SPMM_ERR_INVALID_ARG, "adapters is NULL");
+  int current = 0;  // stays current: this also runs where a program drops the set
+  const bool known = cudaGetDevice(&current) == cudaSuccess;
   cudaSetDevice(a->device);
   cudaDeviceSynchronize();
   free_adapters(a);
+  if (known) cudaSetDevice(current);
   return SPMM_OK;
 }
 
