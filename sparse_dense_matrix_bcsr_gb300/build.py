@@ -22,7 +22,7 @@ SOURCES = ["bcsr_kernel.cu", "bcsr_linear_kernel.cu", "wcsr_kernel.cu", "wcsr64_
            "adapters.cu", "adapter_decode_kernel.cu", "adapter_down_kernel.cu", "adapter_wgrad_kernel.cu",
            "adapter_group_kernel.cu", "route.cu",
            "adapters_api.cu", "format.cpp"]
-HEADERS = ["ptx.cuh", "internal.h", "format.h", "split_reduce.cuh", "handle.h", "segments.cuh"]
+HEADERS = ["ptx.cuh", "internal.h", "format.h", "split_reduce.cuh", "handle.h", "segments.cuh", "adapter_rules.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "-I" + os.path.join(ROOT, "include")]

@@ -214,20 +214,6 @@ spmm_status up_project(spmm_handle h, spmm_adapters a, const spmm::AdapterParams
   return SPMM_OK;
 }
 
-// Whether a batch takes the row kernels (adapter_decode_kernel.cu) or the tiled
-// ones.  The row kernels' time grows with the rows, N * (a + b * rank) (every row
-// meets its U on the CUDA cores), the tiled ones' with the segments (one more
-// stage in every tile a segment touches).  Fitted to GPU times through 18944 x
-// 3584 (us, rows / tiles), which it decides as the faster one does: 64 rows of
-// one adapter, rank 16: 15.6 / 18.4, rank 64: 28.2 / 19.7; 128 rows, rank 16, in
-// 1 segment: 23.6 / 18.9, in 16: 24.5 / 44.5, in 128: 32.8 / 295; 256 rows in 4:
-// 41.0 / 23.5, in 64: 44.1 / 94.8; 512 rows of rank 64 in 64: 192 / 70; 1024 rows
-// of rank 16 in 128: 156 / 132; 300 rows of rank 128 in 300 (3584 x 18944): 182 / 314.
-bool rows_path(int64_t N, int32_t rank, int64_t n_seg) {
-  constexpr int64_t kMostRows = 65535ll * spmm::kAdapterDecodeRows;  // the launch grid's second dimension
-  return N <= kMostRows && N * (rank + 24) < 2300 + 290 * n_seg;
-}
-
 // Sorts the batch's rows by adapter: X (and dY) to their places, p's segments one per
 // adapter.
 spmm_status sort_rows(spmm_adapters a, spmm::AdapterParams &p, const void *&X, const void **dY, int64_t groups, cudaStream_t s) {
@@ -242,40 +228,11 @@ spmm_status sort_rows(spmm_adapters a, spmm::AdapterParams &p, const void *&X, c
   return SPMM_OK;
 }
 
-// As many segments as the sorted rows can have.
-int64_t most_groups(spmm_adapters a, int64_t N, int64_t n_seg) {
-  return std::min({N, n_seg, static_cast<int64_t>(a->n_adapters)});
-}
-
-// Whether the gradients sort the batch's rows by adapter first.  A segment less saves
-// 0.5 us or more, sorting costs ~6 us and 0.5 ps for each of the m + 2 k columns of a
-// row.  Gradients (us) as the rows come / sorted: 432 rows in 432 segments of 4 adapters,
-// 3880 x 16048: 1004 / 66; 500 in 500 of 64, 4096 x 4096: 301 / 79; 16 in 16 of 4,
-// 18944 x 3584: 57 / 40; 1000 in 100 of 20, 4096 x 4096: 71 / 60, in 40: 52 / 62; 300 in 32
-// of 8, 18944 x 3584: 69 / 63; 300 in 16 of 8, 3584 x 18944: 77 / 87.
-bool sorting_pays(spmm_adapters a, int64_t N, int64_t n_seg, int64_t groups) {
-  return N <= spmm::kGroupRows && (n_seg - groups) * 550 > 6000 + N * (a->m + 2 * a->k) / 2000;  // ns
-}
-
-// Whether the projection sorts them and takes the tiled path.  Against the row kernels
-// (us as they come / sorted): 160 single rows of 2 adapters of rank 128, 12424 x 2904: 112 /
-// 31; 421 of 3 of rank 64, 7728 x 3048: 103 / 39; 433 of 25 of rank 24, 12336 x 1056: 86 / 79;
-// 256 of 8 of rank 16, 18944 x 3584: 48 / 42, 3584 x 18944: 33 / 44; 128 of 8: 24 / 35; 512 of
-// 64: 97 / 111.  Against tiles as they come: 1000 rows of rank 64 in 200 segments of 4,
-// 18944 x 3584: 120 / 65; in 100 of 20, rank 32: 85 / 76, 4096 x 4096: 37 / 39; 412 of rank
-// 128 in 109 of 6, 2168 x 624: 69 / 33; 777 in 40 of 24: 70 / 80.  The terms are ns.
-bool sorting_pays_forward(spmm_adapters a, int64_t N, int64_t n_seg, int64_t groups) {
-  if (N > spmm::kGroupRows || n_seg <= groups) return false;
-  if (rows_path(N, a->rank, n_seg))
-    return 26000 + 20 * N + groups * a->m * 7 / 100 < N * (a->rank + 24) * (800 + a->m * 21 / 100) / 1000;
-  return (n_seg - groups) * (150 + a->m / 100) > 14000 + N * (a->k + a->m) / 2000;
-}
-
 spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const void *X, void *Y, const void *down,
                     const void *up, cudaStream_t s) {
   const bool bf16 = h->in_t == SPMM_BF16;
-  const int64_t groups = most_groups(a, p.N, p.n_seg);
-  const bool sorted = sorting_pays_forward(a, p.N, p.n_seg, groups);
+  const int64_t groups = spmm::most_groups(a->n_adapters, p.N, p.n_seg);
+  const bool sorted = spmm::sorting_pays_forward(a->m, a->k, a->rank, p.N, p.n_seg, groups);
   void *const out = Y;
   if (sorted) {
     const spmm_status st = sort_rows(a, p, X, nullptr, groups, s);
@@ -289,7 +246,7 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
   p.up = up;
   p.M = static_cast<int32_t>(h->m);
   p.K = static_cast<int32_t>(h->k);
-  if (sorted || !rows_path(p.N, p.rank, p.n_seg)) {
+  if (sorted || !spmm::rows_path(p.N, p.rank, p.n_seg)) {
     const spmm::LinearTile tile = spmm::linear_adapters_tile(h->n_groups, h->n_units, h->longest, p.N, p.n_seg, bf16,
                                                              h->out_t == SPMM_BF16, p.num_sms);
     spmm_status st = down_project(a, p, {{X, down, a->d_h, nullptr, nullptr, p.K, false}}, spmm::linear_tile_rows(tile), s);
@@ -311,7 +268,7 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
   d.n_seg = p.n_seg;
   d.n_adapters = p.n_adapters;
   d.rank = p.rank;
-  d.tile = p.N <= 16 ? 16 : p.N <= 32 || p.rank > 64 ? 32 : spmm::kAdapterDecodeRows;
+  d.tile = spmm::decode_tile_rows(p.N, p.rank);
   d.M = p.M;
   d.N = p.N;
   d.status = p.status;
@@ -444,8 +401,8 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
     return SPMM_OK;
   }
   void *const out = dX;
-  const int64_t groups = most_groups(a, N, n_seg);
-  const bool sorted = sorting_pays(a, N, n_seg, groups);
+  const int64_t groups = spmm::most_groups(a->n_adapters, N, n_seg);
+  const bool sorted = spmm::sorting_pays(a->m, a->k, N, n_seg, groups);
   if (sorted) {
     st = sort_rows(a, p, X, &dY, groups, s);
     if (st != SPMM_OK) return st;

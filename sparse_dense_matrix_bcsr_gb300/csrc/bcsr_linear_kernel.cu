@@ -97,8 +97,6 @@ constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2, kEpiWarps = 4;
 constexpr int kMiscBytes = 1024;
 constexpr int kHBytes = 128 * 128;               // a box of H: 128 rows x 64 columns
 constexpr int kFewRows = kAdapterFewRows, kFewBoxes = 2;  // boxes of H for short segments
-// Blocks between two drains with adapters; a tile of 512 rows takes no longer block rows.
-__host__ __device__ constexpr int turn_blocks(bool out_bf16) { return out_bf16 ? 64 : 8; }
 
 // A tile of ROWS rows of X, CTAS CTAs per SM.
 template <int ROWS, int CTAS>
@@ -153,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
   constexpr int kAccCols = T::kAccCols, kTmemCols = T::kTmemCols, kTileN = T::kRows;
   constexpr bool kScaled = kAdapt && !IN_BF16;  // the adapters' sums are kept apart and multiplied by their rows' powers of two
   constexpr bool kTurns = kAdapt && T::kRows == 256;
-  constexpr int kTurn = turn_blocks(OUT_BF16);
+  constexpr int kTurn = OUT_BF16 ? kTurnBf16 : kTurnF32;
   static_assert(kTurns || !kScaled, "registers for the sums");
   constexpr int kOutBytes = OUT_BF16 ? 2 : 4;
   constexpr int kBoxCols = T::kBoxBytes / kOutBytes;  // features per box row
@@ -762,27 +760,6 @@ cudaError_t launch_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const 
 }
 
 }  // namespace
-
-// The tile with adapters.  GPU times (us) of 256 rows by one CTA per SM / by two /
-// 512 rows:
-//   no more tiles than SMs (300 rows, 3584 x 18944):                    37 /   41 /   48
-//   more segments than row tiles, whose stages hide behind the other
-//   CTA's blocks (777 rows of 8192 x 8192 in 40):                      111 /   92 /  104
-//   (2048 rows, 18944 x 3584, in 128):                                 223 /  141 /  198
-//   fewer, short block rows, many tiles (65536 rows, 18944 x 3584, 9): 1477 / 1386 / 1218
-//   few tiles (2048 rows in 4):                                         83 /   70 /   71
-//   fewer, block rows of 16 blocks or more (16384 rows, 3584 x 18944):  380 /  411 /  390
-// (bf16 outputs; 512-row tiles need a longest block row of one turn, and fp16 inputs have
-// none, see the top.)
-LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t longest, int64_t N, int64_t n_seg,
-                                bool in_bf16, bool out_bf16, int num_sms) {
-  const int64_t row_tiles = (N + 255) / 256;
-  if (n_block_rows * row_tiles <= num_sms) return LinearTile::k256;
-  if (n_seg >= row_tiles) return LinearTile::k256x2;
-  if (n_blocks >= 16 * n_block_rows) return LinearTile::k256;
-  if (n_block_rows * ((N + 511) / 512) < 8ll * num_sms) return LinearTile::k256x2;
-  return in_bf16 && longest <= turn_blocks(out_bf16) ? LinearTile::k512 : LinearTile::k256x2;
-}
 
 cudaError_t launch_bcsr_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,
                                const BcsrParams &p, bool in_bf16, bool out_bf16, cudaStream_t stream) {

@@ -7,6 +7,8 @@
 
 #include <atomic>
 
+#include "adapter_rules.h"
+
 namespace spmm {
 
 // Raise a kernel's dynamic shared-memory limit to `bytes` on the current
@@ -113,14 +115,6 @@ cudaError_t launch_bcsr(const CUtensorMap &tmA, const CUtensorMap &tmB, const CU
 cudaError_t launch_bcsr_linear(const CUtensorMap &tmA, const CUtensorMap &tmX, const CUtensorMap &tmY,
                                const BcsrParams &p, bool in_bf16, bool out_bf16, cudaStream_t stream);
 
-// The most rows of X per tile of that kernel; with adapters, its tiles: 256 rows
-// by one CTA per SM (as without adapters) or by two, or 512 rows by one.
-constexpr int kMaxTileRows = 512;
-enum class LinearTile : int32_t { k256, k256x2, k512 };
-// longest: blocks of the longest block row.
-LinearTile linear_adapters_tile(int64_t n_block_rows, int64_t n_blocks, int64_t longest, int64_t N, int64_t n_seg,
-                                bool in_bf16, bool out_bf16, int num_sms);
-inline int linear_tile_rows(LinearTile t) { return t == LinearTile::k512 ? 512 : 256; }
 // A segment with an adapter among a tile's rows: rows [begin, end) of the tile.
 struct TileSegment {
   int32_t adapter, begin, end, pad_;
@@ -335,7 +329,6 @@ cudaError_t launch_shrink(const AdapterParams &p, bool bf16, cudaStream_t s);
 // `tile` (16, 32 or, up to rank 64, 64) rows.  tmA as for launch_bcsr, tmX covers X as
 // [N rows, K cols] with tile x 64 boxes, 128-byte swizzle.  Launched as a
 // programmatic dependent of launch_shrink's kernel.
-constexpr int kAdapterDecodeRows = 64;
 struct AdapterDecodeParams {
   const int64_t *block_row_ptr;
   const int32_t *block_col_idx;
@@ -356,7 +349,6 @@ cudaError_t launch_adapter_decode(const CUtensorMap &tmA, const CUtensorMap &tmX
 // Rows of a batch of at most kGroupRows sorted by adapter (adapter_group_kernel.cu):
 // row n's place, and the groups as segments of the sorted batch, n_groups of them
 // (at least as many as there can be adapters among the rows; the rest are empty).
-constexpr int kGroupRows = 1024;
 struct AdapterGroupParams {
   const int64_t *seg_ptr;
   const int32_t *seg_adapter;

@@ -285,3 +285,26 @@ def test_sums_of_one_long_block_row_are_rounded(S, out_t):
     assert layer.check() == S.SPMM_OK
     layer.close()
     aset.close()
+
+
+def test_millions_of_single_rows(S):
+    """More rows than the row kernels' launch grid takes at this rank, every row a request of its own."""
+    import torch
+    m, k, rank, n_adapters, n = 64, 64, 72, 3, 65535 * 32 + 1000
+    c, rng = zero_weight(m, k, 1, ([0, 1], [0]), rank, n_adapters, "bf16", "bf16", 1.0, keep=1.0)
+    D, _ = paired_ranks(rng, n_adapters, rank, k)
+    U = signs(n_adapters, rank, m).transpose(1, 2).contiguous()
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    X = torch.randint(64, 128, (n, k), generator=gen, device="cuda").bfloat16()
+    ids = torch.randint(-1, n_adapters, (n,), generator=gen, device="cuda", dtype=torch.int32)
+    layer, aset = c.layer(S), S.Adapters(m, k, n_adapters, rank, "bf16", max_rows=n, max_segments=n, grad=False)
+    Y = torch.full((n, m), float("nan"), dtype=torch.bfloat16, device="cuda")
+    aset.linear(layer, X, Y, D.bfloat16().cuda(), U.bfloat16().cuda(), torch.ones(n_adapters, device="cuda"),
+                torch.arange(n + 1, device="cuda"), ids)
+    assert layer.check() == S.SPMM_OK
+    for a in range(-1, n_adapters):
+        at = ids == a
+        want = X[at].double() @ (U[a] @ D[a]).t().cuda() if a >= 0 else torch.zeros((int(at.sum()), m), device="cuda").double()
+        assert torch.equal(Y[at].double(), want)
+    layer.close()
+    aset.close()
