@@ -487,7 +487,8 @@ spmm_status check_rows(std::initializer_list<const void *> ps, spmm_dtype dtype)
 int64_t spmm_route_workspace_bytes(int64_t T, int32_t topk, int32_t n_experts) {
   if (T < 0 || topk < 1 || n_experts < 1 || n_experts > spmm::kRouteMaxExperts || T >= (1ll << 31) / topk) return 0;
   const int64_t chunks = spmm::route_chunks(T * topk);
-  return chunks > 1 ? chunks * n_experts * static_cast<int64_t>(sizeof(int32_t)) : 0;
+  const int64_t rows = chunks > spmm::kRouteScanChunks ? chunks + 1 : chunks;
+  return chunks > 1 ? rows * n_experts * static_cast<int64_t>(sizeof(int32_t)) : 0;
 }
 
 spmm_status spmm_route_sort(const int32_t *ids, int64_t T, int32_t topk, int32_t n_experts, int64_t *offsets, int32_t *order,

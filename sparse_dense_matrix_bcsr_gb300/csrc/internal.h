@@ -386,6 +386,7 @@ cudaError_t launch_adapter_wgrad(AdapterWgradParams p, int num_sms, bool bf16, c
 // ---------------------------------------------------------------- expert routing (route.cu)
 constexpr int kRouteOneChunk = 8192;     // ids that one block of the sort takes alone
 constexpr int kRouteChunk = 2048;        // ids per block of longer sorts
+constexpr int kRouteScanChunks = 64;     // more chunks' counts are summed once for all blocks
 constexpr int kRouteMaxExperts = 2048;   // the sort's counts of a block lie in shared memory
 constexpr int kRouteMaxTopk = 32;        // a warp holds a token's positions, one a lane
 
