@@ -247,7 +247,7 @@ spmm_status project(spmm_handle h, spmm_adapters a, spmm::AdapterParams p, const
   p.M = static_cast<int32_t>(h->m);
   p.K = static_cast<int32_t>(h->k);
   if (sorted || !spmm::rows_path(p.N, p.rank, p.n_seg)) {
-    const spmm::LinearTile tile = spmm::linear_adapters_tile(h->n_groups, h->n_units, h->longest, p.N, p.n_seg, bf16,
+    const spmm::LinearTile tile = spmm::linear_adapters_tile(h->n_groups, h->n_units, h->longest, p.N, p.n_seg, p.rank, bf16,
                                                              h->out_t == SPMM_BF16, p.num_sms);
     spmm_status st = down_project(a, p, {{X, down, a->d_h, nullptr, nullptr, p.K, false}}, spmm::linear_tile_rows(tile), s);
     if (st == SPMM_OK) st = up_project(h, a, p, false, tile, s);
@@ -409,7 +409,7 @@ spmm_status spmm_adapters_grad(spmm_handle h_t, spmm_adapters a, const void *X, 
     if (dX) dX = a->d_dxs;
   }
   // H and dH, then dX with the roles of the adapters' two matrices exchanged
-  const spmm::LinearTile tile = spmm::linear_adapters_tile(h_t->n_groups, h_t->n_units, h_t->longest, p.N, p.n_seg, bf16,
+  const spmm::LinearTile tile = spmm::linear_adapters_tile(h_t->n_groups, h_t->n_units, h_t->longest, p.N, p.n_seg, p.rank, bf16,
                                                            h_t->out_t == SPMM_BF16, p.num_sms);
   float *const dh_rows = bf16 ? a->d_dh : a->d_dh_rows;
   const DownJob of_x = bf16 ? DownJob{X, down, a->d_h, nullptr, nullptr, k, false}

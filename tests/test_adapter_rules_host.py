@@ -18,8 +18,8 @@ int sorts(int64_t m, int64_t k, int rank, int64_t n, int64_t segs, int64_t adapt
 int sorts_gradient(int64_t m, int64_t k, int64_t n, int64_t segs, int64_t adapters) {
   return spmm::sorting_pays(m, k, n, segs, spmm::most_groups(adapters, n, segs));
 }
-int tile(int64_t rows, int64_t blocks, int64_t longest, int64_t n, int64_t segs, int in_bf16, int out_bf16) {
-  return static_cast<int>(spmm::linear_adapters_tile(rows, blocks, longest, n, segs, in_bf16, out_bf16, 152));
+int tile(int64_t rows, int64_t blocks, int64_t longest, int64_t n, int64_t segs, int rank, int in_bf16, int out_bf16) {
+  return static_cast<int>(spmm::linear_adapters_tile(rows, blocks, longest, n, segs, rank, in_bf16, out_bf16, 152));
 }
 }
 """
@@ -37,7 +37,7 @@ def rules(tmp_path_factory):
     lib.tile_rows.argtypes = [ctypes.c_int64, ctypes.c_int]
     lib.sorts.argtypes = [ctypes.c_int64] * 2 + [ctypes.c_int] + [ctypes.c_int64] * 3
     lib.sorts_gradient.argtypes = [ctypes.c_int64] * 5
-    lib.tile.argtypes = [ctypes.c_int64] * 5 + [ctypes.c_int] * 2
+    lib.tile.argtypes = [ctypes.c_int64] * 5 + [ctypes.c_int] * 3
     return lib
 
 
@@ -53,9 +53,9 @@ def test_row_kernels_fit_their_launch_grid(rules, rank):
 
 def test_long_block_rows_are_not_left_in_one_accumulator(rules):
     for out_bf16, turn in ((1, 64), (0, 8)):
-        assert rules.tile(296, 1000, turn, 65536, 9, 1, out_bf16) == K512
-        assert rules.tile(296, 1000, turn + 1, 65536, 9, 1, out_bf16) == K256X2
-    assert rules.tile(296, 1000, 1, 65536, 9, 0, 0) == K256X2  # fp16: the adapters' sums are kept apart
+        assert rules.tile(296, 1000, turn, 65536, 9, 16, 1, out_bf16) == K512
+        assert rules.tile(296, 1000, turn + 1, 65536, 9, 16, 1, out_bf16) == K256X2
+    assert rules.tile(296, 1000, 1, 65536, 9, 16, 0, 0) == K256X2  # fp16: the adapters' sums are kept apart
 
 
 def way(rules, rows, cols, n, n_seg, rank, n_adapters, in_bf16, out_bf16, gradient):
@@ -67,7 +67,7 @@ def way(rules, rows, cols, n, n_seg, rank, n_adapters, in_bf16, out_bf16, gradie
     if not gradient and rules.rows_path(n, rank, n_seg):
         return "rows"
     most = -(-cols // 64)  # blocks of a block row: few enough whatever their number
-    return ("tile-256", "two-ctas", "tile-512")[rules.tile(-(-rows // 64), most * -(-rows // 64), most, n, n_seg, in_bf16, out_bf16)]
+    return ("tile-256", "two-ctas", "tile-512")[rules.tile(-(-rows // 64), most * -(-rows // 64), most, n, n_seg, rank, in_bf16, out_bf16)]
 
 
 @pytest.mark.parametrize("out_bf16", [0, 1])

@@ -85,7 +85,7 @@ FORWARD = [
     pytest.param(4104, 136, 700, ragged(700, 40, 9, gaps=True), 72, 9, id="two-ctas-rank-72"),
     pytest.param(4160, 136, 2100, ragged(2100, 20, 4), 32, 4, id="two-ctas-rank-32"),
     pytest.param(8192, 136, 5300, ragged(5300, 9, 4), 16, 4, id="tile-512"),
-    pytest.param(8200, 72, 5300, ragged(5300, 11, 3, gaps=True), 40, 3, id="tile-512-rank-40"),
+    pytest.param(1288, 72, 33000, ragged(33000, 11, 3, gaps=True), 40, 3, id="tile-512-rank-40"),
     pytest.param(1032, 520, 400, singles(400, 3), 128, 3, id="sorted"),
     pytest.param(256, 264, 40, singles(40, 5), 24, 5, id="rows"),
 ]
@@ -111,7 +111,7 @@ BACKWARD = [
     pytest.param(136, 4104, 700, ragged(700, 7, 3), 8, 3, id="two-ctas"),
     pytest.param(136, 4104, 1100, ragged(1100, 40, 9, gaps=True), 72, 9, id="two-ctas-rank-72"),
     pytest.param(136, 8192, 5300, ragged(5300, 9, 4), 16, 4, id="tile-512"),
-    pytest.param(72, 8200, 5300, ragged(5300, 11, 3, gaps=True), 40, 3, id="tile-512-rank-40"),
+    pytest.param(72, 1288, 33000, ragged(33000, 11, 3, gaps=True), 40, 3, id="tile-512-rank-40"),
     pytest.param(520, 1032, 400, singles(400, 3), 128, 3, id="sorted"),
 ]
 
