@@ -51,13 +51,14 @@ inline bool sorting_pays(int64_t m, int64_t k, int64_t N, int64_t n_seg, int64_t
 // 37; 421 of 3 of rank 64, 7728 x 3048: 110 / 33; 433 of 25 of rank 24, 12336 x 1056: 90 / 54;
 // 256 of 8 of rank 16, 18944 x 3584: 51 / 37, 3584 x 18944: 34 / 43; 128 of 8: 26 / 35; 512 of
 // 64: 100 / 89 (missed).  Against tiles as they come: 1000 rows of rank 64 in 200 segments of 4,
-// 18944 x 3584: 375 / 77; in 100 of 20, rank 32: 141 / 88, 4096 x 4096: 50 / 42 (missed); 412 of rank
-// 128 in 109 of 6, 2168 x 624: 159 / 36; 777 in 40 of 24: 137 / 131.  The terms are ns.
+// 18944 x 3584: 375 / 77; in 100 of 20, rank 32: 141 / 88, 4096 x 4096: 50 / 42; 412 of rank
+// 128 in 109 of 6, 2168 x 624: 159 / 36; 402 in 55 of 9, 584 x 8712: 86 / 47; 392 of rank 128 in 14
+// of 8, 6208 x 7408: 62 / 53 (missed); 777 in 40 of 24: 137 / 131 (missed).  The terms are ns.
 inline bool sorting_pays_forward(int64_t m, int64_t k, int32_t rank, int64_t N, int64_t n_seg, int64_t groups) {
   if (N > kGroupRows || n_seg <= groups) return false;
   if (rows_path(N, rank, n_seg))
     return 26000 + 20 * N + groups * m * 7 / 100 < N * (rank + 24) * (800 + m * 21 / 100) / 1000;
-  return (n_seg - groups) * (150 + m / 100) > 14000 + N * (k + m) / 2000;
+  return (n_seg - groups) * (300 + 12 * rank) > 14000 + N * (k + m) / 2000;
 }
 
 // Tiles of the projection with adapters: 256 rows by one CTA per SM (as without

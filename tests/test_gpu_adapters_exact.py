@@ -82,7 +82,8 @@ FORWARD = [
     pytest.param(256, 200, 700, ragged(700, 5, 3), 16, 3, id="tile-256"),
     pytest.param(328, 200, 700, ragged(700, 3, 2), 128, 2, id="tile-256-rank-128"),
     pytest.param(4104, 136, 700, ragged(700, 7, 3), 8, 3, id="two-ctas"),
-    pytest.param(4104, 136, 700, ragged(700, 40, 9, gaps=True), 72, 9, id="two-ctas-rank-72"),
+    pytest.param(4104, 136, 700, ragged(700, 40, 40, gaps=True), 72, 40, id="two-ctas-rank-72"),
+    pytest.param(4104, 136, 700, ragged(700, 40, 9, gaps=True), 72, 9, id="sorted-rank-72"),
     pytest.param(4160, 136, 2100, ragged(2100, 20, 4), 32, 4, id="two-ctas-rank-32"),
     pytest.param(8192, 136, 5300, ragged(5300, 9, 4), 16, 4, id="tile-512"),
     pytest.param(1288, 72, 33000, ragged(33000, 11, 3, gaps=True), 40, 3, id="tile-512-rank-40"),
