@@ -650,60 +650,60 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
         }
 #pragma unroll
         for (int c = 0; c < kAccCols; ++c) sum[c] = 0.0f;
-        continue;
-      }
+      } else {
 #pragma unroll 1
-      for (int box = 0; box < T::kParts * kBoxes; ++box) {
-        const int h = box / kBoxes;               // part of the tile
-        const int c0 = (box % kBoxes) * kBoxCols;  // first feature of the box
-        uint8_t *pst = stg;
-        if (lane == 0) bulk_wait_group_read<0>();
-        __syncwarp();
-        // kBoxCols features = kBoxCols / 16 TMEM loads of 16 columns
-        uint32_t v[kBoxCols / 16][16];
+        for (int box = 0; box < T::kParts * kBoxes; ++box) {
+          const int h = box / kBoxes;               // part of the tile
+          const int c0 = (box % kBoxes) * kBoxCols;  // first feature of the box
+          uint8_t *pst = stg;
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+          // kBoxCols features = kBoxCols / 16 TMEM loads of 16 columns
+          uint32_t v[kBoxCols / 16][16];
 #pragma unroll
-        for (int g = 0; g < kBoxCols / 16; ++g) {
-          if (!zero) {
-            tmem_ld_32x32b_x16(tbase + h * kBlk + c0 + g * 16, v[g]);
-          } else {
+          for (int g = 0; g < kBoxCols / 16; ++g) {
+            if (!zero) {
+              tmem_ld_32x32b_x16(tbase + h * kBlk + c0 + g * 16, v[g]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[g][i] = 0u;
-          }
-        }
-        if (!zero) tmem_ld_wait();
-        uint8_t *row = pst + lane * T::kBoxBytes;
-#pragma unroll
-        for (int g = 0; g < kBoxCols / 16; ++g) {
-          if constexpr (OUT_BF16) {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const __nv_bfloat162 b2 =
-                  __floats2bfloat162_rn(__uint_as_float(v[g][2 * i]), __uint_as_float(v[g][2 * i + 1]));
-              w[i] = *reinterpret_cast<const uint32_t *>(&b2);
+              for (int i = 0; i < 16; ++i) v[g][i] = 0u;
             }
-            const uint32_t u0 = static_cast<uint32_t>(g * 2);
-            *reinterpret_cast<uint4 *>(row + (((u0 + 0) ^ row_sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4 *>(row + (((u0 + 1) ^ row_sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-          } else {
-            const uint32_t u0 = static_cast<uint32_t>(g * 4);
+          }
+          if (!zero) tmem_ld_wait();
+          uint8_t *row = pst + lane * T::kBoxBytes;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4 *>(row + (((u0 + q) ^ row_sw) << 4)) =
-                  make_uint4(v[g][4 * q], v[g][4 * q + 1], v[g][4 * q + 2], v[g][4 * q + 3]);
+          for (int g = 0; g < kBoxCols / 16; ++g) {
+            if constexpr (OUT_BF16) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const __nv_bfloat162 b2 =
+                    __floats2bfloat162_rn(__uint_as_float(v[g][2 * i]), __uint_as_float(v[g][2 * i + 1]));
+                w[i] = *reinterpret_cast<const uint32_t *>(&b2);
+              }
+              const uint32_t u0 = static_cast<uint32_t>(g * 2);
+              *reinterpret_cast<uint4 *>(row + (((u0 + 0) ^ row_sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4 *>(row + (((u0 + 1) ^ row_sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+              const uint32_t u0 = static_cast<uint32_t>(g * 4);
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4 *>(row + (((u0 + q) ^ row_sw) << 4)) =
+                    make_uint4(v[g][4 * q], v[g][4 * q + 1], v[g][4 * q + 2], v[g][4 * q + 3]);
+            }
+          }
+          if (box == T::kParts * kBoxes - 1) tc_fence_before_sync();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (box == T::kParts * kBoxes - 1) mbar_arrive(acce0 + 8 * buf);
+            const int y = n0 + h * 128;
+            if (y < p.N && m0 + c0 < p.M) tma_store_2d(&tmY, smem_addr(pst), m0 + c0, y);
+            bulk_commit_group();
           }
         }
-        if (box == T::kParts * kBoxes - 1) tc_fence_before_sync();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (box == T::kParts * kBoxes - 1) mbar_arrive(acce0 + 8 * buf);
-          const int y = n0 + h * 128;
-          if (y < p.N && m0 + c0 < p.M) tma_store_2d(&tmY, smem_addr(pst), m0 + c0, y);
-          bulk_commit_group();
-        }
+        ++tcount;
       }
-      ++tcount;
     }
     if (lane == 0) bulk_wait_group0();
   }

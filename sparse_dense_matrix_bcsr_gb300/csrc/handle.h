@@ -33,7 +33,7 @@ EncodeTiledFn encode_fn();
 spmm_status encode_2d(CUtensorMap *map, const void *base, bool bf16, uint64_t rows, uint64_t cols,
                       uint64_t pitch_elems, uint32_t box_rows, uint32_t box_cols, uint32_t swizzle_bytes = 128);
 spmm_status encode_3d(CUtensorMap *map, const void *base, bool bf16, uint64_t n, uint64_t rows, uint64_t cols,
-                      uint32_t box_n, uint32_t box_rows, uint32_t box_cols = 64, uint32_t swizzle_bytes = 128);
+                      uint32_t box_n, uint32_t box_rows);
 spmm_status encode_x(CUtensorMap *map, const void *base, bool bf16, uint64_t rows, uint64_t cols);
 spmm_status encode_y(CUtensorMap *map, void *base, bool bf16, uint64_t rows, uint64_t cols, int tile_rows);
 

@@ -371,20 +371,9 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
-// The same with some of the accumulator's lanes left as they are: bit l of
-// off[w] set keeps lane 32 w + l (row 32 w + l of an M = 128 product) out of the
-// update, whatever the operands hold there.
-__device__ __forceinline__ void umma_f16_lanes(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                               uint32_t accumulate, const uint32_t (&off)[4]) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
-      : "memory");
-}
-
-// The same issued by a whole converged warp.
+// The same issued by a whole converged warp, with some of the accumulator's lanes left as
+// they are: bit l of off[w] set keeps lane 32 w + l (row 32 w + l of an M = 128 product) out
+// of the update, whatever the operands hold there.
 __device__ __forceinline__ void umma_f16_lanes_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                      uint32_t accumulate, const uint32_t (&off)[4]) {
   asm volatile(
@@ -396,7 +385,7 @@ __device__ __forceinline__ void umma_f16_lanes_elect(uint32_t d_tmem, uint64_t a
       : "memory");
 }
 
-// Lanes [begin, end) of an M = 128 product enabled, as umma_f16_lanes takes them.
+// Lanes [begin, end) of an M = 128 product enabled, as umma_f16_lanes_elect takes them.
 __device__ __forceinline__ void lanes_off(int begin, int end, uint32_t (&off)[4]) {
 #pragma unroll
   for (int w = 0; w < 4; ++w) {

@@ -81,18 +81,18 @@ spmm_status encode_2d(CUtensorMap *map, const void *base, bool bf16, uint64_t ro
 
 // `n` matrices of rows x cols 16-bit elements one after another, as a 3-D tensor:
 // a box reads zeros past the end of its own matrix, not the next one's rows.
-// Boxes of box_n x box_rows x box_cols, swizzled in the width of box_cols.
+// Boxes of box_n x box_rows x 64, 128-byte swizzle.
 spmm_status encode_3d(CUtensorMap *map, const void *base, bool bf16, uint64_t n, uint64_t rows, uint64_t cols,
-                      uint32_t box_n, uint32_t box_rows, uint32_t box_cols, uint32_t swizzle_bytes) {
+                      uint32_t box_n, uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(SPMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   cuuint64_t dims[3] = {cols, rows, n};
   cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
-  cuuint32_t box[3] = {box_cols, box_rows, box_n};
+  cuuint32_t box[3] = {64, box_rows, box_n};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                   const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle_enum(swizzle_bytes), CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SPMM_ERR_CUDA, "cuTensorMapEncodeTiled (3-D) failed (%d)", static_cast<int>(r));
   return SPMM_OK;
 }
