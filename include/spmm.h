@@ -407,8 +407,8 @@ spmm_status spmm_run_linear_adapters(spmm_handle h, spmm_adapters a, const void 
  *     d_up_a = sum_n dY[n] h[n]^T       d_down_a = sum_n dh[n] X[n]^T
  * the sums over the rows of adapter a, in a fixed order.  On the way h and dh are the
  * sums of three values of in_t; for fp16 those of up to 128 rows of a segment share a
- * power of two in d_up and d_down, where an h below 2^-16 of their largest has fewer
- * than fp32's 24 bits.
+ * power of two in d_up and d_down, where an h below 2^-12 of their largest has fewer
+ * than fp32's 24 bits (36 less what it lies below).
  *   h_t      a BCSR handle of A^T (k x m), of the set's in_t; dX has its out_t.
  *   X, dY    N x k and N x m row-major, in_t, 16-byte aligned.
  *   dX       N x k, or NULL where no gradient of the input is wanted.

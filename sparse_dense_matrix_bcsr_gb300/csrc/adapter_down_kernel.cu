@@ -82,11 +82,14 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
 }
 
 // Powers of two that the fp16 values of a group are multiplied and divided by, from the
-// bits of its largest finite |h|: a value of 2^e .. 2^(e + 1) comes to 2^14 .. 2^15.
+// bits of its largest finite |h|: a value of 2^e .. 2^(e + 1) comes to 2^14 .. 2^15, a
+// piece's, whose e is rounded up to 2, 6, 10, ..., to 2^11 .. 2^15 (so that pieces whose
+// largest values lie about 4, those of h's scale, share a power).
 struct Power {
   float down, up;
-  __device__ __forceinline__ explicit Power(uint32_t max_bits) {
-    const uint32_t e = max(max_bits >> 23, 40u);  // zeros and values below 2^-87: as 2^-87
+  __device__ __forceinline__ explicit Power(uint32_t max_bits, bool piece = false) {
+    uint32_t e = max(max_bits >> 23, 40u);  // zeros and values below 2^-87: as 2^-87
+    if (piece) e = (e + 2) / 4 * 4 + 1;  // biased by 127
     down = __uint_as_float((268u - e) << 23);
     up = __uint_as_float((e - 14u) << 23);
   }
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
             for (int w = 0; w < 4; ++w) piece_top = max(piece_top, mi->row_max[w]);
           }
         }
-        const Power row(top), all(piece_top);
+        const Power row(top), all(piece_top, true);
         if (mine && ok) {
           if (!BF16 && job.rows) p.row_scale[row0 + r] = row.up;
           if (!BF16 && job.sums) job.sum_scale[row0 + r] = all.up;
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const __grid_
           cluster_sync();
           for (int c = 0; c < p.split; ++c) piece_top = max(piece_top, cluster_load_u32(cluster_map(smem_addr(&mi->piece_max), c)));
         }
-        const Power all(piece_top);
+        const Power all(piece_top, true);
         each([&](int r, int j, int at) {
           const Power row(mi->row_max[r]);
           const float4 *own = reinterpret_cast<const float4 *>(smem + at);

@@ -6,15 +6,15 @@
 // kernel does both: the rows are the MMA's K, 128 features of V the M operand
 // and the ranks the N operand, both MN-major as they lie in memory.
 //
-// Work item = (128 features, adapter).  A stage is 64 or 32 rows of one segment (a TMA
+// Work item = (128 features, adapter).  A stage is 64, 48 or 32 rows of one segment (a TMA
 // box may start at any row), so K never runs across a segment; the rows after a
 // segment's end that the last box brings are zeroed in shared memory in both
 // operands before the MMA, as neither operand may hold another request's
-// infinities.  With fp16 a stage does not run across the pieces either that S is divided by
-// powers of two in (see kHParts), and each piece's sums are taken out and multiplied by
-// its power.  Every element of dY and X is read once, so HBM bounds the kernel;
-// S is read again by every feature tile, from L2.  16384 rows of 4 adapters of rank
-// 64, 18944 + 3584 features: 117 us, 6.3 TB/s of activations.
+// infinities.  With fp16 a stage does not run either from one power of two that S is
+// divided by to another (see kHParts), and the sums are taken out and multiplied where the
+// power changes (every piece by itself: 402 us for 301 with 16384 rows of 4 adapters of rank
+// 64, 18944 x 3584, the down projections among them; bf16 279).  Every element of dY and X is read once, so HBM bounds the kernel;
+// S is read again by every feature tile, from L2.
 //
 // S comes in kHParts 16-bit parts, 24 bits of bf16 together, whose sums are added at
 // the end: with h and dh rounded to two, sums that cancel kept 16 bits of theirs.
@@ -71,13 +71,11 @@ constexpr int kNbuf = 2;              // accumulators, where two CTAs have the c
 
 constexpr int kTurnRows = 1024;       // rows between two drains of an accumulator
 constexpr int32_t kTurnSums = 1, kTurnLast = 2;  // it has sums; it is the item's last
-constexpr int32_t kPieceEnd = 1 << 16;
 
 struct Misc {
   uint64_t full[kMaxQ], empty[kMaxQ], acc_full[kNbuf], acc_empty[kNbuf], drained;
-  int32_t rows[kMaxQ];  // rows of the stage, 0: the item has no more stages; fp16: kPieceEnd with a piece's last
-  int32_t row[kMaxQ];   // its first row
-  int32_t turn_row[kNbuf];  // a row of what the accumulator holds
+  int32_t rows[kMaxQ];  // rows of the stage, 0: the item has no more stages
+  float by[kMaxQ], turn_by[kNbuf];  // fp16: what the rows of S in a stage, and in an accumulator, were divided by
   uint32_t tmem;
   int32_t turn[kNbuf];  // what the accumulator holds: kTurnSums | kTurnLast
   volatile int32_t abort_flag;
@@ -194,25 +192,36 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
       auto walk = [&](int64_t begin, int64_t end, int32_t adapter) {
         begin = max(begin, int64_t{0});
         end = min(end, static_cast<int64_t>(p.N));
-        uint32_t todo = __ballot_sync(0xffffffffu, begin < end && adapter == item.a);
+        const bool mine = begin < end && adapter == item.a;
+        uint32_t todo = __ballot_sync(0xffffffffu, mine);
+        // fp16: the power of two of the piece that a row lies in
+        const float *powers = item.up ? p.h_scale : p.dh_scale;
+        const float first_power = !BF16 && mine ? powers[begin] : 1.0f;
         while (todo && ok) {
           const int i = __ffs(todo) - 1;
           todo &= todo - 1;
           const int32_t sb = __shfl_sync(0xffffffffu, static_cast<int32_t>(begin), i);
           const int32_t se = __shfl_sync(0xffffffffu, static_cast<int32_t>(end), i);
-          int32_t next = sb;
+          // where the piece of row n ends, and the next one's power, read ahead
+          int32_t piece_end = (sb / kPieceRows + 1) * kPieceRows, next = sb;
+          float power = __shfl_sync(0xffffffffu, first_power, i), next_power = !BF16 && piece_end < se ? powers[piece_end] : 1.0f;
           for (int32_t n = sb; n < se; n = next) {
             next = se - n > stage_k ? n + stage_k : se;
-            const int32_t piece_end = (n / kPieceRows + 1) * kPieceRows;
-            if (!BF16) next = min(next, piece_end);
+            const float by = power;
+            if (!BF16 && next >= piece_end) {
+              if (next_power != power) next = piece_end;
+              power = next_power;
+              piece_end += kPieceRows;
+              if (piece_end < se) next_power = powers[piece_end];
+            }
             const bool take = turn == part;
             if (++turn == split) turn = 0;
             if (!take) continue;
             ok = claim();
             if (!ok) break;
             if (lane == 0) {
-              mi->rows[stage] = (next - n) | (!BF16 && (SPLIT || next == se || next == piece_end) ? kPieceEnd : 0);
-              mi->row[stage] = n;
+              mi->rows[stage] = next - n;
+              if (!BF16) mi->by[stage] = by;
               const uint32_t fb = smem_addr(&mi->full[stage]);
               const uint32_t st = smem_addr(smem + stage * stage_bytes);
               mbar_arrive_expect_tx(fb, stage_bytes);
@@ -264,12 +273,17 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
         if (!ok) break;
         tc_fence_after_sync();
         int stages = 0;
+        float by = 1.0f;
         while (stages < turn_stages) {
           ok = wait_phase(mi->full[stage], phase);
           if (!ok) break;
-          const int32_t rec = mi->rows[stage], rows = rec & (kPieceEnd - 1);
-          if (!BF16 && lane == 0 && rows > 0) mi->turn_row[buf] = mi->row[stage];
+          const int32_t rows = mi->rows[stage];
           last = rows == 0;
+          if (!BF16 && !last) {  // one power of two a turn
+            const float next_by = mi->by[stage];
+            if (stages > 0 && next_by != by) break;
+            by = next_by;
+          }
           if (!last) {
             const int steps = (rows + 15) / 16;
             if (rows % 16 != 0) {
@@ -298,10 +312,11 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
             stage = 0;
             phase ^= 1u;
           }
-          if (last || (!BF16 && rec & kPieceEnd)) break;
+          if (last) break;
         }
         if (!ok) break;
         if (lane == 0) {
+          if (!BF16) mi->turn_by[buf] = by;
           mi->turn[buf] = (stages > 0 ? kTurnSums : 0) | (last ? kTurnLast : 0);
           mbar_arrive(smem_addr(&mi->acc_full[buf]));
         }
@@ -334,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_wgrad_kernel(const __grid
         turn = mi->turn[buf];
         if (turn & kTurnSums) {
           const uint32_t at = tmem + buf * acc_cols + (static_cast<uint32_t>(sp * 32) << 16);
-          const float by = BF16 ? 1.0f : (item.up ? p.h_scale : p.dh_scale)[mi->turn_row[buf]];
+          const float by = BF16 ? 1.0f : mi->turn_by[buf];
 #pragma unroll
           for (int c0 = 0; c0 < RANKS; c0 += 16) {
             if (c0 >= n16) break;

@@ -130,11 +130,12 @@ struct TileSegment {
 // that one did, 24 bits of bf16 (one part alone moved a bf16 Y by 1.2e-3 of it where the
 // adapters are most of it, two hold 16 bits).
 // fp16 has neither fp32's range nor bits below 2^-24, so there h is first divided by a
-// power of two that brings the largest finite value of its group to 2^14 .. 2^15, and the
-// product's sums are multiplied by it: three parts then hold 24 bits of everything down to
-// 2^-16 of that value.  The group is a row where the product's rows are H's (Y, dX), so
-// that rows stay independent, and a piece of kPieceRows or less of a segment's rows where
-// it sums over them (the weights' gradients).
+// power of two that brings the largest finite value of its group close to fp16's largest,
+// and the product's sums are multiplied by it.  The group is a row where the product's rows
+// are H's (Y, dX), so that rows stay independent: three parts then hold 24 bits of everything
+// down to 2^-16 of the row's largest.  It is a piece of kPieceRows or less of a segment's
+// rows where the product sums over them (the weights' gradients), with powers of 16, so that
+// pieces in a row mostly share one and need not be summed apart: 24 bits down to 2^-12.
 constexpr int kHParts = 3;
 constexpr int kPieceRows = 128;  // pieces end at multiples of it
 // Ranks in H's rows, a whole number of MMA steps; those past the rank hold zeros.

@@ -309,3 +309,26 @@ def test_millions_of_single_rows(S):
         assert torch.equal(Y[at].double(), want)
     layer.close()
     aset.close()
+
+
+@pytest.mark.parametrize("rank", [16, 64, 80, 128])
+def test_weight_gradients_of_rows_of_changing_size_f16(S, rank):
+    """Every other 128 rows are 2^6 smaller, so that the powers that h is divided by change within segments and between
+    them.  Sums are exact still, and the result is their rounding to fp16."""
+    import torch
+    n, m, k = 1500, 456, 328
+    for up in (True, False):
+        c, rng = zero_weight(m, k, n, even(ragged(n, 6, 2, none=0.0)), rank, 2, "f16", "bf16", 1.0)
+        dt, width = c.X.dtype, k if up else m
+        weights = whole(rng, (2, rank, width))
+        weights[:, :, :8] = whole(rng, (2, rank, 8), 1, 16)
+        big = paired_rows(c, rng, width)
+        big[torch.arange(n) // 128 % 2 == 1] *= 2.0 ** -6
+        big, one = big.to(dt), row_signs(c, m if up else k).to(dt)
+        c.X, c.dY = (big, one) if up else (one, big)
+        c.down = (weights if up else torch_zeros(2, rank, k)).to(dt)
+        c.up = (torch_zeros(2, m, rank) if up else weights.transpose(1, 2).contiguous()).to(dt)
+        name = "d_up" if up else "d_down"
+        want = c.reference_grad()[name][0]
+        assert want.abs().max() < 2048 and (want != want.round()).any()
+        assert torch.equal(run_grad(S, c, with_dx=False)[name], want.to(dt)), name
