@@ -364,8 +364,9 @@ spmm_status spmm_wcsr_noalloc_check(void *stream);
  *   max_rows, max_segments   the largest batch that calls will bring (below 2^30
  *                 rows, 2^27 segments).
  *   grad          nonzero to hold the workspace of spmm_adapters_grad too.
- * The workspace is rank values per row (twice with grad) and copies of up to 1024
- * rows of X and Y (and dX), as short batches are sorted by adapter.
+ * The workspace is, for each row, 6 bytes a rank (rank rounded up to 16; twice with grad,
+ * three times for F16 with grad) and 16 (F16: 20, with grad 28), and copies of up to 1024 rows
+ * of X and Y (and dX), 2 k + 4 m (+ 4 k) bytes each, as short batches are sorted by adapter.
  * Errors: INVALID_ARG, UNSUPPORTED (m, k or rank not a multiple of 8, rank
  * above 128), OOM, CUDA.  spmm_adapters_destroy waits for the device and frees
  * the set.

@@ -14,7 +14,8 @@
 // divided by to another (see kHParts), and the sums are taken out and multiplied where the
 // power changes (every piece by itself: 402 us for 301 with 16384 rows of 4 adapters of rank
 // 64, 18944 x 3584, the down projections among them; bf16 279).  Every element of dY and X is read once, so HBM bounds the kernel;
-// S is read again by every feature tile, from L2.
+// S is read again by every feature tile, from L2.  16384 rows of 4 adapters of rank
+// 64, 18944 + 3584 features: 152 us, 4.9 TB/s of activations.
 //
 // S comes in kHParts 16-bit parts, 24 bits of bf16 together, whose sums are added at
 // the end: with h and dh rounded to two, sums that cancel kept 16 bits of theirs.
@@ -425,12 +426,12 @@ cudaError_t launch_adapter_wgrad(AdapterWgradParams p, int num_sms, bool bf16, c
   p.tiles = p.up_tiles + (p.K + kFeat - 1) / kFeat;
   // Items of adapters that can have rows.  While clusters of twice the size still fit
   // beside each other and leave each CTA at least four stages, they are the faster
-  // (us with 1 / 2 / 4 / 8 CTAs an item and one part of S, 16384 rows; 16 items, rank 64: 96 / 60 / 43 /
-  // 36; 64 items, rank 16: 69 / 46 / 41 / 49; 128 items, rank 64: 67 / 53 / 63 / 95); with
-  // more items they only wait for one another (176: 119 / 153 / 150 / 179; 256: 61 / 58 /
-  // 79 / 135, and 30 / 34 / 48 / 76 for 4096 rows).  Clusters are not persistent, so the
-  // items of adapters without rows limit them too (one adapter of 28 with 740 rows, 143
-  // tiles: 25 / 135).
+  // (us with 1 / 2 / 4 / 8 CTAs an item, 16384 rows, the down projections among them; 16
+  // items, rank 64: 182 / 112 / 77 / 63; 64 items, rank 16: 179 / 117 / 90 / 110; 128 items, rank
+  // 64: 271 / 201 / 222 / 281); with more items they only wait for one another (176: 316 /
+  // 331 / 315 / 356; 256: 200 / 212 / 244 / 324, and 67 / 78 / 103 / 158 for 4096 rows).  Clusters
+  // are not persistent, so the items of adapters without rows limit them too (one adapter
+  // of 28 with 740 rows, 176 tiles: 42 / 153).
   const int64_t active = p.n_seg < p.n_adapters ? (p.n_seg > 0 ? p.n_seg : 1) : p.n_adapters;
   p.split = 1;
   while (p.split < 8 && p.tiles * active * p.split * 2 <= 2ll * num_sms && p.N >= 512ll * active * p.split &&
