@@ -21,11 +21,11 @@
 // The gradient wants two such products of a batch, of X and of dY: one launch
 // runs both, so that short batches fill the GPU with their sum.
 //
-// H is kept in 16-bit parts (the value rounded, the rest rounded, ...), kHParts of them,
-// 24 bits of bf16 (two of bf16, 16 bits, left 1.2e-6 of an fp32 Y off where the adapters
-// are most of it, three 0.6e-6).  The sums leave the tensor cores, which cut what an fp32 sum shifts out instead of
-// rounding it (~1e-9 of the sum for every term), every kTurn stages and are added
-// in registers.
+// H is kept in 16-bit parts (the value in 16 bits, the rest in 16 bits, ...), kHParts of
+// them, all 24 bits of a float (two of bf16, 16 bits, left 1.2e-6 of an fp32 Y off where
+// the adapters are most of it, three 0.6e-6).  The sums leave the tensor cores, which cut
+// what an fp32 sum shifts out instead of rounding it (~1e-9 of the sum for every term),
+// every kTurn stages and are added in registers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -65,15 +65,13 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc area");
 
+// Two values as 16-bit parts.  bf16: cut, not rounded: three times 8 bits are a float's 24, and
+// no finite value becomes infinite.
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (BF16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
-  } else {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
-  }
+  if constexpr (BF16) return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&v);
 }
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t u) {
@@ -101,8 +99,8 @@ __device__ __forceinline__ uint32_t finite_bits(float v) {
 
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// Eight ranks of one row of H, rounded; a further part holds what the roundings
-// before it left (nothing of what is infinite in 16 bits).  Ranks past the last are zeros.
+// Eight ranks of one row of H in parts; a further part holds what the ones
+// before it left (nothing of what is infinite).  Ranks past the last are zeros.
 template <bool BF16>
 __device__ __forceinline__ void store_h(uint16_t *H, int64_t row, int32_t rank, int32_t j, const float (&h)[8], float by) {
   const int pitch = rank16(rank);

@@ -332,3 +332,15 @@ def test_weight_gradients_of_rows_of_changing_size_f16(S, rank):
         want = c.reference_grad()[name][0]
         assert want.abs().max() < 2048 and (want != want.round()).any()
         assert torch.equal(run_grad(S, c, with_dx=False)[name], want.to(dt)), name
+
+
+@pytest.mark.parametrize("n", [4, 300])
+def test_h_at_the_end_of_the_range(S, n):
+    """An h above bf16's largest number and below fp32's: 1.998 * 2^127, times up's 2^-100."""
+    import torch
+    c, _ = zero_weight(256, 200, n, ([0, n], [0]), 16, 1, "bf16", "f32", 1.0)
+    c.X, c.down, c.up = c.X * 0, c.down * 0, torch.full_like(c.up, 2.0 ** -100)
+    c.X[:, 0], c.X[:, 1] = 1.9921875 * 2.0 ** 63, 1.5 * 2.0 ** 59
+    c.down[0, 3, 0], c.down[0, 3, 1] = 2.0 ** 64, 2.0 ** 60
+    want = c.reference()[0]
+    assert torch.equal(run(S, c)[0].double(), want) and float(want.max()) == 1.998046875 * 2.0 ** 27
