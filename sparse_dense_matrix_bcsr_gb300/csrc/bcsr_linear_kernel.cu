@@ -53,12 +53,14 @@
 // 18944 features.  The gradient's dX takes D_a where the forward pass takes U_a,
 // as it lies (MN-major).
 //
-// A stage of an adapter loads H by 128 rows, segments of at most two boxes of 16 rows by
+// A stage of an adapter loads H by 128 rows, segments of at most four boxes of 16 rows by
 // 16: in short batches every CTA reads the same lines of H for every adapter, and L2 cannot
 // serve them fast enough (dX of 79 rows with 38 adapters, 13752 features, one part of H: 229
 // us, by 16 rows 122; gradient of 230 rows with 59, 672 x 6984: 306 and 136); in longer ones
-// the small boxes write less to shared memory (8192 rows in 500 segments, 18944 x 3584: 522 us
-// for 536; 2048 in 128: 159 for 169).
+// the small boxes write less to shared memory and up to three of them share a stage
+// (18944 x 3584, 8192 rows of rank 64 in 500 segments: 873 us, with at most two boxes 905,
+// with two columns of boxes a stage as for long segments 1065; 2048 of rank 128 in 40: 209, 226
+// and 248; of rank 16, whose H is one box, 2 % slower for the bookkeeping).
 //
 // The tensor cores cut what their fp32 sums shift out instead of rounding it, ~1e-9
 // of the result for every term.  With adapters the accumulator is therefore handed to the
@@ -96,7 +98,14 @@ constexpr int kThreads = 192;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp0 = 2, kEpiWarps = 4;
 constexpr int kMiscBytes = 1024;
 constexpr int kHBytes = 128 * 128;               // a box of H: 128 rows x 64 columns
-constexpr int kFewRows = kAdapterFewRows, kFewBoxes = 2;  // boxes of H for short segments
+// Boxes of H for short segments of up to kFewBoxes of them, kFewBytes of shared memory.
+constexpr int kFewRows = kAdapterFewRows, kFewBoxes = 4, kFewBytes = kFewBoxes * kFewRows * 128;
+// The segment begin .. end lies in part h0 and in kFewBoxes of its boxes, from `first` on.
+__device__ __forceinline__ bool few_boxes(int begin, int end, int h0, int &first, int &count) {
+  first = (begin - h0 * 128) / kFewRows;
+  count = (end - h0 * 128 + kFewRows - 1) / kFewRows - first;
+  return end <= (h0 + 1) * 128 && count <= kFewBoxes;
+}
 
 // A tile of ROWS rows of X, CTAS CTAs per SM.
 template <int ROWS, int CTAS>
@@ -110,6 +119,7 @@ struct Tile {
   static constexpr int kTmemCols = kNbuf * kAccCols;
   static constexpr int kBoxBytes = ROWS == 256 ? 128 : 64;     // bytes of Y per row of a store box (32 rows)
   static constexpr int kStagingBytes = kEpiWarps * 32 * kBoxBytes;  // one staging buffer per warp
+  static_assert(kXBytes >= 2 * kFewBytes + kHBytes, "the rows that a short segment's MMAs read lie in its stage");
   static constexpr int kSmemBytes = kQ * kStageBytes + kStagingBytes + kMiscBytes + 1024;
   static constexpr int kGroup = 2048 / ROWS;                   // tiles of X that a block row takes in a row
   static_assert(CTAS * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of an SM");
@@ -344,7 +354,10 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
             for (int i = 0; i < cnt && ok; ++i) {
               const int32_t a = __shfl_sync(0xffffffffu, my.adapter, i);
               const int32_t begin = __shfl_sync(0xffffffffu, my.begin, i), end = __shfl_sync(0xffffffffu, my.end, i);
-              const int h0 = begin / 128, h1 = (end + 127) / 128, nh = h1 - h0, per = T::kParts / nh;
+              const int h0 = begin / 128, h1 = (end + 127) / 128, nh = h1 - h0;
+              int first, count;
+              const bool few = few_boxes(begin, end, h0, first, count);
+              const int per = few ? ad.boxes : T::kParts / nh;  // boxes of H a stage
               for (int32_t g = 0; g < ad.groups && ok; ++g) {
                 for (int32_t b0 = 0; b0 < ad.boxes; b0 += per) {
                   const int32_t nb = min(ad.boxes - b0, per);
@@ -355,11 +368,7 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
                     tile_rec[stage] = TileRec{br, nt, last ? kRecLast : 0, b0 | nb << 8 | g << 16, begin | end << 16, {}};
                     const uint32_t fb = full0 + 8 * stage;
                     const uint32_t st = smem_addr(smem + stage * kStageBytes);
-                    // Segments of a few rows can come in boxes of kFewRows: the ones of part h0 that hold them
-                    const int first = (begin - h0 * 128) / kFewRows;
-                    const int small = nh == 1 ? (min(end - h0 * 128, 128) + kFewRows - 1) / kFewRows - first : kFewBoxes + 1;
-                    const bool few = small <= kFewBoxes;
-                    mbar_arrive_expect_tx(fb, kBlk * ad.u_cols * 2 + nb * (few ? small * kFewRows * 128 : nh * kHBytes));
+                    mbar_arrive_expect_tx(fb, kBlk * ad.u_cols * 2 + nb * (few ? count * kFewRows * 128 : nh * kHBytes));
                     if (ad.u_transposed)
                       tma_load_3d(st, &ad.tmU, fb, br * kBlk, g * 64, a);
                     else
@@ -367,9 +376,9 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
                     const int row0 = nt * kTileN;
                     for (int32_t b = b0; b < b0 + nb; ++b) {
                       const int32_t x = ad.groups > 1 ? g * 64 : b * 64, y = ad.groups > 1 ? b : 0;
-                      const uint32_t at = st + kBlkBytes + (b - b0) * nh * kHBytes;
+                      const uint32_t at = st + kBlkBytes + (b - b0) * (few ? kFewBytes : nh * kHBytes);
                       if (few)
-                        for (int r = first; r < first + small; ++r)
+                        for (int r = first; r < first + count; ++r)
                           tma_load_3d(at + r * (kFewRows * 128), &ad.tmHs, fb, x, y, row0 + h0 * 128 + r * kFewRows);
                       else
                         for (int h = h0; h < h1; ++h) tma_load_3d(at + (h - h0) * kHBytes, &ad.tmH, fb, x, y, row0 + h * 128);
@@ -503,15 +512,17 @@ __global__ void __launch_bounds__(kThreads, T::kCtas)
             const uint64_t bdesc0 = smem_desc_add(u_desc, stage * kStageBytes);
             const uint64_t adesc0 = smem_desc_add(x_desc, stage * kStageBytes);
             // the stage's steps: 16 columns of H (16 ranks of one of its parts) by the same
-            // ranks of U; box b starts b * nh * kHBytes after H's first
-            const int nh = h1 - h0;
+            // ranks of U.  A short segment's boxes lie closer than the 128 rows that an MMA
+            // reads: the lanes of the other rows are masked, whatever lies there.
+            int first, count;
+            const int box_bytes = few_boxes(begin, end, h0, first, count) ? kFewBytes : (h1 - h0) * kHBytes;
             auto steps = [&](auto &&mma) {
               uint32_t accumulate = kScaled && seg.stages >> 16 == 0 && b0 == 0 ? 0 : 1;  // the segment's first step
               for (int b = 0; b < nb; ++b) {
                 const int x = ad.groups > 1 ? (seg.stages >> 16) * 64 : (b0 + b) * 64;
                 const int n = min(ad.cols - x, 64) / 16;
                 int u = ad.groups > 1 ? 0 : static_cast<int>(static_cast<uint32_t>(x / 16) % static_cast<uint32_t>(ad.u_steps));
-                uint64_t adesc = smem_desc_add(adesc0, b * nh * kHBytes);
+                uint64_t adesc = smem_desc_add(adesc0, b * box_bytes);
                 for (int k = 0; k < n; ++k) {
                   mma(adesc, smem_desc_add(bdesc0, u * u_step), accumulate);
                   accumulate = 1;
