@@ -69,8 +69,8 @@
 // 6.6e-7 off in place of 2.7e-6 with 777 rows of 8192 x 8192, 75 % zero blocks (90 us
 // either way), and in place of 2.2e-5 with 18944 dense columns; 3584 x 18944, 16384
 // rows, 409 for 398 us.  Every 4 blocks: 3.8e-7, and up to 4 % slower; every 16:
-// 1.2e-6 and as fast as 8.  bf16, every 64: block rows of 148 blocks take 326 for 307 us
-// (4096 rows), of 30 424 for 430.  Tiles of 512 rows, whose sums the registers cannot hold,
+// 1.2e-6 and as fast as 8.  bf16, every 64: 326 us for 307 with block rows of 148 blocks
+// (4096 rows), 430 for 424 with 30, whose sums pass the registers too (16384 rows).  Tiles of 512 rows, whose sums the registers cannot hold,
 // are only for layers whose longest block row is one turn (an fp32 Y of 65536 rows, 18944 x
 // 3584, block rows of up to 14: 1876 for 1746).
 //
